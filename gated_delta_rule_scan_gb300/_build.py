@@ -1,8 +1,9 @@
-"""Build libkda.so in-tree with nvcc for sm_103a (GB300).
+"""Build libkda.so in-tree with nvcc for sm_103a (GB300), and _kda_native.so, the CPython
+marshalling of its latency-bound entry points, with g++ against the installed torch.
 
-One nvcc process per translation unit, run in parallel, then one link.  The library statically
-links the CUDA runtime and reaches the driver's tensor-map encoder through the runtime's entry
-point query, so it needs no libcuda at link time.
+One compiler process per translation unit, run in parallel, then one link each.  The library
+statically links the CUDA runtime and reaches the driver's tensor-map encoder through the runtime's
+entry point query, so it needs no libcuda at link time.
 """
 
 from __future__ import annotations
@@ -10,6 +11,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
+NATIVE_PATH = os.path.join(PKG, "_kda_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-I" + os.path.join(ROOT, "include")]
@@ -34,10 +37,32 @@ def _newest_source_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _run(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{' '.join(cmd[:2])} failed:\n{r.stderr}")
+
+
+def _compile_native():
+    """kda_native.cpp's object file and torch's library folder."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    obj = os.path.join(BUILD_DIR, "kda_native.cpp.o")
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I" + os.path.join(root, "include"),
+          "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          "-I" + sysconfig.get_paths()["include"],
+          "-c", os.path.join(CSRC, "kda_native.cpp"), "-o", obj])
+    return obj, os.path.join(root, "lib")
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile every csrc/*.cu for sm_103a and link gated_delta_rule_scan_gb300/libkda.so."""
-    if (not force and os.path.exists(LIB_PATH)
-            and os.path.getmtime(LIB_PATH) >= _newest_source_mtime()):
+    """Compile every csrc/*.cu for sm_103a and link gated_delta_rule_scan_gb300/libkda.so, and
+    csrc/kda_native.cpp into _kda_native.so beside it."""
+    newest = _newest_source_mtime()
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest
+                         for p in (LIB_PATH, NATIVE_PATH)):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -54,13 +79,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        native = ex.submit(_compile_native)
         objs = list(ex.map(compile_one, srcs))
+        native_obj, torch_lib = native.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    # torch's libraries are loaded before this one; libkda.so is found beside it
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, native_obj, "-L" + PKG, "-l:libkda.so", "-L" + torch_lib,
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, NATIVE_PATH)
     return LIB_PATH
 
 

@@ -17,6 +17,7 @@ __device__ int g_kda_dev_err;
 
 constexpr int kMaxGridY = 65535;  // sequences (and heads) map to gridDim.y
 constexpr int kMaxValueWidth = 1024;   // widest value head: 8 sub-heads of 128
+constexpr long kMaxRingRow = 1L << 28; // floats of one conv ring row of the state pool
 
 // the current device's error word (its address is looked up once per device)
 int* dev_err_ptr() {
@@ -61,6 +62,11 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool overlap(const void* a, const void* b, size_t bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + bytes && y < x + bytes;
+}
+
+inline bool overlap2(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
 }
 
 int check_cu(const int* cu_host, int N, long total) {
@@ -362,6 +368,47 @@ int decode_impl(const void* q_raw, const void* k_raw, const void* v_raw, int raw
 }
 
 
+
+// One row move between an f32 state array and the pool (store: state -> pool).
+int state_q8_impl(bool store, const float* state, float* state_out, void* codes, float* scales,
+                  int format, const int* state_rows, const int* slots, int S, int P, int N, int H,
+                  int Dk, int Dv, const float* ring_src, float* ring_dst, long ring_row,
+                  void* stream) {
+    if (Dk != kHeadDim || Dv <= 0 || Dv % kHeadDim != 0 || Dv > kMaxValueWidth)
+        return KDA_ERR_HEAD_DIM;
+    const long units = (long)H * (Dv / kHeadDim);
+    if (N < 0 || N > kMaxGridY || S < 0 || P < 0 || H <= 0 || units > kMaxGridY) return KDA_ERR_SHAPE;
+    if (format != KDA_Q8_INT8 && format != KDA_Q8_E4M3) return KDA_ERR_ENUM;
+    if (ring_row < 0 || ring_row % 4 != 0 || ring_row > kMaxRingRow) return KDA_ERR_SHAPE;
+    // without an index array row n is row n
+    if ((state_rows == nullptr && N > S) || (slots == nullptr && N > P)) return KDA_ERR_SHAPE;
+    if (N == 0) return KDA_OK;
+    const float* st = store ? state : state_out;
+    if (!st || !codes || !scales) return KDA_ERR_NULL;
+    if (ring_row > 0 && (!ring_src || !ring_dst)) return KDA_ERR_NULL;
+    if (!aligned16(st) || !aligned16(codes) || !aligned16(scales)) return KDA_ERR_ALIGN;
+    if (ring_row > 0 && (!aligned16(ring_src) || !aligned16(ring_dst))) return KDA_ERR_ALIGN;
+    const size_t row = (size_t)units * kHeadDim;
+    const int rows_src = store ? S : P, rows_dst = store ? P : S;
+    if (overlap2(st, S * row * kHeadDim * 4, codes, P * row * kHeadDim) ||
+        overlap2(st, S * row * kHeadDim * 4, scales, P * row * 4) ||
+        overlap2(codes, P * row * kHeadDim, scales, P * row * 4) ||
+        (ring_row > 0 && overlap2(ring_src, (size_t)rows_src * ring_row * 4, ring_dst,
+                                  (size_t)rows_dst * ring_row * 4)))
+        return KDA_ERR_STATE_ALIAS;
+    if (const int sd = check_stream_device(stream)) return sd;
+    StateQ8Args a{};
+    a.state_in = state; a.state_out = state_out; a.codes = codes; a.scales = scales;
+    a.fmt = format == KDA_Q8_E4M3 ? kQ8E4m3 : kQ8Int8;
+    a.src = store ? state_rows : slots; a.dst = store ? slots : state_rows;
+    a.src_rows = rows_src; a.dst_rows = rows_dst;
+    a.N = N; a.units = (int)units;
+    a.ring_src = ring_src; a.ring_dst = ring_dst; a.ring_row = ring_row;
+    a.err = dev_err_ptr();
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(store ? launch_state_store_q8(a, s) : launch_state_load_q8(a, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -385,6 +432,7 @@ const char* kda_status_string(int s) {
             return "the chunked scratch this call needs exceeds KDA_STATIC_SCRATCH_BYTES";
         case KDA_ERR_STREAM_DEVICE:
             return "the stream belongs to a device other than the current one";
+        case KDA_ERR_SLOT: return "a slot lies outside its pool or is named twice";
         default:
             if (s >= KDA_ERR_CUDA_BASE && s < KDA_ERR_CUDA_BASE + 10000) return "CUDA error";
             return "unknown status";
@@ -848,7 +896,7 @@ int kda_device_status(void* stream) {
         const int zero = 0;
         e = cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice);
         if (e != cudaSuccess) return cuda_status(e);
-        return KDA_ERR_TIMEOUT;
+        return (v & kDevErrTimeout) != 0 ? KDA_ERR_TIMEOUT : KDA_ERR_SLOT;
     }
     return KDA_OK;
 }
@@ -891,6 +939,131 @@ int kda_proj6(const float* x, int t, int in_f, const void* w_q, const void* w_k,
     a.ws = workspace;
     a.err = dev_err_ptr();
     return cuda_status(launch_proj6(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_state_store_q8(const float* state, void* codes, float* scales, int format,
+                       const int* state_rows, const int* slots, int S, int P, int N, int H, int Dk,
+                       int Dv, const float* ring, float* ring_pool, long ring_row, void* stream) {
+    return state_q8_impl(true, state, nullptr, codes, scales, format, state_rows, slots, S, P, N,
+                         H, Dk, Dv, ring, ring_pool, ring_row, stream);
+}
+
+int kda_state_load_q8(const void* codes, const float* scales, float* state, int format,
+                      const int* slots, const int* state_rows, int P, int S, int N, int H, int Dk,
+                      int Dv, const float* ring_pool, float* ring, long ring_row, void* stream) {
+    return state_q8_impl(false, nullptr, state, const_cast<void*>(codes),
+                         const_cast<float*>(scales), format, state_rows, slots, S, P, N, H, Dk, Dv,
+                         ring_pool, ring, ring_row, stream);
+}
+
+int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw, int raw_dtype,
+                        const float* conv_w, float* ring_pool, const float* f_raw,
+                        const float* dt_bias, const float* a_log, int gate_mode, float gate_lb,
+                        const float* beta_raw, void* codes, float* scales, int format,
+                        const int* slots, const int* slots_out, const int* keep,
+                        const float* norm_w, const float* gate_raw, float* y, int P, int N, int T,
+                        int H, int Hk, int Dk, int Dv, int K, float l2_eps, float scale,
+                        float rms_eps, void* stream) {
+    const int m = value_subheads(Dk, Dv);
+    if (m == 0) return KDA_ERR_HEAD_DIM;
+    if (N < 0 || N > kMaxGridY || P < 0 || H <= 0 || (long)H * m > kMaxGridY || Hk < 1 || Hk > H ||
+        T < 1 || T > kDecodeMaxT || (slots == nullptr && N > P))
+        return KDA_ERR_SHAPE;
+    if (raw_dtype != KDA_DTYPE_F32 && raw_dtype != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
+    if (format != KDA_Q8_INT8 && format != KDA_Q8_E4M3) return KDA_ERR_ENUM;
+    const bool norm_silu = (gate_mode & KDA_NORM_SILU) != 0;
+    gate_mode &= ~KDA_NORM_SILU;
+    if (gate_mode != KDA_GATE_PER_CHANNEL && gate_mode != KDA_GATE_PER_HEAD) return KDA_ERR_ENUM;
+    if (K < 2 || K > kMaxConvK) return KDA_ERR_CONV_K;
+    if (N == 0) return KDA_OK;
+    if (!q_raw || !k_raw || !v_raw || !conv_w || !ring_pool || !f_raw || !dt_bias || !a_log ||
+        !beta_raw || !codes || !scales || !norm_w || !gate_raw || !y)
+        return KDA_ERR_NULL;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(norm_w) || !aligned16(gate_raw) ||
+        !aligned16(y))
+        return KDA_ERR_ALIGN;
+    // raw rows (and per-channel gate rows) are copied two channels at a time
+    const uintptr_t rmask = raw_dtype == KDA_DTYPE_BF16 ? 3u : 7u;
+    if (((reinterpret_cast<uintptr_t>(q_raw) | reinterpret_cast<uintptr_t>(k_raw) |
+          reinterpret_cast<uintptr_t>(v_raw)) & rmask) != 0)
+        return KDA_ERR_ALIGN;
+    if (gate_mode == KDA_GATE_PER_CHANNEL &&
+        ((reinterpret_cast<uintptr_t>(f_raw) | reinterpret_cast<uintptr_t>(dt_bias)) & 7u) != 0)
+        return KDA_ERR_ALIGN;
+    const size_t rows = (size_t)P * H * Dv;
+    if (overlap2(codes, rows * kHeadDim, scales, rows * 4)) return KDA_ERR_STATE_ALIAS;
+    if (const int sd = check_stream_device(stream)) return sd;
+    DecodeQ8Args a{};
+    DecodeArgs& d = a.d;
+    d.q_raw = q_raw; d.k_raw = k_raw; d.v_raw = v_raw; d.raw_bf16 = raw_dtype == KDA_DTYPE_BF16;
+    d.conv_w = conv_w; d.ring_out = ring_pool;
+    d.f_raw = f_raw; d.dt_bias = dt_bias; d.a_log = a_log; d.gate_mode = gate_mode;
+    d.gate_lb = gate_lb; d.beta_raw = beta_raw;
+    d.norm_w = norm_w; d.gate_raw = gate_raw; d.y = y;
+    d.N = N; d.T = T; d.H = H * m; d.K = K; d.l2_eps = l2_eps; d.scale = scale;
+    d.rms_eps = rms_eps; d.keep = keep; d.Hk = Hk; d.norm_silu = norm_silu ? 1 : 0; d.vsub = m;
+    d.err = dev_err_ptr();
+    a.codes = codes; a.scales = scales; a.fmt = format == KDA_Q8_E4M3 ? kQ8E4m3 : kQ8Int8;
+    a.slots = slots; a.slots_out = slots_out; a.pool_rows = P;
+    return cuda_status(launch_decode_q8(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_proj_w4_workspace_bytes(int t, int in_f) {
+    if (t < 1 || t > kProjMaxT || in_f <= 0 || in_f % kProjKAlign != 0 || in_f > kW4MaxInF) return 0;
+    return proj_w4_workspace_bytes(t, in_f);
+}
+
+int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
+                const void* const* w_host, const void* const* scales_host,
+                const void* const* zeros_host, int scale_dtype, int group, const int* rows_host,
+                float* const* out_host, void* workspace, size_t workspace_bytes, void* stream) {
+    if (t < 0 || t > kProjMaxT || in_f <= 0 || in_f % kProjKAlign != 0 || in_f > kW4MaxInF ||
+        n_weights < 0 || n_weights > kW4MaxWeights)
+        return KDA_ERR_SHAPE;
+    if (x_dtype != KDA_DTYPE_F32 && x_dtype != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
+    if (scale_dtype != KDA_DTYPE_F32 && scale_dtype != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
+    if (group != 32 && group != 64 && group != 128) return KDA_ERR_ENUM;
+    if (n_weights > 0 && (!w_host || !scales_host || !rows_host || !out_host)) return KDA_ERR_NULL;
+    long tiles = 0;
+    for (int i = 0; i < n_weights; ++i) {
+        if (rows_host[i] < 0) return KDA_ERR_SHAPE;
+        tiles += ((long)rows_host[i] + 15) / 16;
+    }
+    if (tiles > (1L << 26)) return KDA_ERR_SHAPE;
+    if (t == 0 || tiles == 0) return KDA_OK;
+    if (!x) return KDA_ERR_NULL;
+    const uintptr_t smask = scale_dtype == KDA_DTYPE_BF16 ? 1u : 3u;
+    if (!aligned16(x)) return KDA_ERR_ALIGN;
+    ProjW4Args a{};
+    for (int i = 0; i < n_weights; ++i) {
+        if (rows_host[i] == 0) continue;
+        const void* z = zeros_host ? zeros_host[i] : nullptr;
+        if (!w_host[i] || !scales_host[i] || (zeros_host && !z) || !out_host[i]) return KDA_ERR_NULL;
+        if (!aligned16(w_host[i]) ||
+            ((reinterpret_cast<uintptr_t>(scales_host[i]) | reinterpret_cast<uintptr_t>(z)) & smask) != 0 ||
+            (reinterpret_cast<uintptr_t>(out_host[i]) & 3u) != 0)
+            return KDA_ERR_ALIGN;
+        a.w[a.nw] = w_host[i];
+        a.scale[a.nw] = scales_host[i];
+        a.zero[a.nw] = z;
+        a.out[a.nw] = out_host[i];
+        a.rows[a.nw] = rows_host[i];
+        ++a.nw;
+    }
+    const size_t need = proj_w4_workspace_bytes(t, in_f);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KDA_ERR_ALIGN;
+    if (const int sd = check_stream_device(stream)) return sd;
+    a.x = x;
+    a.x_bf16 = x_dtype == KDA_DTYPE_BF16;
+    a.t = t;
+    a.in_f = in_f;
+    a.group = group;
+    a.scale_bf16 = scale_dtype == KDA_DTYPE_BF16;
+    a.has_zero = zeros_host != nullptr;
+    a.ws = workspace;
+    a.err = dev_err_ptr();
+    return cuda_status(launch_proj_w4(a, static_cast<cudaStream_t>(stream)));
 }
 
 int kda_scan_varlen_static(const float* q_hat, const float* k_hat, const float* v_hat,

@@ -22,37 +22,6 @@ namespace kda {
 
 constexpr int kDecThreads = 256;
 
-// Asynchronous 4- or 8-byte copies global -> shared (cp.async, completion waited per thread).
-__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_8(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit_wait() {
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_all;" ::: "memory");
-}
-
-// Thread-block cluster barrier (every thread of every CTA of the cluster arrives; release /
-// acquire order the shared-memory writes before it with the remote reads after it).
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// A float in the shared memory of the cluster's CTA `rank`, at the address of `local` there.
-__device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-    return v;
-}
-
 // KW: register window width of the conv (4 when K <= 4, else 8).  WIDE: value heads of
 // a.vsub > 1 units, launched as clusters of a.vsub CTAs.
 template <bool BF16, int GATE_MODE, int KW, bool WIDE>

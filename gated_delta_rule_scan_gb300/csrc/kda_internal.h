@@ -13,6 +13,9 @@ namespace kda {
 
 constexpr int kHeadDim = 128;      // the only head width the kernels are built for
 constexpr int kMaxConvK = 8;       // conv window held in registers (taps 2..8)
+// device error word bits (written by kernels, read by kda_device_status)
+constexpr int kDevErrTimeout = 1;  // a bounded wait gave up
+constexpr int kDevErrSlot = 2;     // a slot outside its pool, or named twice
 constexpr int kMaxDevices = 64;    // per-device caches (symbol addresses, function attributes)
 
 // A value looked up once per device (a symbol address, an attribute that was set).  Every slot
@@ -180,11 +183,51 @@ cudaError_t launch_decode_fused(const DecodeArgs& a, cudaStream_t s);
 
 constexpr int kDecodeMaxT = 16;   // tokens one fused decode/verify call may carry
 
+// The 8-bit state pool (kda_q8.cuh, kda_state_q8.cu, kda_decode_q8.cu).
+constexpr int kQ8Int8 = 0, kQ8E4m3 = 1;
+// Store: f32 rows of state_in / ring_src -> pool rows; load: pool rows -> f32 rows of state_out.
+// src / dst: device int32 [N] row indices (null: row n), negative for padding.
+struct StateQ8Args {
+    const float* state_in; float* state_out;
+    void* codes; float* scales; int fmt;
+    const int* src; const int* dst;
+    int src_rows; int dst_rows;
+    int N; int units;                       // 128-wide value units of a row
+    const float* ring_src; float* ring_dst; long ring_row;   // floats of one ring row; 0: no ring
+    int* err;
+};
+cudaError_t launch_state_store_q8(const StateQ8Args& a, cudaStream_t s);
+cudaError_t launch_state_load_q8(const StateQ8Args& a, cudaStream_t s);
+// The decode step on the pool: DecodeArgs with state and ring rows in pool slots (state_in,
+// state_out, ring_in unused; ring_out is the ring pool).
+struct DecodeQ8Args {
+    DecodeArgs d;
+    void* codes; float* scales; int fmt;
+    const int* slots; const int* slots_out; int pool_rows;
+};
+cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t s);
+
+// Projections by 4-bit weights with group scales (kda_proj_w4.cu).
+constexpr int kW4MaxWeights = 8;        // weights of one call
+constexpr int kW4MaxInF = 32768;        // widest x
+struct ProjW4Args {
+    const void* x; int x_bf16;
+    const void* w[kW4MaxWeights]; const void* scale[kW4MaxWeights]; const void* zero[kW4MaxWeights];
+    float* out[kW4MaxWeights];
+    int rows[kW4MaxWeights];
+    int nw; int t; int in_f; int group; int scale_bf16; int has_zero;
+    void* ws;
+    int* err;
+};
+size_t proj_w4_workspace_bytes(int t, int in_f);
+cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s);
+
 // ---- optional per-kernel timing (kda_timer.cu): a KernelTimer scoped around a launch records a
 // CUDA event before and after it on the launch stream while timing is enabled.
 enum KernelId {
     kKPrep, kKRingRoll, kKScanSeq, kKChunkOffsets, kKChunkIntra, kKChunkInter, kKRmsNorm,
-    kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKernelCount
+    kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKStateStoreQ8, kKStateLoadQ8, kKDecodeQ8,
+    kKRingRollQ8, kKProjW4, kKernelCount
 };
 class KernelTimer {
 public:

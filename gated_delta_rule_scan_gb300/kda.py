@@ -22,12 +22,14 @@ if not os.path.exists(LIB_PATH):
         f"libkda.so not found at {LIB_PATH}; build it first "
         "(python -c 'import __graft_entry__ as g; g.build()')")
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _kda_native  # noqa: E402  (built beside libkda.so, which it calls)
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 GATE_PER_CHANNEL, GATE_PER_HEAD = 0, 1
 GATE_EXP = 2  # flag: g holds decay factors exp(log-decay)
 NORM_SILU = 4  # flag (fused entries): the RMSNorm gates with SiLU(z) instead of sigmoid(z)
 ALGO_AUTO, ALGO_SEQ, ALGO_CHUNK = 0, 1, 2
+Q8_INT8, Q8_E4M3 = 0, 1  # 8-bit state formats
 HEAD_DIM = 128
 DECODE_MAX_T = 16
 STATIC_SCRATCH_BYTES = 32 << 20  # kda_scan_varlen_static's fixed device scratch
@@ -143,6 +145,18 @@ _lib.kda_verify_rollback_dv.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, 
                                         _F, _P]
 _lib.kda_selftest_wait_timeout.restype = _I
 _lib.kda_selftest_wait_timeout.argtypes = [_P]
+_lib.kda_state_store_q8.restype = _I
+_lib.kda_state_store_q8.argtypes = [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _L, _P]
+_lib.kda_state_load_q8.restype = _I
+_lib.kda_state_load_q8.argtypes = [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _L, _P]
+_lib.kda_decode_fused_q8.restype = _I
+_lib.kda_decode_fused_q8.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _F, _P, _P, _P, _I,
+                                     _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F,
+                                     _F, _F, _P]
+_lib.kda_proj_w4_workspace_bytes.restype = _Z
+_lib.kda_proj_w4_workspace_bytes.argtypes = [_I, _I]
+_lib.kda_proj_w4.restype = _I
+_lib.kda_proj_w4.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P]
 
 # every symbol include/kda.h declares
 EXPORTED = ("kda_abi_version", "kda_status_string", "kda_conv_l2norm_prep",
@@ -157,7 +171,9 @@ EXPORTED = ("kda_abi_version", "kda_status_string", "kda_conv_l2norm_prep",
             "kda_prefill_fused_varlen_gqa", "kda_decode_fused_gqa", "kda_verify_rollback_gqa",
             "kda_conv_l2norm_prep_dv", "kda_conv_l2norm_prep_varlen_dv", "kda_scan_dv",
             "kda_scan_varlen_dv", "kda_prefill_fused_dv", "kda_prefill_fused_varlen_dv",
-            "kda_decode_fused_dv", "kda_verify_rollback_dv")
+            "kda_decode_fused_dv", "kda_verify_rollback_dv", "kda_state_store_q8",
+            "kda_state_load_q8", "kda_decode_fused_q8", "kda_proj_w4_workspace_bytes",
+            "kda_proj_w4")
 
 
 class KdaError(RuntimeError):
@@ -192,7 +208,7 @@ def _stream(stream, *tensors) -> int | None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.is_cuda:
-            return torch.cuda.current_stream(t.device).cuda_stream
+            return torch._C._cuda_getCurrentRawStream(t.get_device())
     return None
 
 
@@ -204,7 +220,8 @@ def _check(fn: str, status: int):
 def _call(fn: str, like, *args):
     """Call C entry ``fn`` with the device of tensor ``like`` current: the library keys its
     per-device lookups by the current device and requires the stream to belong to it (40012)."""
-    if isinstance(like, torch.Tensor) and like.is_cuda:
+    if (isinstance(like, torch.Tensor) and like.is_cuda
+            and torch.cuda.current_device() != like.get_device()):
         with torch.cuda.device(like.device):
             status = getattr(_lib, fn)(*args)
     else:
@@ -503,6 +520,64 @@ def kda_proj6(x, w_q, w_k, w_v, w_fa, w_ga, w_b, q_raw, k_raw, v_raw, f_down, g_
           _ptr(workspace), _ws_bytes(workspace), st)
 
 
+def _native(fn: str, like, *args):
+    """Call _kda_native's ``fn``, which checks and unpacks the tensors, with the device of tensor
+    ``like`` current."""
+    if (isinstance(like, torch.Tensor) and like.is_cuda
+            and torch.cuda.current_device() != like.get_device()):
+        with torch.cuda.device(like.device):
+            status = getattr(_kda_native, fn)(*args)
+    else:
+        status = getattr(_kda_native, fn)(*args)
+    if status != 0:
+        raise KdaError("kda_" + fn, status)
+
+
+def kda_state_store_q8(state, codes, scales, *, N, H, src=None, dst=None, Dv=HEAD_DIM, ring=None,
+                       ring_pool=None, stream=None):
+    """Rows src[n] of state [S, H, Dv, 128] (and of ring) into pool slots dst[n].  codes: int8 or
+    float8_e4m3fn, which names the format; src, dst: int32 device [N] or None (n)."""
+    _native("state_move", codes, True, state, codes, scales, src, dst, N, H, Dv, ring, ring_pool,
+            _stream(stream, codes))
+
+
+def kda_state_load_q8(codes, scales, state, *, N, H, src=None, dst=None, Dv=HEAD_DIM,
+                      ring_pool=None, ring=None, stream=None):
+    """Pool slots src[n] into rows dst[n] of state (and of ring); see kda_state_store_q8."""
+    _native("state_move", codes, False, state, codes, scales, dst, src, N, H, Dv, ring, ring_pool,
+            _stream(stream, codes))
+
+
+def kda_decode_fused_q8(q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias, a_log, beta_raw,
+                        codes, scales, norm_w, gate_raw, y, *, N, T, H, slots=None, slots_out=None,
+                        keep=None, K=4, gate_mode=0, gate_lb=-5.0, l2_eps=1e-6, scale=None,
+                        rms_eps=1e-6, stream=None, Hk=None, Dv=HEAD_DIM):
+    """kda_decode_fused on the 8-bit pool: sequence n reads slot slots[n] (None: n) and writes slot
+    slots_out[n] (None: the same); keep: int32 device [N], the rows to take (a rollback)."""
+    _native("decode_fused_q8", codes, q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias, a_log,
+            beta_raw, codes, scales, norm_w, gate_raw, y, slots, slots_out, keep, N, T, H,
+            H if Hk is None else Hk, Dv, K, gate_mode, gate_lb, l2_eps,
+            HEAD_DIM ** -0.5 if scale is None else scale, rms_eps, _stream(stream, codes))
+
+
+def kda_proj_w4_workspace_bytes(t, in_f) -> int:
+    return int(_lib.kda_proj_w4_workspace_bytes(t, in_f))
+
+
+def proj_w4_workspace(t, in_f, device):
+    """A device byte buffer large enough for kda_proj_w4 over t token rows of width in_f (None when
+    none is needed)."""
+    nbytes = kda_proj_w4_workspace_bytes(t, in_f)
+    return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def kda_proj_w4(x, weights, scales, outs, *, group, zeros=None, workspace=None, stream=None):
+    """Projections of x [t, in_f] (f32 or bf16) by 4-bit weights (lists of tensors): weights[i]
+    uint8 [rows_i, in_f/2], scales[i] (and zeros[i]) f32 or bf16 [rows_i, in_f/group], outs[i] f32
+    [t, rows_i]."""
+    _native("proj_w4", x, x, weights, scales, zeros, outs, group, workspace, _stream(stream, x))
+
+
 def kernel_timing(enable: bool) -> bool:
     """Turn per-kernel event timing on (clearing the totals) or off; returns the old setting."""
     return bool(_lib.kda_kernel_timing(1 if enable else 0))
@@ -511,7 +586,7 @@ def kernel_timing(enable: bool) -> bool:
 def kernel_times() -> dict:
     """{kernel name: (launches, total ms)} since the last read, for kernels launched at least once
     (waits for the recorded launches)."""
-    n = 16
+    n = 32
     launches = (ctypes.c_long * n)()
     ms = (ctypes.c_double * n)()
     k = _lib.kda_kernel_times(n, launches, ms)

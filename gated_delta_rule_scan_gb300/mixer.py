@@ -199,6 +199,75 @@ def kda_verify_rollback(*, q_raw, k_raw, v_raw, conv_w, ring_in, f_raw, dt_bias,
     return dict(y=y, state_out=state_out, ring_out=ring_out)
 
 
+def kda_proj_w4(*, x, weights, scales, group, zeros=None, outs=None, workspace=None, stream=None):
+    """Projections of x [t, in_f] by 4-bit weights with group scales (lists, one entry a weight; the
+    layer's six in kda_proj6's order, or any others that read x).  Returns the list of outputs."""
+    t, in_f = x.shape
+    if outs is None:
+        outs = [_empty((t, w.shape[0]), x) for w in weights]
+    if workspace is None:
+        workspace = kda.proj_w4_workspace(t, in_f, x.device)
+    kda.kda_proj_w4(x, weights, scales, outs, group=group, zeros=zeros, workspace=workspace,
+                    stream=stream)
+    return outs
+
+
+class StatePoolQ8:
+    """States and conv rings of up to `slots` sequences, the states in 8 bits (include/kda.h, "The
+    8-bit state pool"): codes [slots, H, Dv, 128], scales [slots, H, Dv], rings [slots, channels,
+    K-1].  `fmt`: "int8" or "e4m3".  Slots are handed out by the caller; index tensors are int32 on
+    the pool's device, negative entries are padding."""
+
+    FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+    def __init__(self, slots, H, device, *, Hk=None, Dv=None, K=4, fmt="int8"):
+        if fmt not in self.FORMATS:
+            raise ValueError(fmt)
+        self.H, self.K = H, K
+        self.Hk = H if Hk is None else Hk
+        self.Dv = kda.HEAD_DIM if Dv is None else Dv
+        channels = 2 * self.Hk * kda.HEAD_DIM + H * self.Dv
+        self.codes = torch.zeros(slots, H, self.Dv, kda.HEAD_DIM, dtype=torch.uint8,
+                                 device=device).view(self.FORMATS[fmt])
+        self.scales = torch.zeros(slots, H, self.Dv, device=device)
+        self.ring = torch.zeros(slots, channels, K - 1, device=device)
+
+    def store(self, state, ring, slots, rows=None, stream=None):
+        """Rows `rows` (None: n) of state and ring, as a prefill returns them, into slots[n]."""
+        kda.kda_state_store_q8(state, self.codes, self.scales, src=rows, dst=slots,
+                               N=slots.numel(), H=self.H, Dv=self.Dv, ring=ring,
+                               ring_pool=self.ring, stream=stream)
+
+    def load(self, slots, state=None, ring=None, rows=None, stream=None):
+        """slots[n] into rows `rows` (None: n) of state and ring; returns both."""
+        n = slots.numel()
+        if state is None:
+            state = torch.zeros(n, self.H, self.Dv, kda.HEAD_DIM, device=self.codes.device)
+        if ring is None:
+            ring = torch.zeros(state.shape[0], *self.ring.shape[1:], device=self.codes.device)
+        kda.kda_state_load_q8(self.codes, self.scales, state, src=slots, dst=rows, N=n, H=self.H,
+                              Dv=self.Dv, ring_pool=self.ring, ring=ring, stream=stream)
+        return state, ring
+
+    def decode(self, *, q_raw, k_raw, v_raw, conv_w, f_raw, dt_bias, a_log, beta_raw, norm_w,
+               gate_raw, slots, T=1, slots_out=None, keep=None, gate_mode=0, gate_lb=-5.0,
+               l2_eps=1e-6, rms_eps=1e-6, scale=None, y=None, norm_gate="sigmoid", stream=None):
+        """One decode step or T-token verify of the sequences in slots[n], written to slots_out[n]
+        (None: in place).  With keep (int32 [N]) only the first keep[n] tokens are taken: the
+        rollback of a verify that ran into other slots.  Returns y (zero in rows not computed when
+        it is allocated here)."""
+        N = slots.numel()
+        if y is None:
+            y = torch.zeros(N * T, self.H * self.Dv, device=self.codes.device)
+        kda.kda_decode_fused_q8(q_raw, k_raw, v_raw, conv_w, self.ring, f_raw, dt_bias, a_log,
+                                beta_raw, self.codes, self.scales, norm_w, gate_raw, y, N=N, T=T,
+                                H=self.H, slots=slots, slots_out=slots_out, keep=keep, K=self.K,
+                                gate_mode=gate_mode | _norm_flag(norm_gate), gate_lb=gate_lb,
+                                l2_eps=l2_eps, scale=scale, rms_eps=rms_eps, stream=stream,
+                                Hk=self.Hk, Dv=self.Dv)
+        return y
+
+
 class HostPrefillStream:
     """Prefill over batches that live in pinned host memory, pipelined over three CUDA streams:
     while batch i runs kda_prefill on the device, batch i+1 is copied in and the results of

@@ -65,6 +65,9 @@ extern "C" {
                                          KDA_STATIC_SCRATCH_BYTES */
 #define KDA_ERR_STREAM_DEVICE 40012   /* the stream belongs to a device other than the current one */
 
+#define KDA_ERR_SLOT 40013            /* a kernel left out rows whose slot lies outside its pool or
+                                         is named twice (kda_device_status) */
+
 /* enums */
 #define KDA_DTYPE_F32 0
 #define KDA_DTYPE_BF16 1
@@ -81,6 +84,9 @@ extern "C" {
 #define KDA_ALGO_AUTO 0
 #define KDA_ALGO_SEQ 1
 #define KDA_ALGO_CHUNK 2
+
+#define KDA_Q8_INT8 0                 /* 8-bit state formats: whole numbers, -127 .. 127 */
+#define KDA_Q8_E4M3 1                 /* e4m3 floats, largest 448 */
 
 #define KDA_HEAD_DIM 128
 #define KDA_STATIC_SCRATCH_BYTES 33554432u  /* kda_scan_varlen_static's fixed scratch (32 MiB) */
@@ -562,6 +568,96 @@ int kda_proj6(const float* x, int t, int in_f, const void* w_q, const void* w_k,
               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The 8-bit state pool: recurrent states and conv rings in P slots that a serving process hands out
+ * to sequences, the states stored as one-byte codes with a scale for each value column.
+ *   codes      [P, H, Dv, 128] one byte each [16B];  scales [P, H, Dv] f32 [16B];
+ *   ring_pool  [P, channels, K-1] f32: the conv rings of the same slots, as f32.
+ * A state row x = state[h][j][0..127] is stored as
+ *     amax = max|x_i|,  scale = amax / M,  code_i = round(x_i * (M / amax)),  x_i ~ code_i * scale
+ * with format KDA_Q8_INT8: M = 127, whole numbers (two's complement bytes), ties to even; format
+ * KDA_Q8_E4M3: M = 448, e4m3 floats, ties to even.  Every operation is one f32 rounding.  int8 is off
+ * by at most amax/254, e4m3 by at most |x_i| / 16 (amax * 2^-10 / 448 for its subnormal codes).  A
+ * row whose amax is below 2^-100 is stored as zeros; a row with a NaN or an infinity reads back as
+ * NaN throughout.
+ * Slot and row indices are device int32 arrays of N entries, or NULL (row n is row n; N must then
+ * not exceed the array, 40005).  A negative index makes row n padding: nothing of it is read or
+ * written.  An index past its array, or a destination that another row of the call names too, would
+ * race: such rows are left out as padding is (of several rows that name one destination the store
+ * and the load keep the first), and kda_device_status reports 40013.
+ * A pool of up to 2^31 - 1 slots is addressed with 64-bit offsets.  The pool needs no initialising:
+ * slots that were never written hold what the memory held.
+ *
+ * kda_state_store_q8: state rows [S, H, Dv, 128] f32 [16B] -> slots; with ring_row > 0 also
+ * ring [S, ring_row] -> ring_pool [P, ring_row] f32 [16B], bit for bit (ring_row = channels * (K-1)
+ * floats, a multiple of 4; 0 leaves the rings alone).
+ * kda_state_load_q8: the reverse.
+ * N = 0 does nothing.  Dk = 128, Dv = 128 * m (40001); overlapping arrays return 40003.
+ */
+int kda_state_store_q8(const float* state, void* codes, float* scales, int format,
+                       const int* state_rows, const int* slots, int S, int P, int N, int H, int Dk,
+                       int Dv, const float* ring, float* ring_pool, long ring_row, void* stream);
+int kda_state_load_q8(const void* codes, const float* scales, float* state, int format,
+                      const int* slots, const int* state_rows, int P, int S, int N, int H, int Dk,
+                      int Dv, const float* ring_pool, float* ring, long ring_row, void* stream);
+
+/*
+ * kda_decode_fused_q8 -- kda_decode_fused_dv (decode T = 1, verify T <= 16) on the 8-bit state pool:
+ * sequence n's state and conv ring are read from slot slots[n] and written to slot slots_out[n]
+ * (slots_out NULL: in place), the state dequantised once, carried in f32 through all T tokens and
+ * rounded to 8 bits once at the end.  y is computed before that rounding.
+ * Arguments as in kda_decode_fused_dv (H value heads of Dv, Hk q/k heads, gate_mode with
+ * KDA_NORM_SILU), and
+ *   ring_pool, codes, scales, format   the pool of P slots, as above;
+ *   slots, slots_out                   as above; slots == NULL is slot n, for N <= P (40005);
+ *   keep       NULL, or device int32 [N]: take only the first keep[n] (clamped to 0..T) rows of
+ *              sequence n, as kda_verify_rollback does: a rollback is the verify call again with
+ *              keep, from the slots of before the round.  keep[n] = 0 copies the slot unchanged.
+ * y rows of padding, of rows left out and of rows t >= keep[n] are not written.
+ * A slot may be read by several rows (a shared prefix); a row whose output slot another row reads
+ * or an earlier row writes is left out (40013, above).  Grouped queries and wide value heads may
+ * roll the ring in place here.  q/k/v raw rows are 4-byte (bf16) or 8-byte (f32) aligned, f_raw and
+ * dt_bias 8-byte (KDA_GATE_PER_CHANNEL).
+ * Unlike kda_decode_fused, a T-token call is not T one-token calls bit for bit: those round the
+ * state T times.  A call's outputs do not depend on the other rows of the batch.
+ */
+int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw, int raw_dtype,
+                        const float* conv_w, float* ring_pool, const float* f_raw,
+                        const float* dt_bias, const float* a_log, int gate_mode, float gate_lb,
+                        const float* beta_raw, void* codes, float* scales, int format,
+                        const int* slots, const int* slots_out, const int* keep,
+                        const float* norm_w, const float* gate_raw, float* y, int P, int N, int T,
+                        int H, int Hk, int Dk, int Dv, int K, float l2_eps, float scale,
+                        float rms_eps, void* stream);
+
+/*
+ * kda_proj_w4 -- projections of t token rows x by up to 8 weights of 4 bits with group scales, in
+ * one call (the layer's six projections as in kda_proj6, an up-projection, an output projection):
+ *     out_i[s][r] = sum_k (q_i[r][k] - z_i[r][k / group]) * c_i[r][k / group] * x[s][k]
+ * x            [t, in_f] f32 or bf16 (x_dtype) [16B], t = 0..256; in_f a multiple of 128, at most
+ *              32768 (40005).
+ * The _host arguments are arrays of n_weights entries in host memory, read before the call returns:
+ * w_host       device pointers to the codes, [rows_i, in_f / 2] bytes [16B]: byte k / 2 of a row
+ *              holds the code 0 .. 15 of the even k in its low 4 bits and of k + 1 in its high 4;
+ * scales_host  device pointers to the scales c, [rows_i, in_f / group] in scale_dtype;
+ * zeros_host   NULL (every zero point is 8), or device pointers to the zero points z, any values,
+ *              layout and type as the scales;
+ * rows_host    rows of each weight (0 allowed);
+ * out_host     device pointers to the outputs, [t, rows_i] f32.
+ * group        32, 64 or 128 consecutive k share a scale (40007 otherwise).
+ * workspace    device scratch [16B] of at least kda_proj_w4_workspace_bytes(t, in_f) bytes, which
+ *              may be 0 (then NULL is accepted); 40009 otherwise.  Calls sharing it must not overlap.
+ * Precision: codes, scales and zero points enter exactly; x enters with 22 significant bits (bf16:
+ * exactly); sums are f32.  One token row's result depends on the other rows of the call only
+ * through the choice of form for t rows.  A NaN or an infinity in x makes every output of its token
+ * row NaN or infinite, and no other row's.
+ */
+size_t kda_proj_w4_workspace_bytes(int t, int in_f);
+int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
+                const void* const* w_host, const void* const* scales_host,
+                const void* const* zeros_host, int scale_dtype, int group, const int* rows_host,
+                float* const* out_host, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kda_selftest_wait_timeout -- a self-test of failure detection (no counterpart in the pages):
  * launches one kernel whose single thread waits, with the bounded wait every kernel here uses,
  * on a barrier that nothing completes.  The wait gives up after about a second, raises the device
@@ -574,7 +670,8 @@ int kda_selftest_wait_timeout(void* stream);
 /*
  * kda_device_status -- synchronises `stream`, then reports and clears the device error word on
  * the current device: 0, or 40008 when a kernel gave up a bounded device wait since the last
- * check (its outputs are then incomplete), or 10000 + cudaError_t.
+ * check (its outputs are then incomplete), or 40013 when rows were left out for their slots (and no
+ * wait was given up), or 10000 + cudaError_t.
  */
 int kda_device_status(void* stream);
 
