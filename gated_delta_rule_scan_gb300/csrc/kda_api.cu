@@ -1029,18 +1029,16 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
         if (rows_host[i] < 0) return KDA_ERR_SHAPE;
         tiles += ((long)rows_host[i] + 15) / 16;
     }
-    if (tiles > (1L << 26)) return KDA_ERR_SHAPE;
+    if (tiles * (in_f / kProjKAlign) >= (1L << 31)) return KDA_ERR_SHAPE;   // work units are ints
     if (t == 0 || tiles == 0) return KDA_OK;
     if (!x) return KDA_ERR_NULL;
-    const uintptr_t smask = scale_dtype == KDA_DTYPE_BF16 ? 1u : 3u;
     if (!aligned16(x)) return KDA_ERR_ALIGN;
     ProjW4Args a{};
     for (int i = 0; i < n_weights; ++i) {
         if (rows_host[i] == 0) continue;
         const void* z = zeros_host ? zeros_host[i] : nullptr;
         if (!w_host[i] || !scales_host[i] || (zeros_host && !z) || !out_host[i]) return KDA_ERR_NULL;
-        if (!aligned16(w_host[i]) ||
-            ((reinterpret_cast<uintptr_t>(scales_host[i]) | reinterpret_cast<uintptr_t>(z)) & smask) != 0 ||
+        if (!aligned16(w_host[i]) || !aligned16(scales_host[i]) || !aligned16(z) ||
             (reinterpret_cast<uintptr_t>(out_host[i]) & 3u) != 0)
             return KDA_ERR_ALIGN;
         a.w[a.nw] = w_host[i];

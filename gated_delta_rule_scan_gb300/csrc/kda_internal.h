@@ -221,13 +221,19 @@ struct ProjW4Args {
 };
 size_t proj_w4_workspace_bytes(int t, int in_f);
 cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s);
+// the form for batches, on tcgen05 (kda_proj_w4_wide.cu)
+constexpr int kW4MaxBlocks = 152;       // its blocks: one per SM
+size_t proj_w4_wide_workspace_bytes(int t, int in_f);
+cudaError_t launch_proj_w4_wide(const ProjW4Args& a, cudaStream_t s);
+// 2-D byte tensor map over [rows, cols] with a [box_rows][64] box in the 64-byte swizzle
+bool make_tensor_map_2d_u8_sw64(CUtensorMap* m, const void* base, long rows, long cols, int box_rows);
 
 // ---- optional per-kernel timing (kda_timer.cu): a KernelTimer scoped around a launch records a
 // CUDA event before and after it on the launch stream while timing is enabled.
 enum KernelId {
     kKPrep, kKRingRoll, kKScanSeq, kKChunkOffsets, kKChunkIntra, kKChunkInter, kKRmsNorm,
     kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKStateStoreQ8, kKStateLoadQ8, kKDecodeQ8,
-    kKRingRollQ8, kKProjW4, kKernelCount
+    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKernelCount
 };
 class KernelTimer {
 public:

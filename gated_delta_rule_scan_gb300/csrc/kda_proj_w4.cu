@@ -361,9 +361,12 @@ cudaError_t launch_group(const W4Params& p, bool x_bf16, int grid, size_t smem, 
 
 }  // namespace
 
-size_t proj_w4_workspace_bytes(int, int) { return 0; }
+size_t proj_w4_workspace_bytes(int t, int in_f) {
+    return t > kTok ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
+}
 
 cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
+    if (a.t > kTok) return launch_proj_w4_wide(a, s);
     W4Params p{};
     p.x = a.x;
     int tiles = 0;

@@ -48,7 +48,7 @@ const char* const kNames[kKernelCount] = {
     "kda_gated_rmsnorm_kernel", "kda_decode_fused_kernel", "kda_chunk_prep_intra_kernel",
     "kda_proj_split_kernel",  "kda_proj6_kernel",       "kda_state_store_q8_kernel",
     "kda_state_load_q8_kernel", "kda_decode_q8_kernel", "kda_ring_roll_q8_kernel",
-    "kda_proj_w4_kernel"};
+    "kda_proj_w4_kernel",     "kda_proj_w4_split_kernel", "kda_proj_w4_wide_kernel"};
 
 }  // namespace
 

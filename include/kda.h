@@ -638,7 +638,7 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
  * The _host arguments are arrays of n_weights entries in host memory, read before the call returns:
  * w_host       device pointers to the codes, [rows_i, in_f / 2] bytes [16B]: byte k / 2 of a row
  *              holds the code 0 .. 15 of the even k in its low 4 bits and of k + 1 in its high 4;
- * scales_host  device pointers to the scales c, [rows_i, in_f / group] in scale_dtype;
+ * scales_host  device pointers to the scales c, [rows_i, in_f / group] in scale_dtype [16B];
  * zeros_host   NULL (every zero point is 8), or device pointers to the zero points z, any values,
  *              layout and type as the scales;
  * rows_host    rows of each weight (0 allowed);
