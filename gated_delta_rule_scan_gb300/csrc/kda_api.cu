@@ -1029,7 +1029,8 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
         if (rows_host[i] < 0) return KDA_ERR_SHAPE;
         tiles += ((long)rows_host[i] + 15) / 16;
     }
-    if (tiles * (in_f / kProjKAlign) >= (1L << 31)) return KDA_ERR_SHAPE;   // work units are ints
+    // at most 2^30 rows, and work units that count in an int
+    if (tiles > (1L << 26) || tiles * (in_f / kProjKAlign) >= (1L << 31)) return KDA_ERR_SHAPE;
     if (t == 0 || tiles == 0) return KDA_OK;
     if (!x) return KDA_ERR_NULL;
     if (!aligned16(x)) return KDA_ERR_ALIGN;

@@ -641,7 +641,7 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
  * scales_host  device pointers to the scales c, [rows_i, in_f / group] in scale_dtype [16B];
  * zeros_host   NULL (every zero point is 8), or device pointers to the zero points z, any values,
  *              layout and type as the scales;
- * rows_host    rows of each weight (0 allowed);
+ * rows_host    rows of each weight (0 allowed), at most 2^30 in all and 2^42 / in_f (40005);
  * out_host     device pointers to the outputs, [t, rows_i] f32.
  * group        32, 64 or 128 consecutive k share a scale (40007 otherwise).
  * workspace    device scratch [16B] of at least kda_proj_w4_workspace_bytes(t, in_f) bytes, which
