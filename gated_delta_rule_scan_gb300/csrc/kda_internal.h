@@ -222,7 +222,8 @@ struct ProjW4Args {
 size_t proj_w4_workspace_bytes(int t, int in_f);
 cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s);
 // the form for batches, on tcgen05 (kda_proj_w4_wide.cu)
-constexpr int kW4MaxBlocks = 152;       // its blocks: one per SM
+constexpr int kW4MaxSms = 152;
+constexpr int kW4MaxBlocks = 2 * kW4MaxSms;   // its blocks: two per SM at most
 size_t proj_w4_wide_workspace_bytes(int t, int in_f);
 cudaError_t launch_proj_w4_wide(const ProjW4Args& a, cudaStream_t s);
 // 2-D byte tensor map over [rows, cols] with a [box_rows][64] box in the 64-byte swizzle

@@ -39,6 +39,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 16;                    // weight rows of a tile: the MMA's M
 constexpr int kChunk = 128;                  // k of one warp step
 constexpr int kTok = 8;                      // tokens of one pass
+// Rows up to which this form is taken: one launch and no workspace.  At 64 heads x 6144 it runs 33
+// us at one row but 91 at eight (two MMA tiles), the form for batches 34 at any of them.
+constexpr int kSmallT = 4;
 constexpr int kXSmem = 72 * 1024;            // x of one block: three blocks per SM
 
 struct W4Params {
@@ -362,11 +365,11 @@ cudaError_t launch_group(const W4Params& p, bool x_bf16, int grid, size_t smem, 
 }  // namespace
 
 size_t proj_w4_workspace_bytes(int t, int in_f) {
-    return t > kTok ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
+    return t > kSmallT ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
 }
 
 cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
-    if (a.t > kTok) return launch_proj_w4_wide(a, s);
+    if (a.t > kSmallT) return launch_proj_w4_wide(a, s);
     W4Params p{};
     p.x = a.x;
     int tiles = 0;
