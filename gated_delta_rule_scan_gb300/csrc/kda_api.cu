@@ -979,8 +979,8 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
     if (!q_raw || !k_raw || !v_raw || !conv_w || !ring_pool || !f_raw || !dt_bias || !a_log ||
         !beta_raw || !codes || !scales || !norm_w || !gate_raw || !y)
         return KDA_ERR_NULL;
-    if (!aligned16(codes) || !aligned16(scales) || !aligned16(norm_w) || !aligned16(gate_raw) ||
-        !aligned16(y))
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(conv_w) || !aligned16(norm_w) ||
+        !aligned16(gate_raw) || !aligned16(y))
         return KDA_ERR_ALIGN;
     // raw rows (and per-channel gate rows) are copied two channels at a time
     const uintptr_t rmask = raw_dtype == KDA_DTYPE_BF16 ? 3u : 7u;

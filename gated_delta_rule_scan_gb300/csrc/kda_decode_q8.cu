@@ -12,13 +12,16 @@
 // once, at the end.
 //
 // GB300 layout.  The bytes are a quarter of the f32 decode's (33 KB of state per (sequence, head)
-// read and written, against 131 KB), so the fixed work of a CTA weighs more, and the f32 layout (a
-// whole 64 KB state in the registers of two CTAs per SM) would leave the memory idle between its
-// phases.  Here a warp owns 16 value columns as two batches of 8 and lane l keys 4l .. 4l+3: the
-// codes of all 16 columns wait in 16 registers as they came (one 128-byte access a column), only 8
-// columns are unpacked at a time, and k, q and the decay are 12 registers that serve every column.
-// That fits three CTAs on an SM.  The 16 sums of a batch (8 columns, P.k and P.q) are finished by
-// one transposed butterfly of 16 shuffles, which leaves value index i in lanes 2i and 2i+1.
+// read and written, against 131 KB), so instructions, not bytes, bound the first form of this
+// kernel (1860 warp instructions a warp at one token, of them 800 to round the state: 77 us at 64
+// sequences x 64 heads against 27 us of bytes).  One CTA owns one (sequence, unit).  8 lanes share
+// 4 value columns, lane r keys 16r .. 16r+15 of each, so that a column's codes are one 16-byte
+// access a lane, its reductions take three steps, and every k, decay and q value read from shared
+// memory serves several columns; the rows of q, k and the decay lie in shared memory in the order
+// that makes those reads conflict-free (key 16r + 4m + e at 32m + 4r + e).  The codes wait packed
+// in 16 registers, and two columns are unpacked at a time: three CTAs fit an SM.  The l2 norms
+// scale the finished sums instead of the vectors.  Of a reduction's lanes each finishes one
+// column: one pair of divisions a lane rounds the state, not one a column.
 #include "kda_q8.cuh"
 
 namespace kda {
@@ -26,57 +29,88 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kColsPerWarp = kHeadDim / (kThreads / 32);   // 16
-constexpr int kBatch = 8;                                   // columns unpacked at a time
+constexpr int kCols = 4;                     // value columns of a group of 8 lanes
+constexpr int kBatch = 2;                    // of them unpacked at a time
 constexpr int kMinBlocks = 3;
 
-// Transposed butterfly over the warp for 16 values per lane: lane l ends with the full sum of value
-// index l >> 1.
-__device__ __forceinline__ float reduce16(const float (&v)[16], int lane) {
-    float k8[8], k4[4], k2[2];
-    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4, b1 = lane & 2;
+// Where key i of a q, k or decay row lies in shared memory.
+__device__ __forceinline__ int key_pos(int i) { return 32 * ((i >> 2) & 3) + 4 * (i >> 4) + (i & 3); }
+
+// 16 codes (keys 16r ..) of one column as pairs: s[2m], s[2m + 1] are keys 4m .. 4m + 3.
+template <int FMT>
+__device__ __forceinline__ void unpack16(float2 (&s)[8], uint4 w, float scale) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        k8[i] = (b4 ? v[8 + i] : v[i]) + __shfl_xor_sync(0xffffffffu, b4 ? v[i] : v[8 + i], 16);
+    for (int m = 0; m < 4; ++m) {
+        const float4 v = q8_decode4<FMT>(u[m], scale);
+        s[2 * m] = make_float2(v.x, v.y);
+        s[2 * m + 1] = make_float2(v.z, v.w);
+    }
+}
+template <int FMT>
+__device__ __forceinline__ uint4 pack16(const float2 (&s)[8], float mul) {
+    uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        k4[i] = (b3 ? k8[4 + i] : k8[i]) + __shfl_xor_sync(0xffffffffu, b3 ? k8[i] : k8[4 + i], 8);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        k2[i] = (b2 ? k4[2 + i] : k4[i]) + __shfl_xor_sync(0xffffffffu, b2 ? k4[i] : k4[2 + i], 4);
-    float s = (b1 ? k2[1] : k2[0]) + __shfl_xor_sync(0xffffffffu, b1 ? k2[0] : k2[1], 2);
-    return s + __shfl_xor_sync(0xffffffffu, s, 1);
+    for (int m = 0; m < 4; ++m)
+        u[m] = q8_encode4<FMT>(make_float4(s[2 * m].x, s[2 * m].y, s[2 * m + 1].x, s[2 * m + 1].y), mul);
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-    const float2 p = __ffma2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w),
-                                __fmul2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y)));
-    return p.x + p.y;
-}
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-    const float2 lo = __fmul2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y));
-    const float2 hi = __fmul2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w));
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
-// a * s + c
-__device__ __forceinline__ float4 fma4(float4 a, float s, float4 c) {
-    const float2 s2 = make_float2(s, s);
-    const float2 lo = __ffma2_rn(make_float2(a.x, a.y), s2, make_float2(c.x, c.y));
-    const float2 hi = __ffma2_rn(make_float2(a.z, a.w), s2, make_float2(c.z, c.w));
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
+// The 16 keys of a lane in a q, k or decay row.
+__device__ __forceinline__ float4 row4(const float* row, int r, int m) {
+    return *reinterpret_cast<const float4*>(row + 32 * m + 4 * r);
 }
 
-// KW: register window of the conv (4 when K <= 4, else 8).  WIDE: value heads of d.vsub > 1 units,
-// one cluster of vsub CTAs each.
-template <int FMT, int GATE_MODE, int KW, bool WIDE>
+// The conv of one channel: K taps over the ring slots and the new samples, oldest first.  KT = 4
+// is a conv of exactly 4 taps (16-byte weights); KT = 8 any width up to 8.
+template <int KT>
+struct Conv {
+    float w[KT], x[KT];
+    __device__ __forceinline__ void load(const float* conv_w, const float* ring, long ch, int K) {
+        if constexpr (KT == 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(conv_w + ch * 4));
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            const float* p = ring + ch * 3;
+            x[0] = 0.0f; x[1] = p[0]; x[2] = p[1]; x[3] = p[2];
+        } else {
+            const float* p = ring + ch * (K - 1);
+#pragma unroll
+            for (int m = 0; m < KT; ++m) {
+                const int jj = m - (KT - K), d = KT - m;
+                w[m] = jj >= 0 ? conv_w[ch * K + jj] : 0.0f;
+                x[m] = d <= K - 1 ? p[K - 1 - d] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ float step(float v, int K) {
+        window_push(x, v);
+        return silu_f(conv_taps_f(w, x, KT == 4 ? 4 : K));
+    }
+    // the last K - 1 samples
+    __device__ __forceinline__ void store(float* ring, long ch, int K) const {
+        if constexpr (KT == 4) {
+            float* p = ring + ch * 3;
+            p[0] = x[1]; p[1] = x[2]; p[2] = x[3];
+        } else {
+            float* p = ring + ch * (K - 1);
+#pragma unroll
+            for (int m = 0; m < KT; ++m) {
+                const int d = KT - 1 - m;
+                if (d < K - 1) p[K - 2 - d] = x[m];
+            }
+        }
+    }
+};
+
+// WIDE: value heads of d.vsub > 1 units, one cluster of vsub CTAs each.
+template <int FMT, int GATE_MODE, int KT, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(const DecodeQ8Args p) {
     extern __shared__ __align__(16) float rows_s[];
-    __shared__ float beta_s[kDecodeMaxT], ascal[kDecodeMaxT], qk_s[kDecodeMaxT];
-    __shared__ float part[3][2][kDecodeMaxT];     // q.q, k.k and q.k of two warps each
-    __shared__ float inv_s[2][kDecodeMaxT];
+    __shared__ float beta_s[kDecodeMaxT], ascal[kDecodeMaxT];
+    __shared__ float part[3][4][kDecodeMaxT];     // q.q, q.k and k.k of four warps
     __shared__ float nss[kDecodeMaxT];            // this unit's RMSNorm sums of squares (WIDE)
     const DecodeArgs& a = p.d;
-    float* qh = rows_s;                           // [T][128] each
+    float* qh = rows_s;                           // [T][128] each; q, k, decay in key_pos order
     float* kh = qh + a.T * kHeadDim;
     float* vh = kh + a.T * kHeadDim;
     float* os = vh + a.T * kHeadDim;
@@ -87,34 +121,48 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
     const int vs = WIDE ? a.vsub : 1;
     const int gh = WIDE ? h / vs : h;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int H = a.H, K = a.K, R = a.K - 1;
-    const long C = (long)H * kHeadDim;
+    const int H = a.H, K = a.K;
     const int Hg = H / vs;
-    const long Cg = (long)Hg * kHeadDim;
     const int Hkq = prep_qk_heads(Hg, a.Hk);
-    const int hq = gh % Hkq;
+    const int hq = gh < Hkq ? gh : gh % Hkq;
     const long row0 = (long)n * a.T;
     const int T = a.keep != nullptr ? min(max(a.keep[n], 0), a.T) : a.T;
 
-    // ---- raw rows on their way to shared memory; they do not depend on the slots
-    const int task = tid >> 6, i0 = 2 * (tid & 63);
-    const int cg = gh * kHeadDim + i0;
-    float* dst = task == 0 ? qh : (task == 1 ? kh : vh);
-    if (task < 3) {
-        const void* raw = task == 0 ? a.q_raw : (task == 1 ? a.k_raw : a.v_raw);
-        const long Cp = plane_width(H, a.Hk, task);
-        const int cp = (task < 2 ? hq : h) * kHeadDim + i0;
-        for (int t = 0; t < T; ++t) {
-            if (a.raw_bf16)
-                cp_async_4(dst + t * kHeadDim + i0,
-                           reinterpret_cast<const __nv_bfloat16*>(raw) + (row0 + t) * Cp + cp);
-            else
-                cp_async_8(dst + t * kHeadDim + i0,
-                           reinterpret_cast<const float*>(raw) + (row0 + t) * Cp + cp);
+    // ---- raw rows on their way to shared memory; they do not depend on the slots.  Warps 0-3: a
+    //      channel of q and k a thread (each pair's even thread copies q, the odd one k); warps
+    //      4-5 a channel pair of v, warps 6-7 of the gate.
+    const bool is_qk = warp < 4, is_v = !is_qk && warp < 6;
+    const int i0 = is_qk ? tid & ~1 : 2 * (tid & 63);          // the pair's even channel
+    {
+        const void* src;
+        long width;
+        float* dst;
+        bool bf16 = a.raw_bf16 != 0;
+        if (is_qk) {
+            const bool odd = tid & 1;
+            width = plane_width(H, a.Hk, 0);
+            src = odd ? a.k_raw : a.q_raw;
+            dst = (odd ? kh : qh) + key_pos(i0);
+        } else if (is_v) {
+            width = (long)H * kHeadDim;
+            src = a.v_raw;
+            dst = vh + i0;
+        } else {
+            width = (long)Hg * kHeadDim;
+            src = a.f_raw;
+            dst = av + key_pos(i0);
+            bf16 = false;
         }
-    } else if (GATE_MODE == 0) {
-        for (int t = 0; t < T; ++t)
-            cp_async_8(av + t * kHeadDim + i0, a.f_raw + (row0 + t) * Cg + cg);
+        const long at = row0 * width + (is_qk ? hq : (is_v ? h : gh)) * kHeadDim + i0;
+        if (is_qk || is_v || GATE_MODE == 0) {
+            if (bf16) {
+                const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(src) + at;
+                for (int t = 0; t < T; ++t, s += width) cp_async_4(dst + t * kHeadDim, s);
+            } else {
+                const float* s = reinterpret_cast<const float*>(src) + at;
+                for (int t = 0; t < T; ++t, s += width) cp_async_8(dst + t * kHeadDim, s);
+            }
+        }
     }
     int slot_in, slot_out;
     const bool ok = pool_row(p.slots, p.slots_out, n, a.N, p.pool_rows, kThreads, a.err, slot_in,
@@ -124,41 +172,36 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
         return;
     }
 
-    // ---- this warp's codes and scales
-    const long unit_in = ((long)slot_in * H + h) * kHeadDim + warp * kColsPerWarp;
-    const long unit_out = ((long)slot_out * H + h) * kHeadDim + warp * kColsPerWarp;
-    const uint32_t* cin = reinterpret_cast<const uint32_t*>(p.codes) + unit_in * (kHeadDim / 4) + lane;
-    uint32_t* cout = reinterpret_cast<uint32_t*>(p.codes) + unit_out * (kHeadDim / 4) + lane;
-    uint32_t code[kColsPerWarp];
+    // ---- this group's codes and scales: 4 columns of 16 codes a lane
+    const int grp = lane >> 3, r = lane & 7;
+    const int col0 = warp * 16 + grp * kCols;
+    const long unit_in = ((long)slot_in * H + h) * kHeadDim + col0;
+    const long unit_out = ((long)slot_out * H + h) * kHeadDim + col0;
+    const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + unit_in * (kHeadDim / 16) + r;
+    uint4* cout = reinterpret_cast<uint4*>(p.codes) + unit_out * (kHeadDim / 16) + r;
+    uint4 code[kCols];
 #pragma unroll
-    for (int c = 0; c < kColsPerWarp; ++c) code[c] = __ldcs(cin + c * (kHeadDim / 4));
-    const float scales = p.scales[unit_in + (lane & (kColsPerWarp - 1))];
+    for (int c = 0; c < kCols; ++c) code[c] = __ldcs(cin + c * (kHeadDim / 16));
+    const float4 scale4 = *reinterpret_cast<const float4*>(p.scales + unit_in);
 
     // ---- conv weights, ring slots, gate inputs
-    float wr[2][KW], win[2][KW];
-    long ring_row = 0;
-    bool ring_owner = false;
+    // a q / k ring row that several units read is rolled by one of them, and only into another
+    // slot: in place it is left to the roll kernel that follows
+    const bool roll_qk = h == gh * vs && gh < Hkq && (Hkq == H || slot_in != slot_out);
+    const long ring_len = ring_channels(H, a.Hk) * (K - 1);
+    const float* ring_in = a.ring_out + (long)slot_in * ring_len;
+    float* ring_out = a.ring_out + (long)slot_out * ring_len;
+    // warps 0-3: channel tid of q and of k; warps 4-5: channels i0 and i0 + 1 of v
+    long ch0 = 0, ch1 = 0;
+    Conv<KT> cv0, cv1;
     float braw = 0.0f, fgate = 0.0f, dtb = 0.0f, alog = 0.0f;
     float2 dt = make_float2(0.0f, 0.0f);
-    const long ring_len = ring_channels(H, a.Hk) * R;
-    if (task < 3) {
-        const long ch = plane_offset(H, a.Hk, task) + (task < 2 ? hq : h) * kHeadDim + i0;
-        // a q / k ring row that several units read is rolled by one of them, and only into
-        // another slot: in place it is left to the roll kernel that follows
-        ring_owner = task == 2 || (h == gh * vs && gh < Hkq && (Hkq == H || slot_in != slot_out));
-        ring_row = ch * R;
-        const float* ring = a.ring_out + (long)slot_in * ring_len + ring_row;
-#pragma unroll
-        for (int m = 0; m < KW; ++m) {
-            const int jj = m - (KW - K);
-            const int d = KW - m;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                wr[e][m] = jj >= 0 ? a.conv_w[(ch + e) * K + jj] : 0.0f;
-                win[e][m] = d <= R ? ring[e * R + (R - d)] : 0.0f;
-            }
-        }
-        if (task == 2 && (tid & 63) < T) {
+    if (is_qk || is_v) {
+        ch0 = is_qk ? hq * kHeadDim + tid : plane_offset(H, a.Hk, 2) + (long)h * kHeadDim + i0;
+        ch1 = is_qk ? plane_offset(H, a.Hk, 1) + ch0 : ch0 + 1;
+        cv0.load(a.conv_w, ring_in, ch0, K);
+        cv1.load(a.conv_w, ring_in, ch1, K);
+        if (is_v && (tid & 63) < T) {
             const long rw = (row0 + (tid & 63)) * Hg + gh;
             braw = a.beta_raw[rw];
             if (GATE_MODE == 1) {
@@ -169,145 +212,200 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
         }
     } else if (GATE_MODE == 0) {
         alog = a.a_log[gh];
-        dt = *reinterpret_cast<const float2*>(a.dt_bias + cg);
+        dt = *reinterpret_cast<const float2*>(a.dt_bias + gh * kHeadDim + i0);
     }
 
     if (T == 0) {       // nothing accepted: the slot passes through unchanged (in place: untouched)
         cp_async_commit_wait();
         if (slot_in != slot_out) {
 #pragma unroll
-            for (int c = 0; c < kColsPerWarp; ++c) __stcs(cout + c * (kHeadDim / 4), code[c]);
-            if (lane < kColsPerWarp) p.scales[unit_out + lane] = scales;
-            if (ring_owner) {
-                float* ring = a.ring_out + (long)slot_out * ring_len + ring_row;
-#pragma unroll
-                for (int m = 0; m < KW; ++m) {
-                    const int d = KW - m;
-                    if (d <= R) {
-                        ring[R - d] = win[0][m];
-                        ring[R + R - d] = win[1][m];
-                    }
-                }
+            for (int c = 0; c < kCols; ++c) __stcs(cout + c * (kHeadDim / 16), code[c]);
+            if (r == 0) *reinterpret_cast<float4*>(p.scales + unit_out) = scale4;
+            if (is_v || (is_qk && roll_qk)) {
+                cv0.store(ring_out, ch0, K);
+                cv1.store(ring_out, ch1, K);
             }
         }
         return;
     }
 
     // ---- prologue: conv + SiLU and the ring roll, beta, the gate
-    if (task < 3) {
-        cp_async_commit_wait();
+    cp_async_commit_wait();
+    if (is_qk) {
+        __syncwarp();                             // the pair's other thread copied one plane
+        const int pos = key_pos(tid), pair = key_pos(i0);
         for (int t = 0; t < T; ++t) {
-            float* x2 = dst + t * kHeadDim + i0;
+            float q, k;
+            if (a.raw_bf16) {
+                const __nv_bfloat162 q2 = *reinterpret_cast<const __nv_bfloat162*>(qh + t * kHeadDim + pair);
+                const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(kh + t * kHeadDim + pair);
+                q = __bfloat162float(tid & 1 ? q2.y : q2.x);
+                k = __bfloat162float(tid & 1 ? k2.y : k2.x);
+            } else {
+                q = qh[t * kHeadDim + pos];
+                k = kh[t * kHeadDim + pos];
+            }
+            q = cv0.step(q, K);
+            k = cv1.step(k, K);
+            __syncwarp();                         // both threads have read the pair's raw samples
+            qh[t * kHeadDim + pos] = q;
+            kh[t * kHeadDim + pos] = k;
+            // three sums over the warp: lanes 0-7 end with q.q, 8-15 with q.k, 16-23 with k.k
+            const float qq = q * q, kk = k * k, qk = q * k;
+            const bool b4 = lane & 16, b3 = lane & 8;
+            const float h0 = (b4 ? kk : qq) + __shfl_xor_sync(0xffffffffu, b4 ? qq : kk, 16);
+            const float h1 = (b4 ? 0.0f : qk) + __shfl_xor_sync(0xffffffffu, b4 ? qk : 0.0f, 16);
+            float s = (b3 ? h1 : h0) + __shfl_xor_sync(0xffffffffu, b3 ? h0 : h1, 8);
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            if ((lane & 7) == 0 && lane < 24) part[lane >> 3][warp][t] = s;
+        }
+        if (roll_qk) {
+            cv0.store(ring_out, ch0, K);
+            cv1.store(ring_out, ch1, K);
+        }
+    } else if (is_v) {
+        for (int t = 0; t < T; ++t) {
+            float2* x2 = reinterpret_cast<float2*>(vh + t * kHeadDim + i0);
             float2 x;
             if (a.raw_bf16) x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x2));
-            else x = *reinterpret_cast<const float2*>(x2);
-            window_push(win[0], x.x);
-            window_push(win[1], x.y);
-            *reinterpret_cast<float2*>(x2) =
-                make_float2(silu_f(conv_taps_f(wr[0], win[0], K)), silu_f(conv_taps_f(wr[1], win[1], K)));
+            else x = *x2;
+            *x2 = make_float2(cv0.step(x.x, K), cv1.step(x.y, K));
         }
-        if (ring_owner) {
-            float* ring = a.ring_out + (long)slot_out * ring_len + ring_row;
-#pragma unroll
-            for (int m = 0; m < KW; ++m) {
-                const int d = KW - 1 - m;
-                if (d < R) {
-                    ring[R - 1 - d] = win[0][m];
-                    ring[R + R - 1 - d] = win[1][m];
-                }
-            }
-        }
-        if (task == 2 && (tid & 63) < T) {
+        cv0.store(ring_out, ch0, K);
+        cv1.store(ring_out, ch1, K);
+        if ((tid & 63) < T) {
             const int t = tid & 63;
             beta_s[t] = sigmoid_f(braw);
             if (GATE_MODE == 1) ascal[t] = decay_f(gdn_gate_f(fgate, dtb, alog));
         }
     } else if (GATE_MODE == 0) {
         const float rate = expf(alog);
-        cp_async_commit_wait();
         for (int t = 0; t < T; ++t) {
-            float2* f2 = reinterpret_cast<float2*>(av + t * kHeadDim + i0);
+            float2* f2 = reinterpret_cast<float2*>(av + t * kHeadDim + key_pos(i0));
             const float2 f = *f2;
             *f2 = make_float2(decay_f(kda_gate_f(f.x, dt.x, rate, a.gate_lb)),
                               decay_f(kda_gate_f(f.y, dt.y, rate, a.gate_lb)));
         }
     }
+    // the epilogue's norm weight and first gate row, requested ahead of the recurrence
+    const long C = (long)H * kHeadDim;
+    const float4 w4 = __ldg(reinterpret_cast<const float4*>(
+        a.norm_w + (WIDE ? (int)blockIdx.x % a.vsub : 0) * kHeadDim + 4 * lane));
+    float4 z_first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (warp < T)
+        z_first = __ldcs(reinterpret_cast<const float4*>(a.gate_raw + (row0 + warp) * C + h * kHeadDim + 4 * lane));
     __syncthreads();
-    // ---- q.q (warps 0-1), k.k (warps 2-3) and q.k (warps 4-5) of the conv outputs
-    if (task < 3) {
-        const float* xa = task == 1 ? kh : qh;
-        const float* xb = task == 0 ? qh : kh;
-        for (int t = 0; t < T; ++t) {
-            const float2 u = *reinterpret_cast<const float2*>(xa + t * kHeadDim + i0);
-            const float2 w = *reinterpret_cast<const float2*>(xb + t * kHeadDim + i0);
-            const float s = warp_sum(__fmul_rn(u.x, w.x) + __fmul_rn(u.y, w.y));
-            if (lane == 0) part[task][warp & 1][t] = s;
-        }
+    // lane t holds token t's l2 scales, normalised q.k and beta
+    float iq_l = 0.0f, ik_l = 0.0f, qk_l = 0.0f, beta_l = 0.0f;
+    if (lane < T) {
+        float s[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            s[j] = (part[j][0][lane] + part[j][1][lane]) + (part[j][2][lane] + part[j][3][lane]);
+        iq_l = l2_inv_f(s[0], a.l2_eps);
+        ik_l = l2_inv_f(s[2], a.l2_eps);
+        qk_l = s[1] * iq_l * ik_l;
+        beta_l = beta_s[lane];
     }
-    __syncthreads();
-    if (tid < T) {
-        const float iq = l2_inv_f(part[0][0][tid] + part[0][1][tid], a.l2_eps);
-        const float ik = l2_inv_f(part[1][0][tid] + part[1][1][tid], a.l2_eps);
-        inv_s[0][tid] = iq;
-        inv_s[1][tid] = ik;
-        qk_s[tid] = (part[2][0][tid] + part[2][1][tid]) * iq * ik;
-    }
-    __syncthreads();
 
-    // ---- the recurrence, 8 columns at a time; q and k are scaled as they are read
-    const float* vcol = vh + warp * kColsPerWarp;
-    float* ocol = os + warp * kColsPerWarp;
+    // ---- the recurrence, two columns of each group at a time
 #pragma unroll
-    for (int b = 0; b < kColsPerWarp; b += kBatch) {
-        float4 S[kBatch];
-#pragma unroll
-        for (int c = 0; c < kBatch; ++c)
-            S[c] = q8_decode4<FMT>(code[b + c], __shfl_sync(0xffffffffu, scales, b + c));
+    for (int b = 0; b < kCols; b += kBatch) {
+        float2 S[kBatch][8];
+        unpack16<FMT>(S[0], code[b], b == 0 ? scale4.x : scale4.z);
+        unpack16<FMT>(S[1], code[b + 1], b == 0 ? scale4.y : scale4.w);
+        const int own = (lane >> 1) & 1;          // the column of the batch whose sums end here
+#pragma unroll 1
         for (int t = 0; t < T; ++t) {
-            const float iq = inv_s[0][t], ik = inv_s[1][t];
-            float4 q = *reinterpret_cast<const float4*>(qh + t * kHeadDim + 4 * lane);
-            float4 k = *reinterpret_cast<const float4*>(kh + t * kHeadDim + 4 * lane);
-            q = make_float4(q.x * iq, q.y * iq, q.z * iq, q.w * iq);
-            k = make_float4(k.x * ik, k.y * ik, k.z * ik, k.w * ik);
-            float4 dec;
-            if (GATE_MODE == 0) dec = *reinterpret_cast<const float4*>(av + t * kHeadDim + 4 * lane);
-            else dec = make_float4(ascal[t], ascal[t], ascal[t], ascal[t]);
-            float v16[16];
+            const float* krow = kh + t * kHeadDim;
+            const float* qrow = qh + t * kHeadDim;
+            const float* arow = av + t * kHeadDim;
+            const float as = GATE_MODE == 0 ? 0.0f : ascal[t];
+            float4 k4[4];
+            float2 dk[kBatch][2], dq[kBatch][2];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                k4[m] = row4(krow, r, m);
+                const float4 q4 = row4(qrow, r, m);
+                const float4 a4 = GATE_MODE == 0 ? row4(arow, r, m) : make_float4(as, as, as, as);
+                const float2 al = make_float2(a4.x, a4.y), ah = make_float2(a4.z, a4.w);
+                const float2 kl = make_float2(k4[m].x, k4[m].y), kh2 = make_float2(k4[m].z, k4[m].w);
+                const float2 ql = make_float2(q4.x, q4.y), qh2 = make_float2(q4.z, q4.w);
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c) {
+                    S[c][2 * m] = __fmul2_rn(S[c][2 * m], al);
+                    S[c][2 * m + 1] = __fmul2_rn(S[c][2 * m + 1], ah);
+                    if (m == 0) {
+                        dk[c][0] = __fmul2_rn(S[c][0], kl);
+                        dk[c][1] = __fmul2_rn(S[c][1], kh2);
+                        dq[c][0] = __fmul2_rn(S[c][0], ql);
+                        dq[c][1] = __fmul2_rn(S[c][1], qh2);
+                    } else {
+                        dk[c][0] = __ffma2_rn(S[c][2 * m], kl, dk[c][0]);
+                        dk[c][1] = __ffma2_rn(S[c][2 * m + 1], kh2, dk[c][1]);
+                        dq[c][0] = __ffma2_rn(S[c][2 * m], ql, dq[c][0]);
+                        dq[c][1] = __ffma2_rn(S[c][2 * m + 1], qh2, dq[c][1]);
+                    }
+                }
+            }
+            // 4 sums over the 8 lanes: lanes with bit 2 clear end with P.k, the others with P.q, of
+            // column `own`
+            const bool b2 = lane & 4, b1 = lane & 2;
+            const float s0 = (dk[0][0].x + dk[0][0].y) + (dk[0][1].x + dk[0][1].y);
+            const float s1 = (dk[1][0].x + dk[1][0].y) + (dk[1][1].x + dk[1][1].y);
+            const float s2 = (dq[0][0].x + dq[0][0].y) + (dq[0][1].x + dq[0][1].y);
+            const float s3 = (dq[1][0].x + dq[1][0].y) + (dq[1][1].x + dq[1][1].y);
+            const float h0 = (b2 ? s2 : s0) + __shfl_xor_sync(0xffffffffu, b2 ? s0 : s2, 4);
+            const float h1 = (b2 ? s3 : s1) + __shfl_xor_sync(0xffffffffu, b2 ? s1 : s3, 4);
+            float red = (b1 ? h1 : h0) + __shfl_xor_sync(0xffffffffu, b1 ? h0 : h1, 2);
+            red += __shfl_xor_sync(0xffffffffu, red, 1);
+            const float iq = __shfl_sync(0xffffffffu, iq_l, t), ik = __shfl_sync(0xffffffffu, ik_l, t);
+            const float qk = __shfl_sync(0xffffffffu, qk_l, t), beta = __shfl_sync(0xffffffffu, beta_l, t);
+            const int col = col0 + b + own;
+            const float w = beta * (vh[t * kHeadDim + col] - ik * red);      // in lanes of P.k
+            const float wo = __shfl_xor_sync(0xffffffffu, w, 4);
+            if (b2 && !(lane & 1)) os[t * kHeadDim + col] = __fmul_rn(a.scale, fmaf(wo, qk, iq * red));
+            const float wk = w * ik;
 #pragma unroll
             for (int c = 0; c < kBatch; ++c) {
-                S[c] = mul4(S[c], dec);
-                v16[c] = dot4(S[c], k);
-                v16[8 + c] = dot4(S[c], q);
-            }
-            const float red = reduce16(v16, lane);
-            const int c_own = (lane >> 1) & 7;
-            // lanes 0-15 hold P.k of column lane >> 1, lanes 16-31 P.q of column (lane - 16) >> 1
-            const float w = beta_s[t] * (vcol[t * kHeadDim + b + c_own] - red);
-            const float wk = __shfl_sync(0xffffffffu, w, lane & 15);
-            if (lane >= 16 && (lane & 1) == 0)
-                ocol[t * kHeadDim + b + c_own] = __fmul_rn(a.scale, fmaf(wk, qk_s[t], red));
+                const float wc = __shfl_sync(0xffffffffu, wk, (lane & ~7) + 2 * c);
+                const float2 w2 = make_float2(wc, wc);
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c)
-                S[c] = fma4(k, __shfl_sync(0xffffffffu, w, 2 * c), S[c]);
+                for (int m = 0; m < 4; ++m) {
+                    S[c][2 * m] = __ffma2_rn(make_float2(k4[m].x, k4[m].y), w2, S[c][2 * m]);
+                    S[c][2 * m + 1] = __ffma2_rn(make_float2(k4[m].z, k4[m].w), w2, S[c][2 * m + 1]);
+                }
+            }
         }
+        // back to 8 bits: lanes with bit 2 clear finish column 0, the others column 1
+        float mx[kBatch];
 #pragma unroll
         for (int c = 0; c < kBatch; ++c) {
-            const uint32_t m = max(max(mag_bits(S[c].x), mag_bits(S[c].y)),
-                                   max(mag_bits(S[c].z), mag_bits(S[c].w)));
-            float scale, mul;
-            q8_row<FMT>(__reduce_max_sync(0xffffffffu, m), scale, mul);
-            __stcs(cout + (b + c) * (kHeadDim / 4), q8_encode4<FMT>(S[c], mul));
-            if (lane == 0) p.scales[unit_out + b + c] = scale;
+            float m = mag_max(S[c][0].x, S[c][0].y);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = mag_max(m, mag_max(S[c][i].x, S[c][i].y));
+            mx[c] = m;
         }
+        const bool b2 = lane & 4;
+        float top = mag_max(b2 ? mx[1] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[1], 4));
+        top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        // even lanes form the scale, odd ones the multiplier
+        const float f = q8_row_part<FMT>(mag_bits(top), lane & 1);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+            __stcs(cout + (b + c) * (kHeadDim / 16),
+                   pack16<FMT>(S[c], __shfl_sync(0xffffffffu, f, (lane & ~7) + 4 * c + 1)));
+        if ((lane & 3) == 0) p.scales[unit_out + b + (b2 ? 1 : 0)] = f;
     }
     __syncthreads();
     // ---- epilogue: gated RMSNorm, one warp per token row (as in kda_decode_fused)
-    const float4 w4 = *reinterpret_cast<const float4*>(
-        a.norm_w + (WIDE ? (int)blockIdx.x % a.vsub : 0) * kHeadDim + 4 * lane);
     if constexpr (WIDE) {
         for (int t = warp; t < T; t += kThreads / 32) {
             const float4 o4 = *reinterpret_cast<const float4*>(os + t * kHeadDim + 4 * lane);
-            const float ss = warp_sum(dot4(o4, o4));
+            const float ss = warp_sum((o4.x * o4.x + o4.y * o4.y) + (o4.z * o4.z + o4.w * o4.w));
             if (lane == 0) nss[t] = ss;
         }
         cluster_sync_all();
@@ -320,10 +418,10 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
             for (int b = 0; b < a.vsub; ++b) tot = tot + ld_cluster_f32(&nss[t], (uint32_t)b);
             inv = rms_inv_w(tot, a.rms_eps, a.vsub * kHeadDim);
         } else {
-            inv = rms_inv_f(warp_sum(dot4(o4, o4)), a.rms_eps);
+            inv = rms_inv_f(warp_sum((o4.x * o4.x + o4.y * o4.y) + (o4.z * o4.z + o4.w * o4.w)), a.rms_eps);
         }
         const long base = (row0 + t) * C + h * kHeadDim + 4 * lane;
-        const float4 z4 = *reinterpret_cast<const float4*>(a.gate_raw + base);
+        const float4 z4 = t == warp ? z_first : *reinterpret_cast<const float4*>(a.gate_raw + base);
         float4 y4;
         if (a.norm_silu) {
             y4.x = gated_norm_f<true>(o4.x, inv, w4.x, z4.x);
@@ -391,9 +489,9 @@ cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
     const size_t smem = (size_t)(GM == 0 ? 5 : 4) * a.d.T * kHeadDim * sizeof(float);
     KernelTimer kt(kKDecodeQ8, s);
     if (a.d.vsub > 1)
-        return a.d.K <= 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, true>, a, smem, s)
+        return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, true>, a, smem, s)
                           : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, true>, a, smem, s);
-    return a.d.K <= 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, false>, a, smem, s)
+    return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, false>, a, smem, s)
                       : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, false>, a, smem, s);
 }
 

@@ -29,6 +29,14 @@ __device__ __forceinline__ float q8_max() { return FMT == kQ8E4m3 ? 448.0f : 127
 // that an integer maximum over a row also finds non-finite elements.
 __device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// The larger magnitude of two values, with either sign, or a NaN if one of them is (as bits without
+// the sign: above every finite value and above inf, so that an integer maximum keeps it).
+__device__ __forceinline__ float mag_max(float a, float b) {
+    float m;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 // Row scale and multiplier from the row's largest magnitude bits.
 template <int FMT>
 __device__ __forceinline__ void q8_row(uint32_t amax_bits, float& scale, float& mul) {
@@ -45,20 +53,30 @@ __device__ __forceinline__ void q8_row(uint32_t amax_bits, float& scale, float& 
     }
 }
 
+// The scale or the multiplier of q8_row: one division, for lanes that share the two out.
+template <int FMT>
+__device__ __forceinline__ float q8_row_part(uint32_t amax_bits, bool want_mul) {
+    const float amax = __uint_as_float(amax_bits);
+    const float q = __fdiv_rn(want_mul ? q8_max<FMT>() : amax, want_mul ? amax : q8_max<FMT>());
+    if (amax_bits >= 0x7f800000u) return want_mul ? 0.0f : __uint_as_float(0x7fc00000u);
+    return amax_bits < 0x0d800000u ? 0.0f : q;
+}
+
 // Four codes as one word, element 0 in the low byte.  mul = 0 gives four zero codes whatever the
 // elements are (a NaN or an infinity times 0 would not).
 template <int FMT>
 __device__ __forceinline__ uint32_t q8_encode4(float4 x, float mul) {
     uint32_t w;
     if constexpr (FMT == kQ8E4m3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fmul_rn(x.x, mul), __fmul_rn(x.y, mul)), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fmul_rn(x.z, mul), __fmul_rn(x.w, mul)), __NV_SATFINITE, __NV_E4M3);
-        w = lo | (hi << 16);
+        const float2 m2 = make_float2(mul, mul);
+        const float2 lo = __fmul2_rn(make_float2(x.x, x.y), m2), hi = __fmul2_rn(make_float2(x.z, x.w), m2);
+        const uint32_t l = __nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t h = __nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3);
+        w = __byte_perm(l, h, 0x5410);
     } else {
         // |x * mul| <= 127 (1 + 2^-23): adding 1.5 * 2^23 rounds it to the nearest whole number,
-        // ties to even, in the low bits of the sum, whose low byte is the two's complement code
+        // ties to even, in the low bits of the sum, whose low byte is the two's complement code.
+        // (Not paired: the paired multiply and add were fused into one rounding.)
         const float big = 12582912.0f;
         const uint32_t a = __float_as_uint(__fadd_rn(__fmul_rn(x.x, mul), big));
         const uint32_t b = __float_as_uint(__fadd_rn(__fmul_rn(x.y, mul), big));
@@ -87,8 +105,9 @@ __device__ __forceinline__ float4 q8_decode4(uint32_t w, float scale) {
         v.z = __fadd_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)), -base);
         v.w = __fadd_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)), -base);
     }
-    return make_float4(__fmul_rn(v.x, scale), __fmul_rn(v.y, scale), __fmul_rn(v.z, scale),
-                       __fmul_rn(v.w, scale));
+    const float2 s2 = make_float2(scale, scale);
+    const float2 lo = __fmul2_rn(make_float2(v.x, v.y), s2), hi = __fmul2_rn(make_float2(v.z, v.w), s2);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
 // The pool rows that batch row n reads and writes.  A negative slot is padding: the row is skipped.
