@@ -982,13 +982,8 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(conv_w) || !aligned16(norm_w) ||
         !aligned16(gate_raw) || !aligned16(y))
         return KDA_ERR_ALIGN;
-    // raw rows (and per-channel gate rows) are copied two channels at a time
-    const uintptr_t rmask = raw_dtype == KDA_DTYPE_BF16 ? 3u : 7u;
-    if (((reinterpret_cast<uintptr_t>(q_raw) | reinterpret_cast<uintptr_t>(k_raw) |
-          reinterpret_cast<uintptr_t>(v_raw)) & rmask) != 0)
-        return KDA_ERR_ALIGN;
-    if (gate_mode == KDA_GATE_PER_CHANNEL &&
-        ((reinterpret_cast<uintptr_t>(f_raw) | reinterpret_cast<uintptr_t>(dt_bias)) & 7u) != 0)
+    if (!aligned16(q_raw) || !aligned16(k_raw) || !aligned16(v_raw) || !aligned16(ring_pool) ||
+        (gate_mode == KDA_GATE_PER_CHANNEL && (!aligned16(f_raw) || !aligned16(dt_bias))))
         return KDA_ERR_ALIGN;
     const size_t rows = (size_t)P * H * Dv;
     if (overlap2(codes, rows * kHeadDim, scales, rows * 4)) return KDA_ERR_STATE_ALIAS;

@@ -12,26 +12,30 @@
 // once, at the end.
 //
 // GB300 layout.  The bytes are a quarter of the f32 decode's (33 KB of state per (sequence, head)
-// read and written, against 131 KB), so instructions, not bytes, bound the first form of this
-// kernel (1860 warp instructions a warp at one token, of them 800 to round the state: 77 us at 64
-// sequences x 64 heads against 27 us of bytes).  One CTA owns one (sequence, unit).  8 lanes share
-// 4 value columns, lane r keys 16r .. 16r+15 of each, so that a column's codes are one 16-byte
-// access a lane, its reductions take three steps, and every k, decay and q value read from shared
-// memory serves several columns; the rows of q, k and the decay lie in shared memory in the order
-// that makes those reads conflict-free (key 16r + 4m + e at 32m + 4r + e).  The codes wait packed
-// in 16 registers, and two columns are unpacked at a time: three CTAs fit an SM.  The l2 norms
-// scale the finished sums instead of the vectors.  Of a reduction's lanes each finishes one
-// column: one pair of divisions a lane rounds the state, not one a column.
+// read and written, against 131 KB), so the instructions around them bound this kernel: at 64
+// sequences x 64 heads it runs 53 us, where its bytes need 27 (a first form with the lanes of a
+// warp across a column: 77 us).  One CTA owns one (sequence, unit), in four warps: thread = channel
+// of q, k, v and the gate in the prologue, so its address work is done by as few warps as the
+// occupancy allows (8 warps a CTA: 61 us).  8 lanes share 8 value columns, lane r keys
+// 16r .. 16r + 15 of each, so that a column's codes are one 16-byte access a lane, its reductions
+// take three steps, and every k, decay and q value read from shared memory serves two columns at a
+// time; the rows of q, k and the decay lie in shared memory in the order that makes those reads
+// conflict-free (key 16r + 4m + e at 32m + 4r + e).  Two columns are unpacked at a time, the codes of
+// the next two to four wait or are on their way in registers (four at a time: 61 us; all loads in
+// shared memory by bulk copies: 66; persistent blocks that prefetch the next sequence: 80).  The l2
+// norms scale the finished sums instead of the vectors.  Of a reduction's lanes each finishes one
+// column: one division a lane rounds the state, not two a column.
 #include "kda_q8.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kCols = 4;                     // value columns of a group of 8 lanes
+constexpr int kThreads = 128;
+constexpr int kCols = 8;                     // value columns of a group of 8 lanes
 constexpr int kBatch = 2;                    // of them unpacked at a time
-constexpr int kMinBlocks = 3;
+constexpr int kAhead = 4;                    // columns whose codes are loaded or on their way
+constexpr int kMinBlocks = 4;
 
 // Where key i of a q, k or decay row lies in shared memory.
 __device__ __forceinline__ int key_pos(int i) { return 32 * ((i >> 2) & 3) + 4 * (i >> 4) + (i & 3); }
@@ -66,18 +70,27 @@ __device__ __forceinline__ float4 row4(const float* row, int r, int m) {
 template <int KT>
 struct Conv {
     float w[KT], x[KT];
-    __device__ __forceinline__ void load(const float* conv_w, const float* ring, long ch, int K) {
+    __device__ __forceinline__ void weights(const float* conv_w, long ch, int K) {
         if constexpr (KT == 4) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(conv_w + ch * 4));
             w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int m = 0; m < KT; ++m) {
+                const int jj = m - (KT - K);
+                w[m] = jj >= 0 ? conv_w[ch * K + jj] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(const float* ring, long ch, int K) {
+        if constexpr (KT == 4) {
             const float* p = ring + ch * 3;
             x[0] = 0.0f; x[1] = p[0]; x[2] = p[1]; x[3] = p[2];
         } else {
             const float* p = ring + ch * (K - 1);
 #pragma unroll
             for (int m = 0; m < KT; ++m) {
-                const int jj = m - (KT - K), d = KT - m;
-                w[m] = jj >= 0 ? conv_w[ch * K + jj] : 0.0f;
+                const int d = KT - m;
                 x[m] = d <= K - 1 ? p[K - 1 - d] : 0.0f;
             }
         }
@@ -109,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
     __shared__ float beta_s[kDecodeMaxT], ascal[kDecodeMaxT];
     __shared__ float part[3][4][kDecodeMaxT];     // q.q, q.k and k.k of four warps
     __shared__ float nss[kDecodeMaxT];            // this unit's RMSNorm sums of squares (WIDE)
+    __shared__ int2 row_s;                        // slots in (-1: left out) and out
     const DecodeArgs& a = p.d;
     float* qh = rows_s;                           // [T][128] each; q, k, decay in key_pos order
     float* kh = qh + a.T * kHeadDim;
@@ -128,166 +142,150 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
     const long row0 = (long)n * a.T;
     const int T = a.keep != nullptr ? min(max(a.keep[n], 0), a.T) : a.T;
 
-    // ---- raw rows on their way to shared memory; they do not depend on the slots.  Warps 0-3: a
-    //      channel of q and k a thread (each pair's even thread copies q, the odd one k); warps
-    //      4-5 a channel pair of v, warps 6-7 of the gate.
-    const bool is_qk = warp < 4, is_v = !is_qk && warp < 6;
-    const int i0 = is_qk ? tid & ~1 : 2 * (tid & 63);          // the pair's even channel
-    {
-        const void* src;
-        long width;
-        float* dst;
-        bool bf16 = a.raw_bf16 != 0;
-        if (is_qk) {
-            const bool odd = tid & 1;
-            width = plane_width(H, a.Hk, 0);
-            src = odd ? a.k_raw : a.q_raw;
-            dst = (odd ? kh : qh) + key_pos(i0);
-        } else if (is_v) {
-            width = (long)H * kHeadDim;
-            src = a.v_raw;
-            dst = vh + i0;
-        } else {
-            width = (long)Hg * kHeadDim;
-            src = a.f_raw;
-            dst = av + key_pos(i0);
-            bf16 = false;
+    // ---- raw rows on their way to shared memory; they do not depend on the slots.  Thread tid has
+    //      channel tid of q, k, v and the gate; two bf16 channels are one copy: the pair's even
+    //      thread copies q and v, the odd one k.
+    const int pos = key_pos(tid), pair = key_pos(tid & ~1);
+    const long wq = plane_width(H, a.Hk, 0), wv = (long)H * kHeadDim, wg = (long)Hg * kHeadDim;
+    if (a.raw_bf16) {
+        const bool odd = tid & 1;
+        const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(odd ? a.k_raw : a.q_raw) +
+                                 row0 * wq + hq * kHeadDim + (tid & ~1);
+        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v_raw) + row0 * wv +
+                                 (long)h * kHeadDim + tid;
+        float* dst = (odd ? kh : qh) + pair;
+        for (int t = 0; t < T; ++t) {
+            cp_async_4(dst + t * kHeadDim, x + t * wq);
+            if (!odd) cp_async_4(vh + t * kHeadDim + tid, v + t * wv);
         }
-        const long at = row0 * width + (is_qk ? hq : (is_v ? h : gh)) * kHeadDim + i0;
-        if (is_qk || is_v || GATE_MODE == 0) {
-            if (bf16) {
-                const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(src) + at;
-                for (int t = 0; t < T; ++t, s += width) cp_async_4(dst + t * kHeadDim, s);
-            } else {
-                const float* s = reinterpret_cast<const float*>(src) + at;
-                for (int t = 0; t < T; ++t, s += width) cp_async_8(dst + t * kHeadDim, s);
-            }
+    } else {
+        const long at = row0 * wq + hq * kHeadDim + tid;
+        const float* q = reinterpret_cast<const float*>(a.q_raw) + at;
+        const float* k = reinterpret_cast<const float*>(a.k_raw) + at;
+        const float* v = reinterpret_cast<const float*>(a.v_raw) + row0 * wv + (long)h * kHeadDim + tid;
+        for (int t = 0; t < T; ++t) {
+            cp_async_4(qh + t * kHeadDim + pos, q + t * wq);
+            cp_async_4(kh + t * kHeadDim + pos, k + t * wq);
+            cp_async_4(vh + t * kHeadDim + tid, v + t * wv);
         }
     }
-    int slot_in, slot_out;
-    const bool ok = pool_row(p.slots, p.slots_out, n, a.N, p.pool_rows, kThreads, a.err, slot_in,
-                             slot_out);
-    if (!ok) {                                    // uniform over the cluster: n decides alone
+    if (GATE_MODE == 0) {
+        const float* f = a.f_raw + row0 * wg + (long)gh * kHeadDim + tid;
+        for (int t = 0; t < T; ++t) cp_async_4(av + t * kHeadDim + pos, f + t * wg);
+    }
+    // ---- warp 3 looks the slots over
+    if (warp == 3) {
+        int in, out;
+        const bool ok = pool_row_warp(p.slots, p.slots_out, n, a.N, p.pool_rows, a.err, in, out);
+        if (lane == 0) row_s = make_int2(ok ? in : -1, out);
+    }
+    // ---- what does not depend on them either: conv weights, gate inputs
+    const int chq = hq * kHeadDim + tid, chk = (int)plane_offset(H, a.Hk, 1) + chq;
+    const int chv = (int)plane_offset(H, a.Hk, 2) + h * kHeadDim + tid;
+    Conv<KT> cq, ck, cv;
+    cq.weights(a.conv_w, chq, K);
+    ck.weights(a.conv_w, chk, K);
+    cv.weights(a.conv_w, chv, K);
+    const float alog = a.a_log[gh];
+    const float dt = GATE_MODE == 0 ? a.dt_bias[(long)gh * kHeadDim + tid] : a.dt_bias[gh];
+    if (tid < T) {
+        const long rw = (row0 + tid) * Hg + gh;
+        beta_s[tid] = sigmoid_f(a.beta_raw[rw]);
+        if (GATE_MODE == 1) ascal[tid] = decay_f(gdn_gate_f(a.f_raw[rw], dt, alog));
+    }
+    __syncthreads();
+    const int slot_in = row_s.x, slot_out = row_s.y;
+    if (slot_in < 0) {                            // uniform over the cluster: n decides alone
         cp_async_commit_wait();
         return;
     }
 
-    // ---- this group's codes and scales: 4 columns of 16 codes a lane
+    // ---- this group's codes and scales: 8 columns of 16 codes a lane, the first 4 now
     const int grp = lane >> 3, r = lane & 7;
-    const int col0 = warp * 16 + grp * kCols;
+    const int col0 = warp * 32 + grp * kCols;
     const long unit_in = ((long)slot_in * H + h) * kHeadDim + col0;
     const long unit_out = ((long)slot_out * H + h) * kHeadDim + col0;
     const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + unit_in * (kHeadDim / 16) + r;
     uint4* cout = reinterpret_cast<uint4*>(p.codes) + unit_out * (kHeadDim / 16) + r;
-    uint4 code[kCols];
+    uint4 code[kAhead];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) code[c] = __ldcs(cin + c * (kHeadDim / 16));
-    const float4 scale4 = *reinterpret_cast<const float4*>(p.scales + unit_in);
+    for (int c = 0; c < kAhead; ++c) code[c] = __ldcs(cin + c * (kHeadDim / 16));
+    const float scale_l = p.scales[unit_in + r];  // lane r: column r's
 
-    // ---- conv weights, ring slots, gate inputs
+    // ---- ring slots
     // a q / k ring row that several units read is rolled by one of them, and only into another
     // slot: in place it is left to the roll kernel that follows
     const bool roll_qk = h == gh * vs && gh < Hkq && (Hkq == H || slot_in != slot_out);
     const long ring_len = ring_channels(H, a.Hk) * (K - 1);
     const float* ring_in = a.ring_out + (long)slot_in * ring_len;
     float* ring_out = a.ring_out + (long)slot_out * ring_len;
-    // warps 0-3: channel tid of q and of k; warps 4-5: channels i0 and i0 + 1 of v
-    long ch0 = 0, ch1 = 0;
-    Conv<KT> cv0, cv1;
-    float braw = 0.0f, fgate = 0.0f, dtb = 0.0f, alog = 0.0f;
-    float2 dt = make_float2(0.0f, 0.0f);
-    if (is_qk || is_v) {
-        ch0 = is_qk ? hq * kHeadDim + tid : plane_offset(H, a.Hk, 2) + (long)h * kHeadDim + i0;
-        ch1 = is_qk ? plane_offset(H, a.Hk, 1) + ch0 : ch0 + 1;
-        cv0.load(a.conv_w, ring_in, ch0, K);
-        cv1.load(a.conv_w, ring_in, ch1, K);
-        if (is_v && (tid & 63) < T) {
-            const long rw = (row0 + (tid & 63)) * Hg + gh;
-            braw = a.beta_raw[rw];
-            if (GATE_MODE == 1) {
-                fgate = a.f_raw[rw];
-                dtb = a.dt_bias[gh];
-                alog = a.a_log[gh];
-            }
-        }
-    } else if (GATE_MODE == 0) {
-        alog = a.a_log[gh];
-        dt = *reinterpret_cast<const float2*>(a.dt_bias + gh * kHeadDim + i0);
-    }
+    cq.load(ring_in, chq, K);
+    ck.load(ring_in, chk, K);
+    cv.load(ring_in, chv, K);
 
     if (T == 0) {       // nothing accepted: the slot passes through unchanged (in place: untouched)
         cp_async_commit_wait();
         if (slot_in != slot_out) {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) __stcs(cout + c * (kHeadDim / 16), code[c]);
-            if (r == 0) *reinterpret_cast<float4*>(p.scales + unit_out) = scale4;
-            if (is_v || (is_qk && roll_qk)) {
-                cv0.store(ring_out, ch0, K);
-                cv1.store(ring_out, ch1, K);
+            for (int c = 0; c < kCols; ++c)
+                __stcs(cout + c * (kHeadDim / 16), c < kAhead ? code[c < kAhead ? c : 0] : __ldcs(cin + c * (kHeadDim / 16)));
+            p.scales[unit_out + r] = scale_l;
+            cv.store(ring_out, chv, K);
+            if (roll_qk) {
+                cq.store(ring_out, chq, K);
+                ck.store(ring_out, chk, K);
             }
         }
         return;
     }
 
-    // ---- prologue: conv + SiLU and the ring roll, beta, the gate
+    // ---- prologue: conv + SiLU and the ring roll, the sums of q and k, the gate
     cp_async_commit_wait();
-    if (is_qk) {
-        __syncwarp();                             // the pair's other thread copied one plane
-        const int pos = key_pos(tid), pair = key_pos(i0);
-        for (int t = 0; t < T; ++t) {
-            float q, k;
-            if (a.raw_bf16) {
-                const __nv_bfloat162 q2 = *reinterpret_cast<const __nv_bfloat162*>(qh + t * kHeadDim + pair);
-                const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(kh + t * kHeadDim + pair);
-                q = __bfloat162float(tid & 1 ? q2.y : q2.x);
-                k = __bfloat162float(tid & 1 ? k2.y : k2.x);
-            } else {
-                q = qh[t * kHeadDim + pos];
-                k = kh[t * kHeadDim + pos];
-            }
-            q = cv0.step(q, K);
-            k = cv1.step(k, K);
-            __syncwarp();                         // both threads have read the pair's raw samples
-            qh[t * kHeadDim + pos] = q;
-            kh[t * kHeadDim + pos] = k;
-            // three sums over the warp: lanes 0-7 end with q.q, 8-15 with q.k, 16-23 with k.k
-            const float qq = q * q, kk = k * k, qk = q * k;
-            const bool b4 = lane & 16, b3 = lane & 8;
-            const float h0 = (b4 ? kk : qq) + __shfl_xor_sync(0xffffffffu, b4 ? qq : kk, 16);
-            const float h1 = (b4 ? 0.0f : qk) + __shfl_xor_sync(0xffffffffu, b4 ? qk : 0.0f, 16);
-            float s = (b3 ? h1 : h0) + __shfl_xor_sync(0xffffffffu, b3 ? h0 : h1, 8);
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            if ((lane & 7) == 0 && lane < 24) part[lane >> 3][warp][t] = s;
+    __syncwarp();                                 // a pair's two threads copied for each other
+    const float rate = GATE_MODE == 0 ? expf(alog) : 0.0f;
+    for (int t = 0; t < T; ++t) {
+        float* qr = qh + t * kHeadDim;
+        float* kr = kh + t * kHeadDim;
+        float* vr = vh + t * kHeadDim;
+        float q, k, v;
+        if (a.raw_bf16) {
+            const __nv_bfloat162 q2 = *reinterpret_cast<const __nv_bfloat162*>(qr + pair);
+            const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(kr + pair);
+            const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162*>(vr + (tid & ~1));
+            q = __bfloat162float(tid & 1 ? q2.y : q2.x);
+            k = __bfloat162float(tid & 1 ? k2.y : k2.x);
+            v = __bfloat162float(tid & 1 ? v2.y : v2.x);
+        } else {
+            q = qr[pos];
+            k = kr[pos];
+            v = vr[tid];
         }
-        if (roll_qk) {
-            cv0.store(ring_out, ch0, K);
-            cv1.store(ring_out, ch1, K);
+        q = cq.step(q, K);
+        k = ck.step(k, K);
+        v = cv.step(v, K);
+        __syncwarp();                             // both threads have read the pair's raw samples
+        qr[pos] = q;
+        kr[pos] = k;
+        vr[tid] = v;
+        if (GATE_MODE == 0) {
+            float* ar = av + t * kHeadDim + pos;
+            *ar = decay_f(kda_gate_f(*ar, dt, rate, a.gate_lb));
         }
-    } else if (is_v) {
-        for (int t = 0; t < T; ++t) {
-            float2* x2 = reinterpret_cast<float2*>(vh + t * kHeadDim + i0);
-            float2 x;
-            if (a.raw_bf16) x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x2));
-            else x = *x2;
-            *x2 = make_float2(cv0.step(x.x, K), cv1.step(x.y, K));
-        }
-        cv0.store(ring_out, ch0, K);
-        cv1.store(ring_out, ch1, K);
-        if ((tid & 63) < T) {
-            const int t = tid & 63;
-            beta_s[t] = sigmoid_f(braw);
-            if (GATE_MODE == 1) ascal[t] = decay_f(gdn_gate_f(fgate, dtb, alog));
-        }
-    } else if (GATE_MODE == 0) {
-        const float rate = expf(alog);
-        for (int t = 0; t < T; ++t) {
-            float2* f2 = reinterpret_cast<float2*>(av + t * kHeadDim + key_pos(i0));
-            const float2 f = *f2;
-            *f2 = make_float2(decay_f(kda_gate_f(f.x, dt.x, rate, a.gate_lb)),
-                              decay_f(kda_gate_f(f.y, dt.y, rate, a.gate_lb)));
-        }
+        // three sums over the warp: lanes 0-7 end with q.q, 8-15 with q.k, 16-23 with k.k
+        const float qq = q * q, kk = k * k, qk = q * k;
+        const bool b4 = lane & 16, b3 = lane & 8;
+        const float h0 = (b4 ? kk : qq) + __shfl_xor_sync(0xffffffffu, b4 ? qq : kk, 16);
+        const float h1 = (b4 ? 0.0f : qk) + __shfl_xor_sync(0xffffffffu, b4 ? qk : 0.0f, 16);
+        float s = (b3 ? h1 : h0) + __shfl_xor_sync(0xffffffffu, b3 ? h0 : h1, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        if ((lane & 7) == 0 && lane < 24) part[lane >> 3][warp][t] = s;
+    }
+    cv.store(ring_out, chv, K);
+    if (roll_qk) {
+        cq.store(ring_out, chq, K);
+        ck.store(ring_out, chk, K);
     }
     // the epilogue's norm weight and first gate row, requested ahead of the recurrence
     const long C = (long)H * kHeadDim;
@@ -311,11 +309,18 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
     }
 
     // ---- the recurrence, two columns of each group at a time
-#pragma unroll
+    // (rolled: four copies of it would not fit the instruction cache)
+#pragma unroll 1
     for (int b = 0; b < kCols; b += kBatch) {
         float2 S[kBatch][8];
-        unpack16<FMT>(S[0], code[b], b == 0 ? scale4.x : scale4.z);
-        unpack16<FMT>(S[1], code[b + 1], b == 0 ? scale4.y : scale4.w);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+            unpack16<FMT>(S[c], code[c], __shfl_sync(0xffffffffu, scale_l, (lane & ~7) + b + c));
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+            code[c] = code[kBatch + c];
+            if (b + kAhead < kCols) code[kBatch + c] = __ldcs(cin + (b + kAhead + c) * (kHeadDim / 16));
+        }
         const int own = (lane >> 1) & 1;          // the column of the batch whose sums end here
 #pragma unroll 1
         for (int t = 0; t < T; ++t) {
@@ -446,8 +451,7 @@ __global__ void __launch_bounds__(kThreads) kda_ring_roll_q8_kernel(const Decode
     const int n = blockIdx.y, R = a.K - 1;
     int slot_in, slot_out;
     // (the decode kernel has reported bad slots already)
-    if (!pool_row(p.slots, p.slots_out, n, a.N, p.pool_rows, kThreads, nullptr, slot_in, slot_out))
-        return;
+    if (!pool_row_warp(p.slots, p.slots_out, n, a.N, p.pool_rows, nullptr, slot_in, slot_out)) return;
     const int T = a.keep != nullptr ? min(max(a.keep[n], 0), a.T) : a.T;
     if (slot_in != slot_out || T == 0) return;
     const int width = (int)plane_width(a.H, a.Hk, 0);

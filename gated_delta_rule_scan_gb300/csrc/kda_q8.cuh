@@ -113,22 +113,23 @@ __device__ __forceinline__ float4 q8_decode4(uint32_t w, float scale) {
 // The pool rows that batch row n reads and writes.  A negative slot is padding: the row is skipped.
 // A slot past the pool, and an output slot that another row reads or an earlier row writes, raise
 // the error word and the row is skipped too, so that no two blocks race on a slot.  Every thread of
-// the block calls it; `threads` is the block's size.
-__device__ __forceinline__ bool pool_row(const int* slots, const int* slots_out, int n, int N,
-                                         int pool_rows, int threads, int* err, int& in, int& out) {
+// the warp calls it.
+__device__ __forceinline__ bool pool_row_warp(const int* slots, const int* slots_out, int n, int N,
+                                              int pool_rows, int* err, int& in, int& out) {
+    const int lane = threadIdx.x & 31;
     in = slots ? slots[n] : n;
     out = slots_out ? slots_out[n] : in;
     const bool live = in >= 0 && out >= 0;
     bool bad = in >= pool_rows || out >= pool_rows;
     if (slots || slots_out) {
-        for (int m = threadIdx.x; m < N; m += threads) {
+        for (int m = lane; m < N; m += 32) {
             const int im = slots ? slots[m] : m;
             const int om = slots_out ? slots_out[m] : im;
             if (m != n && im >= 0 && om >= 0) bad |= im == out || (m < n && om == out);
         }
     }
-    const bool any = __syncthreads_or(live && bad) != 0;
-    if (any && threadIdx.x == 0 && err) atomicOr(err, kDevErrSlot);
+    const bool any = __any_sync(0xffffffffu, live && bad);
+    if (any && lane == 0 && err) atomicOr(err, kDevErrSlot);
     return live && !any;
 }
 

@@ -615,8 +615,8 @@ int kda_state_load_q8(const void* codes, const float* scales, float* state, int 
  * y rows of padding, of rows left out and of rows t >= keep[n] are not written.
  * A slot may be read by several rows (a shared prefix); a row whose output slot another row reads
  * or an earlier row writes is left out (40013, above).  Grouped queries and wide value heads may
- * roll the ring in place here.  conv_w is [16B]; q/k/v raw rows are 4-byte (bf16) or 8-byte (f32) aligned, f_raw and
- * dt_bias 8-byte (KDA_GATE_PER_CHANNEL).
+ * roll the ring in place here.  q_raw, k_raw, v_raw, conv_w, ring_pool, codes, scales, norm_w,
+ * gate_raw, y and, with KDA_GATE_PER_CHANNEL, f_raw and dt_bias are [16B].
  * Unlike kda_decode_fused, a T-token call is not T one-token calls bit for bit: those round the
  * state T times.  A call's outputs do not depend on the other rows of the batch.
  */
