@@ -34,15 +34,12 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 8;                    // warps of a team: they split K of a tile
+constexpr int kTeam = kWarps * 32;
 constexpr int kRows = 16;                    // weight rows of a tile: the MMA's M
 constexpr int kChunk = 128;                  // k of one warp step
-constexpr int kTok = 8;                      // tokens of one pass
-// Rows up to which this form is taken: one launch and no workspace.  At 64 heads x 6144 it runs 33
-// us at one row but 91 at eight (two MMA tiles), the form for batches 34 at any of them.
-constexpr int kSmallT = 4;
-constexpr int kXSmem = 72 * 1024;            // x of one block: three blocks per SM
+constexpr int kTok = 8;                      // tokens at most: the MMA's N, for a bf16 x
+constexpr int kXSmem = 160 * 1024;           // x of one block at most
 
 struct W4Params {
     const void* x;
@@ -59,13 +56,13 @@ struct W4Params {
 struct W4Smem {
     int x, factor, xsum, red, total;
 };
-__host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group) {
+__host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group, int teams) {
     W4Smem m;
     m.x = 0;                                                   // f16 [chunk][4][cols][4][8]
     m.factor = chunks * kChunk * cols * 2;                     // f32 [chunk][8]
     m.xsum = m.factor + chunks * kTok * 4;                     // f32 [group][8]
-    m.red = m.xsum + chunks * (kChunk / group) * kTok * 4;     // f32 [2][warps][8][16]
-    m.total = m.red + 2 * kWarps * kTok * kRows * 4;
+    m.red = m.xsum + chunks * (kChunk / group) * kTok * 4;     // f32 [teams][2][warps][8][16]
+    m.total = m.red + teams * (2 * kWarps * kTok * kRows * 4);
     return m;
 }
 
@@ -107,58 +104,110 @@ __device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
     }
 }
 
-__device__ __forceinline__ float load_param(const void* p, long i, int bf16) {
-    return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
-                : reinterpret_cast<const float*>(p)[i];
-}
+// N = 1, 2 or 4 consecutive scales or zero points as they lie in memory; value() is the i-th.
+template <int N, bool BF16>
+struct W4Par {
+    static constexpr int kWords = BF16 ? (N + 1) / 2 : N;
+    uint32_t u[kWords];
+    __device__ __forceinline__ void load(const void* p) {
+        if constexpr (BF16 && N == 1) {
+            u[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+        } else if constexpr (kWords == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+        } else if constexpr (kWords == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            u[0] = v.x; u[1] = v.y;
+        } else {
+            u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        }
+    }
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (BF16) return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+        else return __uint_as_float(u[i]);
+    }
+};
 
 // Codes, scales and zero points of 16 rows x 128 k as one warp holds them: lane 4g + c has, of rows
 // g and g + 8 and of each group, the c-th quarter's codes.
-template <int G>
+template <int G, bool SBF16, bool ZERO>
 struct W4Frag {
     uint32_t w[2][4];
-    float c[2][kChunk / G];
-    float z[2][kChunk / G];
+    W4Par<kChunk / G, SBF16> c[2];
+    W4Par<kChunk / G, SBF16> z[ZERO ? 2 : 1];
 };
 
-template <int G>
-__device__ __forceinline__ void frag_load(W4Frag<G>& f, const W4Params& p, int tile, int chunk,
-                                          int lane) {
-    int wi = 0;
-    while (wi + 1 < p.nw && tile >= p.tile_start[wi + 1]) ++wi;
-    const int row0 = (tile - p.tile_start[wi]) * kRows;
-    const int g = lane >> 2, c = lane & 3;
-    const int ng = p.in_f / G;
+// The chunks of one warp in the order of their use: its share of K for each of its block's tiles.
+template <int G, bool SBF16, bool ZERO>
+struct W4Stream {
+    const uint8_t* w[2];                         // rows g and g + 8 at the next chunk
+    const uint8_t* c[2];
+    const uint8_t* z[ZERO ? 2 : 1];
+    int tile, left;                              // its tile, its chunks left
+
+    __device__ __forceinline__ void open(const W4Params& p, int chunk, int chunks, int lane) {
+        constexpr int kSize = SBF16 ? 2 : 4;
+        int wi = 0;
+        while (wi + 1 < p.nw && tile >= p.tile_start[wi + 1]) ++wi;
+        const int row0 = (tile - p.tile_start[wi]) * kRows + (lane >> 2);
+        left = chunks;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        // rows past the weight repeat its last one; their sums are not written
-        const long row = min(row0 + g + 8 * r, p.rows[wi] - 1);
-        const uint8_t* base = p.w[wi] + row * (p.in_f / 2) + chunk * (kChunk / 2) + c * (G / 8);
-#pragma unroll
-        for (int q = 0; q < kChunk / G; ++q) {
-            load_words<G / 8>(&f.w[r][q * (G / 32)], base + q * (G / 2));
-            const long gi = row * ng + chunk * (kChunk / G) + q;
-            f.c[r][q] = load_param(p.scale[wi], gi, p.scale_bf16);
-            f.z[r][q] = p.has_zero ? load_param(p.zero[wi], gi, p.scale_bf16) : 8.0f;
+        for (int i = 0; i < 2; ++i) {
+            // rows past the weight repeat its last one; their sums are not written
+            const long row = min(row0 + 8 * i, p.rows[wi] - 1);
+            const long par = (row * (p.in_f / G) + chunk * (kChunk / G)) * kSize;
+            w[i] = p.w[wi] + row * (p.in_f / 2) + chunk * (kChunk / 2) + (lane & 3) * (G == 32 ? 8 : G / 8);
+            c[i] = static_cast<const uint8_t*>(p.scale[wi]) + par;
+            if constexpr (ZERO) z[i] = static_cast<const uint8_t*>(p.zero[wi]) + par;
         }
     }
+    __device__ __forceinline__ void fetch(W4Frag<G, SBF16, ZERO>& f) {
+        constexpr int kStep = kChunk / G * (SBF16 ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (G == 32) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) load_words<8>(&f.w[i][q * 2], w[i] + q * 32);
+            } else {
+#pragma unroll
+                for (int q = 0; q < kChunk / G; ++q)
+                    load_words<G / 8>(&f.w[i][q * (G / 32)], w[i] + q * (G / 2));
+            }
+            f.c[i].load(c[i]);
+            w[i] += kChunk / 2;
+            c[i] += kStep;
+            if constexpr (ZERO) {
+                f.z[i].load(z[i]);
+                z[i] += kStep;
+            }
+        }
+    }
+};
+
+// Teams of a block, at most: three, but two where three requests' scales and zero points do not fit
+// in 80 registers (f32 ones of 32 k each: 49 us against 71 at 64 heads x 6144).
+constexpr int w4_teams(int group, bool scale_bf16, bool zero) {
+    return group == 32 && !scale_bf16 && zero ? 2 : 3;
 }
 
-// x of the block's chunks [ch0, ch0 + chunks) and tokens [tok0, tok0 + nt): MMA operands, power-of-
-// two factors and group sums.  A half warp takes one (chunk, token): lane u holds k = 8u .. 8u+7.
+__device__ __forceinline__ void team_sync(int team) {
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam) : "memory");
+}
+
+// x of the block's chunks [ch0, ch0 + chunks): MMA operands, power-of-two factors and group sums.  A half warp takes one (chunk, token): lane u holds k = 8u .. 8u+7.
 template <int G, bool XBF16>
 __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, const W4Smem& lay,
-                                        int ch0, int chunks, int tok0, int nt, int cols) {
+                                        int ch0, int chunks, int nt, int cols) {
     const int half = threadIdx.x >> 4, u = threadIdx.x & 15;
     float* factor = reinterpret_cast<float*>(smem + lay.factor);
     float* xsum = reinterpret_cast<float*>(smem + lay.xsum);
     const int total = chunks * nt;
-    for (int i0 = 0; i0 < total; i0 += kThreads / 16) {
+    for (int i0 = 0; i0 < total; i0 += blockDim.x / 16) {
         const int i = i0 + half;
         const bool live = i < total;
         const int ch = live ? i / nt : 0, tk = live ? i % nt : 0;
         float v[8];
-        const long at = (long)(tok0 + tk) * p.in_f + (long)(ch0 + ch) * kChunk + 8 * u;
+        const long at = (long)tk * p.in_f + (long)(ch0 + ch) * kChunk + 8 * u;
         if constexpr (XBF16) {
             const uint4 r = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.x) + at));
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -200,7 +249,7 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
         // k = 8u is word jj of quarter c of its group
         const int k0 = 8 * u, q = k0 / G, c = (k0 % G) / (G / 4), jj = q * (G / 32) + (k0 % (G / 4)) / 8;
         uint4* xs = reinterpret_cast<uint4*>(smem + lay.x);
-        const long base = (long)(ch * 4 + jj) * cols * 4 + c;
+        const long base = (long)(ch * 4 + jj) * cols * 4 + (G == 32 ? (c >> 1) + 2 * (c & 1) : c);
         if constexpr (XBF16) {
             xs[base + tk * 4] = *reinterpret_cast<const uint4*>(hi);
         } else {
@@ -212,91 +261,106 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
     }
 }
 
-// NT: 8-column MMA tiles (f32 x: 4 tokens each; bf16 x: 8).
-template <int G, bool XBF16, int NT>
-__global__ void __launch_bounds__(kThreads, 3) kda_proj_w4_kernel(const __grid_constant__ W4Params p) {
+template <int G, bool XBF16, bool SBF16, bool ZERO>
+__global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_kernel(const __grid_constant__ W4Params p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int team = threadIdx.x / kTeam, teams = blockDim.x / kTeam;
+    const int warp = threadIdx.x % kTeam >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int rank = blockIdx.x % p.ksplit, group_id = blockIdx.x / p.ksplit;
-    const int stride = gridDim.x / p.ksplit;
-    const int tok0 = blockIdx.y * kTok, nt = min(kTok, p.t - tok0);
-    const int cols = XBF16 ? nt : 2 * nt;
+    const int rank = blockIdx.x % p.ksplit;
+    const int blocks = gridDim.x / p.ksplit, stride = blocks * teams;
+    const int first = team * blocks + blockIdx.x / p.ksplit;
+    const int nt = p.t, cols = XBF16 ? nt : 2 * nt;
     const int all = p.in_f / kChunk;
     const int ch0 = all * rank / p.ksplit, ch1 = all * (rank + 1) / p.ksplit;
     const int chunks = ch1 - ch0;
-    const W4Smem lay = w4_smem((all + p.ksplit - 1) / p.ksplit, cols, G);
+    const W4Smem lay = w4_smem((all + p.ksplit - 1) / p.ksplit, cols, G, teams);
     const int tiles = p.tile_start[p.nw];
     const float* factor = reinterpret_cast<const float*>(smem + lay.factor);
     const float* xsum = reinterpret_cast<const float*>(smem + lay.xsum);
-    const uint4* xs = reinterpret_cast<const uint4*>(smem + lay.x);
-    float* red = reinterpret_cast<float*>(smem + lay.red);
+    float* red = reinterpret_cast<float*>(smem + lay.red) + team * (2 * kWarps * kTok * kRows);
 
     const int w0 = chunks * warp / kWarps, w1 = chunks * (warp + 1) / kWarps;
-    W4Frag<G> cur;
-    if (group_id < tiles && w0 < w1) frag_load<G>(cur, p, group_id, ch0 + w0, lane);
-    stage_x<G, XBF16>(p, smem, lay, ch0, chunks, tok0, nt, cols);
+    const int mine = w1 - w0;
+    W4Stream<G, SBF16, ZERO> in;
+    in.tile = first;
+    if (mine > 0 && in.tile < tiles) in.open(p, ch0 + w0, mine, lane);
+    const auto fetch = [&](W4Frag<G, SBF16, ZERO>& f) {
+        if (mine == 0 || in.tile >= tiles) return;
+        in.fetch(f);
+        if (--in.left == 0) {
+            in.tile += stride;
+            if (in.tile < tiles) in.open(p, ch0 + w0, mine, lane);
+        }
+    };
+    W4Frag<G, SBF16, ZERO> f0, f1, f2;
+    fetch(f0);
+    fetch(f1);
+    stage_x<G, XBF16>(p, smem, lay, ch0, chunks, nt, cols);
     __syncthreads();
 
+    // Columns of the MMA past the batch repeat its last one: a column of the result depends on its
+    // own column of x alone.
+    const uint4* xs0 = reinterpret_cast<const uint4*>(smem + lay.x) + min(g, cols - 1) * 4 + c;
     int buf = 0;
-    for (int tile = group_id; tile < tiles; tile += stride, buf ^= 1) {
-        // acc[i][r][e]: f32 x: token 4 i + c of row g + 8 r (e = 0); bf16: token 2 c + e
-        float acc[NT][2][2] = {};
-        for (int ch = w0; ch < w1; ++ch) {
-            W4Frag<G> nxt;
-            const bool last = ch + 1 == w1;
-            const int ntile = last ? tile + stride : tile;
-            const bool more = ntile < tiles;
-            if (more) frag_load<G>(nxt, p, ntile, ch0 + (last ? w0 : ch + 1), lane);
+    // All teams of a cluster go through the same number of tiles, the last one past the end maybe.
+    for (int tile = first; tile - team * blocks < tiles; tile += stride, buf ^= 1) {
+        // acc[r][e]: f32 x: token c of row g + 8 r (e = 0); bf16: token 2 c + e
+        float acc[2][2] = {};
+        const uint4* xs = xs0 + w0 * 16 * cols;
+        for (int ch = tile < tiles ? w0 : w1; ch < w1; ++ch, xs += 16 * cols) {
+            fetch(f2);
+            if constexpr (G == 32) {
 #pragma unroll
-            for (int q = 0; q < kChunk / G; ++q) {
-                float d[NT][4] = {};
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = q * (G / 32); j < (q + 1) * (G / 32); ++j) {
-                    const uint32_t u0 = cur.w[0][j], u1 = cur.w[1][j];
-                    const uint32_t a0 = nib_lo(u0), a1 = nib_lo(u1), a2 = nib_hi(u0), a3 = nib_hi(u1);
-                    const uint32_t e0 = nib_lo(u0 >> 8), e1 = nib_lo(u1 >> 8);
-                    const uint32_t e2 = nib_hi(u0 >> 8), e3 = nib_hi(u1 >> 8);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        uint4 b = make_uint4(0u, 0u, 0u, 0u);
-                        if (8 * i + g < cols) b = xs[((ch * 4 + j) * cols + 8 * i + g) * 4 + c];
-                        mma_16816(d[i], a0, a1, a2, a3, b.x, b.y);
-                        mma_16816(d[i], e0, e1, e2, e3, b.z, b.w);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int e = 0; e < (XBF16 ? 2 : 1); ++e) {
-                        const int tk = XBF16 ? 2 * c + e : 4 * i + c;
-                        const float f = factor[ch * kTok + tk];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float s = XBF16 ? d[i][2 * r + e] : d[i][2 * r] + d[i][2 * r + 1];
-                            acc[i][r][e] = fmaf(s * f, cur.c[r][q], acc[i][r][e]);
-                            if (p.has_zero)
-                                acc[i][r][e] = fmaf((8.0f - cur.z[r][q]) * cur.c[r][q],
-                                                    xsum[(ch * (kChunk / G) + q) * kTok + tk],
-                                                    acc[i][r][e]);
-                        }
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t& a = f0.w[i][q];
+                        uint32_t& b = f0.w[i][q + 1];
+                        const bool up = c >= 2;
+                        const uint32_t r = __shfl_xor_sync(0xffffffffu, up ? a : b, 2);
+                        a = up ? r : a;
+                        b = up ? b : r;
                     }
             }
-            if (more) cur = nxt;
+#pragma unroll
+            for (int q = 0; q < kChunk / G; ++q) {
+                float d[4] = {};
+#pragma unroll
+                for (int j = q * (G / 32); j < (q + 1) * (G / 32); ++j) {
+                    const uint32_t u0 = f0.w[0][j], u1 = f0.w[1][j];
+                    const uint4 b = xs[j * 4 * cols];
+                    mma_16816(d, nib_lo(u0), nib_lo(u1), nib_hi(u0), nib_hi(u1), b.x, b.y);
+                    mma_16816(d, nib_lo(u0 >> 8), nib_lo(u1 >> 8), nib_hi(u0 >> 8), nib_hi(u1 >> 8), b.z, b.w);
+                }
+#pragma unroll
+                for (int e = 0; e < (XBF16 ? 2 : 1); ++e) {
+                    const int tk = XBF16 ? 2 * c + e : c;
+                    const float f = factor[ch * kTok + tk];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float s = XBF16 ? d[2 * r + e] : d[2 * r] + d[2 * r + 1];
+                        acc[r][e] = fmaf(s * f, f0.c[r].value(q), acc[r][e]);
+                        if constexpr (ZERO)
+                            acc[r][e] = fmaf((8.0f - f0.z[r].value(q)) * f0.c[r].value(q),
+                                             xsum[(ch * (kChunk / G) + q) * kTok + tk], acc[r][e]);
+                    }
+                }
+            }
+            f0 = f1;
+            f1 = f2;
         }
         // this tile's sums of all warps, in warp order
         float* rb = red + buf * (kWarps * kTok * kRows);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int e = 0; e < (XBF16 ? 2 : 1); ++e)
 #pragma unroll
-            for (int e = 0; e < (XBF16 ? 2 : 1); ++e)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    rb[(warp * kTok + (XBF16 ? 2 * c + e : 4 * i + c)) * kRows + g + 8 * r] = acc[i][r][e];
-        __syncthreads();
+            for (int r = 0; r < 2; ++r)
+                rb[(warp * kTok + (XBF16 ? 2 * c + e : c)) * kRows + g + 8 * r] = acc[r][e];
+        team_sync(team);
         int wi = 0;
         while (wi + 1 < p.nw && tile >= p.tile_start[wi + 1]) ++wi;
-        const int tk = threadIdx.x / kRows, r = threadIdx.x % kRows;
+        const int tk = threadIdx.x % kTeam / kRows, r = threadIdx.x % kRows;
         const int row = (tile - p.tile_start[wi]) * kRows + r;
         float sum = 0.0f;
         if (tk < nt) {
@@ -307,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_proj_w4_kernel(const __grid_c
             // the cluster's CTAs: each leaves its sums where warp 0's were, then rank 0 adds them.
             // Its reads of this buffer end before any CTA passes the next tile's barrier and fills
             // the buffer after that one.
-            __syncthreads();
+            team_sync(team);
             if (tk < nt) rb[tk * kRows + r] = sum;
             cluster_sync_all();
             if (rank == 0 && tk < nt) {
@@ -315,19 +379,19 @@ __global__ void __launch_bounds__(kThreads, 3) kda_proj_w4_kernel(const __grid_c
                 for (int k = 0; k < p.ksplit; ++k) sum += ld_cluster_f32(&rb[tk * kRows + r], (uint32_t)k);
             }
         }
-        if (rank == 0 && tk < nt && row < p.rows[wi])
-            p.out[wi][(long)(tok0 + tk) * p.rows[wi] + row] = sum;
+        if (rank == 0 && tk < nt && tile < tiles && row < p.rows[wi])
+            p.out[wi][(long)tk * p.rows[wi] + row] = sum;
     }
     if (p.ksplit > 1) cluster_sync_all();        // rank 0 has read the last tile's sums
 }
 
-template <int G, bool XBF16, int NT>
-cudaError_t launch_rows(const W4Params& p, int grid, size_t smem, cudaStream_t s) {
+template <int G, bool XBF16, bool SBF16, bool ZERO>
+cudaError_t launch_rows(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
     static PerDevice<int> smem_set_for;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const auto kernel = kda_proj_w4_kernel<G, XBF16, NT>;
+    const auto kernel = kda_proj_w4_kernel<G, XBF16, SBF16, ZERO>;
     const bool cached = dev >= 0 && dev < kMaxDevices;
     if (smem > 48 * 1024 && (!cached || smem_set_for[dev].load(std::memory_order_acquire) < (int)smem)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -340,8 +404,8 @@ cudaError_t launch_rows(const W4Params& p, int grid, size_t smem, cudaStream_t s
         }
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.t + kTok - 1) / kTok));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)(teams * kTeam));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -355,21 +419,29 @@ cudaError_t launch_rows(const W4Params& p, int grid, size_t smem, cudaStream_t s
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int G, bool XBF16>
+cudaError_t launch_params(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
+    if (p.has_zero)
+        return p.scale_bf16 ? launch_rows<G, XBF16, true, true>(p, grid, teams, smem, s)
+                            : launch_rows<G, XBF16, false, true>(p, grid, teams, smem, s);
+    return p.scale_bf16 ? launch_rows<G, XBF16, true, false>(p, grid, teams, smem, s)
+                        : launch_rows<G, XBF16, false, false>(p, grid, teams, smem, s);
+}
+
 template <int G>
-cudaError_t launch_group(const W4Params& p, bool x_bf16, int grid, size_t smem, cudaStream_t s) {
-    if (x_bf16) return launch_rows<G, true, 1>(p, grid, smem, s);
-    return p.t <= 4 ? launch_rows<G, false, 1>(p, grid, smem, s)
-                    : launch_rows<G, false, 2>(p, grid, smem, s);
+cudaError_t launch_group(const W4Params& p, bool x_bf16, int grid, int teams, size_t smem, cudaStream_t s) {
+    return x_bf16 ? launch_params<G, true>(p, grid, teams, smem, s) : launch_params<G, false>(p, grid, teams, smem, s);
 }
 
 }  // namespace
 
 size_t proj_w4_workspace_bytes(int t, int in_f) {
-    return t > kSmallT ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
+    // (a bf16 x takes the form for few rows up to 8, an f32 x, in two parts, up to 4)
+    return t > kTok / 2 ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
 }
 
 cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
-    if (a.t > kSmallT) return launch_proj_w4_wide(a, s);
+    if (a.t > (a.x_bf16 ? kTok : kTok / 2)) return launch_proj_w4_wide(a, s);
     W4Params p{};
     p.x = a.x;
     int tiles = 0;
@@ -386,25 +458,23 @@ cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
     if (tiles == 0) return cudaSuccess;
     p.nw = a.nw; p.t = a.t; p.in_f = a.in_f; p.scale_bf16 = a.scale_bf16; p.has_zero = a.has_zero;
     // the fewest CTAs along K whose share of x fits
-    const int nt = a.t < kTok ? a.t : kTok, cols = a.x_bf16 ? nt : 2 * nt;
+    const int cols = a.x_bf16 ? a.t : 2 * a.t;
     const int all = a.in_f / kChunk;
     int ks = 1;
     while (ks < 8 && (all + ks - 1) / ks * (kChunk * cols * 2) > kXSmem) ks *= 2;
     p.ksplit = ks;
-    const W4Smem lay = w4_smem((all + ks - 1) / ks, cols, a.group);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    int per_sm = 220 * 1024 / (lay.total + 1024);
-    per_sm = per_sm > 3 ? 3 : (per_sm < 1 ? 1 : per_sm);
-    int groups = sms * per_sm / ks;
-    if (groups > tiles) groups = tiles;
-    if (groups < 1) groups = 1;
+    const int blocks = tiles < sms / ks ? tiles : (sms / ks < 1 ? 1 : sms / ks);
+    const int most = w4_teams(a.group, a.scale_bf16 != 0, a.has_zero != 0);
+    const int want = (tiles + blocks - 1) / blocks, teams = want < most ? want : most;
+    const W4Smem lay = w4_smem((all + ks - 1) / ks, cols, a.group, teams);
     switch (a.group) {
-        case 32: return launch_group<32>(p, a.x_bf16 != 0, groups * ks, (size_t)lay.total, s);
-        case 64: return launch_group<64>(p, a.x_bf16 != 0, groups * ks, (size_t)lay.total, s);
-        default: return launch_group<128>(p, a.x_bf16 != 0, groups * ks, (size_t)lay.total, s);
+        case 32: return launch_group<32>(p, a.x_bf16 != 0, blocks * ks, teams, (size_t)lay.total, s);
+        case 64: return launch_group<64>(p, a.x_bf16 != 0, blocks * ks, teams, (size_t)lay.total, s);
+        default: return launch_group<128>(p, a.x_bf16 != 0, blocks * ks, teams, (size_t)lay.total, s);
     }
 }
 
