@@ -5,26 +5,34 @@
 // for up to 8 weights that read one x.  q is a 4-bit code (two to a byte, the even k in the low
 // nibble), c the scale and z the zero point of G consecutive k (z = 8 without zero points).
 //
-// Mathematics.  A code minus 8 is an integer of -8 .. 7, exact in f16, so the products run on the
-// tensor cores with the integers themselves and the scale multiplies each group's f32 sum: no
-// weight is ever rounded.  x is split over 128 k at a time into f16 hi + lo after scaling by the
-// power of two that brings the largest of the 128 magnitudes to [2^14, 2^15); hi + lo hold 22
-// significant bits of every element that matters to the sum, and the power of two goes back in
-// with the group's scale.  A bf16 x needs the hi part only: its 8 bits fit.  Zero points other
-// than 8 add (8 - z) c sum_group(x), from f32 sums of x over each group.
+// Mathematics.  Codes become f16 integers and the products run on the tensor cores with them: no
+// weight is ever rounded.  The zero point comes off each group's f32 sum, which the scale then
+// multiplies:
+//     out = sum over groups of c (sum_k q x - z / 8 sum_k 8 x).
+// x is scaled over 128 k at a time by the power of two that brings the largest magnitude of the 128
+// to [2^14, 2^15), split into f16 hi + lo, and the power of two goes back in with the group's scale.
+// hi is a multiple of 4, so that sum_k q hi and sum_k 8 hi, at most 15 * 2^15 * 128 < 2^24 such
+// steps, are exact in f32 and so is their difference: subtracting after the sum loses nothing, and a
+// code needs no more than a logical operation to become a number (taking 8 off each code first: 22.8
+// us against 19.1 at one row x 6144, 64 heads).  hi + lo is x within 2^-23 of the element's own
+// magnitude or 2^-25 of the largest of the 128, whichever is more.
+//     5 to 8 rows of a bf16 x take hi alone (8 bits fit, in any order of magnitude), to stay within
+// the MMA's 8 columns.  Its sums are rounded, so there the codes have 8 taken off first.
 //
-// The form for few rows (t <= 8 per pass).  The weights' bytes are read once and bound the launch,
-// so the kernel is built around their stream: a warp takes 16 weight rows x 128 k (1 KB of codes,
-// two wide loads a lane straight into registers, the next 1 KB requested before the present one is
-// used), and turns them into mma.sync m16n8k16 operands with two logical operations and two f16
-// multiply-adds for 8 weights each way.  The order of k inside an MMA is free as long as both
-// operands agree, so x is laid out in shared memory once per block in the order in which the
-// nibbles of a word come out, and one 16-byte shared load feeds two MMAs.  The 8 columns of the
-// MMA carry hi and lo of 4 tokens (f32 x) or 8 tokens (bf16 x).
-// Blocks are persistent over 16-row tiles; the 8 warps of a block split K, and their partial sums
-// meet in shared memory in warp order.  Where x of all of K does not fit, the CTAs of a cluster
-// split K further and add their sums through distributed shared memory in rank order.  No atomics:
-// results do not depend on timing.
+// The form for few rows: t <= 4, or 8 of a bf16 x.  The weights' bytes are read once and bound the
+// launch, so the kernel is built around their stream: a warp takes 16 weight rows x 128 k (1 KB of
+// codes, wide loads straight into registers, the next 1 KB asked for before the present one is used;
+// two ahead: 19.1 us against 17.7), and turns them into mma.sync m16n8k16 operands.  The order of k inside
+// an MMA is free as long as both operands agree, so x is laid out in shared memory once per block in
+// the order in which the nibbles of a word come out, and one 16-byte shared load feeds two MMAs.
+// The 8 columns of the MMA carry hi and lo of 4 tokens, or hi of 8.
+// One block per SM holds x for up to three teams of 8 warps (three blocks staged it three times: 32
+// us against 25 at four rows, before the codes' centring went).  Each team takes tiles of 16 rows in turn; its warps split K, and
+// their partial sums meet in shared memory in warp order.  Where x of all of K does not fit, the
+// CTAs of a cluster split K further and add their sums through distributed shared memory in rank
+// order.  No atomics: results do not depend on timing.  At 64 heads x 6144 and groups of 128: one row
+// 17.7 us (4.5 TB/s of codes and scales; the shared loads, MMAs and logical operations of a chunk
+// cost about as much again as its bytes), four rows 20.4, eight bf16 rows 24.9.
 #include <cuda_fp16.h>
 
 #include "kda_device.cuh"
@@ -39,6 +47,7 @@ constexpr int kTeam = kWarps * 32;
 constexpr int kRows = 16;                    // weight rows of a tile: the MMA's M
 constexpr int kChunk = 128;                  // k of one warp step
 constexpr int kTok = 8;                      // tokens at most: the MMA's N, for a bf16 x
+constexpr float kMagic = 50331648.0f;        // 1.5 * 2^25
 constexpr int kXSmem = 160 * 1024;           // x of one block at most
 
 struct W4Params {
@@ -49,32 +58,36 @@ struct W4Params {
     float* out[kW4MaxWeights];
     int rows[kW4MaxWeights];
     int tile_start[kW4MaxWeights + 1];
-    int nw, t, in_f, scale_bf16, has_zero, ksplit;
+    int nw, t, in_f, x_bf16, scale_bf16, has_zero, ksplit;
 };
 
 // Bytes of the block's shared memory for `chunks` chunks of k and `cols` MMA columns.
 struct W4Smem {
-    int x, factor, xsum, red, total;
+    int x, factor, eights, red, total;
 };
 __host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group, int teams) {
     W4Smem m;
     m.x = 0;                                                   // f16 [chunk][4][cols][4][8]
     m.factor = chunks * kChunk * cols * 2;                     // f32 [chunk][8]
-    m.xsum = m.factor + chunks * kTok * 4;                     // f32 [group][8]
-    m.red = m.xsum + chunks * (kChunk / group) * kTok * 4;     // f32 [teams][2][warps][8][16]
+    m.eights = m.factor + chunks * kTok * 4;                   // f32 [group][8]
+    m.red = m.eights + chunks * (kChunk / group) * kTok * 4;     // f32 [teams][2][warps][8][16]
     m.total = m.red + teams * (2 * kWarps * kTok * kRows * 4);
     return m;
 }
 
-// Nibbles p and p + 4 (lo) or p + 1 and p + 5 (hi) of the word w >> 4p as f16 pairs minus 8.  A
-// nibble or-ed into the mantissa of 1024 (0x6400) is 1024 + q in its low place and 1024 + 16 q one
-// place up; both corrections are exact.
+// Nibbles 0 and 4 (lo) or 1 and 5 (hi) of a word as f16 pairs.  Alone in its place of the mantissa,
+// with no exponent, a code q is the f16 number q 2^-24 or 16 q 2^-24.  CENTRED: q - 8, from 1024 + q
+// and 1024 + 16 q (the code or-ed into the mantissa of 1024); both corrections are exact.
+template <bool CENTRED>
 __device__ __forceinline__ uint32_t nib_lo(uint32_t w) {
+    if constexpr (!CENTRED) return w & 0x000f000fu;
     const uint32_t v = (w & 0x000f000fu) | 0x64006400u;
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1032.0f));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+template <bool CENTRED>
 __device__ __forceinline__ uint32_t nib_hi(uint32_t w) {
+    if constexpr (!CENTRED) return w & 0x00f000f0u;
     const uint32_t v = (w & 0x00f000f0u) | 0x64006400u;
     const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f),
                               __float2half2_rn(-72.0f));
@@ -129,7 +142,8 @@ struct W4Par {
 };
 
 // Codes, scales and zero points of 16 rows x 128 k as one warp holds them: lane 4g + c has, of rows
-// g and g + 8 and of each group, the c-th quarter's codes.
+// g and g + 8 and of each group, the c-th quarter's codes.  (Groups of 32 are loaded two at a time,
+// 8 bytes a lane, and sorted by a shuffle when used: 28.4 us against 31.9 with 4-byte loads.)
 template <int G, bool SBF16, bool ZERO>
 struct W4Frag {
     uint32_t w[2][4];
@@ -184,8 +198,9 @@ struct W4Stream {
     }
 };
 
-// Teams of a block, at most: three, but two where three requests' scales and zero points do not fit
-// in 80 registers (f32 ones of 32 k each: 49 us against 71 at 64 heads x 6144).
+// Teams of a block, at most: three (four of 64 registers a thread are as fast: 17.7 us at one row x
+// 6144 and 64 heads either way), but two where f32 scales and zero points of 32 k each need more
+// registers (33.8 us against 36.1).
 constexpr int w4_teams(int group, bool scale_bf16, bool zero) {
     return group == 32 && !scale_bf16 && zero ? 2 : 3;
 }
@@ -194,13 +209,13 @@ __device__ __forceinline__ void team_sync(int team) {
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam) : "memory");
 }
 
-// x of the block's chunks [ch0, ch0 + chunks): MMA operands, power-of-two factors and group sums.  A half warp takes one (chunk, token): lane u holds k = 8u .. 8u+7.
-template <int G, bool XBF16>
+// x of the block's chunks [ch0, ch0 + chunks): MMA operands and power-of-two factors.  A half warp
+// takes one (chunk, token): lane u holds k = 8u .. 8u+7.
+template <int G, bool ONE>
 __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, const W4Smem& lay,
                                         int ch0, int chunks, int nt, int cols) {
     const int half = threadIdx.x >> 4, u = threadIdx.x & 15;
     float* factor = reinterpret_cast<float*>(smem + lay.factor);
-    float* xsum = reinterpret_cast<float*>(smem + lay.xsum);
     const int total = chunks * nt;
     for (int i0 = 0; i0 < total; i0 += blockDim.x / 16) {
         const int i = i0 + half;
@@ -208,7 +223,7 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
         const int ch = live ? i / nt : 0, tk = live ? i % nt : 0;
         float v[8];
         const long at = (long)tk * p.in_f + (long)(ch0 + ch) * kChunk + 8 * u;
-        if constexpr (XBF16) {
+        if (ONE || p.x_bf16) {
             const uint4 r = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.x) + at));
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -223,16 +238,10 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
         uint32_t m = 0;
-        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-            sum += v[j];
-        }
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll
-        for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         // 2^(14 - e) for the largest magnitude's exponent e (at least -100); 1 when it is not finite
         const int e = max((int)(m >> 23) - 127, -100);
         const bool fin = m < 0x7f800000u;
@@ -243,25 +252,32 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
         for (int j = 0; j < 8; ++j) {
             const float y = __fmul_rn(v[j], up);
             const int at8 = j < 4 ? 2 * j : 2 * (j - 4) + 1;     // nibble order (0 4 1 5 2 6 3 7)
-            hi[at8] = __float2half_rn(y);
-            lo[at8] = __float2half_rn(y - __half2float(hi[at8]));
+            if constexpr (ONE) {
+                hi[at8] = __float2half_rn(y);
+            } else {
+                // to a multiple of 4 (a step of f32 at 2^25), then to f16's 11 bits
+                const float h = __half2float(__float2half_rn(__fsub_rn(__fadd_rn(y, kMagic), kMagic)));
+                const float w = j & 1 ? 0.0625f : 1.0f;          // odd codes come times 16
+                hi[at8] = __float2half_rn(h * w);
+                lo[at8] = __float2half_rn(__fsub_rn(y, h) * w);
+            }
         }
         // k = 8u is word jj of quarter c of its group
         const int k0 = 8 * u, q = k0 / G, c = (k0 % G) / (G / 4), jj = q * (G / 32) + (k0 % (G / 4)) / 8;
         uint4* xs = reinterpret_cast<uint4*>(smem + lay.x);
+        // (G = 32: after the trade, lanes 1 and 2 hold words 2 and 1 of their group)
         const long base = (long)(ch * 4 + jj) * cols * 4 + (G == 32 ? (c >> 1) + 2 * (c & 1) : c);
-        if constexpr (XBF16) {
+        if constexpr (ONE) {
             xs[base + tk * 4] = *reinterpret_cast<const uint4*>(hi);
         } else {
             xs[base + (2 * tk) * 4] = *reinterpret_cast<const uint4*>(hi);
             xs[base + (2 * tk + 1) * 4] = *reinterpret_cast<const uint4*>(lo);
         }
         if (u == 0) factor[ch * kTok + tk] = fin ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.0f;
-        if (u % (G / 8) == 0) xsum[(ch * (kChunk / G) + u / (G / 8)) * kTok + tk] = sum;
     }
 }
 
-template <int G, bool XBF16, bool SBF16, bool ZERO>
+template <int G, bool ONE, bool SBF16, bool ZERO>
 __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_kernel(const __grid_constant__ W4Params p) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int team = threadIdx.x / kTeam, teams = blockDim.x / kTeam;
@@ -270,14 +286,14 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
     const int rank = blockIdx.x % p.ksplit;
     const int blocks = gridDim.x / p.ksplit, stride = blocks * teams;
     const int first = team * blocks + blockIdx.x / p.ksplit;
-    const int nt = p.t, cols = XBF16 ? nt : 2 * nt;
+    const int nt = p.t, cols = ONE ? nt : 2 * nt;
     const int all = p.in_f / kChunk;
     const int ch0 = all * rank / p.ksplit, ch1 = all * (rank + 1) / p.ksplit;
     const int chunks = ch1 - ch0;
     const W4Smem lay = w4_smem((all + p.ksplit - 1) / p.ksplit, cols, G, teams);
     const int tiles = p.tile_start[p.nw];
     const float* factor = reinterpret_cast<const float*>(smem + lay.factor);
-    const float* xsum = reinterpret_cast<const float*>(smem + lay.xsum);
+    float* eights = reinterpret_cast<float*>(smem + lay.eights);
     float* red = reinterpret_cast<float*>(smem + lay.red) + team * (2 * kWarps * kTok * kRows);
 
     const int w0 = chunks * warp / kWarps, w1 = chunks * (warp + 1) / kWarps;
@@ -293,23 +309,45 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
             if (in.tile < tiles) in.open(p, ch0 + w0, mine, lane);
         }
     };
-    W4Frag<G, SBF16, ZERO> f0, f1, f2;
+    W4Frag<G, SBF16, ZERO> f0, f1;
     fetch(f0);
-    fetch(f1);
-    stage_x<G, XBF16>(p, smem, lay, ch0, chunks, nt, cols);
+    stage_x<G, ONE>(p, smem, lay, ch0, chunks, nt, cols);
     __syncthreads();
 
     // Columns of the MMA past the batch repeat its last one: a column of the result depends on its
     // own column of x alone.
     const uint4* xs0 = reinterpret_cast<const uint4*>(smem + lay.x) + min(g, cols - 1) * 4 + c;
+    // The sums of a group whose codes are all 8, by the very steps that sum the groups below: what
+    // a zero point of 8 takes off.  A group that holds nothing but its zero point comes out as 0.
+    for (int ch = !ONE || ZERO ? threadIdx.x >> 5 : chunks; ch < chunks; ch += blockDim.x >> 5) {
+#pragma unroll
+        for (int q = 0; q < kChunk / G; ++q) {
+            float d[4] = {};
+#pragma unroll
+            for (int j = q * (G / 32); j < (q + 1) * (G / 32); ++j) {
+                const uint4 b = xs0[(ch * 4 + j) * 4 * cols];
+                const uint32_t lo = ONE ? 0x48004800u : nib_lo<false>(0x88888888u);      // 8 in f16
+                const uint32_t hi = ONE ? 0x48004800u : nib_hi<false>(0x88888888u);
+                mma_16816(d, lo, lo, hi, hi, b.x, b.y);
+                mma_16816(d, lo, lo, hi, hi, b.z, b.w);
+            }
+            if (g == 0) {
+                float* o = eights + (ch * (kChunk / G) + q) * kTok;
+                if constexpr (ONE) *reinterpret_cast<float2*>(o + 2 * c) = make_float2(d[0], d[1]);
+                else o[c] = d[0] + d[1];
+            }
+        }
+    }
+    __syncthreads();
     int buf = 0;
     // All teams of a cluster go through the same number of tiles, the last one past the end maybe.
     for (int tile = first; tile - team * blocks < tiles; tile += stride, buf ^= 1) {
-        // acc[r][e]: f32 x: token c of row g + 8 r (e = 0); bf16: token 2 c + e
+        // acc[r][e]: token c of row g + 8 r (e = 0), ONE: token 2 c + e
         float acc[2][2] = {};
         const uint4* xs = xs0 + w0 * 16 * cols;
         for (int ch = tile < tiles ? w0 : w1; ch < w1; ++ch, xs += 16 * cols) {
-            fetch(f2);
+            fetch(f1);
+            // groups of 32: the lane's 8 bytes are of one group; trade for a word of either
             if constexpr (G == 32) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -330,33 +368,35 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
                 for (int j = q * (G / 32); j < (q + 1) * (G / 32); ++j) {
                     const uint32_t u0 = f0.w[0][j], u1 = f0.w[1][j];
                     const uint4 b = xs[j * 4 * cols];
-                    mma_16816(d, nib_lo(u0), nib_lo(u1), nib_hi(u0), nib_hi(u1), b.x, b.y);
-                    mma_16816(d, nib_lo(u0 >> 8), nib_lo(u1 >> 8), nib_hi(u0 >> 8), nib_hi(u1 >> 8), b.z, b.w);
+                    mma_16816(d, nib_lo<ONE>(u0), nib_lo<ONE>(u1), nib_hi<ONE>(u0), nib_hi<ONE>(u1), b.x, b.y);
+                    mma_16816(d, nib_lo<ONE>(u0 >> 8), nib_lo<ONE>(u1 >> 8), nib_hi<ONE>(u0 >> 8), nib_hi<ONE>(u1 >> 8), b.z, b.w);
                 }
 #pragma unroll
-                for (int e = 0; e < (XBF16 ? 2 : 1); ++e) {
-                    const int tk = XBF16 ? 2 * c + e : c;
+                for (int e = 0; e < (ONE ? 2 : 1); ++e) {
+                    const int tk = ONE ? 2 * c + e : c;
                     const float f = factor[ch * kTok + tk];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float s = XBF16 ? d[2 * r + e] : d[2 * r] + d[2 * r + 1];
-                        acc[r][e] = fmaf(s * f, f0.c[r].value(q), acc[r][e]);
-                        if constexpr (ZERO)
-                            acc[r][e] = fmaf((8.0f - f0.z[r].value(q)) * f0.c[r].value(q),
-                                             xsum[(ch * (kChunk / G) + q) * kTok + tk], acc[r][e]);
+                        const float s = ONE ? d[2 * r + e] : d[2 * r] + d[2 * r + 1];
+                        float v = s;
+                        if constexpr (!ONE || ZERO) {
+                            const float o = eights[(ch * (kChunk / G) + q) * kTok + tk];
+                            if constexpr (ZERO) v = fmaf((ONE ? 1.0f : 0.0f) - 0.125f * f0.z[r].value(q), o, s);
+                            else v = s - o;
+                        }
+                        acc[r][e] = fmaf(v * f, f0.c[r].value(q), acc[r][e]);
                     }
                 }
             }
             f0 = f1;
-            f1 = f2;
         }
         // this tile's sums of all warps, in warp order
         float* rb = red + buf * (kWarps * kTok * kRows);
 #pragma unroll
-        for (int e = 0; e < (XBF16 ? 2 : 1); ++e)
+        for (int e = 0; e < (ONE ? 2 : 1); ++e)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                rb[(warp * kTok + (XBF16 ? 2 * c + e : c)) * kRows + g + 8 * r] = acc[r][e];
+                rb[(warp * kTok + (ONE ? 2 * c + e : c)) * kRows + g + 8 * r] = ONE ? acc[r][e] : acc[r][e] * 16777216.0f;
         team_sync(team);
         int wi = 0;
         while (wi + 1 < p.nw && tile >= p.tile_start[wi + 1]) ++wi;
@@ -385,13 +425,13 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
     if (p.ksplit > 1) cluster_sync_all();        // rank 0 has read the last tile's sums
 }
 
-template <int G, bool XBF16, bool SBF16, bool ZERO>
+template <int G, bool ONE, bool SBF16, bool ZERO>
 cudaError_t launch_rows(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
     static PerDevice<int> smem_set_for;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const auto kernel = kda_proj_w4_kernel<G, XBF16, SBF16, ZERO>;
+    const auto kernel = kda_proj_w4_kernel<G, ONE, SBF16, ZERO>;
     const bool cached = dev >= 0 && dev < kMaxDevices;
     if (smem > 48 * 1024 && (!cached || smem_set_for[dev].load(std::memory_order_acquire) < (int)smem)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -419,18 +459,18 @@ cudaError_t launch_rows(const W4Params& p, int grid, int teams, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int G, bool XBF16>
+template <int G, bool ONE>
 cudaError_t launch_params(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
     if (p.has_zero)
-        return p.scale_bf16 ? launch_rows<G, XBF16, true, true>(p, grid, teams, smem, s)
-                            : launch_rows<G, XBF16, false, true>(p, grid, teams, smem, s);
-    return p.scale_bf16 ? launch_rows<G, XBF16, true, false>(p, grid, teams, smem, s)
-                        : launch_rows<G, XBF16, false, false>(p, grid, teams, smem, s);
+        return p.scale_bf16 ? launch_rows<G, ONE, true, true>(p, grid, teams, smem, s)
+                            : launch_rows<G, ONE, false, true>(p, grid, teams, smem, s);
+    return p.scale_bf16 ? launch_rows<G, ONE, true, false>(p, grid, teams, smem, s)
+                        : launch_rows<G, ONE, false, false>(p, grid, teams, smem, s);
 }
 
 template <int G>
-cudaError_t launch_group(const W4Params& p, bool x_bf16, int grid, int teams, size_t smem, cudaStream_t s) {
-    return x_bf16 ? launch_params<G, true>(p, grid, teams, smem, s) : launch_params<G, false>(p, grid, teams, smem, s);
+cudaError_t launch_group(const W4Params& p, bool one, int grid, int teams, size_t smem, cudaStream_t s) {
+    return one ? launch_params<G, true>(p, grid, teams, smem, s) : launch_params<G, false>(p, grid, teams, smem, s);
 }
 
 }  // namespace
@@ -456,9 +496,10 @@ cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
     }
     p.tile_start[a.nw] = tiles;
     if (tiles == 0) return cudaSuccess;
-    p.nw = a.nw; p.t = a.t; p.in_f = a.in_f; p.scale_bf16 = a.scale_bf16; p.has_zero = a.has_zero;
+    p.nw = a.nw; p.t = a.t; p.in_f = a.in_f; p.x_bf16 = a.x_bf16; p.scale_bf16 = a.scale_bf16; p.has_zero = a.has_zero;
     // the fewest CTAs along K whose share of x fits
-    const int cols = a.x_bf16 ? a.t : 2 * a.t;
+    const bool one = a.t > kTok / 2;
+    const int cols = one ? a.t : 2 * a.t;
     const int all = a.in_f / kChunk;
     int ks = 1;
     while (ks < 8 && (all + ks - 1) / ks * (kChunk * cols * 2) > kXSmem) ks *= 2;
@@ -472,9 +513,9 @@ cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
     const int want = (tiles + blocks - 1) / blocks, teams = want < most ? want : most;
     const W4Smem lay = w4_smem((all + ks - 1) / ks, cols, a.group, teams);
     switch (a.group) {
-        case 32: return launch_group<32>(p, a.x_bf16 != 0, blocks * ks, teams, (size_t)lay.total, s);
-        case 64: return launch_group<64>(p, a.x_bf16 != 0, blocks * ks, teams, (size_t)lay.total, s);
-        default: return launch_group<128>(p, a.x_bf16 != 0, blocks * ks, teams, (size_t)lay.total, s);
+        case 32: return launch_group<32>(p, one, blocks * ks, teams, (size_t)lay.total, s);
+        case 64: return launch_group<64>(p, one, blocks * ks, teams, (size_t)lay.total, s);
+        default: return launch_group<128>(p, one, blocks * ks, teams, (size_t)lay.total, s);
     }
 }
 

@@ -131,6 +131,39 @@ def test_extreme_magnitudes(t):
     _check(c, _gpu(c))
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [1, 4, 7, 20])
+def test_groups_of_the_zero_point_are_zero(t, x):
+    """Codes of 8 (and any codes at a scale of 0) add nothing, however large x is there."""
+    c = _case(80 + t, t, 512, (70,), 64, x)
+    c["w"][0][:, 64:192] = 0x88               # k = 128 .. 383
+    c["x"][:, 128:384] *= 1000.0
+    if t <= 4:                                # x is scaled by 128 k (beyond: by rows)
+        with_them = _gpu(c)[0]
+        c["x"][:, 128:384] = 0.0
+        assert torch.equal(_gpu(c)[0], with_them)
+    c["w"][0][:] = 0x88
+    assert not _gpu(c)[0].any()
+
+
+@pytest.mark.parametrize("outlier", [1e2, 1e4, 1e6])
+@pytest.mark.parametrize("t", [2, 4])
+def test_small_elements_beside_a_large_one(t, outlier):
+    """A large element whose codes are 8 costs the others no more than 2^-25 of it each, and the
+    f32 sums nothing: they are differences of exact sums."""
+    c = _case(90 + t, t, 256, (48,), 128)
+    c["x"][:, 17] = outlier
+    c["w"][0][:, 8] = (c["w"][0][:, 8] & 15) | 0x80
+    refs, tols = _reference(c)
+    # |code - 8| <= 8, 128 k to a largest element; then lo's sums, below 2^-11 of the largest
+    # element, in 10 steps of f32 each: 2^-11 * 15 * 128 * 10 * 2^-24
+    s = c["s"][0].double()[:, 0]
+    more = outlier * s * (128 * 8 * 2.0 ** -25 + 15 * 128 * 10 * 2.0 ** -35)
+    out = _gpu(c)[0].cpu().double()
+    own = _reference(dict(c, x=torch.where(c["x"].abs() >= outlier, 0.0, c["x"])))[1][0]
+    assert ((out - refs[0]).abs() <= own + more).all()
+
+
 @pytest.mark.parametrize("t", [3, 7, 40])
 def test_non_finite_rows_stay_apart(t):
     c = _case(60 + t, t, 384, (50, 130), 64)
