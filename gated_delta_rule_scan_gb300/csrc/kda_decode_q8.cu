@@ -33,9 +33,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kCols = 8;                     // value columns of a group of 8 lanes
-constexpr int kBatch = 2;                    // of them unpacked at a time
+constexpr int kManyT = 2;                     // tokens from which four columns are unpacked at a time
 constexpr int kAhead = 4;                    // columns whose codes are loaded or on their way
-constexpr int kMinBlocks = 4;
 
 // Where key i of a q, k or decay row lies in shared memory.
 __device__ __forceinline__ int key_pos(int i) { return 32 * ((i >> 2) & 3) + 4 * (i >> 4) + (i & 3); }
@@ -63,6 +62,20 @@ __device__ __forceinline__ uint4 pack16(const float2 (&s)[8], float mul) {
 // The 16 keys of a lane in a q, k or decay row.
 __device__ __forceinline__ float4 row4(const float* row, int r, int m) {
     return *reinterpret_cast<const float4*>(row + 32 * m + 4 * r);
+}
+
+// B sums of columns over the four lanes that differ in bits 0 and 1: lane 2j (B = 2) or j (B = 4)
+// of them, and with B = 2 lane 2j + 1 too, ends with column j's.
+__device__ __forceinline__ float reduce_columns(const float (&s)[2], int lane) {
+    const bool b1 = lane & 2;
+    const float x = (b1 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[1], 2);
+    return x + __shfl_xor_sync(0xffffffffu, x, 1);
+}
+__device__ __forceinline__ float reduce_columns(const float (&s)[4], int lane) {
+    const bool b1 = lane & 2, b0 = lane & 1;
+    const float x = (b1 ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[2], 2);
+    const float y = (b1 ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, b1 ? s[1] : s[3], 2);
+    return (b0 ? y : x) + __shfl_xor_sync(0xffffffffu, b0 ? x : y, 1);
 }
 
 // The conv of one channel: K taps over the ring slots and the new samples, oldest first.  KT = 4
@@ -116,8 +129,9 @@ struct Conv {
 };
 
 // WIDE: value heads of d.vsub > 1 units, one cluster of vsub CTAs each.
-template <int FMT, int GATE_MODE, int KT, bool WIDE>
-__global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(const DecodeQ8Args p) {
+// B: columns of a group unpacked at a time.
+template <int FMT, int GATE_MODE, int KT, bool WIDE, int B>
+__global__ void __launch_bounds__(kThreads, B == 2 ? 4 : 3) kda_decode_q8_kernel(const DecodeQ8Args p) {
     extern __shared__ __align__(16) float rows_s[];
     __shared__ float beta_s[kDecodeMaxT], ascal[kDecodeMaxT];
     __shared__ float part[3][4][kDecodeMaxT];     // q.q, q.k and k.k of four warps
@@ -310,18 +324,19 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
 
     // ---- the recurrence, two columns of each group at a time
     // (rolled: four copies of it would not fit the instruction cache)
+    const bool b2 = lane & 4;
+    const int own = B == 4 ? lane & 3 : (lane >> 1) & 1;      // the column whose sums end here
 #pragma unroll 1
-    for (int b = 0; b < kCols; b += kBatch) {
-        float2 S[kBatch][8];
+    for (int b = 0; b < kCols; b += B) {
+        float2 S[B][8];
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c)
+        for (int c = 0; c < B; ++c)
             unpack16<FMT>(S[c], code[c], __shfl_sync(0xffffffffu, scale_l, (lane & ~7) + b + c));
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
-            code[c] = code[kBatch + c];
-            if (b + kAhead < kCols) code[kBatch + c] = __ldcs(cin + (b + kAhead + c) * (kHeadDim / 16));
+        for (int c = 0; c < kAhead; ++c) {
+            if (c + B < kAhead) code[c] = code[c + B];
+            else if (b + B + c < kCols) code[c] = __ldcs(cin + (b + B + c) * (kHeadDim / 16));
         }
-        const int own = (lane >> 1) & 1;          // the column of the batch whose sums end here
 #pragma unroll 1
         for (int t = 0; t < T; ++t) {
             const float* krow = kh + t * kHeadDim;
@@ -329,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
             const float* arow = av + t * kHeadDim;
             const float as = GATE_MODE == 0 ? 0.0f : ascal[t];
             float4 k4[4];
-            float2 dk[kBatch][2], dq[kBatch][2];
+            float2 dk[B][2], dq[B][2];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 k4[m] = row4(krow, r, m);
@@ -339,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
                 const float2 kl = make_float2(k4[m].x, k4[m].y), kh2 = make_float2(k4[m].z, k4[m].w);
                 const float2 ql = make_float2(q4.x, q4.y), qh2 = make_float2(q4.z, q4.w);
 #pragma unroll
-                for (int c = 0; c < kBatch; ++c) {
+                for (int c = 0; c < B; ++c) {
                     S[c][2 * m] = __fmul2_rn(S[c][2 * m], al);
                     S[c][2 * m + 1] = __fmul2_rn(S[c][2 * m + 1], ah);
                     if (m == 0) {
@@ -355,27 +370,27 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
                     }
                 }
             }
-            // 4 sums over the 8 lanes: lanes with bit 2 clear end with P.k, the others with P.q, of
+            // 2 B sums over the 8 lanes: lanes with bit 2 clear end with P.k, the others with P.q, of
             // column `own`
-            const bool b2 = lane & 4, b1 = lane & 2;
-            const float s0 = (dk[0][0].x + dk[0][0].y) + (dk[0][1].x + dk[0][1].y);
-            const float s1 = (dk[1][0].x + dk[1][0].y) + (dk[1][1].x + dk[1][1].y);
-            const float s2 = (dq[0][0].x + dq[0][0].y) + (dq[0][1].x + dq[0][1].y);
-            const float s3 = (dq[1][0].x + dq[1][0].y) + (dq[1][1].x + dq[1][1].y);
-            const float h0 = (b2 ? s2 : s0) + __shfl_xor_sync(0xffffffffu, b2 ? s0 : s2, 4);
-            const float h1 = (b2 ? s3 : s1) + __shfl_xor_sync(0xffffffffu, b2 ? s1 : s3, 4);
-            float red = (b1 ? h1 : h0) + __shfl_xor_sync(0xffffffffu, b1 ? h0 : h1, 2);
-            red += __shfl_xor_sync(0xffffffffu, red, 1);
+            float sum[B];
+#pragma unroll
+            for (int c = 0; c < B; ++c) {
+                const float sk = (dk[c][0].x + dk[c][0].y) + (dk[c][1].x + dk[c][1].y);
+                const float sq = (dq[c][0].x + dq[c][0].y) + (dq[c][1].x + dq[c][1].y);
+                sum[c] = (b2 ? sq : sk) + __shfl_xor_sync(0xffffffffu, b2 ? sk : sq, 4);
+            }
+            const float red = reduce_columns(sum, lane);
             const float iq = __shfl_sync(0xffffffffu, iq_l, t), ik = __shfl_sync(0xffffffffu, ik_l, t);
             const float qk = __shfl_sync(0xffffffffu, qk_l, t), beta = __shfl_sync(0xffffffffu, beta_l, t);
             const int col = col0 + b + own;
             const float w = beta * (vh[t * kHeadDim + col] - ik * red);      // in lanes of P.k
             const float wo = __shfl_xor_sync(0xffffffffu, w, 4);
-            if (b2 && !(lane & 1)) os[t * kHeadDim + col] = __fmul_rn(a.scale, fmaf(wo, qk, iq * red));
+            if (b2 && (B == 4 || !(lane & 1)))
+                os[t * kHeadDim + col] = __fmul_rn(a.scale, fmaf(wo, qk, iq * red));
             const float wk = w * ik;
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) {
-                const float wc = __shfl_sync(0xffffffffu, wk, (lane & ~7) + 2 * c);
+            for (int c = 0; c < B; ++c) {
+                const float wc = __shfl_sync(0xffffffffu, wk, (lane & ~7) + (B == 4 ? c : 2 * c));
                 const float2 w2 = make_float2(wc, wc);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -384,26 +399,34 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_kernel(con
                 }
             }
         }
-        // back to 8 bits: lanes with bit 2 clear finish column 0, the others column 1
-        float mx[kBatch];
+        // back to 8 bits: lane l of a group finishes column l / 4 of 2, or l / 2 of 4; even lanes
+        // form the scale, odd ones the multiplier
+        float mx[B];
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < B; ++c) {
             float m = mag_max(S[c][0].x, S[c][0].y);
 #pragma unroll
             for (int i = 1; i < 8; ++i) m = mag_max(m, mag_max(S[c][i].x, S[c][i].y));
             mx[c] = m;
         }
-        const bool b2 = lane & 4;
-        float top = mag_max(b2 ? mx[1] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[1], 4));
-        top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float top;
+        if constexpr (B == 4) {
+            const float m0 = mag_max(b2 ? mx[2] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[2], 4));
+            const float m1 = mag_max(b2 ? mx[3] : mx[1], __shfl_xor_sync(0xffffffffu, b2 ? mx[1] : mx[3], 4));
+            const bool b1 = lane & 2;
+            top = mag_max(b1 ? m1 : m0, __shfl_xor_sync(0xffffffffu, b1 ? m0 : m1, 2));
+        } else {
+            top = mag_max(b2 ? mx[1] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[1], 4));
+            top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        }
         top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        // even lanes form the scale, odd ones the multiplier
+        constexpr int kLanes = 8 / B;             // lanes that finish a column
         const float f = q8_row_part<FMT>(mag_bits(top), lane & 1);
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c)
+        for (int c = 0; c < B; ++c)
             __stcs(cout + (b + c) * (kHeadDim / 16),
-                   pack16<FMT>(S[c], __shfl_sync(0xffffffffu, f, (lane & ~7) + 4 * c + 1)));
-        if ((lane & 3) == 0) p.scales[unit_out + b + (b2 ? 1 : 0)] = f;
+                   pack16<FMT>(S[c], __shfl_sync(0xffffffffu, f, (lane & ~7) + kLanes * c + 1)));
+        if (lane % kLanes == 0) p.scales[unit_out + b + r / kLanes] = f;
     }
     __syncthreads();
     // ---- epilogue: gated RMSNorm, one warp per token row (as in kda_decode_fused)
@@ -487,16 +510,21 @@ cudaError_t launch_kernel(Kern kernel, const DecodeQ8Args& a, size_t smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int FMT, int GM>
-cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
+template <int FMT, int GM, int B>
+cudaError_t launch_b(const DecodeQ8Args& a, cudaStream_t s) {
     // at most 5 * 16 rows of 512 bytes: 40 KB, within the default limit
     const size_t smem = (size_t)(GM == 0 ? 5 : 4) * a.d.T * kHeadDim * sizeof(float);
     KernelTimer kt(kKDecodeQ8, s);
     if (a.d.vsub > 1)
-        return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, true>, a, smem, s)
-                          : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, true>, a, smem, s);
-    return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, false>, a, smem, s)
-                      : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, false>, a, smem, s);
+        return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, true, B>, a, smem, s)
+                          : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, true, B>, a, smem, s);
+    return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, false, B>, a, smem, s)
+                      : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, false, B>, a, smem, s);
+}
+
+template <int FMT, int GM>
+cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
+    return a.d.T >= kManyT ? launch_b<FMT, GM, 4>(a, s) : launch_b<FMT, GM, 2>(a, s);
 }
 
 }  // namespace
