@@ -25,7 +25,7 @@
 // shared memory by bulk copies: 66; persistent blocks that prefetch the next sequence: 80).  The l2
 // norms scale the finished sums instead of the vectors.  Of a reduction's lanes each finishes one
 // column: one division a lane rounds the state, not two a column.
-#include "kda_q8.cuh"
+#include "kda_decode_q8.cuh"
 
 namespace kda {
 
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kCols = 8;                     // value columns of a group of 8 lanes
-constexpr int kManyT = 2;                     // tokens from which four columns are unpacked at a time
+constexpr int B = 4;                         // of them unpacked at a time
 constexpr int kAhead = 4;                    // columns whose codes are loaded or on their way
 
 // Where key i of a q, k or decay row lies in shared memory.
@@ -78,60 +78,9 @@ __device__ __forceinline__ float reduce_columns(const float (&s)[4], int lane) {
     return (b0 ? y : x) + __shfl_xor_sync(0xffffffffu, b0 ? x : y, 1);
 }
 
-// The conv of one channel: K taps over the ring slots and the new samples, oldest first.  KT = 4
-// is a conv of exactly 4 taps (16-byte weights); KT = 8 any width up to 8.
-template <int KT>
-struct Conv {
-    float w[KT], x[KT];
-    __device__ __forceinline__ void weights(const float* conv_w, long ch, int K) {
-        if constexpr (KT == 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(conv_w + ch * 4));
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-        } else {
-#pragma unroll
-            for (int m = 0; m < KT; ++m) {
-                const int jj = m - (KT - K);
-                w[m] = jj >= 0 ? conv_w[ch * K + jj] : 0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ void load(const float* ring, long ch, int K) {
-        if constexpr (KT == 4) {
-            const float* p = ring + ch * 3;
-            x[0] = 0.0f; x[1] = p[0]; x[2] = p[1]; x[3] = p[2];
-        } else {
-            const float* p = ring + ch * (K - 1);
-#pragma unroll
-            for (int m = 0; m < KT; ++m) {
-                const int d = KT - m;
-                x[m] = d <= K - 1 ? p[K - 1 - d] : 0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ float step(float v, int K) {
-        window_push(x, v);
-        return silu_f(conv_taps_f(w, x, KT == 4 ? 4 : K));
-    }
-    // the last K - 1 samples
-    __device__ __forceinline__ void store(float* ring, long ch, int K) const {
-        if constexpr (KT == 4) {
-            float* p = ring + ch * 3;
-            p[0] = x[1]; p[1] = x[2]; p[2] = x[3];
-        } else {
-            float* p = ring + ch * (K - 1);
-#pragma unroll
-            for (int m = 0; m < KT; ++m) {
-                const int d = KT - 1 - m;
-                if (d < K - 1) p[K - 2 - d] = x[m];
-            }
-        }
-    }
-};
-
 // WIDE: value heads of d.vsub > 1 units, one cluster of vsub CTAs each.
-// B: columns of a group unpacked at a time.
-template <int FMT, int GATE_MODE, int KT, bool WIDE, int B>
-__global__ void __launch_bounds__(kThreads, B == 2 ? 4 : 3) kda_decode_q8_kernel(const DecodeQ8Args p) {
+template <int FMT, int GATE_MODE, int KT, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const DecodeQ8Args p) {
     extern __shared__ __align__(16) float rows_s[];
     __shared__ float beta_s[kDecodeMaxT], ascal[kDecodeMaxT];
     __shared__ float part[3][4][kDecodeMaxT];     // q.q, q.k and k.k of four warps
@@ -510,21 +459,15 @@ cudaError_t launch_kernel(Kern kernel, const DecodeQ8Args& a, size_t smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int FMT, int GM, int B>
-cudaError_t launch_b(const DecodeQ8Args& a, cudaStream_t s) {
-    // at most 5 * 16 rows of 512 bytes: 40 KB, within the default limit
-    const size_t smem = (size_t)(GM == 0 ? 5 : 4) * a.d.T * kHeadDim * sizeof(float);
-    KernelTimer kt(kKDecodeQ8, s);
-    if (a.d.vsub > 1)
-        return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, true, B>, a, smem, s)
-                          : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, true, B>, a, smem, s);
-    return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, false, B>, a, smem, s)
-                      : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, false, B>, a, smem, s);
-}
-
 template <int FMT, int GM>
 cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
-    return a.d.T >= kManyT ? launch_b<FMT, GM, 4>(a, s) : launch_b<FMT, GM, 2>(a, s);
+    // at most 5 * 16 rows of 512 bytes: 40 KB, within the default limit
+    const size_t smem = (size_t)(GM == 0 ? 5 : 4) * a.d.T * kHeadDim * sizeof(float);
+    if (a.d.vsub > 1)
+        return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, true>, a, smem, s)
+                          : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, true>, a, smem, s);
+    return a.d.K == 4 ? launch_kernel(kda_decode_q8_kernel<FMT, GM, 4, false>, a, smem, s)
+                      : launch_kernel(kda_decode_q8_kernel<FMT, GM, kMaxConvK, false>, a, smem, s);
 }
 
 }  // namespace
@@ -532,10 +475,16 @@ cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t s) {
     if (a.d.N == 0) return cudaSuccess;
     cudaError_t e;
-    if (a.fmt == kQ8E4m3)
-        e = a.d.gate_mode == 0 ? launch_t<kQ8E4m3, 0>(a, s) : launch_t<kQ8E4m3, 1>(a, s);
-    else
-        e = a.d.gate_mode == 0 ? launch_t<kQ8Int8, 0>(a, s) : launch_t<kQ8Int8, 1>(a, s);
+    {
+        KernelTimer kt(kKDecodeQ8, s);
+        // (a positive gate bound lets decays grow past 1, out of the range of the form for few)
+        if (a.d.T <= kDecodeQ8FewT && (a.d.gate_mode != 0 || a.d.gate_lb <= 0.0f))
+            e = launch_decode_q8_few(a, s);
+        else if (a.fmt == kQ8E4m3)
+            e = a.d.gate_mode == 0 ? launch_t<kQ8E4m3, 0>(a, s) : launch_t<kQ8E4m3, 1>(a, s);
+        else
+            e = a.d.gate_mode == 0 ? launch_t<kQ8Int8, 0>(a, s) : launch_t<kQ8Int8, 1>(a, s);
+    }
     if (e != cudaSuccess || a.d.Hk == a.d.H) return e;
     KernelTimer kt(kKRingRollQ8, s);
     const int blocks = (int)((2 * plane_width(a.d.H, a.d.Hk, 0) + kThreads - 1) / kThreads);

@@ -1,0 +1,504 @@
+// kda_decode_q8_few.cu -- the decode step on the 8-bit pool (kda_decode_q8.cu) for up to four tokens,
+// with the state's codes as a tensor-core operand.
+//
+// Mathematics.  Unrolled over the call's tokens, everything that token t wants of the state is a dot
+// product of the state that came in: with A_t the product of the decays up to token t, D_st that of
+// the tokens after s up to t, and k, q normalised,
+//     S_j,t-1 decayed, . k_t = S_j . (A_t k_t) + sum_{s<t} w_s (D_st k_s . k_t),
+//     w_t = beta_t (v_t - that),      o_t = scale (S_j . (A_t q_t) + sum_{s<=t} w_s (D_st k_s . q_t)),
+//     S_j out = A_T S_j + sum_s w_s (D_sT k_s).
+// The products D_st k_s . k_t and D_st k_s . q_t belong to the token rows, not to a value column: at
+// four tokens they are 16 sums over 128 channels for the whole unit.  The products with the incoming
+// state are a matrix product, 128 columns x 128 keys by 2 T vectors: its left side are the codes
+// themselves, whole numbers or e4m3 values, exact in f16, the row scale going on afterwards; its
+// right side the vectors times 2^12, as f16 hi + lo (of a unit vector each element to 2^-23 of itself
+// or 2^-37), so mma.sync sums them to f32's accuracy.  Decays are at most 1, which keeps the vectors
+// in range; a positive gate bound takes the other form.  The new state is formed once, in f32, from
+// the codes, and rounded back to 8 bits.
+//
+// What it saves: one pass over the state's f32 values for all tokens instead of two per token.
+// GB300 layout.  One CTA of four warps owns one (sequence, unit).  Thread = channel of q, k, v and
+// the gate, and = value column: its v, its row scale and its solve stay in registers.  A warp owns
+// 32 columns as two 16-row MMA tiles; lane 4g + c holds of rows g and g + 8 the key words that the MMA
+// wants of it, chosen as keys 64 half + 16c .. 16c + 15 so that a row is read and written in 16-byte
+// pieces; the same registers are the MMA's left side and, unpacked, the state.
+#include <cuda_fp16.h>
+
+#include "kda_decode_q8.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kVecBytes = 320;               // one f16 vector: 256 bytes, and 64 against bank conflicts
+constexpr int kDotRow = 136;                 // floats: four lanes' columns land in different banks
+constexpr float kVecScale = 4096.0f;
+
+// Key i is byte e of word m (0 .. 7) of lane c: i = 64 (m / 4) + 16 c + 4 (m % 4) + e.
+__device__ __forceinline__ int key_word(int i) { return ((i >> 6) << 2) | ((i >> 2) & 3); }
+__device__ __forceinline__ int key_lane(int i) { return (i >> 4) & 3; }
+// Where it lies in an f32 row (a lane's word is 16 bytes) and in an f16 vector (two words are).
+__device__ __forceinline__ int key_pos32(int i) { return (key_word(i) * 4 + key_lane(i)) * 4 + (i & 3); }
+__device__ __forceinline__ int key_pos16(int i) {
+    const int m = key_word(i);
+    return ((m >> 1) * 4 + key_lane(i)) * 8 + (m & 1) * 4 + (i & 3);
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four codes as two f16 pairs, exact.
+template <int FMT>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (FMT == kQ8E4m3) {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        // code + 128 in the mantissa of 1024
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 off = __float2half2_rn(1152.0f);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), off);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    }
+}
+
+// N sums over the warp's lanes, N a power of two: lane l ends with sum l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+    int bit = 16;
+#pragma unroll
+    for (int n = N / 2; n >= 1; n /= 2, bit /= 2) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int j = 0; j < n; ++j)
+            v[j] = (up ? v[j + n] : v[j]) + __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + n], bit);
+    }
+    float s = v[0];
+#pragma unroll
+    for (int b = 16 / N; b >= 1; b /= 2) s += __shfl_xor_sync(0xffffffffu, s, b);
+    return s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float raw_at(const void* p, long i) {
+    return BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
+                : reinterpret_cast<const float*>(p)[i];
+}
+
+// TT: tokens of the call at most.  The sums over channels are numbered q.q (t), k.k (TT + t), then
+// D k_s . k_t for s < t and D k_s . q_t for s <= t, by t and then s.
+template <int TT>
+struct Sums {
+    static constexpr int kk = TT, kt = 2 * TT, qt = kt + TT * (TT - 1) / 2, n = qt + TT * (TT + 1) / 2;
+    static constexpr int padded = n <= 4 ? 4 : n <= 8 ? 8 : 32;
+    static constexpr int lanes = 32 / padded;
+    __host__ __device__ static constexpr int kk_at(int s, int t) { return kt + t * (t - 1) / 2 + s; }
+    __host__ __device__ static constexpr int qk_at(int s, int t) { return qt + t * (t + 1) / 2 + s; }
+};
+
+template <int TT>
+struct FewSmem {
+    static constexpr int kTiles = (TT + 1) / 2;              // MMA tiles of 8 columns: two tokens each
+    uint4 vec[8 * kTiles * kVecBytes / 16];                  // hi, lo of k, then of q, token by token
+    float row[(TT + 1) * kHeadDim];                          // D_sT k_s, then A_T
+    float dot[4 * kTiles * kDotRow];                         // (token, k or q) x columns
+    float part[4][Sums<TT>::padded];
+    float beta[TT], decay[TT], nss[TT], osum[4][TT];
+    int2 slots;
+};
+
+template <int FMT, int GATE_MODE, int KT, bool WIDE, int TT>
+__global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const DecodeQ8Args p) {
+    __shared__ __align__(16) FewSmem<TT> sm;
+    using S_ = Sums<TT>;
+    const DecodeArgs& a = p.d;
+
+    // unit h: value column block h % vs of value head gh, which reads q/k head hq
+    const int h = blockIdx.x, n = blockIdx.y;
+    const int vs = WIDE ? a.vsub : 1;
+    const int gh = WIDE ? h / vs : h;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = a.H, K = a.K;
+    const int Hg = H / vs;
+    const int Hkq = prep_qk_heads(Hg, a.Hk);
+    const int hq = gh < Hkq ? gh : gh % Hkq;
+    const long row0 = (long)n * a.T;
+    const int T = a.keep != nullptr ? min(max(a.keep[n], 0), a.T) : a.T;
+
+    // ---- raw samples, conv weights and gate inputs: nothing of them depends on the slots
+    const long wq = plane_width(H, a.Hk, 0), wv = (long)H * kHeadDim, wg = (long)Hg * kHeadDim;
+    float q[TT], k[TT], v[TT], ga[TT];
+    {
+        const long aq = row0 * wq + hq * kHeadDim + tid, av = row0 * wv + (long)h * kHeadDim + tid;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            q[t] = k[t] = v[t] = ga[t] = 0.0f;
+            if (t >= T) continue;
+            if (a.raw_bf16) {
+                q[t] = raw_at<true>(a.q_raw, aq + t * wq);
+                k[t] = raw_at<true>(a.k_raw, aq + t * wq);
+                v[t] = raw_at<true>(a.v_raw, av + t * wv);
+            } else {
+                q[t] = raw_at<false>(a.q_raw, aq + t * wq);
+                k[t] = raw_at<false>(a.k_raw, aq + t * wq);
+                v[t] = raw_at<false>(a.v_raw, av + t * wv);
+            }
+            if (GATE_MODE == 0) ga[t] = a.f_raw[(row0 + t) * wg + gh * kHeadDim + tid];
+        }
+    }
+    if (warp == 3) {
+        int in, out;
+        const bool ok = pool_row_warp(p.slots, p.slots_out, n, a.N, p.pool_rows, a.err, in, out);
+        if (lane == 0) sm.slots = make_int2(ok ? in : -1, out);
+    }
+    const int chq = hq * kHeadDim + tid, chk = (int)plane_offset(H, a.Hk, 1) + chq;
+    const int chv = (int)plane_offset(H, a.Hk, 2) + h * kHeadDim + tid;
+    Conv<KT> cq, ck, cv;
+    cq.weights(a.conv_w, chq, K);
+    ck.weights(a.conv_w, chk, K);
+    cv.weights(a.conv_w, chv, K);
+    const float alog = a.a_log[gh];
+    const float dt = GATE_MODE == 0 ? a.dt_bias[(long)gh * kHeadDim + tid] : a.dt_bias[gh];
+    if (tid < T) {
+        const long rw = (row0 + tid) * Hg + gh;
+        sm.beta[tid] = sigmoid_f(a.beta_raw[rw]);
+        if (GATE_MODE == 1) sm.decay[tid] = decay_f(gdn_gate_f(a.f_raw[rw], dt, alog));
+    }
+    __syncthreads();
+    const int slot_in = sm.slots.x, slot_out = sm.slots.y;
+    if (slot_in < 0) return;                      // uniform over the cluster: n decides alone
+
+    // ---- the codes of this warp's two tiles, its columns' scales
+    const int g = lane >> 2, c = lane & 3;
+    const long unit_in = ((long)slot_in * H + h) * kHeadDim, unit_out = ((long)slot_out * H + h) * kHeadDim;
+    // [row g, row g + 8][half]: 8 pieces of 16 bytes a row, this lane's at c and 4 + c
+    const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + (unit_in + warp * 32 + g) * 8 + c;
+    uint4* cout = reinterpret_cast<uint4*>(p.codes) + (unit_out + warp * 32 + g) * 8 + c;
+    uint4 cur[2][2], nxt[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            cur[r][f] = __ldcs(cin + r * 64 + f * 4);
+            nxt[r][f] = __ldcs(cin + 128 + r * 64 + f * 4);
+        }
+    const float scale_l = p.scales[unit_in + tid];
+
+    // ---- ring slots: a q / k ring row that several units read is rolled by one of them, and only
+    //      into another slot: in place it is left to the roll kernel that follows
+    const bool roll_qk = h == gh * vs && gh < Hkq && (Hkq == H || slot_in != slot_out);
+    const long ring_len = ring_channels(H, a.Hk) * (K - 1);
+    const float* ring_in = a.ring_out + (long)slot_in * ring_len;
+    float* ring_out = a.ring_out + (long)slot_out * ring_len;
+    cq.load(ring_in, chq, K);
+    ck.load(ring_in, chk, K);
+    cv.load(ring_in, chv, K);
+
+    if (T == 0) {       // nothing accepted: the slot passes through unchanged (in place: untouched)
+        if (slot_in != slot_out) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    __stcs(cout + r * 64 + f * 4, cur[r][f]);
+                    __stcs(cout + 128 + r * 64 + f * 4, nxt[r][f]);
+                }
+            p.scales[unit_out + tid] = scale_l;
+            cv.store(ring_out, chv, K);
+            if (roll_qk) {
+                cq.store(ring_out, chq, K);
+                ck.store(ring_out, chk, K);
+            }
+        }
+        return;
+    }
+
+    // ---- conv + SiLU and the ring roll, the gate, the sums over channels
+    const float rate = GATE_MODE == 0 ? expf(alog) : 0.0f;
+    float kd[TT], cum[TT];                        // D_st k_s so far, A_t
+    {
+        float sum[S_::padded] = {};
+        float run = 1.0f;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            kd[t] = cum[t] = 0.0f;
+            if (t >= T) continue;
+            q[t] = cq.step(q[t], K);
+            k[t] = ck.step(k[t], K);
+            v[t] = cv.step(v[t], K);
+            const float dec = GATE_MODE == 0 ? decay_f(kda_gate_f(ga[t], dt, rate, a.gate_lb)) : sm.decay[t];
+            run *= dec;
+            cum[t] = run;
+            sum[t] = q[t] * q[t];
+            sum[S_::kk + t] = k[t] * k[t];
+#pragma unroll
+            for (int s = 0; s < t; ++s) {
+                kd[s] *= dec;
+                sum[S_::kk_at(s, t)] = kd[s] * k[t];
+                sum[S_::qk_at(s, t)] = kd[s] * q[t];
+            }
+            kd[t] = k[t];
+            sum[S_::qk_at(t, t)] = k[t] * q[t];
+        }
+        const float s = warp_sums(sum, lane);
+        if (lane % S_::lanes == 0) sm.part[warp][lane / S_::lanes] = s;
+    }
+    cv.store(ring_out, chv, K);
+    if (roll_qk) {
+        cq.store(ring_out, chq, K);
+        ck.store(ring_out, chk, K);
+    }
+    __syncthreads();
+    // lane l: sum l / lanes of the unit; then the l2 scales in its place for q.q and k.k
+    const int own = lane / S_::lanes;
+    const float total = (sm.part[0][own] + sm.part[1][own]) + (sm.part[2][own] + sm.part[3][own]);
+    const float coef = own < 2 * TT ? l2_inv_f(total, a.l2_eps) : total;
+    const auto coef_at = [&](int i) { return __shfl_sync(0xffffffffu, coef, i * S_::lanes); };
+    float iq[TT], ik[TT];
+    {
+        float run = 0.0f;
+        __half* vec = reinterpret_cast<__half*>(sm.vec) + key_pos16(tid);
+        float* row = sm.row + key_pos32(tid);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            iq[t] = coef_at(t);
+            ik[t] = coef_at(S_::kk + t);
+            // (tokens from T on are zeros)
+            const float x = k[t] * (t < T ? ik[t] : 0.0f) * cum[t] * kVecScale;
+            const float y = q[t] * (t < T ? iq[t] : 0.0f) * cum[t] * kVecScale;
+            const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
+            __half* at = vec + 4 * t * (kVecBytes / 2);
+            at[0] = xh;
+            at[kVecBytes / 2] = __float2half_rn(x - __half2float(xh));
+            at[2 * (kVecBytes / 2)] = yh;
+            at[3 * (kVecBytes / 2)] = __float2half_rn(y - __half2float(yh));
+            row[t * kHeadDim] = t < T ? kd[t] * ik[t] : 0.0f;
+            if (t < T) run = cum[t];
+        }
+        if (GATE_MODE == 0) row[TT * kHeadDim] = run;
+        else if (tid == 0) row[TT * kHeadDim] = run;
+    }
+    // the epilogue's inputs, requested ahead of the work on the state
+    const long C = (long)H * kHeadDim;
+    const float nw = __ldg(a.norm_w + (WIDE ? (int)blockIdx.x % a.vsub : 0) * kHeadDim + tid);
+    float z[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+        z[t] = t < T ? __ldcs(a.gate_raw + (row0 + t) * C + h * kHeadDim + tid) : 0.0f;
+    __syncthreads();
+
+    // ---- the incoming state's products, 16 columns at a time
+    const auto swap_tiles = [&] {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const uint4 x = cur[r][f];
+                cur[r][f] = nxt[r][f];
+                nxt[r][f] = x;
+            }
+    };
+    constexpr int kTiles = FewSmem<TT>::kTiles;
+    const int cols = 4 * TT;                      // columns past them repeat the last one
+#pragma unroll 1
+    for (int mt = 0; mt < 2; ++mt) {
+        float d[kTiles][4] = {};
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const uint32_t u[2][4] = {{cur[0][f].x, cur[0][f].y, cur[0][f].z, cur[0][f].w},
+                                      {cur[1][f].x, cur[1][f].y, cur[1][f].z, cur[1][f].w}};
+#pragma unroll
+            for (int m = 0; m < 4; m += 2) {
+                uint4 b[kTiles];
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+                    b[i] = sm.vec[min(8 * i + g, cols - 1) * (kVecBytes / 16) + (f * 2 + m / 2) * 4 + c];
+                uint32_t a0, a1, a2, a3;
+                codes_f16<FMT>(u[0][m], a0, a2);
+                codes_f16<FMT>(u[1][m], a1, a3);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) mma_16816(d[i], a0, a1, a2, a3, b[i].x, b[i].y);
+                codes_f16<FMT>(u[0][m + 1], a0, a2);
+                codes_f16<FMT>(u[1][m + 1], a1, a3);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) mma_16816(d[i], a0, a1, a2, a3, b[i].z, b[i].w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+            if (TT > 1 || c < 2) {
+                float* o = sm.dot + (4 * i + c) * kDotRow + warp * 32 + mt * 16 + g;
+                o[0] = d[i][0] + d[i][1];
+                o[8] = d[i][2] + d[i][3];
+            }
+        swap_tiles();
+    }
+    __syncwarp();
+
+    // ---- the solve: thread = value column
+    float w[TT], o[TT];
+    {
+        const float sc = scale_l * (1.0f / kVecScale);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            float x = sm.dot[2 * t * kDotRow + tid] * sc, y = sm.dot[(2 * t + 1) * kDotRow + tid] * sc;
+#pragma unroll
+            for (int s = 0; s < t; ++s) {
+                x = fmaf(w[s], coef_at(S_::kk_at(s, t)) * (ik[s] * ik[t]), x);
+                y = fmaf(w[s], coef_at(S_::qk_at(s, t)) * (ik[s] * iq[t]), y);
+            }
+            const float qk = coef_at(S_::qk_at(t, t)) * (ik[t] * iq[t]);
+            w[t] = t < T ? sm.beta[t] * (v[t] - x) : 0.0f;
+            o[t] = __fmul_rn(a.scale, fmaf(w[t], qk, y));
+            const float ss = t < T ? warp_sum(o[t] * o[t]) : 0.0f;
+            if (lane == 0) sm.osum[warp][t] = ss;
+        }
+    }
+
+    // ---- the new state, 16 columns at a time
+#pragma unroll 1
+    for (int mt = 0; mt < 2; ++mt) {
+        float2 S[2][16];
+        float wr[2][TT], sr[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int src = 16 * mt + 8 * r + g;
+            sr[r] = __shfl_sync(0xffffffffu, scale_l, src);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) wr[r][t] = __shfl_sync(0xffffffffu, w[t], src);
+        }
+        const float as = GATE_MODE == 0 ? 0.0f : sm.row[TT * kHeadDim];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            const float4* rows = reinterpret_cast<const float4*>(sm.row) + m * 4 + c;
+            const float4 a4 = GATE_MODE == 0 ? rows[TT * (kHeadDim / 4)] : make_float4(as, as, as, as);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint4 w4 = cur[r][m >> 2];
+                const uint32_t word = (m & 3) == 0 ? w4.x : (m & 3) == 1 ? w4.y : (m & 3) == 2 ? w4.z : w4.w;
+                const float4 x = q8_decode4<FMT>(word, sr[r]);
+                S[r][2 * m] = __fmul2_rn(make_float2(x.x, x.y), make_float2(a4.x, a4.y));
+                S[r][2 * m + 1] = __fmul2_rn(make_float2(x.z, x.w), make_float2(a4.z, a4.w));
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float4 k4 = rows[t * (kHeadDim / 4)];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 w2 = make_float2(wr[r][t], wr[r][t]);
+                    S[r][2 * m] = __ffma2_rn(make_float2(k4.x, k4.y), w2, S[r][2 * m]);
+                    S[r][2 * m + 1] = __ffma2_rn(make_float2(k4.z, k4.w), w2, S[r][2 * m + 1]);
+                }
+            }
+        }
+        // back to 8 bits: of a row pair's four lanes 0 and 2 form the scales, 1 and 3 the multipliers
+        float mx[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float x = mag_max(S[r][0].x, S[r][0].y);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) x = mag_max(x, mag_max(S[r][i].x, S[r][i].y));
+            mx[r] = x;
+        }
+        const bool up = c & 2;
+        float top = mag_max(up ? mx[1] : mx[0], __shfl_xor_sync(0xffffffffu, up ? mx[0] : mx[1], 2));
+        top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        const float f = q8_row_part<FMT>(mag_bits(top), c & 1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float mul = __shfl_sync(0xffffffffu, f, 4 * g + 2 * r + 1);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t u[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float2 lo = S[r][2 * (4 * y + m)], hi = S[r][2 * (4 * y + m) + 1];
+                    u[m] = q8_encode4<FMT>(make_float4(lo.x, lo.y, hi.x, hi.y), mul);
+                }
+                __stcs(cout + mt * 128 + r * 64 + y * 4, make_uint4(u[0], u[1], u[2], u[3]));
+            }
+        }
+        if (!(c & 1)) p.scales[unit_out + warp * 32 + mt * 16 + 4 * c + g] = f;
+        swap_tiles();
+    }
+    __syncthreads();
+
+    // ---- epilogue: gated RMSNorm, thread = channel
+    float ss[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+        ss[t] = (sm.osum[0][t] + sm.osum[1][t]) + (sm.osum[2][t] + sm.osum[3][t]);
+    if constexpr (WIDE) {
+        if (tid == 0) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) sm.nss[t] = ss[t];
+        }
+        cluster_sync_all();
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        if (t >= T) continue;
+        float inv;
+        if constexpr (WIDE) {
+            float tot = 0.0f;
+            for (int b = 0; b < a.vsub; ++b) tot = tot + ld_cluster_f32(&sm.nss[t], (uint32_t)b);
+            inv = rms_inv_w(tot, a.rms_eps, a.vsub * kHeadDim);
+        } else {
+            inv = rms_inv_f(ss[t], a.rms_eps);
+        }
+        a.y[(row0 + t) * C + h * kHeadDim + tid] =
+            a.norm_silu ? gated_norm_f<true>(o[t], inv, nw, z[t]) : gated_norm_f(o[t], inv, nw, z[t]);
+    }
+    if constexpr (WIDE) cluster_sync_all();       // the other units have read this unit's sums
+}
+
+template <int FMT, int GM, int KT, bool WIDE, int TT>
+cudaError_t launch_one(const DecodeQ8Args& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.d.H, (unsigned)a.d.N);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.d.vsub;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = WIDE ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kda_decode_q8_few_kernel<FMT, GM, KT, WIDE, TT>, a);
+}
+
+template <int FMT, int GM, int TT>
+cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
+    if (a.d.vsub > 1)
+        return a.d.K == 4 ? launch_one<FMT, GM, 4, true, TT>(a, s) : launch_one<FMT, GM, kMaxConvK, true, TT>(a, s);
+    return a.d.K == 4 ? launch_one<FMT, GM, 4, false, TT>(a, s) : launch_one<FMT, GM, kMaxConvK, false, TT>(a, s);
+}
+
+template <int FMT, int GM>
+cudaError_t launch_gm(const DecodeQ8Args& a, cudaStream_t s) {
+    if (a.d.T == 1) return launch_t<FMT, GM, 1>(a, s);
+    return a.d.T == 2 ? launch_t<FMT, GM, 2>(a, s) : launch_t<FMT, GM, 4>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_q8_few(const DecodeQ8Args& a, cudaStream_t s) {
+    if (a.fmt == kQ8E4m3)
+        return a.d.gate_mode == 0 ? launch_gm<kQ8E4m3, 0>(a, s) : launch_gm<kQ8E4m3, 1>(a, s);
+    return a.d.gate_mode == 0 ? launch_gm<kQ8Int8, 0>(a, s) : launch_gm<kQ8Int8, 1>(a, s);
+}
+
+}  // namespace kda
