@@ -55,7 +55,7 @@ __device__ __forceinline__ uint4 pack16(const float2 (&s)[8], float mul) {
     uint32_t u[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
-        u[m] = q8_encode4<FMT>(make_float4(s[2 * m].x, s[2 * m].y, s[2 * m + 1].x, s[2 * m + 1].y), mul);
+        u[m] = q8_encode4_once<FMT>(make_float4(s[2 * m].x, s[2 * m].y, s[2 * m + 1].x, s[2 * m + 1].y), mul);
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
         for (int c = 0; c < B; ++c) {
             float m = mag_max(S[c][0].x, S[c][0].y);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) m = mag_max(m, mag_max(S[c][i].x, S[c][i].y));
+            for (int i = 1; i < 8; ++i) m = mag_max3(m, S[c][i].x, S[c][i].y);
             mx[c] = m;
         }
         float top;

@@ -158,6 +158,26 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
             if (GATE_MODE == 0) ga[t] = a.f_raw[(row0 + t) * wg + gh * kHeadDim + tid];
         }
     }
+    // ---- codes, scales and ring of the slot in, asked for before the slots are looked over (warp 3
+    //      does that meanwhile): what a row that is left out reads so is dropped
+    const int want = p.slots ? p.slots[n] : n;
+    const int from = min(max(want, 0), p.pool_rows - 1);
+    const int g = lane >> 2, c = lane & 3;
+    const long unit_in = ((long)from * H + h) * kHeadDim;
+    // [row g, row g + 8][half]: 8 pieces of 16 bytes a row, this lane's at c and 4 + c
+    const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + (unit_in + warp * 32 + g) * 8 + c;
+    uint4 cur[2][2], nxt[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            cur[r][f] = __ldcs(cin + r * 64 + f * 4);
+            nxt[r][f] = __ldcs(cin + 128 + r * 64 + f * 4);
+        }
+    const float scale_l = p.scales[unit_in + tid];
+
+    const long ring_len = ring_channels(H, a.Hk) * (K - 1);
+    const float* ring_in = a.ring_out + (long)from * ring_len;
     if (warp == 3) {
         int in, out;
         const bool ok = pool_row_warp(p.slots, p.slots_out, n, a.N, p.pool_rows, a.err, in, out);
@@ -169,6 +189,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
     cq.weights(a.conv_w, chq, K);
     ck.weights(a.conv_w, chk, K);
     cv.weights(a.conv_w, chv, K);
+    cq.load(ring_in, chq, K);
+    ck.load(ring_in, chk, K);
+    cv.load(ring_in, chv, K);
     const float alog = a.a_log[gh];
     const float dt = GATE_MODE == 0 ? a.dt_bias[(long)gh * kHeadDim + tid] : a.dt_bias[gh];
     if (tid < T) {
@@ -179,32 +202,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
     __syncthreads();
     const int slot_in = sm.slots.x, slot_out = sm.slots.y;
     if (slot_in < 0) return;                      // uniform over the cluster: n decides alone
-
-    // ---- the codes of this warp's two tiles, its columns' scales
-    const int g = lane >> 2, c = lane & 3;
-    const long unit_in = ((long)slot_in * H + h) * kHeadDim, unit_out = ((long)slot_out * H + h) * kHeadDim;
-    // [row g, row g + 8][half]: 8 pieces of 16 bytes a row, this lane's at c and 4 + c
-    const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + (unit_in + warp * 32 + g) * 8 + c;
+    const long unit_out = ((long)slot_out * H + h) * kHeadDim;
     uint4* cout = reinterpret_cast<uint4*>(p.codes) + (unit_out + warp * 32 + g) * 8 + c;
-    uint4 cur[2][2], nxt[2][2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            cur[r][f] = __ldcs(cin + r * 64 + f * 4);
-            nxt[r][f] = __ldcs(cin + 128 + r * 64 + f * 4);
-        }
-    const float scale_l = p.scales[unit_in + tid];
-
-    // ---- ring slots: a q / k ring row that several units read is rolled by one of them, and only
-    //      into another slot: in place it is left to the roll kernel that follows
+    // a q / k ring row that several units read is rolled by one of them, and only into another slot:
+    // in place it is left to the roll kernel that follows
     const bool roll_qk = h == gh * vs && gh < Hkq && (Hkq == H || slot_in != slot_out);
-    const long ring_len = ring_channels(H, a.Hk) * (K - 1);
-    const float* ring_in = a.ring_out + (long)slot_in * ring_len;
     float* ring_out = a.ring_out + (long)slot_out * ring_len;
-    cq.load(ring_in, chq, K);
-    ck.load(ring_in, chk, K);
-    cv.load(ring_in, chv, K);
 
     if (T == 0) {       // nothing accepted: the slot passes through unchanged (in place: untouched)
         if (slot_in != slot_out) {
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
         for (int r = 0; r < 2; ++r) {
             float x = mag_max(S[r][0].x, S[r][0].y);
 #pragma unroll
-            for (int i = 1; i < 16; ++i) x = mag_max(x, mag_max(S[r][i].x, S[r][i].y));
+            for (int i = 1; i < 16; ++i) x = mag_max3(x, S[r][i].x, S[r][i].y);
             mx[r] = x;
         }
         const bool up = c & 2;
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float2 lo = S[r][2 * (4 * y + m)], hi = S[r][2 * (4 * y + m) + 1];
-                    u[m] = q8_encode4<FMT>(make_float4(lo.x, lo.y, hi.x, hi.y), mul);
+                    u[m] = q8_encode4_once<FMT>(make_float4(lo.x, lo.y, hi.x, hi.y), mul);
                 }
                 __stcs(cout + mt * 128 + r * 64 + y * 4, make_uint4(u[0], u[1], u[2], u[3]));
             }

@@ -37,6 +37,13 @@ __device__ __forceinline__ float mag_max(float a, float b) {
     return m;
 }
 
+// The largest magnitude of three, without a sign (NaN as above).
+__device__ __forceinline__ float mag_max3(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
 // Row scale and multiplier from the row's largest magnitude bits.
 template <int FMT>
 __device__ __forceinline__ void q8_row(uint32_t amax_bits, float& scale, float& mul) {
@@ -87,6 +94,18 @@ __device__ __forceinline__ uint32_t q8_encode4(float4 x, float mul) {
     return mul != 0.0f ? w : 0u;
 }
 
+// The same for values that are nobody's but the caller's (a decode step's new state): int8 codes are
+// rounded once, from the exact product.
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_encode4_once(float4 x, float mul) {
+    if constexpr (FMT == kQ8E4m3) return q8_encode4<FMT>(x, mul);
+    const float2 m2 = make_float2(mul, mul), big = make_float2(12582912.0f, 12582912.0f);
+    const float2 lo = __ffma2_rn(make_float2(x.x, x.y), m2, big), hi = __ffma2_rn(make_float2(x.z, x.w), m2, big);
+    const uint32_t w = __byte_perm(__byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x0040),
+                                   __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x0040), 0x5410);
+    return mul != 0.0f ? w : 0u;
+}
+
 // The values of four codes times their row's scale.
 template <int FMT>
 __device__ __forceinline__ float4 q8_decode4(uint32_t w, float scale) {
@@ -99,11 +118,12 @@ __device__ __forceinline__ float4 q8_decode4(uint32_t w, float scale) {
     } else {
         // code + 128 under the exponent of 2^23, then minus (2^23 + 128): exact
         const uint32_t u = w ^ 0x80808080u;
-        const float base = 8388736.0f;
-        v.x = __fadd_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)), -base);
-        v.y = __fadd_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)), -base);
-        v.z = __fadd_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)), -base);
-        v.w = __fadd_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)), -base);
+        const float2 base = make_float2(-8388736.0f, -8388736.0f);
+        const float2 a = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)),
+                                                __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441))), base);
+        const float2 b = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)),
+                                                __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443))), base);
+        v = make_float4(a.x, a.y, b.x, b.y);
     }
     const float2 s2 = make_float2(scale, scale);
     const float2 lo = __fmul2_rn(make_float2(v.x, v.y), s2), hi = __fmul2_rn(make_float2(v.z, v.w), s2);
