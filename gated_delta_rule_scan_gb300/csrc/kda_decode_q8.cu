@@ -477,8 +477,9 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t s) {
     cudaError_t e;
     {
         KernelTimer kt(kKDecodeQ8, s);
-        // (a positive gate bound lets decays grow past 1, out of the range of the form for few)
-        if (a.d.T <= kDecodeQ8FewT && (a.d.gate_mode != 0 || a.d.gate_lb <= 0.0f))
+        // (a positive gate bound lets decays grow past 1, out of the range of the form for few,
+        // which reads a slot before it knows whether the pool has it)
+        if (a.d.T <= kDecodeQ8FewT && a.pool_rows > 0 && (a.d.gate_mode != 0 || a.d.gate_lb <= 0.0f))
             e = launch_decode_q8_few(a, s);
         else if (a.fmt == kQ8E4m3)
             e = a.d.gate_mode == 0 ? launch_t<kQ8E4m3, 0>(a, s) : launch_t<kQ8E4m3, 1>(a, s);

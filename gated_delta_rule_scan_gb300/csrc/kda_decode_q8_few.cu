@@ -21,7 +21,13 @@
 // the gate, and = value column: its v, its row scale and its solve stay in registers.  A warp owns
 // 32 columns as two 16-row MMA tiles; lane 4g + c holds of rows g and g + 8 the key words that the MMA
 // wants of it, chosen as keys 64 half + 16c .. 16c + 15 so that a row is read and written in 16-byte
-// pieces; the same registers are the MMA's left side and, unpacked, the state.
+// pieces; the same words are the MMA's left side and, unpacked, the state.  Everything a block reads
+// is asked for at once, before its slots have been looked over; codes and output gates wait in shared
+// memory (in registers: 4 blocks an SM and spills, 45 us at one token and 85 at four, 64 x 64 heads).
+// There it runs 41 us at one token, 50 at two and 66 at four, where its bytes need 27 to 32; the other
+// form takes 53, 70 and 100.  What is left is the wait for a block's first bytes, about a third of its
+// life, overlapped by four other blocks only.  (Persistent blocks that fetch the next unit by bulk
+// copies meanwhile: 62 us; issuing some fifteen small copies a unit takes longer than the wait.)
 #include <cuda_fp16.h>
 
 #include "kda_decode_q8.cuh"
@@ -34,6 +40,7 @@ constexpr int kThreads = 128;
 constexpr int kVecBytes = 320;               // one f16 vector: 256 bytes, and 64 against bank conflicts
 constexpr int kDotRow = 136;                 // floats: four lanes' columns land in different banks
 constexpr float kVecScale = 4096.0f;
+constexpr int kMinBlocks = 5;                // an SM: 41 us at one token, 64 x 64 heads (4: 44, 6: 42)
 
 // Key i is byte e of word m (0 .. 7) of lane c: i = 64 (m / 4) + 16 c + 4 (m % 4) + e.
 __device__ __forceinline__ int key_word(int i) { return ((i >> 6) << 2) | ((i >> 2) & 3); }
@@ -74,6 +81,10 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     }
 }
 
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // N sums over the warp's lanes, N a power of two: lane l ends with sum l / (32 / N).
 template <int N>
 __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
@@ -91,11 +102,13 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
     return s;
 }
 
-template <bool BF16>
-__device__ __forceinline__ float raw_at(const void* p, long i) {
-    return BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
-                : reinterpret_cast<const float*>(p)[i];
+// A raw sample as it lies in memory, and its value.  (Converted when used: a conversion next to the
+// load waits for it, token by token: 93 us against 85 at four tokens, 64 x 64 heads.)
+__device__ __forceinline__ uint32_t raw_bits(const void* p, long i, bool bf16) {
+    if (bf16) return reinterpret_cast<const unsigned short*>(p)[i];
+    return reinterpret_cast<const uint32_t*>(p)[i];
 }
+__device__ __forceinline__ float raw_value(uint32_t x, bool bf16) { return __uint_as_float(bf16 ? x << 16 : x); }
 
 // TT: tokens of the call at most.  The sums over channels are numbered q.q (t), k.k (TT + t), then
 // D k_s . k_t for s < t and D k_s . q_t for s <= t, by t and then s.
@@ -110,17 +123,18 @@ struct Sums {
 
 template <int TT>
 struct FewSmem {
+    uint4 code[kHeadDim * 8];
     static constexpr int kTiles = (TT + 1) / 2;              // MMA tiles of 8 columns: two tokens each
     uint4 vec[8 * kTiles * kVecBytes / 16];                  // hi, lo of k, then of q, token by token
     float row[(TT + 1) * kHeadDim];                          // D_sT k_s, then A_T
     float dot[4 * kTiles * kDotRow];                         // (token, k or q) x columns
     float part[4][Sums<TT>::padded];
-    float beta[TT], decay[TT], nss[TT], osum[4][TT];
-    int2 slots;
+    float z[TT][kHeadDim];
+    float beta[TT], nss[TT], osum[4][TT];
 };
 
 template <int FMT, int GATE_MODE, int KT, bool WIDE, int TT>
-__global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const DecodeQ8Args p) {
+__global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel(const DecodeQ8Args p) {
     __shared__ __align__(16) FewSmem<TT> sm;
     using S_ = Sums<TT>;
     const DecodeArgs& a = p.d;
@@ -139,50 +153,42 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
 
     // ---- raw samples, conv weights and gate inputs: nothing of them depends on the slots
     const long wq = plane_width(H, a.Hk, 0), wv = (long)H * kHeadDim, wg = (long)Hg * kHeadDim;
-    float q[TT], k[TT], v[TT], ga[TT];
+    const bool bf16 = a.raw_bf16 != 0;
+    uint32_t qr[TT], kr[TT], vr[TT];
+    float ga[TT];
     {
         const long aq = row0 * wq + hq * kHeadDim + tid, av = row0 * wv + (long)h * kHeadDim + tid;
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            q[t] = k[t] = v[t] = ga[t] = 0.0f;
+            qr[t] = kr[t] = vr[t] = 0u;
+            ga[t] = 0.0f;
             if (t >= T) continue;
-            if (a.raw_bf16) {
-                q[t] = raw_at<true>(a.q_raw, aq + t * wq);
-                k[t] = raw_at<true>(a.k_raw, aq + t * wq);
-                v[t] = raw_at<true>(a.v_raw, av + t * wv);
-            } else {
-                q[t] = raw_at<false>(a.q_raw, aq + t * wq);
-                k[t] = raw_at<false>(a.k_raw, aq + t * wq);
-                v[t] = raw_at<false>(a.v_raw, av + t * wv);
-            }
-            if (GATE_MODE == 0) ga[t] = a.f_raw[(row0 + t) * wg + gh * kHeadDim + tid];
+            qr[t] = raw_bits(a.q_raw, aq + t * wq, bf16);
+            kr[t] = raw_bits(a.k_raw, aq + t * wq, bf16);
+            vr[t] = raw_bits(a.v_raw, av + t * wv, bf16);
+            ga[t] = GATE_MODE == 0 ? a.f_raw[(row0 + t) * wg + gh * kHeadDim + tid] : a.f_raw[(row0 + t) * Hg + gh];
+            cp_async_4(&sm.z[t][tid], a.gate_raw + av + t * wv);
         }
     }
-    // ---- codes, scales and ring of the slot in, asked for before the slots are looked over (warp 3
-    //      does that meanwhile): what a row that is left out reads so is dropped
-    const int want = p.slots ? p.slots[n] : n;
-    const int from = min(max(want, 0), p.pool_rows - 1);
+    const float nw = __ldg(a.norm_w + (WIDE ? (int)blockIdx.x % a.vsub : 0) * kHeadDim + tid);
+    // ---- codes, scales and ring of the slot in, asked for before the slots are looked over: what a
+    //      row that is left out reads so is dropped
+    const int slot_in = p.slots ? p.slots[n] : n;
+    const int slot_out = p.slots_out ? p.slots_out[n] : slot_in;
+    const int from = min(max(slot_in, 0), p.pool_rows - 1);
     const int g = lane >> 2, c = lane & 3;
     const long unit_in = ((long)from * H + h) * kHeadDim;
     // [row g, row g + 8][half]: 8 pieces of 16 bytes a row, this lane's at c and 4 + c
     const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + (unit_in + warp * 32 + g) * 8 + c;
-    uint4 cur[2][2], nxt[2][2];
+    uint4* code_s = sm.code + (warp * 32 + g) * 8 + c;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            cur[r][f] = __ldcs(cin + r * 64 + f * 4);
-            nxt[r][f] = __ldcs(cin + 128 + r * 64 + f * 4);
-        }
+        for (int f = 0; f < 2; ++f) cp_async_16(code_s + r * 64 + f * 4, cin + r * 64 + f * 4);
     const float scale_l = p.scales[unit_in + tid];
 
     const long ring_len = ring_channels(H, a.Hk) * (K - 1);
     const float* ring_in = a.ring_out + (long)from * ring_len;
-    if (warp == 3) {
-        int in, out;
-        const bool ok = pool_row_warp(p.slots, p.slots_out, n, a.N, p.pool_rows, a.err, in, out);
-        if (lane == 0) sm.slots = make_int2(ok ? in : -1, out);
-    }
     const int chq = hq * kHeadDim + tid, chk = (int)plane_offset(H, a.Hk, 1) + chq;
     const int chv = (int)plane_offset(H, a.Hk, 2) + h * kHeadDim + tid;
     Conv<KT> cq, ck, cv;
@@ -194,14 +200,61 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
     cv.load(ring_in, chv, K);
     const float alog = a.a_log[gh];
     const float dt = GATE_MODE == 0 ? a.dt_bias[(long)gh * kHeadDim + tid] : a.dt_bias[gh];
-    if (tid < T) {
-        const long rw = (row0 + tid) * Hg + gh;
-        sm.beta[tid] = sigmoid_f(a.beta_raw[rw]);
-        if (GATE_MODE == 1) sm.decay[tid] = decay_f(gdn_gate_f(a.f_raw[rw], dt, alog));
+    const float beta_raw = tid < T ? a.beta_raw[(row0 + tid) * Hg + gh] : 0.0f;
+    // the first rows' slots that this thread looks over below
+    const int other = min(tid, a.N - 1);
+    const int im = p.slots ? p.slots[other] : other, om = p.slots_out ? p.slots_out[other] : im;
+    // ---- conv + SiLU, the gate, the sums over channels
+    const float rate = GATE_MODE == 0 ? expf(alog) : 0.0f;
+    float q[TT], k[TT], v[TT];
+    float kd[TT], cum[TT];                        // D_st k_s so far, A_t
+    {
+        float sum[S_::padded] = {};
+        float run = 1.0f;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            q[t] = k[t] = v[t] = kd[t] = cum[t] = 0.0f;
+            if (t >= T) continue;
+            q[t] = cq.step(raw_value(qr[t], bf16), K);
+            k[t] = ck.step(raw_value(kr[t], bf16), K);
+            v[t] = cv.step(raw_value(vr[t], bf16), K);
+            const float dec = decay_f(GATE_MODE == 0 ? kda_gate_f(ga[t], dt, rate, a.gate_lb)
+                                                     : gdn_gate_f(ga[t], dt, alog));
+            run *= dec;
+            cum[t] = run;
+            // (no products fused into sums: a call's results do not depend on TT)
+            sum[t] = __fmul_rn(q[t], q[t]);
+            sum[S_::kk + t] = __fmul_rn(k[t], k[t]);
+#pragma unroll
+            for (int s = 0; s < t; ++s) {
+                kd[s] *= dec;
+                sum[S_::kk_at(s, t)] = __fmul_rn(kd[s], k[t]);
+                sum[S_::qk_at(s, t)] = __fmul_rn(kd[s], q[t]);
+            }
+            kd[t] = k[t];
+            sum[S_::qk_at(t, t)] = __fmul_rn(k[t], q[t]);
+        }
+        const float s = warp_sums(sum, lane);
+        if (lane % S_::lanes == 0) sm.part[warp][lane / S_::lanes] = s;
     }
-    __syncthreads();
-    const int slot_in = sm.slots.x, slot_out = sm.slots.y;
-    if (slot_in < 0) return;                      // uniform over the cluster: n decides alone
+    if (tid < T) sm.beta[tid] = sigmoid_f(beta_raw);
+    // The slots (the rules of pool_row_warp, here looked over by the whole block).
+    const bool live = slot_in >= 0 && slot_out >= 0;
+    bool bad = slot_in >= p.pool_rows || slot_out >= p.pool_rows;
+    if (p.slots || p.slots_out) {
+        if (tid < a.N) bad |= pool_rows_clash(im, om, n, slot_out, tid);
+        for (int m = tid + kThreads; m < a.N; m += kThreads) {
+            const int mi = p.slots ? p.slots[m] : m;
+            bad |= pool_rows_clash(mi, p.slots_out ? p.slots_out[m] : mi, n, slot_out, m);
+        }
+    }
+    const bool clash = __syncthreads_or(live && bad);
+    if (clash && tid == 0 && a.err) atomicOr(a.err, kDevErrSlot);
+    if (!live || clash) {                         // uniform over the cluster: n decides alone
+        cp_async_commit_wait();
+        return;
+    }
+
     const long unit_out = ((long)slot_out * H + h) * kHeadDim;
     uint4* cout = reinterpret_cast<uint4*>(p.codes) + (unit_out + warp * 32 + g) * 8 + c;
     // a q / k ring row that several units read is rolled by one of them, and only into another slot:
@@ -210,14 +263,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
     float* ring_out = a.ring_out + (long)slot_out * ring_len;
 
     if (T == 0) {       // nothing accepted: the slot passes through unchanged (in place: untouched)
+        cp_async_commit_wait();
         if (slot_in != slot_out) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    __stcs(cout + r * 64 + f * 4, cur[r][f]);
-                    __stcs(cout + 128 + r * 64 + f * 4, nxt[r][f]);
-                }
+                for (int f = 0; f < 2; ++f) __stcs(cout + r * 64 + f * 4, code_s[r * 64 + f * 4]);
             p.scales[unit_out + tid] = scale_l;
             cv.store(ring_out, chv, K);
             if (roll_qk) {
@@ -227,43 +278,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
         }
         return;
     }
-
-    // ---- conv + SiLU and the ring roll, the gate, the sums over channels
-    const float rate = GATE_MODE == 0 ? expf(alog) : 0.0f;
-    float kd[TT], cum[TT];                        // D_st k_s so far, A_t
-    {
-        float sum[S_::padded] = {};
-        float run = 1.0f;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            kd[t] = cum[t] = 0.0f;
-            if (t >= T) continue;
-            q[t] = cq.step(q[t], K);
-            k[t] = ck.step(k[t], K);
-            v[t] = cv.step(v[t], K);
-            const float dec = GATE_MODE == 0 ? decay_f(kda_gate_f(ga[t], dt, rate, a.gate_lb)) : sm.decay[t];
-            run *= dec;
-            cum[t] = run;
-            sum[t] = q[t] * q[t];
-            sum[S_::kk + t] = k[t] * k[t];
-#pragma unroll
-            for (int s = 0; s < t; ++s) {
-                kd[s] *= dec;
-                sum[S_::kk_at(s, t)] = kd[s] * k[t];
-                sum[S_::qk_at(s, t)] = kd[s] * q[t];
-            }
-            kd[t] = k[t];
-            sum[S_::qk_at(t, t)] = k[t] * q[t];
-        }
-        const float s = warp_sums(sum, lane);
-        if (lane % S_::lanes == 0) sm.part[warp][lane / S_::lanes] = s;
-    }
     cv.store(ring_out, chv, K);
     if (roll_qk) {
         cq.store(ring_out, chq, K);
         ck.store(ring_out, chk, K);
     }
-    __syncthreads();
     // lane l: sum l / lanes of the unit; then the l2 scales in its place for q.q and k.k
     const int own = lane / S_::lanes;
     const float total = (sm.part[0][own] + sm.part[1][own]) + (sm.part[2][own] + sm.part[3][own]);
@@ -279,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
             iq[t] = coef_at(t);
             ik[t] = coef_at(S_::kk + t);
             // (tokens from T on are zeros)
-            const float x = k[t] * (t < T ? ik[t] : 0.0f) * cum[t] * kVecScale;
-            const float y = q[t] * (t < T ? iq[t] : 0.0f) * cum[t] * kVecScale;
+            const float x = __fmul_rn(__fmul_rn(k[t], t < T ? ik[t] : 0.0f), __fmul_rn(cum[t], kVecScale));
+            const float y = __fmul_rn(__fmul_rn(q[t], t < T ? iq[t] : 0.0f), __fmul_rn(cum[t], kVecScale));
             const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
             __half* at = vec + 4 * t * (kVecBytes / 2);
             at[0] = xh;
@@ -293,31 +312,20 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
         if (GATE_MODE == 0) row[TT * kHeadDim] = run;
         else if (tid == 0) row[TT * kHeadDim] = run;
     }
-    // the epilogue's inputs, requested ahead of the work on the state
-    const long C = (long)H * kHeadDim;
-    const float nw = __ldg(a.norm_w + (WIDE ? (int)blockIdx.x % a.vsub : 0) * kHeadDim + tid);
-    float z[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-        z[t] = t < T ? __ldcs(a.gate_raw + (row0 + t) * C + h * kHeadDim + tid) : 0.0f;
     __syncthreads();
 
     // ---- the incoming state's products, 16 columns at a time
-    const auto swap_tiles = [&] {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const uint4 x = cur[r][f];
-                cur[r][f] = nxt[r][f];
-                nxt[r][f] = x;
-            }
-    };
+    cp_async_commit_wait();                       // (each lane reads what it copied)
     constexpr int kTiles = FewSmem<TT>::kTiles;
     const int cols = 4 * TT;                      // columns past them repeat the last one
 #pragma unroll 1
     for (int mt = 0; mt < 2; ++mt) {
         float d[kTiles][4] = {};
+        uint4 cur[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) cur[r][f] = code_s[mt * 128 + r * 64 + f * 4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
             const uint32_t u[2][4] = {{cur[0][f].x, cur[0][f].y, cur[0][f].z, cur[0][f].w},
@@ -346,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
                 o[0] = d[i][0] + d[i][1];
                 o[8] = d[i][2] + d[i][3];
             }
-        swap_tiles();
     }
     __syncwarp();
 
@@ -356,16 +363,17 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
         const float sc = scale_l * (1.0f / kVecScale);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            float x = sm.dot[2 * t * kDotRow + tid] * sc, y = sm.dot[(2 * t + 1) * kDotRow + tid] * sc;
+            float x = __fmul_rn(sm.dot[2 * t * kDotRow + tid], sc);
+            float y = __fmul_rn(sm.dot[(2 * t + 1) * kDotRow + tid], sc);
 #pragma unroll
             for (int s = 0; s < t; ++s) {
                 x = fmaf(w[s], coef_at(S_::kk_at(s, t)) * (ik[s] * ik[t]), x);
                 y = fmaf(w[s], coef_at(S_::qk_at(s, t)) * (ik[s] * iq[t]), y);
             }
             const float qk = coef_at(S_::qk_at(t, t)) * (ik[t] * iq[t]);
-            w[t] = t < T ? sm.beta[t] * (v[t] - x) : 0.0f;
+            w[t] = t < T ? __fmul_rn(sm.beta[t], v[t] - x) : 0.0f;
             o[t] = __fmul_rn(a.scale, fmaf(w[t], qk, y));
-            const float ss = t < T ? warp_sum(o[t] * o[t]) : 0.0f;
+            const float ss = t < T ? warp_sum(__fmul_rn(o[t], o[t])) : 0.0f;
             if (lane == 0) sm.osum[warp][t] = ss;
         }
     }
@@ -389,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
             const float4 a4 = GATE_MODE == 0 ? rows[TT * (kHeadDim / 4)] : make_float4(as, as, as, as);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint4 w4 = cur[r][m >> 2];
-                const uint32_t word = (m & 3) == 0 ? w4.x : (m & 3) == 1 ? w4.y : (m & 3) == 2 ? w4.z : w4.w;
+                const uint32_t word = reinterpret_cast<const uint32_t*>(code_s + mt * 128 + r * 64 + (m >> 2) * 4)[m & 3];
                 const float4 x = q8_decode4<FMT>(word, sr[r]);
                 S[r][2 * m] = __fmul2_rn(make_float2(x.x, x.y), make_float2(a4.x, a4.y));
                 S[r][2 * m + 1] = __fmul2_rn(make_float2(x.z, x.w), make_float2(a4.z, a4.w));
@@ -434,7 +441,6 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
             }
         }
         if (!(c & 1)) p.scales[unit_out + warp * 32 + mt * 16 + 4 * c + g] = f;
-        swap_tiles();
     }
     __syncthreads();
 
@@ -461,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_decode_q8_few_kernel(const De
         } else {
             inv = rms_inv_f(ss[t], a.rms_eps);
         }
-        a.y[(row0 + t) * C + h * kHeadDim + tid] =
-            a.norm_silu ? gated_norm_f<true>(o[t], inv, nw, z[t]) : gated_norm_f(o[t], inv, nw, z[t]);
+        a.y[(row0 + t) * wv + h * kHeadDim + tid] =
+            a.norm_silu ? gated_norm_f<true>(o[t], inv, nw, sm.z[t][tid]) : gated_norm_f(o[t], inv, nw, sm.z[t][tid]);
     }
     if constexpr (WIDE) cluster_sync_all();       // the other units have read this unit's sums
 }

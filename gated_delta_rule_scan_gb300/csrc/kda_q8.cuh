@@ -130,6 +130,12 @@ __device__ __forceinline__ float4 q8_decode4(uint32_t w, float scale) {
     return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
+// Whether batch row m, with slots im and om, keeps row n from writing slot `out`: it reads that slot,
+// or writes it first.
+__device__ __forceinline__ bool pool_rows_clash(int im, int om, int n, int out, int m) {
+    return m != n && im >= 0 && om >= 0 && (im == out || (m < n && om == out));
+}
+
 // The pool rows that batch row n reads and writes.  A negative slot is padding: the row is skipped.
 // A slot past the pool, and an output slot that another row reads or an earlier row writes, raise
 // the error word and the row is skipped too, so that no two blocks race on a slot.  Every thread of
@@ -144,8 +150,7 @@ __device__ __forceinline__ bool pool_row_warp(const int* slots, const int* slots
     if (slots || slots_out) {
         for (int m = lane; m < N; m += 32) {
             const int im = slots ? slots[m] : m;
-            const int om = slots_out ? slots_out[m] : im;
-            if (m != n && im >= 0 && om >= 0) bad |= im == out || (m < n && om == out);
+            bad |= pool_rows_clash(im, slots_out ? slots_out[m] : im, n, out, m);
         }
     }
     const bool any = __any_sync(0xffffffffu, live && bad);
