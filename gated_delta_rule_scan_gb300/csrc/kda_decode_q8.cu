@@ -11,20 +11,22 @@
 // per token.  The state is f32 in registers over all tokens of the call and is rounded to 8 bits
 // once, at the end.
 //
+// Up to four tokens take the form of kda_decode_q8_few.cu, which reads the state once for all of
+// them; this one serves longer verify windows (and a positive gate bound): its state stays in
+// registers from token to token, whatever their number.
+//
 // GB300 layout.  The bytes are a quarter of the f32 decode's (33 KB of state per (sequence, head)
 // read and written, against 131 KB), so the instructions around them bound this kernel: at 64
-// sequences x 64 heads it runs 53 us, where its bytes need 27 (a first form with the lanes of a
-// warp across a column: 77 us).  One CTA owns one (sequence, unit), in four warps: thread = channel
-// of q, k, v and the gate in the prologue, so its address work is done by as few warps as the
-// occupancy allows (8 warps a CTA: 61 us).  8 lanes share 8 value columns, lane r keys
-// 16r .. 16r + 15 of each, so that a column's codes are one 16-byte access a lane, its reductions
-// take three steps, and every k, decay and q value read from shared memory serves two columns at a
-// time; the rows of q, k and the decay lie in shared memory in the order that makes those reads
-// conflict-free (key 16r + 4m + e at 32m + 4r + e).  Two columns are unpacked at a time, the codes of
-// the next two to four wait or are on their way in registers (four at a time: 61 us; all loads in
-// shared memory by bulk copies: 66; persistent blocks that prefetch the next sequence: 80).  The l2
-// norms scale the finished sums instead of the vectors.  Of a reduction's lanes each finishes one
-// column: one division a lane rounds the state, not two a column.
+// sequences x 64 heads x 8 tokens it runs 161 us, where its bytes need 38.  One CTA owns one
+// (sequence, unit), in four warps: thread = channel of q, k, v and the gate in the prologue, so its
+// address work is done by few warps.  8 lanes share 8 value columns, lane r keys 16r .. 16r + 15 of
+// each, so that a column's codes are one 16-byte access a lane, its reductions take three steps, and
+// every k, decay and q value read from shared memory serves four columns at a time (two: 172 us; the
+// shared reads were the most used unit, 69 % of their peak at four tokens); the rows of q, k and the
+// decay lie in shared memory in the order that makes those reads conflict-free (key 16r + 4m + e at
+// 32m + 4r + e).  The codes of the next four columns are on their way meanwhile.  The l2 norms scale
+// the finished sums instead of the vectors.  Of a reduction's lanes each finishes one column: one
+// division a lane rounds the state, not two a column.
 #include "kda_decode_q8.cuh"
 
 namespace kda {
@@ -33,8 +35,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kCols = 8;                     // value columns of a group of 8 lanes
-constexpr int B = 4;                         // of them unpacked at a time
-constexpr int kAhead = 4;                    // columns whose codes are loaded or on their way
+constexpr int kB = 4;                        // of them unpacked at a time
 
 // Where key i of a q, k or decay row lies in shared memory.
 __device__ __forceinline__ int key_pos(int i) { return 32 * ((i >> 2) & 3) + 4 * (i >> 4) + (i & 3); }
@@ -64,13 +65,8 @@ __device__ __forceinline__ float4 row4(const float* row, int r, int m) {
     return *reinterpret_cast<const float4*>(row + 32 * m + 4 * r);
 }
 
-// B sums of columns over the four lanes that differ in bits 0 and 1: lane 2j (B = 2) or j (B = 4)
-// of them, and with B = 2 lane 2j + 1 too, ends with column j's.
-__device__ __forceinline__ float reduce_columns(const float (&s)[2], int lane) {
-    const bool b1 = lane & 2;
-    const float x = (b1 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[1], 2);
-    return x + __shfl_xor_sync(0xffffffffu, x, 1);
-}
+// Four columns' sums over the four lanes that differ in bits 0 and 1: lane j of them ends with column
+// j's.
 __device__ __forceinline__ float reduce_columns(const float (&s)[4], int lane) {
     const bool b1 = lane & 2, b0 = lane & 1;
     const float x = (b1 ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[2], 2);
@@ -170,9 +166,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
     const long unit_out = ((long)slot_out * H + h) * kHeadDim + col0;
     const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + unit_in * (kHeadDim / 16) + r;
     uint4* cout = reinterpret_cast<uint4*>(p.codes) + unit_out * (kHeadDim / 16) + r;
-    uint4 code[kAhead];
+    uint4 code[kB];                               // the batch's, then the next one's
 #pragma unroll
-    for (int c = 0; c < kAhead; ++c) code[c] = __ldcs(cin + c * (kHeadDim / 16));
+    for (int c = 0; c < kB; ++c) code[c] = __ldcs(cin + c * (kHeadDim / 16));
     const float scale_l = p.scales[unit_in + r];  // lane r: column r's
 
     // ---- ring slots
@@ -191,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
         if (slot_in != slot_out) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
-                __stcs(cout + c * (kHeadDim / 16), c < kAhead ? code[c < kAhead ? c : 0] : __ldcs(cin + c * (kHeadDim / 16)));
+                __stcs(cout + c * (kHeadDim / 16), c < kB ? code[c < kB ? c : 0] : __ldcs(cin + c * (kHeadDim / 16)));
             p.scales[unit_out + r] = scale_l;
             cv.store(ring_out, chv, K);
             if (roll_qk) {
@@ -271,21 +267,19 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
         beta_l = beta_s[lane];
     }
 
-    // ---- the recurrence, two columns of each group at a time
+    // ---- the recurrence, four columns of each group at a time
     // (rolled: four copies of it would not fit the instruction cache)
     const bool b2 = lane & 4;
-    const int own = B == 4 ? lane & 3 : (lane >> 1) & 1;      // the column whose sums end here
+    const int own = lane & 3;                     // the column whose sums end here
 #pragma unroll 1
-    for (int b = 0; b < kCols; b += B) {
-        float2 S[B][8];
+    for (int b = 0; b < kCols; b += kB) {
+        float2 S[kB][8];
 #pragma unroll
-        for (int c = 0; c < B; ++c)
+        for (int c = 0; c < kB; ++c)
             unpack16<FMT>(S[c], code[c], __shfl_sync(0xffffffffu, scale_l, (lane & ~7) + b + c));
 #pragma unroll
-        for (int c = 0; c < kAhead; ++c) {
-            if (c + B < kAhead) code[c] = code[c + B];
-            else if (b + B + c < kCols) code[c] = __ldcs(cin + (b + B + c) * (kHeadDim / 16));
-        }
+        for (int c = 0; c < kB; ++c)
+            if (b + kB + c < kCols) code[c] = __ldcs(cin + (b + kB + c) * (kHeadDim / 16));
 #pragma unroll 1
         for (int t = 0; t < T; ++t) {
             const float* krow = kh + t * kHeadDim;
@@ -293,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
             const float* arow = av + t * kHeadDim;
             const float as = GATE_MODE == 0 ? 0.0f : ascal[t];
             float4 k4[4];
-            float2 dk[B][2], dq[B][2];
+            float2 dk[kB][2], dq[kB][2];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 k4[m] = row4(krow, r, m);
@@ -303,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
                 const float2 kl = make_float2(k4[m].x, k4[m].y), kh2 = make_float2(k4[m].z, k4[m].w);
                 const float2 ql = make_float2(q4.x, q4.y), qh2 = make_float2(q4.z, q4.w);
 #pragma unroll
-                for (int c = 0; c < B; ++c) {
+                for (int c = 0; c < kB; ++c) {
                     S[c][2 * m] = __fmul2_rn(S[c][2 * m], al);
                     S[c][2 * m + 1] = __fmul2_rn(S[c][2 * m + 1], ah);
                     if (m == 0) {
@@ -319,11 +313,11 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
                     }
                 }
             }
-            // 2 B sums over the 8 lanes: lanes with bit 2 clear end with P.k, the others with P.q, of
+            // 8 sums over the 8 lanes: lanes with bit 2 clear end with P.k, the others with P.q, of
             // column `own`
-            float sum[B];
+            float sum[kB];
 #pragma unroll
-            for (int c = 0; c < B; ++c) {
+            for (int c = 0; c < kB; ++c) {
                 const float sk = (dk[c][0].x + dk[c][0].y) + (dk[c][1].x + dk[c][1].y);
                 const float sq = (dq[c][0].x + dq[c][0].y) + (dq[c][1].x + dq[c][1].y);
                 sum[c] = (b2 ? sq : sk) + __shfl_xor_sync(0xffffffffu, b2 ? sk : sq, 4);
@@ -334,12 +328,11 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
             const int col = col0 + b + own;
             const float w = beta * (vh[t * kHeadDim + col] - ik * red);      // in lanes of P.k
             const float wo = __shfl_xor_sync(0xffffffffu, w, 4);
-            if (b2 && (B == 4 || !(lane & 1)))
-                os[t * kHeadDim + col] = __fmul_rn(a.scale, fmaf(wo, qk, iq * red));
+            if (b2) os[t * kHeadDim + col] = __fmul_rn(a.scale, fmaf(wo, qk, iq * red));
             const float wk = w * ik;
 #pragma unroll
-            for (int c = 0; c < B; ++c) {
-                const float wc = __shfl_sync(0xffffffffu, wk, (lane & ~7) + (B == 4 ? c : 2 * c));
+            for (int c = 0; c < kB; ++c) {
+                const float wc = __shfl_sync(0xffffffffu, wk, (lane & ~7) + c);
                 const float2 w2 = make_float2(wc, wc);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -348,34 +341,27 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
                 }
             }
         }
-        // back to 8 bits: lane l of a group finishes column l / 4 of 2, or l / 2 of 4; even lanes
-        // form the scale, odd ones the multiplier
-        float mx[B];
+        // back to 8 bits: lane l of a group finishes column l / 2; even lanes form the scale, odd ones
+        // the multiplier
+        float mx[kB];
 #pragma unroll
-        for (int c = 0; c < B; ++c) {
+        for (int c = 0; c < kB; ++c) {
             float m = mag_max(S[c][0].x, S[c][0].y);
 #pragma unroll
             for (int i = 1; i < 8; ++i) m = mag_max3(m, S[c][i].x, S[c][i].y);
             mx[c] = m;
         }
-        float top;
-        if constexpr (B == 4) {
-            const float m0 = mag_max(b2 ? mx[2] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[2], 4));
-            const float m1 = mag_max(b2 ? mx[3] : mx[1], __shfl_xor_sync(0xffffffffu, b2 ? mx[1] : mx[3], 4));
-            const bool b1 = lane & 2;
-            top = mag_max(b1 ? m1 : m0, __shfl_xor_sync(0xffffffffu, b1 ? m0 : m1, 2));
-        } else {
-            top = mag_max(b2 ? mx[1] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[1], 4));
-            top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        }
+        const bool b1 = lane & 2;
+        const float m0 = mag_max(b2 ? mx[2] : mx[0], __shfl_xor_sync(0xffffffffu, b2 ? mx[0] : mx[2], 4));
+        const float m1 = mag_max(b2 ? mx[3] : mx[1], __shfl_xor_sync(0xffffffffu, b2 ? mx[1] : mx[3], 4));
+        float top = mag_max(b1 ? m1 : m0, __shfl_xor_sync(0xffffffffu, b1 ? m0 : m1, 2));
         top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        constexpr int kLanes = 8 / B;             // lanes that finish a column
         const float f = q8_row_part<FMT>(mag_bits(top), lane & 1);
 #pragma unroll
-        for (int c = 0; c < B; ++c)
+        for (int c = 0; c < kB; ++c)
             __stcs(cout + (b + c) * (kHeadDim / 16),
-                   pack16<FMT>(S[c], __shfl_sync(0xffffffffu, f, (lane & ~7) + kLanes * c + 1)));
-        if (lane % kLanes == 0) p.scales[unit_out + b + r / kLanes] = f;
+                   pack16<FMT>(S[c], __shfl_sync(0xffffffffu, f, (lane & ~7) + 2 * c + 1)));
+        if (!(lane & 1)) p.scales[unit_out + b + r / 2] = f;
     }
     __syncthreads();
     // ---- epilogue: gated RMSNorm, one warp per token row (as in kda_decode_fused)

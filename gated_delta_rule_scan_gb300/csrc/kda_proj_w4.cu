@@ -11,11 +11,12 @@
 //     out = sum over groups of c (sum_k q x - z / 8 sum_k 8 x).
 // x is scaled over 128 k at a time by the power of two that brings the largest magnitude of the 128
 // to [2^14, 2^15), split into f16 hi + lo, and the power of two goes back in with the group's scale.
-// hi is a multiple of 4, so that sum_k q hi and sum_k 8 hi, at most 15 * 2^15 * 128 < 2^24 such
-// steps, are exact in f32 and so is their difference: subtracting after the sum loses nothing, and a
-// code needs no more than a logical operation to become a number (taking 8 off each code first: 22.8
-// us against 19.1 at one row x 6144, 64 heads).  hi + lo is x within 2^-23 of the element's own
-// magnitude or 2^-25 of the largest of the 128, whichever is more.
+// hi is a whole number, so that sum_k q hi and sum_k 8 hi are exact in f32, and so is their
+// difference, as long as they stay below 2^24: 128 elements of a quarter of the largest's magnitude,
+// all of one sign, still do; larger sums are rounded as any f32 sum.  Subtracting after the sum
+// then loses nothing, and a code needs no more than a logical operation to become a number (taking 8
+// off each code first: 22.8 us against 19.1 at one row x 6144, 64 heads).  hi + lo is x within 2^-23
+// of the element's own magnitude or 2^-27 of the largest of the 128, whichever is more.
 //     5 to 8 rows of a bf16 x take hi alone (8 bits fit, in any order of magnitude), to stay within
 // the MMA's 8 columns.  Its sums are rounded, so there the codes have 8 taken off first.
 //
@@ -47,7 +48,7 @@ constexpr int kTeam = kWarps * 32;
 constexpr int kRows = 16;                    // weight rows of a tile: the MMA's M
 constexpr int kChunk = 128;                  // k of one warp step
 constexpr int kTok = 8;                      // tokens at most: the MMA's N, for a bf16 x
-constexpr float kMagic = 50331648.0f;        // 1.5 * 2^25
+constexpr float kMagic = 12582912.0f;        // 1.5 * 2^23
 constexpr int kXSmem = 160 * 1024;           // x of one block at most
 
 struct W4Params {
@@ -255,7 +256,7 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
             if constexpr (ONE) {
                 hi[at8] = __float2half_rn(y);
             } else {
-                // to a multiple of 4 (a step of f32 at 2^25), then to f16's 11 bits
+                // to a whole number (a step of f32 at 2^23), then to f16's 11 bits
                 const float h = __half2float(__float2half_rn(__fsub_rn(__fadd_rn(y, kMagic), kMagic)));
                 const float w = j & 1 ? 0.0625f : 1.0f;          // odd codes come times 16
                 hi[at8] = __float2half_rn(h * w);

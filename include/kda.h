@@ -618,7 +618,9 @@ int kda_state_load_q8(const void* codes, const float* scales, float* state, int 
  * roll the ring in place here.  q_raw, k_raw, v_raw, conv_w, ring_pool, codes, scales, norm_w,
  * gate_raw, y and, with KDA_GATE_PER_CHANNEL, f_raw and dt_bias are [16B].
  * Unlike kda_decode_fused, a T-token call is not T one-token calls bit for bit: those round the
- * state T times.  A call's outputs do not depend on the other rows of the batch.
+ * state T times.  A call's outputs do not depend on the other rows of the batch.  With T <= 4 its
+ * first keep[n] rows are those of a call of keep[n] tokens, bit for bit; calls of more tokens differ
+ * from those in the last bits of f32.
  */
 int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw, int raw_dtype,
                         const float* conv_w, float* ring_pool, const float* f_raw,

@@ -242,6 +242,59 @@ def test_padding_conflicts_and_bad_slots():
     assert kda.kda_device_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 6])
+def test_conflicts_among_many_rows(T):
+    """More rows than a block has threads: conflicts with rows far behind are found all the same."""
+    from gated_delta_rule_scan_gb300 import kda
+    N = 300
+    w = Work(12, N=N, T=T, H=1, P=2 * N + 1, slots=list(range(N)))
+    out = list(range(N, 2 * N))
+    good = w.decode(slots_out=_idx(out))
+    want = [t.clone() for t in (w.pool.codes.view(torch.uint8), w.pool.scales, w.pool.ring)]
+    w.reset()
+    out[290] = out[5]                          # row 5 has it
+    out[131] = 299                             # row 299 reads it
+    out[260] = 2 * N + 1                       # past the pool
+    slots = list(range(N))
+    slots[200] = -3                            # padding
+    y = w.decode(slots=slots, slots_out=_idx(out))
+    gone = {290, 131, 260, 200}
+    for n in range(N):
+        rows = y[n * T:(n + 1) * T]
+        assert (rows == 77.0).all() if n in gone else torch.equal(rows, good[n * T:(n + 1) * T])
+    left = [out[n] for n in range(N) if n not in gone]
+    for t, f in zip((w.pool.codes.view(torch.uint8), w.pool.scales, w.pool.ring), want):
+        assert torch.equal(t[left], f[left])
+    w.others_untouched(left)
+    assert kda.kda_device_status() == 40013
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("raw", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+def test_every_short_length(T, raw, fmt):
+    w = Work(400 + T, N=3, T=T, H=3, P=4, raw=raw, fmt=fmt)
+    y = w.decode()
+    w.check(y, w.slots)
+    w.others_untouched(w.slots)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_decays_beyond_one(T):
+    """A positive gate bound (decays up to e^2 a token): against kda_decode_fused from the pool's
+    values."""
+    from gated_delta_rule_scan_gb300 import mixer
+    w = Work(500 + T, N=2, T=T, H=2, P=3)
+    state, ring = w.pool.load(_idx(w.slots))
+    ref = mixer.kda_decode(state_in=state, ring_in=ring, N=2, T=T, H=2, gate_lb=2.0, **w.rows())
+    y = w.decode(gate_lb=2.0)
+    assert rel_linf(y, ref["y"].double().cpu().numpy()) <= TOL
+    got, _ = w.pool.load(_idx(w.slots))
+    want = ref["state_out"].reshape(got.shape)
+    amax = want.abs().amax(-1, keepdim=True)
+    assert ((got - want).abs() <= amax * (1 / 254 + 2.7e-4 * T) * 1.001).all()
+
+
 def test_non_finite_state_stays_in_its_head():
     w = Work(9, N=2, T=1, H=2, P=2)
     clean = w.decode()
