@@ -77,6 +77,7 @@ __device__ __forceinline__ float reduce_columns(const float (&s)[4], int lane) {
 // WIDE: value heads of d.vsub > 1 units, one cluster of vsub CTAs each.
 template <int FMT, int GATE_MODE, int KT, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const DecodeQ8Args p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) float rows_s[];
     __shared__ float beta_s[kDecodeMaxT], ascal[kDecodeMaxT];
     __shared__ float part[3][4][kDecodeMaxT];     // q.q, q.k and k.k of four warps
@@ -403,8 +404,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_decode_q8_kernel(const Decode
 }
 
 // The q and k ring rows of in-place rows whose q/k heads several units read: rolled after every
-// unit has read them.  One thread per channel.
+// unit has read them.  One thread per channel.  Launched as the decode kernel's programmatic dependent.
 __global__ void __launch_bounds__(kThreads) kda_ring_roll_q8_kernel(const DecodeQ8Args p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const DecodeArgs& a = p.d;
     const int n = blockIdx.y, R = a.K - 1;
     int slot_in, slot_out;
@@ -475,8 +477,16 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, cudaStream_t s) {
     if (e != cudaSuccess || a.d.Hk == a.d.H) return e;
     KernelTimer kt(kKRingRollQ8, s);
     const int blocks = (int)((2 * plane_width(a.d.H, a.d.Hk, 0) + kThreads - 1) / kThreads);
-    kda_ring_roll_q8_kernel<<<dim3((unsigned)blocks, (unsigned)a.d.N), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)a.d.N);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_ring_roll_q8_kernel, a);
 }
 
 }  // namespace kda

@@ -135,6 +135,7 @@ struct FewSmem {
 
 template <int FMT, int GATE_MODE, int KT, bool WIDE, int TT>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel(const DecodeQ8Args p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // (the ring roll, if one follows)
     __shared__ __align__(16) FewSmem<TT> sm;
     using S_ = Sums<TT>;
     const DecodeArgs& a = p.d;
