@@ -24,8 +24,8 @@
 // pieces; the same words are the MMA's left side and, unpacked, the state.  Everything a block reads
 // is asked for at once, before its slots have been looked over; codes and output gates wait in shared
 // memory (in registers: 4 blocks an SM and spills, 45 us at one token and 85 at four, 64 x 64 heads).
-// There it runs 41 us at one token, 50 at two and 66 at four, where its bytes need 27 to 32; the other
-// form takes 53, 70 and 100.  What is left is the wait for a block's first bytes, about a third of its
+// There it runs 39.5 us at one token, 48 at two and 62 at four, where its bytes need 27 to 32; the
+// other form takes 53, 70 and 100.  What is left is the wait for a block's first bytes, about a third of its
 // life, overlapped by four other blocks only.  (Persistent blocks that fetch the next unit by bulk
 // copies meanwhile: 62 us; issuing some fifteen small copies a unit takes longer than the wait.)
 #include <cuda_fp16.h>
@@ -40,7 +40,8 @@ constexpr int kThreads = 128;
 constexpr int kVecBytes = 320;               // one f16 vector: 256 bytes, and 64 against bank conflicts
 constexpr int kDotRow = 136;                 // floats: four lanes' columns land in different banks
 constexpr float kVecScale = 4096.0f;
-constexpr int kMinBlocks = 5;                // an SM: 41 us at one token, 64 x 64 heads (4: 44, 6: 42)
+constexpr int kMinBlocks = 5;                // an SM: 39.5 us at one token and 62 at four, 64 x 64 heads
+                                             // (4: 43 and 67, 6: 40 and 71)
 
 // Key i is byte e of word m (0 .. 7) of lane c: i = 64 (m / 4) + 16 c + 4 (m % 4) + e.
 __device__ __forceinline__ int key_word(int i) { return ((i >> 6) << 2) | ((i >> 2) & 3); }
@@ -181,11 +182,12 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
     const long unit_in = ((long)from * H + h) * kHeadDim;
     // [row g, row g + 8][half]: 8 pieces of 16 bytes a row, this lane's at c and 4 + c
     const uint4* cin = reinterpret_cast<const uint4*>(p.codes) + (unit_in + warp * 32 + g) * 8 + c;
-    uint4* code_s = sm.code + (warp * 32 + g) * 8 + c;
+    // (a lane reads what it copied itself, so its pieces lie 32 lanes apart: no bank conflicts)
+    uint4* code_s = sm.code + warp * 256 + lane;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) cp_async_16(code_s + r * 64 + f * 4, cin + r * 64 + f * 4);
+        for (int f = 0; f < 2; ++f) cp_async_16(code_s + (2 * r + f) * 32, cin + r * 64 + f * 4);
     const float scale_l = p.scales[unit_in + tid];
 
     const long ring_len = ring_channels(H, a.Hk) * (K - 1);
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int f = 0; f < 2; ++f) __stcs(cout + r * 64 + f * 4, code_s[r * 64 + f * 4]);
+                for (int f = 0; f < 2; ++f) __stcs(cout + r * 64 + f * 4, code_s[(2 * r + f) * 32]);
             p.scales[unit_out + tid] = scale_l;
             cv.store(ring_out, chv, K);
             if (roll_qk) {
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int f = 0; f < 2; ++f) cur[r][f] = code_s[mt * 128 + r * 64 + f * 4];
+            for (int f = 0; f < 2; ++f) cur[r][f] = code_s[(4 * mt + 2 * r + f) * 32];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
             const uint32_t u[2][4] = {{cur[0][f].x, cur[0][f].y, cur[0][f].z, cur[0][f].w},
@@ -392,13 +394,18 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
             for (int t = 0; t < TT; ++t) wr[r][t] = __shfl_sync(0xffffffffu, w[t], src);
         }
         const float as = GATE_MODE == 0 ? 0.0f : sm.row[TT * kHeadDim];
+        uint4 w4[2];
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
+            if (m % 4 == 0) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) w4[r] = code_s[(4 * mt + 2 * r + m / 4) * 32];
+            }
             const float4* rows = reinterpret_cast<const float4*>(sm.row) + m * 4 + c;
             const float4 a4 = GATE_MODE == 0 ? rows[TT * (kHeadDim / 4)] : make_float4(as, as, as, as);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint32_t word = reinterpret_cast<const uint32_t*>(code_s + mt * 128 + r * 64 + (m >> 2) * 4)[m & 3];
+                const uint32_t word = m % 4 == 0 ? w4[r].x : m % 4 == 1 ? w4[r].y : m % 4 == 2 ? w4[r].z : w4[r].w;
                 const float4 x = q8_decode4<FMT>(word, sr[r]);
                 S[r][2 * m] = __fmul2_rn(make_float2(x.x, x.y), make_float2(a4.x, a4.y));
                 S[r][2 * m + 1] = __fmul2_rn(make_float2(x.z, x.w), make_float2(a4.z, a4.w));
