@@ -23,17 +23,18 @@
 // The form for few rows: t <= 4, or 8 of a bf16 x.  The weights' bytes are read once and bound the
 // launch, so the kernel is built around their stream: a warp takes 16 weight rows x 128 k (1 KB of
 // codes, wide loads straight into registers, the next 1 KB asked for before the present one is used;
-// two ahead: 19.1 us against 17.7), and turns them into mma.sync m16n8k16 operands.  The order of k inside
-// an MMA is free as long as both operands agree, so x is laid out in shared memory once per block in
-// the order in which the nibbles of a word come out, and one 16-byte shared load feeds two MMAs.
+// two ahead: 19.1 us against 17.7), and turns them into mma.sync m16n8k16 operands.  The order of k
+// inside an MMA is free as long as both operands agree, so x is laid out in shared memory once per
+// block in the order in which the nibbles of a word come out, and one 16-byte shared load feeds two
+// MMAs.
 // The 8 columns of the MMA carry hi and lo of 4 tokens, or hi of 8.
 // One block per SM holds x for up to three teams of 8 warps (three blocks staged it three times: 32
-// us against 25 at four rows, before the codes' centring went).  Each team takes tiles of 16 rows in turn; its warps split K, and
-// their partial sums meet in shared memory in warp order.  Where x of all of K does not fit, the
-// CTAs of a cluster split K further and add their sums through distributed shared memory in rank
-// order.  No atomics: results do not depend on timing.  At 64 heads x 6144 and groups of 128: one row
-// 17.7 us (4.5 TB/s of codes and scales; the shared loads, MMAs and logical operations of a chunk
-// cost about as much again as its bytes), four rows 20.4, eight bf16 rows 24.9.
+// us against 25 at four rows, before the codes' centring went).  Each team takes tiles of 16 rows in
+// turn; its warps split K, and their partial sums meet in shared memory in warp order.  Where x of
+// all of K does not fit, the CTAs of a cluster split K further and add their sums through
+// distributed shared memory in rank order.  No atomics: results do not depend on timing.  At 64 heads x 6144 and groups of 128: one row
+// 17.9 us (4.4 TB/s of codes and scales: the shared loads, MMAs and logical operations of a chunk
+// cost about half its bytes' time again), four rows 20.7, eight bf16 rows 25.0.
 #include <cuda_fp16.h>
 
 #include "kda_device.cuh"
@@ -70,7 +71,7 @@ __host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group, int t
     W4Smem m;
     m.x = 0;                                                   // f16 [chunk][4][cols][4][8]
     m.factor = chunks * kChunk * cols * 2;                     // f32 [chunk][8]
-    m.eights = m.factor + chunks * kTok * 4;                   // f32 [group][8]
+    m.eights = m.factor + chunks * kTok * 4;                   // f32 [group][8 columns]
     m.red = m.eights + chunks * (kChunk / group) * kTok * 4;     // f32 [teams][2][warps][8][16]
     m.total = m.red + teams * (2 * kWarps * kTok * kRows * 4);
     return m;
@@ -201,7 +202,7 @@ struct W4Stream {
 
 // Teams of a block, at most: three (four of 64 registers a thread are as fast: 17.7 us at one row x
 // 6144 and 64 heads either way), but two where f32 scales and zero points of 32 k each need more
-// registers (33.8 us against 36.1).
+// registers (34 us against 36 at one row).
 constexpr int w4_teams(int group, bool scale_bf16, bool zero) {
     return group == 32 && !scale_bf16 && zero ? 2 : 3;
 }
@@ -334,8 +335,7 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
             }
             if (g == 0) {
                 float* o = eights + (ch * (kChunk / G) + q) * kTok;
-                if constexpr (ONE) *reinterpret_cast<float2*>(o + 2 * c) = make_float2(d[0], d[1]);
-                else o[c] = d[0] + d[1];
+                *reinterpret_cast<float2*>(o + 2 * c) = make_float2(d[0], d[1]);
             }
         }
     }
@@ -378,12 +378,20 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
                     const float f = factor[ch * kTok + tk];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float s = ONE ? d[2 * r + e] : d[2 * r] + d[2 * r + 1];
-                        float v = s;
-                        if constexpr (!ONE || ZERO) {
-                            const float o = eights[(ch * (kChunk / G) + q) * kTok + tk];
-                            if constexpr (ZERO) v = fmaf((ONE ? 1.0f : 0.0f) - 0.125f * f0.z[r].value(q), o, s);
-                            else v = s - o;
+                        const float* o = eights + (ch * (kChunk / G) + q) * kTok;
+                        float v;
+                        if constexpr (ONE) {
+                            v = d[2 * r + e];
+                            if constexpr (ZERO) v = fmaf(1.0f - 0.125f * f0.z[r].value(q), o[tk], v);
+                        } else {
+                            // hi and lo apart: the difference of the hi sums is exact
+                            const float2 o2 = *reinterpret_cast<const float2*>(o + 2 * c);
+                            if constexpr (ZERO) {
+                                const float z = -0.125f * f0.z[r].value(q);
+                                v = fmaf(z, o2.x, d[2 * r]) + fmaf(z, o2.y, d[2 * r + 1]);
+                            } else {
+                                v = (d[2 * r] - o2.x) + (d[2 * r + 1] - o2.y);
+                            }
                         }
                         acc[r][e] = fmaf(v * f, f0.c[r].value(q), acc[r][e]);
                     }
