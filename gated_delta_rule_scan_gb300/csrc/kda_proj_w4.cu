@@ -17,24 +17,25 @@
 // then loses nothing, and a code needs no more than a logical operation to become a number (taking 8
 // off each code first: 22.8 us against 19.1 at one row x 6144, 64 heads).  hi + lo is x within 2^-23
 // of the element's own magnitude or 2^-27 of the largest of the 128, whichever is more.
-//     5 to 8 rows of a bf16 x take hi alone (8 bits fit, in any order of magnitude), to stay within
-// the MMA's 8 columns.  Its sums are rounded, so there the codes have 8 taken off first.
+//     5 rows or more of a bf16 x take hi alone (8 bits fit, in any order of magnitude), for half the
+// MMA's columns.  Its sums are rounded, so there the codes have 8 taken off first.
 //
-// The form for few rows: t <= 4, or 8 of a bf16 x.  The weights' bytes are read once and bound the
+// The form for few rows: up to 16, by the rule at its launch.  The weights' bytes are read once and bound the
 // launch, so the kernel is built around their stream: a warp takes 16 weight rows x 128 k (1 KB of
 // codes, wide loads straight into registers, the next 1 KB asked for before the present one is used;
 // two ahead: 19.1 us against 17.7), and turns them into mma.sync m16n8k16 operands.  The order of k
 // inside an MMA is free as long as both operands agree, so x is laid out in shared memory once per
 // block in the order in which the nibbles of a word come out, and one 16-byte shared load feeds two
 // MMAs.
-// The 8 columns of the MMA carry hi and lo of 4 tokens, or hi of 8.
+// The MMA's 8 columns carry hi and lo of 4 tokens, or hi of 8; up to four such tiles go over one
+// fetch of the codes.
 // One block per SM holds x for up to three teams of 8 warps (three blocks staged it three times: 32
 // us against 25 at four rows, before the codes' centring went).  Each team takes tiles of 16 rows in
 // turn; its warps split K, and their partial sums meet in shared memory in warp order.  Where x of
 // all of K does not fit, the CTAs of a cluster split K further and add their sums through
 // distributed shared memory in rank order.  No atomics: results do not depend on timing.  At 64 heads x 6144 and groups of 128: one row
 // 17.9 us (4.4 TB/s of codes and scales: the shared loads, MMAs and logical operations of a chunk
-// cost about half its bytes' time again), four rows 20.7, eight bf16 rows 25.0.
+// cost about half its bytes' time again), four rows 20.7, eight bf16 rows 25.0, five f32 rows 28.
 #include <cuda_fp16.h>
 
 #include "kda_device.cuh"
@@ -48,9 +49,11 @@ constexpr int kWarps = 8;                    // warps of a team: they split K of
 constexpr int kTeam = kWarps * 32;
 constexpr int kRows = 16;                    // weight rows of a tile: the MMA's M
 constexpr int kChunk = 128;                  // k of one warp step
-constexpr int kTok = 8;                      // tokens at most: the MMA's N, for a bf16 x
+// Tokens that NT MMA tiles of 8 columns hold.
+template <bool ONE, int NT>
+constexpr int kTok = (ONE ? 8 : 4) * NT;
 constexpr float kMagic = 12582912.0f;        // 1.5 * 2^23
-constexpr int kXSmem = 160 * 1024;           // x of one block at most
+constexpr int kXSmem = 152 * 1024;           // x of one block at most
 
 struct W4Params {
     const void* x;
@@ -67,13 +70,13 @@ struct W4Params {
 struct W4Smem {
     int x, factor, eights, red, total;
 };
-__host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group, int teams) {
+__host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group, int teams, int tok, int nt) {
     W4Smem m;
     m.x = 0;                                                   // f16 [chunk][4][cols][4][8]
-    m.factor = chunks * kChunk * cols * 2;                     // f32 [chunk][8]
-    m.eights = m.factor + chunks * kTok * 4;                   // f32 [group][8 columns]
-    m.red = m.eights + chunks * (kChunk / group) * kTok * 4;     // f32 [teams][2][warps][8][16]
-    m.total = m.red + teams * (2 * kWarps * kTok * kRows * 4);
+    m.factor = chunks * kChunk * cols * 2;                     // f32 [chunk][tok]
+    m.eights = m.factor + chunks * tok * 4;                    // f32 [group][8 nt columns]
+    m.red = m.eights + chunks * (kChunk / group) * 8 * nt * 4; // f32 [teams][2][warps][tok][16]
+    m.total = m.red + teams * (2 * kWarps * tok * kRows * 4);
     return m;
 }
 
@@ -203,8 +206,8 @@ struct W4Stream {
 // Teams of a block, at most: three (four of 64 registers a thread are as fast: 17.7 us at one row x
 // 6144 and 64 heads either way), but two where f32 scales and zero points of 32 k each need more
 // registers (34 us against 36 at one row).
-constexpr int w4_teams(int group, bool scale_bf16, bool zero) {
-    return group == 32 && !scale_bf16 && zero ? 2 : 3;
+constexpr int w4_teams(int group, bool scale_bf16, bool zero, int nt) {
+    return nt == 4 || (group == 32 && !scale_bf16 && zero) ? 2 : 3;
 }
 
 __device__ __forceinline__ void team_sync(int team) {
@@ -213,7 +216,7 @@ __device__ __forceinline__ void team_sync(int team) {
 
 // x of the block's chunks [ch0, ch0 + chunks): MMA operands and power-of-two factors.  A half warp
 // takes one (chunk, token): lane u holds k = 8u .. 8u+7.
-template <int G, bool ONE>
+template <int G, bool ONE, int TOK>
 __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, const W4Smem& lay,
                                         int ch0, int chunks, int nt, int cols) {
     const int half = threadIdx.x >> 4, u = threadIdx.x & 15;
@@ -275,13 +278,14 @@ __device__ __forceinline__ void stage_x(const W4Params& p, unsigned char* smem, 
             xs[base + (2 * tk) * 4] = *reinterpret_cast<const uint4*>(hi);
             xs[base + (2 * tk + 1) * 4] = *reinterpret_cast<const uint4*>(lo);
         }
-        if (u == 0) factor[ch * kTok + tk] = fin ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.0f;
+        if (u == 0) factor[ch * TOK + tk] = fin ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.0f;
     }
 }
 
-template <int G, bool ONE, bool SBF16, bool ZERO>
-__global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_kernel(const __grid_constant__ W4Params p) {
+template <int G, bool ONE, bool SBF16, bool ZERO, int NT>
+__global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO, NT)) kda_proj_w4_kernel(const __grid_constant__ W4Params p) {
     extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int TOK = kTok<ONE, NT>;
     const int team = threadIdx.x / kTeam, teams = blockDim.x / kTeam;
     const int warp = threadIdx.x % kTeam >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -292,11 +296,11 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
     const int all = p.in_f / kChunk;
     const int ch0 = all * rank / p.ksplit, ch1 = all * (rank + 1) / p.ksplit;
     const int chunks = ch1 - ch0;
-    const W4Smem lay = w4_smem((all + p.ksplit - 1) / p.ksplit, cols, G, teams);
+    const W4Smem lay = w4_smem((all + p.ksplit - 1) / p.ksplit, cols, G, teams, TOK, NT);
     const int tiles = p.tile_start[p.nw];
     const float* factor = reinterpret_cast<const float*>(smem + lay.factor);
     float* eights = reinterpret_cast<float*>(smem + lay.eights);
-    float* red = reinterpret_cast<float*>(smem + lay.red) + team * (2 * kWarps * kTok * kRows);
+    float* red = reinterpret_cast<float*>(smem + lay.red) + team * (2 * kWarps * TOK * kRows);
 
     const int w0 = chunks * warp / kWarps, w1 = chunks * (warp + 1) / kWarps;
     const int mine = w1 - w0;
@@ -313,29 +317,36 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
     };
     W4Frag<G, SBF16, ZERO> f0, f1;
     fetch(f0);
-    stage_x<G, ONE>(p, smem, lay, ch0, chunks, nt, cols);
+    stage_x<G, ONE, TOK>(p, smem, lay, ch0, chunks, nt, cols);
     __syncthreads();
 
     // Columns of the MMA past the batch repeat its last one: a column of the result depends on its
     // own column of x alone.
-    const uint4* xs0 = reinterpret_cast<const uint4*>(smem + lay.x) + min(g, cols - 1) * 4 + c;
+    const uint4* xs0 = reinterpret_cast<const uint4*>(smem + lay.x) + c;
+    int col[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) col[i] = min(8 * i + g, cols - 1) * 4;
     // The sums of a group whose codes are all 8, by the very steps that sum the groups below: what
     // a zero point of 8 takes off.  A group that holds nothing but its zero point comes out as 0.
     for (int ch = !ONE || ZERO ? threadIdx.x >> 5 : chunks; ch < chunks; ch += blockDim.x >> 5) {
 #pragma unroll
         for (int q = 0; q < kChunk / G; ++q) {
-            float d[4] = {};
+            float d[NT][4] = {};
 #pragma unroll
             for (int j = q * (G / 32); j < (q + 1) * (G / 32); ++j) {
-                const uint4 b = xs0[(ch * 4 + j) * 4 * cols];
                 const uint32_t lo = ONE ? 0x48004800u : nib_lo<false>(0x88888888u);      // 8 in f16
                 const uint32_t hi = ONE ? 0x48004800u : nib_hi<false>(0x88888888u);
-                mma_16816(d, lo, lo, hi, hi, b.x, b.y);
-                mma_16816(d, lo, lo, hi, hi, b.z, b.w);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const uint4 b = xs0[(ch * 4 + j) * 4 * cols + col[i]];
+                    mma_16816(d[i], lo, lo, hi, hi, b.x, b.y);
+                    mma_16816(d[i], lo, lo, hi, hi, b.z, b.w);
+                }
             }
             if (g == 0) {
-                float* o = eights + (ch * (kChunk / G) + q) * kTok;
-                *reinterpret_cast<float2*>(o + 2 * c) = make_float2(d[0], d[1]);
+                float* o = eights + (ch * (kChunk / G) + q) * (8 * NT) + 2 * c;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) *reinterpret_cast<float2*>(o + 8 * i) = make_float2(d[i][0], d[i][1]);
             }
         }
     }
@@ -343,8 +354,8 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
     int buf = 0;
     // All teams of a cluster go through the same number of tiles, the last one past the end maybe.
     for (int tile = first; tile - team * blocks < tiles; tile += stride, buf ^= 1) {
-        // acc[r][e]: token c of row g + 8 r (e = 0), ONE: token 2 c + e
-        float acc[2][2] = {};
+        // acc[i][r][e]: token 4 i + c of row g + 8 r (e = 0), ONE: token 8 i + 2 c + e
+        float acc[NT][2][2] = {};
         const uint4* xs = xs0 + w0 * 16 * cols;
         for (int ch = tile < tiles ? w0 : w1; ch < w1; ++ch, xs += 16 * cols) {
             fetch(f1);
@@ -364,48 +375,59 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
             }
 #pragma unroll
             for (int q = 0; q < kChunk / G; ++q) {
-                float d[4] = {};
+                float d[NT][4] = {};
 #pragma unroll
                 for (int j = q * (G / 32); j < (q + 1) * (G / 32); ++j) {
                     const uint32_t u0 = f0.w[0][j], u1 = f0.w[1][j];
-                    const uint4 b = xs[j * 4 * cols];
-                    mma_16816(d, nib_lo<ONE>(u0), nib_lo<ONE>(u1), nib_hi<ONE>(u0), nib_hi<ONE>(u1), b.x, b.y);
-                    mma_16816(d, nib_lo<ONE>(u0 >> 8), nib_lo<ONE>(u1 >> 8), nib_hi<ONE>(u0 >> 8), nib_hi<ONE>(u1 >> 8), b.z, b.w);
+                    const uint32_t a0 = nib_lo<ONE>(u0), a1 = nib_lo<ONE>(u1), a2 = nib_hi<ONE>(u0), a3 = nib_hi<ONE>(u1);
+                    const uint32_t a4 = nib_lo<ONE>(u0 >> 8), a5 = nib_lo<ONE>(u1 >> 8);
+                    const uint32_t a6 = nib_hi<ONE>(u0 >> 8), a7 = nib_hi<ONE>(u1 >> 8);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 b = xs[j * 4 * cols + col[i]];
+                        mma_16816(d[i], a0, a1, a2, a3, b.x, b.y);
+                        mma_16816(d[i], a4, a5, a6, a7, b.z, b.w);
+                    }
                 }
+                const float* o = eights + (ch * (kChunk / G) + q) * (8 * NT) + 2 * c;
 #pragma unroll
-                for (int e = 0; e < (ONE ? 2 : 1); ++e) {
-                    const int tk = ONE ? 2 * c + e : c;
-                    const float f = factor[ch * kTok + tk];
+                for (int i = 0; i < NT; ++i) {
+                    float2 o2 = make_float2(0.0f, 0.0f);
+                    if constexpr (!ONE || ZERO) o2 = *reinterpret_cast<const float2*>(o + 8 * i);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float* o = eights + (ch * (kChunk / G) + q) * kTok;
-                        float v;
-                        if constexpr (ONE) {
-                            v = d[2 * r + e];
-                            if constexpr (ZERO) v = fmaf(1.0f - 0.125f * f0.z[r].value(q), o[tk], v);
-                        } else {
-                            // hi and lo apart: the difference of the hi sums is exact
-                            const float2 o2 = *reinterpret_cast<const float2*>(o + 2 * c);
-                            if constexpr (ZERO) {
+                    for (int e = 0; e < (ONE ? 2 : 1); ++e) {
+                        const float f = factor[ch * TOK + (ONE ? 8 * i + 2 * c + e : 4 * i + c)];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float v;
+                            if constexpr (ONE) {
+                                v = d[i][2 * r + e];
+                                if constexpr (ZERO)
+                                    v = fmaf(1.0f - 0.125f * f0.z[r].value(q), e ? o2.y : o2.x, v);
+                            } else if constexpr (ZERO) {
+                                // hi and lo apart: the difference of the hi sums is exact
                                 const float z = -0.125f * f0.z[r].value(q);
-                                v = fmaf(z, o2.x, d[2 * r]) + fmaf(z, o2.y, d[2 * r + 1]);
+                                v = fmaf(z, o2.x, d[i][2 * r]) + fmaf(z, o2.y, d[i][2 * r + 1]);
                             } else {
-                                v = (d[2 * r] - o2.x) + (d[2 * r + 1] - o2.y);
+                                v = (d[i][2 * r] - o2.x) + (d[i][2 * r + 1] - o2.y);
                             }
+                            acc[i][r][e] = fmaf(v * f, f0.c[r].value(q), acc[i][r][e]);
                         }
-                        acc[r][e] = fmaf(v * f, f0.c[r].value(q), acc[r][e]);
                     }
                 }
             }
             f0 = f1;
         }
         // this tile's sums of all warps, in warp order
-        float* rb = red + buf * (kWarps * kTok * kRows);
+        float* rb = red + buf * (kWarps * TOK * kRows);
 #pragma unroll
-        for (int e = 0; e < (ONE ? 2 : 1); ++e)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                rb[(warp * kTok + (ONE ? 2 * c + e : c)) * kRows + g + 8 * r] = ONE ? acc[r][e] : acc[r][e] * 16777216.0f;
+            for (int e = 0; e < (ONE ? 2 : 1); ++e)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    rb[(warp * TOK + (ONE ? 8 * i + 2 * c + e : 4 * i + c)) * kRows + g + 8 * r] =
+                        ONE ? acc[i][r][e] : acc[i][r][e] * 16777216.0f;
         team_sync(team);
         int wi = 0;
         while (wi + 1 < p.nw && tile >= p.tile_start[wi + 1]) ++wi;
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
         float sum = 0.0f;
         if (tk < nt) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += rb[(w * kTok + tk) * kRows + r];
+            for (int w = 0; w < kWarps; ++w) sum += rb[(w * TOK + tk) * kRows + r];
         }
         if (p.ksplit > 1) {
             // the cluster's CTAs: each leaves its sums where warp 0's were, then rank 0 adds them.
@@ -434,13 +456,13 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO)) kda_proj_w4_
     if (p.ksplit > 1) cluster_sync_all();        // rank 0 has read the last tile's sums
 }
 
-template <int G, bool ONE, bool SBF16, bool ZERO>
+template <int G, bool ONE, bool SBF16, bool ZERO, int NT>
 cudaError_t launch_rows(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
     static PerDevice<int> smem_set_for;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const auto kernel = kda_proj_w4_kernel<G, ONE, SBF16, ZERO>;
+    const auto kernel = kda_proj_w4_kernel<G, ONE, SBF16, ZERO, NT>;
     const bool cached = dev >= 0 && dev < kMaxDevices;
     if (smem > 48 * 1024 && (!cached || smem_set_for[dev].load(std::memory_order_acquire) < (int)smem)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -468,29 +490,40 @@ cudaError_t launch_rows(const W4Params& p, int grid, int teams, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int G, bool ONE>
+template <int G, bool ONE, int NT>
 cudaError_t launch_params(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
     if (p.has_zero)
-        return p.scale_bf16 ? launch_rows<G, ONE, true, true>(p, grid, teams, smem, s)
-                            : launch_rows<G, ONE, false, true>(p, grid, teams, smem, s);
-    return p.scale_bf16 ? launch_rows<G, ONE, true, false>(p, grid, teams, smem, s)
-                        : launch_rows<G, ONE, false, false>(p, grid, teams, smem, s);
+        return p.scale_bf16 ? launch_rows<G, ONE, true, true, NT>(p, grid, teams, smem, s)
+                            : launch_rows<G, ONE, false, true, NT>(p, grid, teams, smem, s);
+    return p.scale_bf16 ? launch_rows<G, ONE, true, false, NT>(p, grid, teams, smem, s)
+                        : launch_rows<G, ONE, false, false, NT>(p, grid, teams, smem, s);
 }
 
 template <int G>
-cudaError_t launch_group(const W4Params& p, bool one, int grid, int teams, size_t smem, cudaStream_t s) {
-    return one ? launch_params<G, true>(p, grid, teams, smem, s) : launch_params<G, false>(p, grid, teams, smem, s);
+cudaError_t launch_group(const W4Params& p, bool one, int nt, int grid, int teams, size_t smem, cudaStream_t s) {
+    if (one)
+        return nt == 1 ? launch_params<G, true, 1>(p, grid, teams, smem, s)
+                       : launch_params<G, true, 2>(p, grid, teams, smem, s);
+    return nt == 1   ? launch_params<G, false, 1>(p, grid, teams, smem, s)
+           : nt == 2 ? launch_params<G, false, 2>(p, grid, teams, smem, s)
+                     : launch_params<G, false, 4>(p, grid, teams, smem, s);
 }
 
 }  // namespace
 
 size_t proj_w4_workspace_bytes(int t, int in_f) {
-    // (a bf16 x takes the form for few rows up to 8, an f32 x, in two parts, up to 4)
-    return t > kTok / 2 ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
+    // (more than a call of up to 16 rows needs whose weights are few)
+    return t > 4 ? proj_w4_wide_workspace_bytes(t, in_f) : 0;
 }
 
 cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
-    if (a.t > (a.x_bf16 ? kTok : kTok / 2)) return launch_proj_w4_wide(a, s);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const bool one = a.x_bf16 && a.t > 4;
+    const int cols = one ? a.t : 2 * a.t, nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+    const int all = a.in_f / kChunk;
     W4Params p{};
     p.x = a.x;
     int tiles = 0;
@@ -505,26 +538,29 @@ cudaError_t launch_proj_w4(const ProjW4Args& a, cudaStream_t s) {
     }
     p.tile_start[a.nw] = tiles;
     if (tiles == 0) return cudaSuccess;
-    p.nw = a.nw; p.t = a.t; p.in_f = a.in_f; p.x_bf16 = a.x_bf16; p.scale_bf16 = a.scale_bf16; p.has_zero = a.has_zero;
     // the fewest CTAs along K whose share of x fits
-    const bool one = a.t > kTok / 2;
-    const int cols = one ? a.t : 2 * a.t;
-    const int all = a.in_f / kChunk;
     int ks = 1;
     while (ks < 8 && (all + ks - 1) / ks * (kChunk * cols * 2) > kXSmem) ks *= 2;
+    // This form or the one for batches.  With one MMA tile of columns this one is faster at any size
+    // (64 heads x 6144: 25 us against 34 at eight bf16 rows).  With two, while x of all of K fits into
+    // one block (28 against 34 us at five f32 rows; cut along K: 35 at eight, 40 at sixteen bf16
+    // rows); with two or four, while the weights are few, where its single launch tells: 128 chunks of
+    // 1 KB an SM (16 heads x 2176: 8 against 14 us at eight f32 rows), or 64 of them (13 against 14 at
+    // 13 rows; 32 heads x 2048, 83 chunks an SM: 14 - 16 against 14.5).
+    const long work = (long)tiles * all;
+    const bool few = nt == 1 || (nt == 2 && ks == 1) || work <= (long)sms * (nt == 4 ? 64 : 128);
+    if (a.t > 16 || !few || (all + ks - 1) / ks * (kChunk * cols * 2) > kXSmem)
+        return launch_proj_w4_wide(a, s);
+    p.nw = a.nw; p.t = a.t; p.in_f = a.in_f; p.x_bf16 = a.x_bf16; p.scale_bf16 = a.scale_bf16; p.has_zero = a.has_zero;
     p.ksplit = ks;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
     const int blocks = tiles < sms / ks ? tiles : (sms / ks < 1 ? 1 : sms / ks);
-    const int most = w4_teams(a.group, a.scale_bf16 != 0, a.has_zero != 0);
+    const int most = w4_teams(a.group, a.scale_bf16 != 0, a.has_zero != 0, nt);
     const int want = (tiles + blocks - 1) / blocks, teams = want < most ? want : most;
-    const W4Smem lay = w4_smem((all + ks - 1) / ks, cols, a.group, teams);
+    const W4Smem lay = w4_smem((all + ks - 1) / ks, cols, a.group, teams, one ? 8 * nt : 4 * nt, nt);
     switch (a.group) {
-        case 32: return launch_group<32>(p, one, blocks * ks, teams, (size_t)lay.total, s);
-        case 64: return launch_group<64>(p, one, blocks * ks, teams, (size_t)lay.total, s);
-        default: return launch_group<128>(p, one, blocks * ks, teams, (size_t)lay.total, s);
+        case 32: return launch_group<32>(p, one, nt, blocks * ks, teams, (size_t)lay.total, s);
+        case 64: return launch_group<64>(p, one, nt, blocks * ks, teams, (size_t)lay.total, s);
+        default: return launch_group<128>(p, one, nt, blocks * ks, teams, (size_t)lay.total, s);
     }
 }
 

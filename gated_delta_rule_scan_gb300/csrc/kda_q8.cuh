@@ -8,7 +8,8 @@
 // (ties to even) for int8, and M = 448 (the largest finite e4m3 value) and codes rounded to the
 // nearest e4m3 value for e4m3.  Both quotients are IEEE divisions in f32 and the products are
 // single f32 roundings, so the codes of a row are one exact function of its f32 values, on the
-// device or anywhere else.  An int8 code is off by at most half a step, amax / 254 for every
+// device or anywhere else.  (A decode step, whose new state nobody else sees, rounds an int8 code
+// once, from the exact product.)  An int8 code is off by at most half a step, amax / 254 for every
 // element of the row; an e4m3 code by at most 2^-4 of the element (and amax * 2^-10 / 448 below
 // the normal range): int8 is the finer one for rows without outliers.
 // A row with amax below 2^-100 (where M / amax would leave the normal range) is stored as zeros

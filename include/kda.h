@@ -649,8 +649,8 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
  * workspace    device scratch [16B] of at least kda_proj_w4_workspace_bytes(t, in_f) bytes, which
  *              may be 0 (then NULL is accepted); 40009 otherwise.  Calls sharing it must not overlap.
  * Precision: codes, scales and zero points enter exactly; x enters within 2^-22 of an element's
- * magnitude plus 2^-25 of the largest of its 128 k (t <= 4) or 2^-31 of its row's largest (more
- * rows); sums are f32.  One token row's result depends on the other rows of the call only
+ * magnitude plus 2^-25 of the largest of its 128 k (forms for few rows) or 2^-31 of its row's largest
+ * (batches); sums are f32.  One token row's result depends on the other rows of the call only
  * through the choice of form for t rows.  A NaN or an infinity in x makes every output of its token
  * row NaN or infinite, and no other row's.
  */

@@ -98,10 +98,26 @@ def test_large_batches(t, in_f, rows, group, x, zeros):
 
 
 @pytest.mark.parametrize("t,in_f,x", [(1, 32768, "f32"), (8, 16384, "f32"), (8, 20480, "bf16"),
-                                      (5, 9984, "f32"), (20, 16384, "f32")])
+                                      (5, 9984, "f32"), (20, 16384, "f32"), (16, 8192, "f32"),
+                                      (11, 3968, "f32"), (16, 32768, "bf16"), (9, 32768, "f32")])
 def test_wide_inputs(t, in_f, x):
     """x wider than one block's shared memory holds, with uneven shares of K."""
     c = _case(in_f + t, t, in_f, (40, 3), 128, x, "bf16", True)
+    _check(c, _gpu(c))
+
+
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [6, 9, 12, 15, 16])
+def test_up_to_sixteen_rows(t, x, group, zeros):
+    c = _case(t * 7 + group, t, 640, (200, 1, 16, 33), group, x, "f32" if group == 64 else "bf16", zeros)
+    _check(c, _gpu(c))
+
+
+@pytest.mark.parametrize("t,rows,x", [(13, 4096, "f32"), (9, 4112, "f32"), (16, 8192, "bf16")])
+def test_few_rows_of_large_weights(t, rows, x):
+    """Rows past which the form for batches is taken at this size."""
+    c = _case(70 + t, t, 5120, (rows,), 128, x)
     _check(c, _gpu(c))
 
 
