@@ -33,9 +33,10 @@
 // us against 25 at four rows, before the codes' centring went).  Each team takes tiles of 16 rows in
 // turn; its warps split K, and their partial sums meet in shared memory in warp order.  Where x of
 // all of K does not fit, the CTAs of a cluster split K further and add their sums through
-// distributed shared memory in rank order.  No atomics: results do not depend on timing.  At 64 heads x 6144 and groups of 128: one row
-// 17.9 us (4.4 TB/s of codes and scales: the shared loads, MMAs and logical operations of a chunk
-// cost about half its bytes' time again), four rows 20.7, eight bf16 rows 25.0, five f32 rows 28.
+// distributed shared memory in rank order.  No atomics: results do not depend on timing.
+// At 64 heads x 6144 and groups of 128: one row 17.9 us (4.4 TB/s of codes and scales: the shared
+// loads, MMAs and logical operations of a chunk cost about half its bytes' time again), four rows
+// 20.7, eight bf16 rows 25.0, five f32 rows 28.
 #include <cuda_fp16.h>
 
 #include "kda_device.cuh"

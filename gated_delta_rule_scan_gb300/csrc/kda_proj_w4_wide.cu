@@ -27,6 +27,8 @@
 // cut between blocks.  Its parts meet in the workspace, added in block order whoever adds them, so
 // results do not depend on timing: usually the block that holds a tile's first units ends last,
 // finds the other parts there, and adds them to its registers.
+// At 64 heads x 6144 with groups of 128: 16 rows 34 us, 64 rows 45.5 (the tensor pipe active 41 % of
+// the time), 256 rows 116 (60 %).
 #include <cuda_fp16.h>
 
 #include "kda_chunk_common.cuh"
