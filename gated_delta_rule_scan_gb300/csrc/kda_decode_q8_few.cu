@@ -24,7 +24,7 @@
 // pieces; the same words are the MMA's left side and, unpacked, the state.  Everything a block reads
 // is asked for at once, before its slots have been looked over; codes and output gates wait in shared
 // memory (in registers: 4 blocks an SM and spills, 45 us at one token and 85 at four, 64 x 64 heads).
-// There it runs 39.5 us at one token, 48 at two and 62 at four, where its bytes need 27 to 32; the
+// There it runs 39.5 us at one token, 48 at two, 57 at three and 62 at four, where its bytes need 27 to 32; the
 // other form takes 53, 70 and 100.  What is left is the wait for a block's first bytes, about a third of its
 // life, overlapped by four other blocks only.  (Persistent blocks that fetch the next unit by bulk
 // copies meanwhile: 62 us; issuing some fifteen small copies a unit takes longer than the wait.)
@@ -116,7 +116,7 @@ __device__ __forceinline__ float raw_value(uint32_t x, bool bf16) { return __uin
 template <int TT>
 struct Sums {
     static constexpr int kk = TT, kt = 2 * TT, qt = kt + TT * (TT - 1) / 2, n = qt + TT * (TT + 1) / 2;
-    static constexpr int padded = n <= 4 ? 4 : n <= 8 ? 8 : 32;
+    static constexpr int padded = n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32;
     static constexpr int lanes = 32 / padded;
     __host__ __device__ static constexpr int kk_at(int s, int t) { return kt + t * (t - 1) / 2 + s; }
     __host__ __device__ static constexpr int qk_at(int s, int t) { return qt + t * (t + 1) / 2 + s; }
@@ -507,7 +507,8 @@ cudaError_t launch_t(const DecodeQ8Args& a, cudaStream_t s) {
 template <int FMT, int GM>
 cudaError_t launch_gm(const DecodeQ8Args& a, cudaStream_t s) {
     if (a.d.T == 1) return launch_t<FMT, GM, 1>(a, s);
-    return a.d.T == 2 ? launch_t<FMT, GM, 2>(a, s) : launch_t<FMT, GM, 4>(a, s);
+    if (a.d.T == 2) return launch_t<FMT, GM, 2>(a, s);
+    return a.d.T == 3 ? launch_t<FMT, GM, 3>(a, s) : launch_t<FMT, GM, 4>(a, s);
 }
 
 }  // namespace
