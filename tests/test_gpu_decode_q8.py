@@ -336,6 +336,69 @@ def test_graph_replay_and_other_stream():
     assert torch.equal(y, eager[0])
 
 
+@pytest.mark.parametrize("T", [1, 3, 4])
+def test_non_finite_samples_stay_in_their_heads(T):
+    """A NaN in a token's k and an infinity in another row's v reach their own heads' rows only."""
+    w = Work(13, N=3, T=T, H=3, P=3, raw="f32")
+    clean = w.decode()
+    after = w.pool.scales.clone()
+    w.reset()
+    w.inp.k_raw[0 * T, 128 + 7] = float("nan")            # row 0, head 1
+    w.inp.v_raw[2 * T, 256 + 9] = float("inf")            # row 2, head 2
+    y = w.decode()
+    hit = torch.zeros(3, 3, dtype=torch.bool)
+    hit[0, 1] = hit[2, 2] = True
+    for n in range(3):
+        for h in range(3):
+            a = y[n * T:(n + 1) * T, h * D:(h + 1) * D]
+            b = clean[n * T:(n + 1) * T, h * D:(h + 1) * D]
+            if hit[n, h]:
+                assert not torch.isfinite(a[0]).all()
+            else:
+                assert torch.equal(a, b)
+                assert torch.equal(w.pool.scales[w.slots[n], h], after[w.slots[n], h])
+    assert torch.isnan(w.pool.scales[w.slots[0], 1]).all()
+    assert torch.isnan(w.pool.scales[w.slots[2], 2, 9])
+
+
+def test_calls_at_once_on_two_streams():
+    """Decode steps of two pools and projections of two sizes, on two streams at the same time."""
+    from gated_delta_rule_scan_gb300 import kda, mixer
+    jobs = []
+    for i, (T, t) in enumerate([(1, 3), (3, 24)]):
+        w = Work(600 + i, N=8, T=T, H=16, P=8, Hk=4, gdn=bool(i))
+        g = torch.Generator().manual_seed(i)
+        w4 = torch.randint(0, 256, (700, 1024), generator=g, dtype=torch.uint8).cuda()
+        sc = torch.rand(700, 2048 // 64, generator=g).cuda()
+        x = torch.randn(t, 2048, generator=g).cuda()
+        jobs.append(dict(w=w, d=w.rows(), slots=_idx(w.slots), w4=w4, sc=sc, x=x,
+                         y=torch.zeros(8 * T, w.inp.C, device="cuda"),
+                         out=torch.zeros(t, 700, device="cuda"),
+                         ws=kda.proj_w4_workspace(t, 2048, "cuda"), s=torch.cuda.Stream()))
+
+    def step(j, stream):
+        w = j["w"]
+        w.pool.decode(slots=j["slots"], T=w.T, y=j["y"], gate_mode=int(w.gdn), stream=stream, **j["d"])
+        kda.kda_proj_w4(j["x"], [j["w4"]], [j["sc"]], [j["out"]], group=64, workspace=j["ws"],
+                        stream=stream)
+    want = []
+    for j in jobs:
+        for _ in range(6):
+            step(j, None)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (j["y"], j["out"], j["w"].pool.codes.view(torch.uint8),
+                                         j["w"].pool.ring)])
+        j["w"].reset()
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for j in jobs:
+            step(j, j["s"])
+    torch.cuda.synchronize()
+    for j, f in zip(jobs, want):
+        for a, b in zip((j["y"], j["out"], j["w"].pool.codes.view(torch.uint8), j["w"].pool.ring), f):
+            assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     """A slot whose code offset passes 2^32."""
     H, P = 64, 4100
