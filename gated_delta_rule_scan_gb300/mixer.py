@@ -6,6 +6,8 @@ value is computed by the library's kernels.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import kda
@@ -19,6 +21,31 @@ def _norm_flag(norm_gate):
 
 def _empty(shape, like):
     return torch.empty(shape, dtype=torch.float32, device=like.device)
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """Where a call makes its own buffers: on the stream that it runs on (None: the current one).
+    Made elsewhere, a fill could land after the kernels' results, and a workspace dropped on return
+    be handed out again while they still run."""
+    if stream is None:
+        return _CURRENT
+    if isinstance(stream, int):
+        # (ExternalStream takes a handle of 0 for none given and opens a stream of its own)
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors):
+    """Results made on `stream` go to the caller, whose work on the current stream their memory
+    outlives: it is not handed out again before that work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t.is_cuda:
+                t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def kda_forward(*, q_raw, k_raw, v_raw, f_raw, dt_bias, a_log, beta_raw, state_in, H,
@@ -203,12 +230,16 @@ def kda_proj_w4(*, x, weights, scales, group, zeros=None, outs=None, workspace=N
     """Projections of x [t, in_f] by 4-bit weights with group scales (lists, one entry a weight; the
     layer's six in kda_proj6's order, or any others that read x).  Returns the list of outputs."""
     t, in_f = x.shape
-    if outs is None:
-        outs = [_empty((t, w.shape[0]), x) for w in weights]
-    if workspace is None:
-        workspace = kda.proj_w4_workspace(t, in_f, x.device)
+    made = outs is None
+    with _on(stream, x.device):
+        if made:
+            outs = [_empty((t, w.shape[0]), x) for w in weights]
+        if workspace is None:
+            workspace = kda.proj_w4_workspace(t, in_f, x.device)
     kda.kda_proj_w4(x, weights, scales, outs, group=group, zeros=zeros, workspace=workspace,
                     stream=stream)
+    if made:
+        _hand_over(stream, *outs)
     return outs
 
 
@@ -240,13 +271,17 @@ class StatePoolQ8:
 
     def load(self, slots, state=None, ring=None, rows=None, stream=None):
         """slots[n] into rows `rows` (None: n) of state and ring; returns both."""
-        n = slots.numel()
-        if state is None:
-            state = torch.zeros(n, self.H, self.Dv, kda.HEAD_DIM, device=self.codes.device)
-        if ring is None:
-            ring = torch.zeros(state.shape[0], *self.ring.shape[1:], device=self.codes.device)
+        n, made = slots.numel(), []
+        with _on(stream, self.codes.device):
+            if state is None:
+                state = torch.zeros(n, self.H, self.Dv, kda.HEAD_DIM, device=self.codes.device)
+                made.append(state)
+            if ring is None:
+                ring = torch.zeros(state.shape[0], *self.ring.shape[1:], device=self.codes.device)
+                made.append(ring)
         kda.kda_state_load_q8(self.codes, self.scales, state, src=slots, dst=rows, N=n, H=self.H,
                               Dv=self.Dv, ring_pool=self.ring, ring=ring, stream=stream)
+        _hand_over(stream, *made)
         return state, ring
 
     def decode(self, *, q_raw, k_raw, v_raw, conv_w, f_raw, dt_bias, a_log, beta_raw, norm_w,
@@ -256,15 +291,18 @@ class StatePoolQ8:
         (None: in place).  With keep (int32 [N]) only the first keep[n] tokens are taken: the
         rollback of a verify that ran into other slots.  Returns y (zero in rows not computed when
         it is allocated here)."""
-        N = slots.numel()
-        if y is None:
-            y = torch.zeros(N * T, self.H * self.Dv, device=self.codes.device)
+        N, made = slots.numel(), y is None
+        if made:
+            with _on(stream, self.codes.device):
+                y = torch.zeros(N * T, self.H * self.Dv, device=self.codes.device)
         kda.kda_decode_fused_q8(q_raw, k_raw, v_raw, conv_w, self.ring, f_raw, dt_bias, a_log,
                                 beta_raw, self.codes, self.scales, norm_w, gate_raw, y, N=N, T=T,
                                 H=self.H, slots=slots, slots_out=slots_out, keep=keep, K=self.K,
                                 gate_mode=gate_mode | _norm_flag(norm_gate), gate_lb=gate_lb,
                                 l2_eps=l2_eps, scale=scale, rms_eps=rms_eps, stream=stream,
                                 Hk=self.Hk, Dv=self.Dv)
+        if made:
+            _hand_over(stream, y)
         return y
 
 
