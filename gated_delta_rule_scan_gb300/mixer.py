@@ -23,6 +23,11 @@ def _empty(shape, like):
     return torch.empty(shape, dtype=torch.float32, device=like.device)
 
 
+def _made(made, t):
+    made.append(t)
+    return t
+
+
 _CURRENT = contextlib.nullcontext()
 
 
@@ -78,23 +83,25 @@ def kda_forward(*, q_raw, k_raw, v_raw, f_raw, dt_bias, a_log, beta_raw, state_i
     if not varlen:
         assert N is not None and T is not None and N * T == rows
     n_seq = (cu_seqlens_host.numel() - 1) if varlen else N
-    buf = out if out is not None else {}
+    buf, made = out if out is not None else {}, []
 
     def take(name, shape):
         t = buf.get(name)
-        return t if t is not None else _empty(shape, q_raw)
-    q_hat = take("q_hat", (rows, Cq))
-    k_hat = take("k_hat", (rows, Cq))
-    v_hat = take("v_hat", (rows, C))
-    g = take("g", (rows, Cg) if gate_mode == 0 else (rows, H))
-    beta = take("beta", (rows, H))
-    o = take("o", (rows, C))
-    if state_out is None:
-        state_out = torch.empty_like(state_in)
-    if conv_w is not None and ring_out is None:
-        ring_out = torch.empty_like(ring_in)
-    if workspace is None and algo != kda.ALGO_SEQ:
-        workspace = kda.scan_workspace(n_seq, rows, H * Dv // D, q_raw.device, algo)
+        return t if t is not None else _made(made, _empty(shape, q_raw))
+    with _on(stream, q_raw.device):
+        q_hat = take("q_hat", (rows, Cq))
+        k_hat = take("k_hat", (rows, Cq))
+        v_hat = take("v_hat", (rows, C))
+        g = take("g", (rows, Cg) if gate_mode == 0 else (rows, H))
+        beta = take("beta", (rows, H))
+        o = take("o", (rows, C))
+        y = take("y", (rows, C)) if norm_w is not None else None
+        if state_out is None:
+            state_out = _made(made, torch.empty_like(state_in))
+        if conv_w is not None and ring_out is None:
+            ring_out = _made(made, torch.empty_like(ring_in))
+        if workspace is None and algo != kda.ALGO_SEQ:
+            workspace = kda.scan_workspace(n_seq, rows, H * Dv // D, q_raw.device, algo)
     if gate_exp is None:
         gate_exp = algo == kda.ALGO_SEQ
     gm = gate_mode | (kda.GATE_EXP if gate_exp else 0)
@@ -135,12 +142,11 @@ def kda_forward(*, q_raw, k_raw, v_raw, f_raw, dt_bias, a_log, beta_raw, state_i
             kda.kda_scan(*scan_args, N=N, T=T, **scan_kw)
         else:
             kda.kda_scan_gqa(*scan_args, N=N, T=T, Hk=Hk, **scan_kw)
-    y = None
     if norm_w is not None:
-        y = take("y", (rows, C))
         _norm_flag(norm_gate)
         norm = kda.kda_gated_rmsnorm_silu_out if norm_gate == "silu" else kda.kda_gated_rmsnorm_out
         norm(o, norm_w, gate_raw, y, rows=rows * H, eps=rms_eps, D=Dv, stream=stream)
+    _hand_over(stream, *made)
     return dict(q_hat=q_hat, k_hat=k_hat, v_hat=v_hat, g=g, beta=beta, o=o, y=y,
                 state_out=state_out, ring_out=ring_out, n_seq=n_seq)
 
@@ -164,14 +170,16 @@ def kda_prefill(*, q_raw, k_raw, v_raw, f_raw, dt_bias, a_log, beta_raw, state_i
     if not varlen:
         assert N is not None and T is not None and N * T == rows
     n_seq = (cu_seqlens_host.numel() - 1) if varlen else N
-    if y is None:
-        y = _empty((rows, C), q_raw)
-    if state_out is None:
-        state_out = torch.empty_like(state_in)
-    if ring_out is None and conv_w is not None:
-        ring_out = torch.empty_like(ring_in)
-    if workspace is None:
-        workspace = kda.prefill_workspace(n_seq, rows, units, q_raw.device, gate_mode)
+    made = []
+    with _on(stream, q_raw.device):
+        if y is None:
+            y = _made(made, _empty((rows, C), q_raw))
+        if state_out is None:
+            state_out = _made(made, torch.empty_like(state_in))
+        if ring_out is None and conv_w is not None:
+            ring_out = _made(made, torch.empty_like(ring_in))
+        if workspace is None:
+            workspace = kda.prefill_workspace(n_seq, rows, units, q_raw.device, gate_mode)
     args = (q_raw, k_raw, v_raw, conv_w, ring_in, ring_out, f_raw, dt_bias, a_log, beta_raw,
             state_in, state_out, norm_w, gate_raw, y, workspace)
     common = dict(H=H, K=K, gate_mode=gate_mode | _norm_flag(norm_gate), gate_lb=gate_lb,
@@ -180,6 +188,7 @@ def kda_prefill(*, q_raw, k_raw, v_raw, f_raw, dt_bias, a_log, beta_raw, state_i
         kda.kda_prefill_fused_varlen(*args, cu_seqlens, cu_seqlens_host, **common)
     else:
         kda.kda_prefill_fused(*args, N=N, T=T, **common)
+    _hand_over(stream, *made)
     return dict(y=y, state_out=state_out, ring_out=ring_out, n_seq=n_seq)
 
 
@@ -190,17 +199,20 @@ def kda_decode(*, q_raw, k_raw, v_raw, conv_w, ring_in, f_raw, dt_bias, a_log, b
     """One fused decode (T=1) or T-token verify launch.  ring_out may be ring_in and state_out
     state_in (in place).  norm_gate: "sigmoid" (KDA) or "silu" (GDN's gated_rmsnorm).
     Dv: value heads Dv wide (kda_decode_fused_dv)."""
-    if state_out is None:
-        state_out = torch.empty_like(state_in)
-    if ring_out is None:
-        ring_out = torch.empty_like(ring_in)
-    if y is None:
-        y = _empty((q_raw.shape[0], H * (kda.HEAD_DIM if Dv is None else Dv)), q_raw)
+    made = []
+    with _on(stream, q_raw.device):
+        if state_out is None:
+            state_out = _made(made, torch.empty_like(state_in))
+        if ring_out is None:
+            ring_out = _made(made, torch.empty_like(ring_in))
+        if y is None:
+            y = _made(made, _empty((q_raw.shape[0], H * (kda.HEAD_DIM if Dv is None else Dv)), q_raw))
     kda.kda_decode_fused(q_raw, k_raw, v_raw, conv_w, ring_in, ring_out, f_raw, dt_bias, a_log,
                          beta_raw, state_in, state_out, norm_w, gate_raw, y, N=N, T=T, H=H, K=K,
                          gate_mode=gate_mode | _norm_flag(norm_gate), gate_lb=gate_lb,
                          l2_eps=l2_eps, scale=scale,
                          rms_eps=rms_eps, stream=stream, Hk=Hk, Dv=Dv)
+    _hand_over(stream, *made)
     return dict(y=y, state_out=state_out, ring_out=ring_out)
 
 
@@ -211,18 +223,21 @@ def kda_verify_rollback(*, q_raw, k_raw, v_raw, conv_w, ring_in, f_raw, dt_bias,
                         Dv=None):
     """Roll a T-token verify round back to the accepted prefixes: keep (int32 device [N]) tokens
     of each sequence, from the pre-round state_in and ring_in.  ring_out may be ring_in."""
-    if state_out is None:
-        state_out = torch.empty_like(state_in)
-    if ring_out is None:
-        ring_out = torch.empty_like(ring_in)
-    if y is None:
-        y = torch.zeros((q_raw.shape[0], H * (kda.HEAD_DIM if Dv is None else Dv)),
-                        dtype=torch.float32, device=q_raw.device)
+    made = []
+    with _on(stream, q_raw.device):
+        if state_out is None:
+            state_out = _made(made, torch.empty_like(state_in))
+        if ring_out is None:
+            ring_out = _made(made, torch.empty_like(ring_in))
+        if y is None:
+            y = _made(made, torch.zeros((q_raw.shape[0], H * (kda.HEAD_DIM if Dv is None else Dv)),
+                                        dtype=torch.float32, device=q_raw.device))
     kda.kda_verify_rollback(q_raw, k_raw, v_raw, conv_w, ring_in, ring_out, f_raw, dt_bias,
                             a_log, beta_raw, state_in, state_out, norm_w, gate_raw, y, keep,
                             N=N, T=T, H=H, K=K, gate_mode=gate_mode | _norm_flag(norm_gate),
                             gate_lb=gate_lb, l2_eps=l2_eps, scale=scale, rms_eps=rms_eps,
                             stream=stream, Hk=Hk, Dv=Dv)
+    _hand_over(stream, *made)
     return dict(y=y, state_out=state_out, ring_out=ring_out)
 
 
@@ -274,11 +289,11 @@ class StatePoolQ8:
         n, made = slots.numel(), []
         with _on(stream, self.codes.device):
             if state is None:
-                state = torch.zeros(n, self.H, self.Dv, kda.HEAD_DIM, device=self.codes.device)
-                made.append(state)
+                state = _made(made, torch.zeros(n, self.H, self.Dv, kda.HEAD_DIM,
+                                                device=self.codes.device))
             if ring is None:
-                ring = torch.zeros(state.shape[0], *self.ring.shape[1:], device=self.codes.device)
-                made.append(ring)
+                ring = _made(made, torch.zeros(state.shape[0], *self.ring.shape[1:],
+                                               device=self.codes.device))
         kda.kda_state_load_q8(self.codes, self.scales, state, src=slots, dst=rows, N=n, H=self.H,
                               Dv=self.Dv, ring_pool=self.ring, ring=ring, stream=stream)
         _hand_over(stream, *made)

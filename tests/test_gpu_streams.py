@@ -101,3 +101,23 @@ def test_results_outlive_the_callers_work():
     assert all(o.data_ptr() != at for o in others)
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+def test_f32_calls_beside_a_busy_stream():
+    """Prefill, the staged mixer, decode and a rollback (whose untaken rows are zeros), each with
+    buffers of its own."""
+    from gated_delta_rule_scan_gb300 import mixer
+    N, T, H = 2, 3, 2
+    d = _batch(4, N, T, H)
+    keep = torch.tensor([1, 3], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    for call, extra in ((mixer.kda_prefill, {}), (mixer.kda_forward, {}), (mixer.kda_decode, {}),
+                        (mixer.kda_verify_rollback, dict(keep=keep))):
+        want = call(N=N, T=T, H=H, **d, **extra)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        got = [call(N=N, T=T, H=H, stream=side, **d, **extra) for _ in range(4)]
+        torch.cuda.synchronize()
+        for g in got:
+            for k in ("y", "state_out", "ring_out"):
+                assert torch.equal(g[k], want[k]), (call, k)

@@ -32,7 +32,9 @@ def made(monkeypatch):
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
     for name in ("empty", "zeros", "empty_like"):
         monkeypatch.setattr(torch, name, noted(getattr(torch, name)))
-    for name in ("kda_proj_w4", "kda_state_load_q8", "kda_decode_fused_q8"):
+    for name in ("kda_proj_w4", "kda_state_load_q8", "kda_decode_fused_q8", "kda_decode_fused",
+                 "kda_verify_rollback", "kda_prefill_fused", "kda_conv_l2norm_prep", "kda_scan",
+                 "kda_gated_rmsnorm_out"):
         monkeypatch.setattr(kda, name, lambda *args, **kw: None)
     return seen
 
@@ -60,3 +62,17 @@ def test_low_bit_buffers_are_made_on_the_calls_stream(made, stream, want):
     x, w = torch.ones(5, 256), torch.ones(3, 128, dtype=torch.uint8)
     mixer.kda_proj_w4(x=x, weights=[w, w], scales=[x, x], group=128, stream=stream)
     assert made == [want] * 3                  # two outputs and the workspace
+
+
+@pytest.mark.parametrize("stream,want", STREAMS)
+def test_f32_buffers_are_made_on_the_calls_stream(made, stream, want):
+    from gated_delta_rule_scan_gb300 import mixer
+    x, state, ring = torch.ones(6, 256), torch.ones(2, 2, 128, 128), torch.ones(2, 768, 3)
+    args = dict(q_raw=x, k_raw=x, v_raw=x, conv_w=x, ring_in=ring, f_raw=x, dt_bias=x, a_log=x,
+                beta_raw=x, state_in=state, norm_w=x, gate_raw=x, N=2, T=3, H=2, stream=stream)
+    for call, buffers, extra in ((mixer.kda_decode, 3, {}), (mixer.kda_verify_rollback, 3, dict(keep=x)),
+                                 (mixer.kda_prefill, 4, {}), (mixer.kda_forward, 10, {})):
+        made.clear()
+        out = call(**args, **extra)
+        assert made == [want] * buffers, call
+        assert out["y"].shape == (6, 256) and out["state_out"].shape == state.shape
