@@ -11,10 +11,13 @@
 // four tokens they are 16 sums over 128 channels for the whole unit.  The products with the incoming
 // state are a matrix product, 128 columns x 128 keys by 2 T vectors: its left side are the codes
 // themselves, whole numbers or e4m3 values, exact in f16, the row scale going on afterwards; its
-// right side the vectors times 2^12, as f16 hi + lo (of a unit vector each element to 2^-23 of itself
-// or 2^-37), so mma.sync sums them to f32's accuracy.  Decays are at most 1, which keeps the vectors
-// in range; a positive gate bound takes the other form.  The new state is formed once, in f32, from
-// the codes, and rounded back to 8 bits.
+// right side the vectors A_t k_t and A_t q_t, each times the power of two that brings its largest
+// element (read to 8 bits) to [2^11, 2^13), as f16 hi + lo: an element is held to 2^-22 of itself or
+// 2^-36 of the vector's largest, whichever is more, and mma.sync sums in f32.  (One power of two for
+// all vectors loses the readout of a state that has faded, where nothing new covers it: relative
+// errors of 2e-2 behind a decay of e^-20, of 1 behind e^-25.)  Decays are at most 1, which keeps the
+// vectors finite; a positive gate bound takes the other form.  The new state is formed once, in f32,
+// from the codes, and rounded back to 8 bits.
 //
 // What it saves: one pass over the state's f32 values for all tokens instead of two per token.
 // GB300 layout.  One CTA of four warps owns one (sequence, unit).  Thread = channel of q, k, v and
@@ -39,7 +42,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kVecBytes = 320;               // one f16 vector: 256 bytes, and 64 against bank conflicts
 constexpr int kDotRow = 136;                 // floats: four lanes' columns land in different banks
-constexpr float kVecScale = 4096.0f;
+constexpr int kVecExp = 11;                  // exponent of a vector's largest element in f16
 constexpr int kMinBlocks = 5;                // an SM: 39.5 us at one token and 62 at four, 64 x 64 heads
                                              // (4: 43 and 67, 6: 40 and 71)
 
@@ -111,6 +114,18 @@ __device__ __forceinline__ uint32_t raw_bits(const void* p, long i, bool bf16) {
 }
 __device__ __forceinline__ float raw_value(uint32_t x, bool bf16) { return __uint_as_float(bf16 ? x << 16 : x); }
 
+// Two magnitudes by their upper 16 bits, as a bf16 pair; the larger of two pairs, NaN above all.
+__device__ __forceinline__ uint32_t mag_pair(float lo, float hi) {
+    return __byte_perm(mag_bits(lo), mag_bits(hi), 0x7632);
+}
+// The power of two that brings magnitude m to [2^kVecExp, 2^(kVecExp + 1)), or one below 2^-100 as
+// far as 2^-100 would come; 1 where m is not finite.
+__device__ __forceinline__ float vec_factor(float m) {
+    const uint32_t bits = mag_bits(m);
+    const int e = max((int)(bits >> 23) - 127, -100);
+    return bits < 0x7f800000u ? __uint_as_float((uint32_t)(127 + kVecExp - e) << 23) : 1.0f;
+}
+
 // TT: tokens of the call at most.  The sums over channels are numbered q.q (t), k.k (TT + t), then
 // D k_s . k_t for s < t and D k_s . q_t for s <= t, by t and then s.
 template <int TT>
@@ -130,6 +145,7 @@ struct FewSmem {
     float row[(TT + 1) * kHeadDim];                          // D_sT k_s, then A_T
     float dot[4 * kTiles * kDotRow];                         // (token, k or q) x columns
     float part[4][Sums<TT>::padded];
+    uint4 top[2 * TT];                           // largest |A q| of each token, then |A k|: four warps'
     float z[TT][kHeadDim];
     float beta[TT], nss[TT], osum[4][TT];
 };
@@ -213,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
     float kd[TT], cum[TT];                        // D_st k_s so far, A_t
     {
         float sum[S_::padded] = {};
+        uint32_t top[TT] = {};
         float run = 1.0f;
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
@@ -236,9 +253,19 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
             }
             kd[t] = k[t];
             sum[S_::qk_at(t, t)] = __fmul_rn(k[t], q[t]);
+            top[t] = mag_pair(__fmul_rn(k[t], run), __fmul_rn(q[t], run));
         }
         const float s = warp_sums(sum, lane);
         if (lane % S_::lanes == 0) sm.part[warp][lane / S_::lanes] = s;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const uint32_t mq = __reduce_max_sync(0xffffffffu, top[t] >> 16);
+            const uint32_t mk = __reduce_max_sync(0xffffffffu, top[t] & 0xffffu);
+            if (lane == 0) {
+                reinterpret_cast<uint32_t*>(&sm.top[t])[warp] = mq << 16;
+                reinterpret_cast<uint32_t*>(&sm.top[TT + t])[warp] = mk << 16;
+            }
+        }
     }
     if (tid < T) sm.beta[tid] = sigmoid_f(beta_raw);
     // The slots (the rules of pool_row_warp, here looked over by the whole block).
@@ -291,6 +318,14 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
     const float total = (sm.part[0][own] + sm.part[1][own]) + (sm.part[2][own] + sm.part[3][own]);
     const float coef = own < 2 * TT ? l2_inv_f(total, a.l2_eps) : total;
     const auto coef_at = [&](int i) { return __shfl_sync(0xffffffffu, coef, i * S_::lanes); };
+    // and each vector's factor, by the very products that form its elements below
+    float up = 1.0f;
+    if (own < 2 * TT && own % TT < T) {
+        const uint4 m = sm.top[own];
+        up = vec_factor(__fmul_rn(__uint_as_float(max(max(m.x, m.y), max(m.z, m.w))), coef));
+    }
+    const float coef_up = __fmul_rn(coef, up);
+    const auto coef_up_at = [&](int i) { return __shfl_sync(0xffffffffu, coef_up, i * S_::lanes); };
     float iq[TT], ik[TT];
     {
         float run = 0.0f;
@@ -301,8 +336,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
             iq[t] = coef_at(t);
             ik[t] = coef_at(S_::kk + t);
             // (tokens from T on are zeros)
-            const float x = __fmul_rn(__fmul_rn(k[t], t < T ? ik[t] : 0.0f), __fmul_rn(cum[t], kVecScale));
-            const float y = __fmul_rn(__fmul_rn(q[t], t < T ? iq[t] : 0.0f), __fmul_rn(cum[t], kVecScale));
+            const float kc = coef_up_at(S_::kk + t), qc = coef_up_at(t);
+            const float x = __fmul_rn(__fmul_rn(k[t], cum[t]), t < T ? kc : 0.0f);
+            const float y = __fmul_rn(__fmul_rn(q[t], cum[t]), t < T ? qc : 0.0f);
             const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
             __half* at = vec + 4 * t * (kVecBytes / 2);
             at[0] = xh;
@@ -321,6 +357,14 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
     cp_async_commit_wait();                       // (each lane reads what it copied)
     constexpr int kTiles = FewSmem<TT>::kTiles;
     const int cols = 4 * TT;                      // columns past them repeat the last one
+    // this lane's columns of tile i are those of vector 4 i + c: one over its factor
+    float down[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const int v = 2 * i + (c >> 1);
+        const float u = __shfl_sync(0xffffffffu, up, (c & 1 ? v : S_::kk + v) * S_::lanes);
+        down[i] = __uint_as_float((254u << 23) - __float_as_uint(u));
+    }
 #pragma unroll 1
     for (int mt = 0; mt < 2; ++mt) {
         float d[kTiles][4] = {};
@@ -354,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
         for (int i = 0; i < kTiles; ++i)
             if (TT > 1 || c < 2) {
                 float* o = sm.dot + (4 * i + c) * kDotRow + warp * 32 + mt * 16 + g;
-                o[0] = d[i][0] + d[i][1];
-                o[8] = d[i][2] + d[i][3];
+                o[0] = __fmul_rn(d[i][0] + d[i][1], down[i]);
+                o[8] = __fmul_rn(d[i][2] + d[i][3], down[i]);
             }
     }
     __syncwarp();
@@ -363,11 +407,10 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
     // ---- the solve: thread = value column
     float w[TT], o[TT];
     {
-        const float sc = scale_l * (1.0f / kVecScale);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            float x = __fmul_rn(sm.dot[2 * t * kDotRow + tid], sc);
-            float y = __fmul_rn(sm.dot[(2 * t + 1) * kDotRow + tid], sc);
+            float x = __fmul_rn(sm.dot[2 * t * kDotRow + tid], scale_l);
+            float y = __fmul_rn(sm.dot[(2 * t + 1) * kDotRow + tid], scale_l);
 #pragma unroll
             for (int s = 0; s < t; ++s) {
                 x = fmaf(w[s], coef_at(S_::kk_at(s, t)) * (ik[s] * ik[t]), x);

@@ -87,6 +87,8 @@ def test_results_outlive_the_callers_work():
     pool.store(d["state_in"], d["ring_in"], slots)
     want, _ = pool.load(slots)
     side = torch.cuda.Stream()
+    # (a kernel's first use loads its module, which may wait for the device)
+    assert torch.full_like(want * 1.0, 9.0).all()
     torch.cuda.synchronize()
     state, ring = pool.load(slots, stream=side)
     torch.cuda.current_stream().wait_stream(side)
