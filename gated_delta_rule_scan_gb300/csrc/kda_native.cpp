@@ -3,7 +3,8 @@
 // token's kernels run a few microseconds; checking and unpacking 17 to 28 tensors attribute by
 // attribute in Python took 9 to 16 us a call, here it takes about one.  Each function checks that
 // every tensor is a contiguous CUDA tensor of the right type and size on one device (ValueError or
-// TypeError otherwise), calls the C entry of the same name and returns its status.
+// TypeError otherwise), calls the C entry of the same name and returns its status.  What torch throws
+// on the way (a tensor without storage or strides) leaves as RuntimeError.
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -278,10 +279,27 @@ PyObject* proj_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                  scale_dtype, (int)group, rows, o, ws, ws_bytes, stream));
 }
 
+using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
+
+// No C++ exception passes the interpreter's C frames: that would end the process.
+template <Fast F>
+PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    try {
+        return F(self, a, n);
+    } catch (const c10::Error& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    }
+    return nullptr;
+}
+
 PyMethodDef methods[] = {
-    {"state_move", (PyCFunction)(void (*)(void))state_move, METH_FASTCALL, nullptr},
-    {"decode_fused_q8", (PyCFunction)(void (*)(void))decode_fused_q8, METH_FASTCALL, nullptr},
-    {"proj_w4", (PyCFunction)(void (*)(void))proj_w4, METH_FASTCALL, nullptr},
+    {"state_move", (PyCFunction)(void (*)(void))guarded<state_move>, METH_FASTCALL, nullptr},
+    {"decode_fused_q8", (PyCFunction)(void (*)(void))guarded<decode_fused_q8>, METH_FASTCALL, nullptr},
+    {"proj_w4", (PyCFunction)(void (*)(void))guarded<proj_w4>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_native", nullptr, -1, methods,
