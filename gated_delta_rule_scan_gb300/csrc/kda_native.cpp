@@ -116,13 +116,27 @@ struct Call {
     }
 };
 
+// The C entries run without the interpreter's lock, as through ctypes: a launch may wait for room in
+// the stream's queue.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename Call>
+PyObject* status(const Call& entry) {
+    int rc;
+    {
+        const Unlocked unlocked;
+        rc = entry();
+    }
+    return PyLong_FromLong(rc);
+}
+
 bool arity(const char* name, Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return true;
     PyErr_Format(PyExc_TypeError, "%s: expected %zd arguments, got %zd", name, want, n);
     return false;
 }
-
-PyObject* status(const Call& c, int rc) { return c.failed ? nullptr : PyLong_FromLong(rc); }
 
 // (store, state, codes, scales, state_rows, slots, N, H, Dv, ring, ring_pool, stream)
 PyObject* state_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -159,14 +173,14 @@ PyObject* state_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     void* stream = c.stream(a[11]);
     if (c.failed) return nullptr;
-    const int rc =
-        store ? kda_state_store_q8((float*)state, codes, (float*)scales, format, (int*)rows, (int*)slots,
-                                   (int)S, (int)P, (int)N, (int)H, (int)kHead, (int)Dv, (float*)ring,
-                                   (float*)ring_pool, ring_row, stream)
-              : kda_state_load_q8(codes, (float*)scales, (float*)state, format, (int*)slots, (int*)rows,
-                                  (int)P, (int)S, (int)N, (int)H, (int)kHead, (int)Dv,
-                                  (float*)ring_pool, (float*)ring, ring_row, stream);
-    return status(c, rc);
+    return status([&] {
+        return store ? kda_state_store_q8((float*)state, codes, (float*)scales, format, (int*)rows,
+                                          (int*)slots, (int)S, (int)P, (int)N, (int)H, (int)kHead, (int)Dv,
+                                          (float*)ring, (float*)ring_pool, ring_row, stream)
+                     : kda_state_load_q8(codes, (float*)scales, (float*)state, format, (int*)slots,
+                                         (int*)rows, (int)P, (int)S, (int)N, (int)H, (int)kHead, (int)Dv,
+                                         (float*)ring_pool, (float*)ring, ring_row, stream);
+    });
 }
 
 // (q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias, a_log, beta_raw, codes, scales, norm_w,
@@ -204,12 +218,13 @@ PyObject* decode_fused_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* keep = c.maybe(a[16], "keep", i32, N);
     void* stream = c.stream(a[28]);
     if (c.failed) return nullptr;
-    return status(c, kda_decode_fused_q8(
-                         q, k, vr, raw_dtype, (float*)conv_w, (float*)ring, (float*)f, (float*)dt,
-                         (float*)a_log, (int)mode, gate_lb, (float*)beta, codes, (float*)scales, format,
-                         (int*)slots, (int*)slots_out, (int*)keep, (float*)norm_w, (float*)z, (float*)y,
-                         (int)P, (int)N, (int)T, (int)H, (int)Hk, (int)kHead, (int)Dv, (int)K, l2_eps,
-                         scale, rms_eps, stream));
+    return status([&] {
+        return kda_decode_fused_q8(
+            q, k, vr, raw_dtype, (float*)conv_w, (float*)ring, (float*)f, (float*)dt, (float*)a_log,
+            (int)mode, gate_lb, (float*)beta, codes, (float*)scales, format, (int*)slots, (int*)slots_out,
+            (int*)keep, (float*)norm_w, (float*)z, (float*)y, (int)P, (int)N, (int)T, (int)H, (int)Hk,
+            (int)kHead, (int)Dv, (int)K, l2_eps, scale, rms_eps, stream);
+    });
 }
 
 // (x, weights, scales, zeros or None, outs, group, workspace or None, stream)
@@ -275,8 +290,10 @@ PyObject* proj_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     void* stream = c.stream(a[7]);
     if (c.failed) return nullptr;
-    return status(c, kda_proj_w4(x, x_dtype, (int)t, (int)in_f, (int)nw, w, s, parts == 4 ? z : nullptr,
-                                 scale_dtype, (int)group, rows, o, ws, ws_bytes, stream));
+    return status([&] {
+        return kda_proj_w4(x, x_dtype, (int)t, (int)in_f, (int)nw, w, s, parts == 4 ? z : nullptr,
+                           scale_dtype, (int)group, rows, o, ws, ws_bytes, stream);
+    });
 }
 
 using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);

@@ -1,5 +1,9 @@
-"""GPU tests of calls that run on another stream than the current one and make their own buffers:
-the current stream is kept busy meanwhile, so that work put on it would land after the results."""
+"""GPU tests of calls on streams: calls that run on another stream than the current one and make
+their own buffers (the current stream is kept busy meanwhile, so that work put on it would land after
+the results), and launches that wait for a full queue."""
+
+import threading
+import time
 
 import pytest
 import torch
@@ -123,3 +127,35 @@ def test_f32_calls_beside_a_busy_stream():
         for g in got:
             for k in ("y", "state_out", "ring_out"):
                 assert torch.equal(g[k], want[k]), (call, k)
+
+
+def test_a_full_queue_holds_up_no_other_thread():
+    """More launches than a stream's queue takes behind a pause: the launching thread waits there,
+    without the interpreter's lock."""
+    from gated_delta_rule_scan_gb300 import mixer
+    pool = mixer.StatePoolQ8(1, 1, "cuda")
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    state, ring = pool.load(slots)
+    torch.cuda.synchronize()
+    gap, stop = [0.0], threading.Event()
+
+    def ticks():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gap[0], last = max(gap[0], now - last), now
+    t = threading.Thread(target=ticks)
+    t.start()
+    try:
+        start = time.perf_counter()
+        torch.cuda._sleep(8 * BUSY)            # 0.8 s
+        for _ in range(6000):
+            pool.load(slots, state=state, ring=ring)
+        took = time.perf_counter() - start
+        torch.cuda.synchronize()
+    finally:
+        stop.set()
+        t.join()
+    assert took > 0.5, took                    # (the queue was full)
+    assert gap[0] < 0.25, (gap, took)
