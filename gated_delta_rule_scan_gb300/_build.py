@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
@@ -32,6 +33,12 @@ def _nvcc() -> str:
     return "nvcc"
 
 
+def _cuda_include() -> str:
+    """The headers of the toolkit that nvcc belongs to."""
+    nvcc = shutil.which(_nvcc()) or "/usr/local/cuda/bin/nvcc"
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+
+
 def _newest_source_mtime() -> float:
     files = glob.glob(os.path.join(CSRC, "*")) + [os.path.join(ROOT, "include", "kda.h")]
     return max(os.path.getmtime(f) for f in files)
@@ -49,10 +56,10 @@ def _compile_native():
     root = os.path.dirname(os.path.abspath(torch.__file__))
     obj = os.path.join(BUILD_DIR, "kda_native.cpp.o")
     _run(["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
           "-I" + os.path.join(root, "include"),
           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
-          "-I" + sysconfig.get_paths()["include"],
+          "-I" + sysconfig.get_paths()["include"], "-I" + _cuda_include(),
           "-c", os.path.join(CSRC, "kda_native.cpp"), "-o", obj])
     return obj, os.path.join(root, "lib")
 
@@ -91,7 +98,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     # torch's libraries are loaded before this one; libkda.so is found beside it
     tmp = NATIVE_PATH + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, native_obj, "-L" + PKG, "-l:libkda.so", "-L" + torch_lib,
-          "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"])
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, NATIVE_PATH)
     return LIB_PATH
 

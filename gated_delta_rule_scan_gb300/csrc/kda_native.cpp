@@ -6,6 +6,7 @@
 // TypeError otherwise), calls the C entry of the same name and returns its status.  What torch throws
 // on the way (a tensor without storage or strides) leaves as RuntimeError.
 #define PY_SSIZE_T_CLEAN
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/kda.h"
@@ -77,9 +78,10 @@ struct Call {
         if (v == -1.0 && PyErr_Occurred()) failed = true;
         return (float)v;
     }
-    // the stream handle, an int or None (the legacy default stream)
+    // the stream handle: an int, or None for torch's current stream of the tensors' device
     void* stream(PyObject* o) {
-        if (failed || o == Py_None) return nullptr;
+        if (failed) return nullptr;
+        if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
         void* p = PyLong_AsVoidPtr(o);
         if (p == nullptr && PyErr_Occurred()) failed = true;
         return p;

@@ -208,7 +208,7 @@ def _stream(stream, *tensors) -> int | None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.is_cuda:
-            return torch._C._cuda_getCurrentRawStream(t.get_device())
+            return torch.cuda.current_stream(t.device).cuda_stream
     return None
 
 
@@ -520,9 +520,12 @@ def kda_proj6(x, w_q, w_k, w_v, w_fa, w_ga, w_b, q_raw, k_raw, v_raw, f_down, g_
           _ptr(workspace), _ws_bytes(workspace), st)
 
 
-def _native(fn: str, like, *args):
+def _native(fn: str, like, stream, *args):
     """Call _kda_native's ``fn``, which checks and unpacks the tensors, with the device of tensor
-    ``like`` current."""
+    ``like`` current, on ``stream`` (None: it looks up the current one)."""
+    if stream is not None and not isinstance(stream, int):
+        stream = stream.cuda_stream
+    args = (*args, stream)
     if (isinstance(like, torch.Tensor) and like.is_cuda
             and torch.cuda.current_device() != like.get_device()):
         with torch.cuda.device(like.device):
@@ -537,15 +540,15 @@ def kda_state_store_q8(state, codes, scales, *, N, H, src=None, dst=None, Dv=HEA
                        ring_pool=None, stream=None):
     """Rows src[n] of state [S, H, Dv, 128] (and of ring) into pool slots dst[n].  codes: int8 or
     float8_e4m3fn, which names the format; src, dst: int32 device [N] or None (n)."""
-    _native("state_move", codes, True, state, codes, scales, src, dst, N, H, Dv, ring, ring_pool,
-            _stream(stream, codes))
+    _native("state_move", codes, stream, True, state, codes, scales, src, dst, N, H, Dv, ring,
+            ring_pool)
 
 
 def kda_state_load_q8(codes, scales, state, *, N, H, src=None, dst=None, Dv=HEAD_DIM,
                       ring_pool=None, ring=None, stream=None):
     """Pool slots src[n] into rows dst[n] of state (and of ring); see kda_state_store_q8."""
-    _native("state_move", codes, False, state, codes, scales, dst, src, N, H, Dv, ring, ring_pool,
-            _stream(stream, codes))
+    _native("state_move", codes, stream, False, state, codes, scales, dst, src, N, H, Dv, ring,
+            ring_pool)
 
 
 def kda_decode_fused_q8(q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias, a_log, beta_raw,
@@ -554,10 +557,10 @@ def kda_decode_fused_q8(q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias, 
                         rms_eps=1e-6, stream=None, Hk=None, Dv=HEAD_DIM):
     """kda_decode_fused on the 8-bit pool: sequence n reads slot slots[n] (None: n) and writes slot
     slots_out[n] (None: the same); keep: int32 device [N], the rows to take (a rollback)."""
-    _native("decode_fused_q8", codes, q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias, a_log,
-            beta_raw, codes, scales, norm_w, gate_raw, y, slots, slots_out, keep, N, T, H,
+    _native("decode_fused_q8", codes, stream, q_raw, k_raw, v_raw, conv_w, ring_pool, f_raw, dt_bias,
+            a_log, beta_raw, codes, scales, norm_w, gate_raw, y, slots, slots_out, keep, N, T, H,
             H if Hk is None else Hk, Dv, K, gate_mode, gate_lb, l2_eps,
-            HEAD_DIM ** -0.5 if scale is None else scale, rms_eps, _stream(stream, codes))
+            HEAD_DIM ** -0.5 if scale is None else scale, rms_eps)
 
 
 def kda_proj_w4_workspace_bytes(t, in_f) -> int:
@@ -575,7 +578,7 @@ def kda_proj_w4(x, weights, scales, outs, *, group, zeros=None, workspace=None, 
     """Projections of x [t, in_f] (f32 or bf16) by 4-bit weights (lists of tensors): weights[i]
     uint8 [rows_i, in_f/2], scales[i] (and zeros[i]) f32 or bf16 [rows_i, in_f/group], outs[i] f32
     [t, rows_i]."""
-    _native("proj_w4", x, x, weights, scales, zeros, outs, group, workspace, _stream(stream, x))
+    _native("proj_w4", x, stream, x, weights, scales, zeros, outs, group, workspace)
 
 
 def kernel_timing(enable: bool) -> bool:

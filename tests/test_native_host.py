@@ -53,3 +53,19 @@ def test_tensors_without_storage_raise():
     r = _python(STORAGELESS)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
     assert r.stdout.split() == ["RuntimeError", "True"] * 3, r.stdout
+
+
+def test_streams_come_from_public_calls(monkeypatch):
+    """Every entry's default stream is torch.cuda.current_stream's; nothing private stands in."""
+    from types import SimpleNamespace
+    import torch
+    from gated_delta_rule_scan_gb300 import kda
+
+    class OnGpu(torch.Tensor):
+        is_cuda, device = True, "cuda:3"
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda device=None: SimpleNamespace(cuda_stream=(device, 123)))
+    assert kda._stream(None, None, torch.zeros(1).as_subclass(OnGpu)) == ("cuda:3", 123)
+    assert kda._stream(5, None) == 5
+    assert kda._stream(SimpleNamespace(cuda_stream=7), None) == 7
+    assert "torch._C" not in open(kda.__file__).read()
