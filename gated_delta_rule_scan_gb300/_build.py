@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
 NATIVE_PATH = os.path.join(PKG, "_kda_native.so")
+NATIVE_STAMP = os.path.join(BUILD_DIR, "kda_native.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-I" + os.path.join(ROOT, "include")]
@@ -50,6 +52,21 @@ def _run(cmd):
         raise RuntimeError(f"{' '.join(cmd[:2])} failed:\n{r.stderr}")
 
 
+def _native_stamp() -> str:
+    """What _kda_native.so is bound to besides its source: the interpreter's and torch's ABI."""
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__}"
+
+
+def native_matches() -> bool:
+    """Whether _kda_native.so is there and was built for this Python and torch."""
+    try:
+        with open(NATIVE_STAMP) as f:
+            return os.path.exists(NATIVE_PATH) and f.read() == _native_stamp()
+    except OSError:
+        return False
+
+
 def _compile_native():
     """kda_native.cpp's object file and torch's library folder."""
     import torch
@@ -66,14 +83,19 @@ def _compile_native():
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile every csrc/*.cu for sm_103a and link gated_delta_rule_scan_gb300/libkda.so, and
-    csrc/kda_native.cpp into _kda_native.so beside it."""
+    csrc/kda_native.cpp into _kda_native.so beside it.  Where the second cannot be built (no torch
+    headers, say) the first is there all the same: a warning names the cause, the package works, and
+    the calls that need _kda_native.so raise."""
     newest = _newest_source_mtime()
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest
-                         for p in (LIB_PATH, NATIVE_PATH)):
+    lib_current = (not force and os.path.exists(LIB_PATH)
+                   and os.path.getmtime(LIB_PATH) >= newest)
+    native_current = (not force and native_matches()
+                      and os.path.getmtime(NATIVE_PATH) >= newest)
+    if lib_current and native_current:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = [] if lib_current else sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     flags = NVCC_FLAGS + list(extra_flags or [])
 
     def compile_one(src):
@@ -87,20 +109,34 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        native = ex.submit(_compile_native)
+        native = None if native_current else ex.submit(_compile_native)
         objs = list(ex.map(compile_one, srcs))
-        native_obj, torch_lib = native.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+    if not lib_current:
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        os.replace(tmp, LIB_PATH)
+    if native is not None:
+        try:
+            _link_native(*native.result())
+        except (OSError, RuntimeError) as e:
+            # an older one is for other sources or another torch
+            for p in (NATIVE_PATH, NATIVE_STAMP):
+                if os.path.exists(p):
+                    os.remove(p)
+            warnings.warn(f"_kda_native.so was not built, the low-bit calls will raise: {e}")
+    return LIB_PATH
+
+
+def _link_native(obj, torch_lib):
     # torch's libraries are loaded before this one; libkda.so is found beside it
     tmp = NATIVE_PATH + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, native_obj, "-L" + PKG, "-l:libkda.so", "-L" + torch_lib,
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libkda.so", "-L" + torch_lib,
           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, NATIVE_PATH)
-    return LIB_PATH
+    with open(NATIVE_STAMP, "w") as f:
+        f.write(_native_stamp())
 
 
 if __name__ == "__main__":

@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from . import _build
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkda.so")
 
@@ -22,7 +24,12 @@ if not os.path.exists(LIB_PATH):
         f"libkda.so not found at {LIB_PATH}; build it first "
         "(python -c 'import __graft_entry__ as g; g.build()')")
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _kda_native  # noqa: E402  (built beside libkda.so, which it calls)
+try:  # built beside libkda.so, which it calls; only the low-bit calls need it
+    if not _build.native_matches():
+        raise ImportError("_kda_native.so is missing or was built for another Python or torch")
+    from . import _kda_native  # noqa: E402
+except ImportError as e:
+    _kda_native, _native_missing = None, e
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 GATE_PER_CHANNEL, GATE_PER_HEAD = 0, 1
@@ -523,6 +530,10 @@ def kda_proj6(x, w_q, w_k, w_v, w_fa, w_ga, w_b, q_raw, k_raw, v_raw, f_down, g_
 def _native(fn: str, like, stream, *args):
     """Call _kda_native's ``fn``, which checks and unpacks the tensors, with the device of tensor
     ``like`` current, on ``stream`` (None: it looks up the current one)."""
+    if _kda_native is None:
+        raise ImportError("this call needs _kda_native.so, which was not built for this Python and "
+                          "torch; build it (python -c 'import __graft_entry__ as g; g.build()')"
+                          ) from _native_missing
     if stream is not None and not isinstance(stream, int):
         stream = stream.cuda_stream
     args = (*args, stream)

@@ -69,3 +69,78 @@ def test_streams_come_from_public_calls(monkeypatch):
     assert kda._stream(5, None) == 5
     assert kda._stream(SimpleNamespace(cuda_stream=7), None) == 7
     assert "torch._C" not in open(kda.__file__).read()
+
+
+def test_the_package_works_without_the_compiled_marshalling():
+    """Blocked, as on a machine where it was not built: the f32 entries load and check as ever, and a
+    low-bit call says what is missing."""
+    r = _python("""
+import sys
+sys.modules["gated_delta_rule_scan_gb300._kda_native"] = None
+import torch
+from gated_delta_rule_scan_gb300 import kda, mixer
+print(kda.abi_version() > 0, kda.library().kda_scan is not None)
+try:
+    kda.kda_gated_rmsnorm_out(None, None, None, None, rows=1)
+except kda.KdaError as e:
+    print(e.status)
+x, w, s, o = torch.zeros(1, 128), torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4), torch.zeros(1, 4)
+try:
+    kda.kda_proj_w4(x, [w], [s], [o], group=32)
+except ImportError as e:
+    print("_kda_native.so" in str(e))
+""")
+    assert r.returncode == 0, r.stderr[-500:]
+    assert r.stdout.split() == ["True", "True", "40004", "True"], r.stdout
+
+
+@pytest.fixture
+def scratch_build(tmp_path, monkeypatch):
+    """_build with its outputs in a folder of their own and the compilers replaced; the list collects
+    what was made."""
+    from gated_delta_rule_scan_gb300 import _build
+    made = []
+    for name, path in (("BUILD_DIR", tmp_path), ("LIB_PATH", tmp_path / "libkda.so"),
+                       ("NATIVE_PATH", tmp_path / "_kda_native.so"),
+                       ("NATIVE_STAMP", tmp_path / "stamp")):
+        monkeypatch.setattr(_build, name, str(path))
+
+    class Done:
+        returncode, stderr = 0, ""
+
+    def run(cmd, **kw):
+        out = cmd[cmd.index("-o") + 1]
+        made.append(os.path.basename(out).split(".tmp")[0])
+        open(out, "w").close()
+        return Done
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    return _build, made
+
+
+def test_a_change_of_torch_rebuilds_the_marshalling(scratch_build, monkeypatch):
+    import torch
+    build, made = scratch_build
+    build.build()
+    assert "libkda.so" in made and "_kda_native.so" in made
+    made.clear()
+    build.build()
+    assert made == [] and build.native_matches()
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert not build.native_matches()          # (the package then leaves it unloaded)
+    build.build()
+    assert made == ["kda_native.cpp.o", "_kda_native.so"]
+    made.clear()
+    build.build()
+    assert made == []
+
+
+def test_without_torchs_headers_the_library_is_built(scratch_build, monkeypatch):
+    build, made = scratch_build
+
+    def fails():
+        raise RuntimeError("no headers")
+    monkeypatch.setattr(build, "_compile_native", fails)
+    with pytest.warns(UserWarning, match="no headers"):
+        assert build.build() == build.LIB_PATH
+    assert "libkda.so" in made and os.path.exists(build.LIB_PATH)
+    assert not os.path.exists(build.NATIVE_PATH)
