@@ -25,6 +25,24 @@ constexpr int kMaxDevices = 64;    // per-device caches (symbol addresses, funct
 template <typename T>
 using PerDevice = std::atomic<T>[kMaxDevices];
 
+constexpr int kMaxBlockSmem = 227 * 1024;   // dynamic shared memory one block can opt into
+
+// Opt a kernel into `bytes` of dynamic shared memory once per device; `done` is the caller's own
+// per-device flag array (one per template instantiation).  `bytes` is one constant for a kernel,
+// whatever a launch needs: the call sets a value, not a maximum, so that host threads with different
+// values would undo one another's.
+template <typename K>
+inline cudaError_t set_smem(K kernel, size_t bytes, PerDevice<int>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool cached = dev >= 0 && dev < kMaxDevices;
+    if (cached && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && cached) done[dev].store(1, std::memory_order_release);
+    return e;
+}
+
 // Row ranges of the packed token-major arrays.  When cu_seqlens is null every sequence has
 // T_uniform tokens and sequence n owns rows [n*T, (n+1)*T).
 struct SeqLayout {

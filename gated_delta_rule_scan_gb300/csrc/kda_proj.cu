@@ -239,23 +239,9 @@ cudaError_t launch_proj6(const Proj6Args& a, cudaStream_t s) {
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    static PerDevice<int> smem_set_for;    // the largest dynamic shared memory opted into so far
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static PerDevice<int> done;
+    const cudaError_t e = set_smem(kda_proj6_kernel, kMaxBlockSmem, done);
     if (e != cudaSuccess) return e;
-    const bool cached = dev >= 0 && dev < kMaxDevices;
-    if (!cached || smem_set_for[dev].load(std::memory_order_acquire) < (int)smem) {
-        e = cudaFuncSetAttribute(kda_proj6_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
-        if (e != cudaSuccess) return e;
-        if (cached) {
-            int cur = smem_set_for[dev].load(std::memory_order_acquire);
-            while (cur < (int)smem &&
-                   !smem_set_for[dev].compare_exchange_weak(cur, (int)smem,
-                                                            std::memory_order_acq_rel)) {
-            }
-        }
-    }
     // launched as a programmatic dependent of the split kernel: its CTAs may start (and stream
     // weights) while the split is still running
     cudaLaunchConfig_t cfg = {};

@@ -459,22 +459,10 @@ __global__ void __launch_bounds__(kTeam * w4_teams(G, SBF16, ZERO, NT)) kda_proj
 
 template <int G, bool ONE, bool SBF16, bool ZERO, int NT>
 cudaError_t launch_rows(const W4Params& p, int grid, int teams, size_t smem, cudaStream_t s) {
-    static PerDevice<int> smem_set_for;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     const auto kernel = kda_proj_w4_kernel<G, ONE, SBF16, ZERO, NT>;
-    const bool cached = dev >= 0 && dev < kMaxDevices;
-    if (smem > 48 * 1024 && (!cached || smem_set_for[dev].load(std::memory_order_acquire) < (int)smem)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        if (cached) {
-            int cur = smem_set_for[dev].load(std::memory_order_acquire);
-            while (cur < (int)smem &&
-                   !smem_set_for[dev].compare_exchange_weak(cur, (int)smem, std::memory_order_acq_rel)) {
-            }
-        }
-    }
+    static PerDevice<int> done;
+    const cudaError_t e = set_smem(kernel, kMaxBlockSmem, done);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)(teams * kTeam));

@@ -764,22 +764,10 @@ cudaError_t launch_wide(const WideMaps& maps, WideParams& p, int units, int sms,
     xn = xn > kMaxXStages ? kMaxXStages : (xn < 1 ? 1 : xn);
     p.x_stages = xn;
     const int smem = fixed + xn * x_stage;
-    static PerDevice<int> smem_set_for;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     const auto kernel = kda_proj_w4_wide_kernel<G, CTAS, ZERO>;
-    const bool cached = dev >= 0 && dev < kMaxDevices;
-    if (!cached || smem_set_for[dev].load(std::memory_order_acquire) < smem) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        if (cached) {
-            int cur = smem_set_for[dev].load(std::memory_order_acquire);
-            while (cur < smem &&
-                   !smem_set_for[dev].compare_exchange_weak(cur, smem, std::memory_order_acq_rel)) {
-            }
-        }
-    }
+    static PerDevice<int> done;
+    const cudaError_t e = set_smem(kernel, kMaxBlockSmem, done);
+    if (e != cudaSuccess) return e;
     int nb = sms * CTAS / ny;
     if (nb > units) nb = units;
     // a programmatic dependent of the split: codes stream and unpack while x is being split

@@ -237,3 +237,31 @@ def test_refusals_on_device():
         kda.kda_proj_w4(x, w, [v[:, :1].contiguous() for v in s], outs, group=256)
     assert e.value.status == 40007
     _check(c, _gpu(c))
+
+
+def test_first_calls_of_many_threads():
+    """Host threads whose calls want different amounts of shared memory of the same kernels, at once;
+    the largest still launch afterwards."""
+    import threading
+    cases = [_case(500 + n, t, in_f, (130,), 128, x) for n, (t, in_f, x) in enumerate(
+        [(1, 512, "f32"), (4, 9728, "f32"), (2, 19456, "f32"), (3, 128, "f32"), (5, 4864, "f32"),
+         (7, 512, "f32"), (24, 512, "f32"), (64, 512, "f32"), (80, 256, "f32"), (128, 256, "f32")])]
+    start, got, errors = threading.Barrier(len(cases)), [None] * len(cases), []
+
+    def work(n):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                got[n] = _gpu(cases[n])
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for c, o in zip(cases, got):
+        _check(c, o)
+    for c, o in zip(cases, got):
+        assert all(torch.equal(a, b) for a, b in zip(_gpu(c), o))
