@@ -272,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kda_decode_q8_few_kernel
     const bool live = slot_in >= 0 && slot_out >= 0;
     bool bad = slot_in >= p.pool_rows || slot_out >= p.pool_rows;
     if (p.slots || p.slots_out) {
-        if (tid < a.N) bad |= pool_rows_clash(im, om, n, slot_out, tid);
+        if (tid < a.N) bad |= pool_rows_clash(im, om, n, slot_out, tid, p.pool_rows);
         for (int m = tid + kThreads; m < a.N; m += kThreads) {
             const int mi = p.slots ? p.slots[m] : m;
-            bad |= pool_rows_clash(mi, p.slots_out ? p.slots_out[m] : mi, n, slot_out, m);
+            bad |= pool_rows_clash(mi, p.slots_out ? p.slots_out[m] : mi, n, slot_out, m, p.pool_rows);
         }
     }
     const bool clash = __syncthreads_or(live && bad);

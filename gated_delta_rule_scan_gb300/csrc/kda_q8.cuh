@@ -132,9 +132,10 @@ __device__ __forceinline__ float4 q8_decode4(uint32_t w, float scale) {
 }
 
 // Whether batch row m, with slots im and om, keeps row n from writing slot `out`: it reads that slot,
-// or writes it first.
-__device__ __forceinline__ bool pool_rows_clash(int im, int om, int n, int out, int m) {
-    return m != n && im >= 0 && om >= 0 && (im == out || (m < n && om == out));
+// or writes it first.  Padding and rows with a slot past the pool do neither.
+__device__ __forceinline__ bool pool_rows_clash(int im, int om, int n, int out, int m, int pool_rows) {
+    return m != n && (unsigned)im < (unsigned)pool_rows && (unsigned)om < (unsigned)pool_rows &&
+           (im == out || (m < n && om == out));
 }
 
 // The pool rows that batch row n reads and writes.  A negative slot is padding: the row is skipped.
@@ -151,7 +152,7 @@ __device__ __forceinline__ bool pool_row_warp(const int* slots, const int* slots
     if (slots || slots_out) {
         for (int m = lane; m < N; m += 32) {
             const int im = slots ? slots[m] : m;
-            bad |= pool_rows_clash(im, slots_out ? slots_out[m] : im, n, out, m);
+            bad |= pool_rows_clash(im, slots_out ? slots_out[m] : im, n, out, m, pool_rows);
         }
     }
     const bool any = __any_sync(0xffffffffu, live && bad);

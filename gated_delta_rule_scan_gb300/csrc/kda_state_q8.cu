@@ -22,7 +22,8 @@ constexpr int kRingVecs = 4;                 // float4 of a ring row per thread
 constexpr int kUnit = kHeadDim * kHeadDim;   // elements of one unit
 
 // Row n's source and destination rows.  A negative index is padding.  An index past its end, or a
-// destination that an earlier row names already, raises the error word; nothing is written.
+// destination that an earlier row writes already, raises the error word; nothing is written.  (Rows
+// that are padding or have an index past its end write nothing and claim no destination.)
 __device__ __forceinline__ bool move_ok(const StateQ8Args& a, int n, long& src, long& dst) {
     src = a.src ? a.src[n] : n;
     dst = a.dst ? a.dst[n] : n;
@@ -30,7 +31,7 @@ __device__ __forceinline__ bool move_ok(const StateQ8Args& a, int n, long& src, 
     if (a.dst && dst >= 0) {
         bool taken = false;
         for (int i = threadIdx.x; i < n; i += kThreads)
-            taken |= a.dst[i] == (int)dst && (!a.src || a.src[i] >= 0);
+            taken |= a.dst[i] == (int)dst && (unsigned)(a.src ? a.src[i] : i) < (unsigned)a.src_rows;
         bad |= taken;
     }
     const bool live = src >= 0 && dst >= 0;

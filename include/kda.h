@@ -581,9 +581,10 @@ int kda_proj6(const float* x, int t, int in_f, const void* w_q, const void* w_k,
  * NaN throughout.
  * Slot and row indices are device int32 arrays of N entries, or NULL (row n is row n; N must then
  * not exceed the array, 40005).  A negative index makes row n padding: nothing of it is read or
- * written.  An index past its array, or a destination that another row of the call names too, would
- * race: such rows are left out as padding is (of several rows that name one destination the store
- * and the load keep the first), and kda_device_status reports 40013.
+ * written.  A row with an index past its array, or with a destination that another row of the call
+ * writes too (that would race), is left out as padding is: of several rows that name one destination
+ * the store and the load keep the first that is neither padding nor past its array.
+ * kda_device_status then reports 40013.
  * A pool of up to 2^31 - 1 slots is addressed with 64-bit offsets.  The pool needs no initialising:
  * slots that were never written hold what the memory held.
  *
@@ -614,7 +615,8 @@ int kda_state_load_q8(const void* codes, const float* scales, float* state, int 
  *              keep, from the slots of before the round.  keep[n] = 0 copies the slot unchanged.
  * y rows of padding, of rows left out and of rows t >= keep[n] are not written.
  * A slot may be read by several rows (a shared prefix); a row whose output slot another row reads
- * or an earlier row writes is left out (40013, above).  Grouped queries and wide value heads may
+ * or an earlier row writes is left out (40013, above; padding and rows with a slot past the pool read
+ * and write none).  Grouped queries and wide value heads may
  * roll the ring in place here.  q_raw, k_raw, v_raw, conv_w, ring_pool, codes, scales, norm_w,
  * gate_raw, y and, with KDA_GATE_PER_CHANNEL, f_raw and dt_bias are [16B].
  * Unlike kda_decode_fused, a T-token call is not T one-token calls bit for bit: those round the

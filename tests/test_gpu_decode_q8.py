@@ -497,3 +497,24 @@ def test_refusals_on_device():
     assert e.value.status == 40005
     assert (y == 77.0).all()
     w.others_untouched([])
+
+
+@pytest.mark.parametrize("T", [2, 6])
+def test_a_row_left_out_claims_no_slot(T):
+    """Rows with a slot past the pool, or of padding, read and write nothing: others may write the
+    slots that they name."""
+    from gated_delta_rule_scan_gb300 import kda
+    w = Work(14, N=6, T=T, H=2, P=12, slots=[0, 1, 2, 3, 4, 5])
+    good = w.decode(slots_out=_idx([6, 7, 8, 9, 10, 11]))
+    want = [t.clone() for t in (w.pool.codes.view(torch.uint8), w.pool.scales, w.pool.ring)]
+    w.reset()
+    # row 0's source and row 2's target are outside; rows 1 and 3 write what those name
+    y = w.decode(slots=[12, 1, 8, 3, -1, 5], slots_out=_idx([7, 7, 12, 8, 11, 11]))
+    assert kda.kda_device_status() == 40013
+    for n in range(6):
+        rows = y[n * T:(n + 1) * T]
+        assert torch.equal(rows, good[n * T:(n + 1) * T]) if n in (1, 3, 5) else (rows == 77.0).all()
+    for slot, n in ((7, 1), (8, 3), (11, 5)):
+        for t, f in zip((w.pool.codes.view(torch.uint8), w.pool.scales, w.pool.ring), want):
+            assert torch.equal(t[slot], f[6 + n])
+    w.others_untouched([7, 8, 11])

@@ -245,3 +245,33 @@ def test_refusals_on_device():
         kda.kda_state_store_q8(st, codes, scales, N=4, H=2)
     assert e.value.status == 40005
     assert (codes.view(torch.uint8) == 0x55).all()
+
+
+def test_a_row_left_out_claims_no_destination():
+    """An earlier row whose source lies past its array is left out; the next row that names its
+    destination is the first of those that store, and is kept (in both directions)."""
+    from gated_delta_rule_scan_gb300 import kda
+    H, P, S = 2, 5, 4
+    state = _state(70, S, H, 128).cuda()
+    src = torch.tensor([S, 1, -1, 2, 2147483647, 3, 0], dtype=torch.int32, device="cuda")
+    dst = torch.tensor([3, 3, 0, 0, 4, 4, 3], dtype=torch.int32, device="cuda")
+    want = {3: 1, 0: 2, 4: 3}                  # slot: row; the last row finds slot 3 taken
+    codes, scales = _pool(P, H, 128, "int8")[:2]
+    before = codes.clone(), scales.clone()
+    kda.kda_state_store_q8(state, codes, scales, src=src, dst=dst, N=7, H=H)
+    assert kda.kda_device_status() == 40013
+    ref_codes, ref_scales = quantise(state.cpu(), "int8")
+    for p in range(P):
+        c, s = codes[p].view(torch.uint8).cpu(), scales[p].cpu()
+        if p in want:
+            assert torch.equal(c, ref_codes[want[p]]) and torch.equal(s, ref_scales[want[p]])
+        else:
+            assert torch.equal(codes[p], before[0][p]) and torch.equal(scales[p], before[1][p])
+    kda.kda_state_store_q8(state, codes, scales, N=4, H=H)
+    out = torch.full((P, H, 128, 128), 9.0, device="cuda")
+    src[0] = P
+    kda.kda_state_load_q8(codes, scales, out, src=src, dst=dst, N=7, H=H)
+    assert kda.kda_device_status() == 40013
+    back = codes.float() * scales[..., None]
+    for p in range(P):
+        assert torch.equal(out[p], back[want[p]]) if p in want else (out[p] == 9.0).all()
