@@ -64,9 +64,19 @@ inline bool overlap(const void* a, const void* b, size_t bytes) {
     return x < y + bytes && y < x + bytes;
 }
 
-inline bool overlap2(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
+// Arrays of one call by address and bytes (0: left out), no two of which may overlap.
+struct Span {
+    const void* at;
+    size_t bytes;
+};
+template <int N>
+bool any_overlap(const Span (&s)[N]) {
+    for (int i = 0; i < N; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(s[i].at), y = reinterpret_cast<uintptr_t>(s[j].at);
+            if (s[i].bytes > 0 && s[j].bytes > 0 && x < y + s[j].bytes && y < x + s[i].bytes) return true;
+        }
+    return false;
 }
 
 int check_cu(const int* cu_host, int N, long total) {
@@ -388,14 +398,14 @@ int state_q8_impl(bool store, const float* state, float* state_out, void* codes,
     if (ring_row > 0 && (!ring_src || !ring_dst)) return KDA_ERR_NULL;
     if (!aligned16(st) || !aligned16(codes) || !aligned16(scales)) return KDA_ERR_ALIGN;
     if (ring_row > 0 && (!aligned16(ring_src) || !aligned16(ring_dst))) return KDA_ERR_ALIGN;
-    const size_t row = (size_t)units * kHeadDim;
+    const size_t row = (size_t)units * kHeadDim, ring_bytes = (size_t)ring_row * 4;
     const int rows_src = store ? S : P, rows_dst = store ? P : S;
-    if (overlap2(st, S * row * kHeadDim * 4, codes, P * row * kHeadDim) ||
-        overlap2(st, S * row * kHeadDim * 4, scales, P * row * 4) ||
-        overlap2(codes, P * row * kHeadDim, scales, P * row * 4) ||
-        (ring_row > 0 && overlap2(ring_src, (size_t)rows_src * ring_row * 4, ring_dst,
-                                  (size_t)rows_dst * ring_row * 4)))
-        return KDA_ERR_STATE_ALIAS;
+    const Span spans[] = {{st, S * row * kHeadDim * 4},
+                          {codes, P * row * kHeadDim},
+                          {scales, P * row * 4},
+                          {ring_src, rows_src * ring_bytes},
+                          {ring_dst, rows_dst * ring_bytes}};
+    if (any_overlap(spans)) return KDA_ERR_STATE_ALIAS;
     if (const int sd = check_stream_device(stream)) return sd;
     StateQ8Args a{};
     a.state_in = state; a.state_out = state_out; a.codes = codes; a.scales = scales;
@@ -985,8 +995,11 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
     if (!aligned16(q_raw) || !aligned16(k_raw) || !aligned16(v_raw) || !aligned16(ring_pool) ||
         (gate_mode == KDA_GATE_PER_CHANNEL && (!aligned16(f_raw) || !aligned16(dt_bias))))
         return KDA_ERR_ALIGN;
-    const size_t rows = (size_t)P * H * Dv;
-    if (overlap2(codes, rows * kHeadDim, scales, rows * 4)) return KDA_ERR_STATE_ALIAS;
+    const size_t rows = (size_t)P * H * Dv, channels = 2 * (size_t)Hk * kHeadDim + (size_t)H * Dv;
+    const Span spans[] = {{codes, rows * kHeadDim},
+                          {scales, rows * 4},
+                          {ring_pool, P * channels * (K - 1) * 4}};
+    if (any_overlap(spans)) return KDA_ERR_STATE_ALIAS;
     if (const int sd = check_stream_device(stream)) return sd;
     DecodeQ8Args a{};
     DecodeArgs& d = a.d;

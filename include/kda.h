@@ -618,7 +618,8 @@ int kda_state_load_q8(const void* codes, const float* scales, float* state, int 
  * or an earlier row writes is left out (40013, above; padding and rows with a slot past the pool read
  * and write none).  Grouped queries and wide value heads may
  * roll the ring in place here.  q_raw, k_raw, v_raw, conv_w, ring_pool, codes, scales, norm_w,
- * gate_raw, y and, with KDA_GATE_PER_CHANNEL, f_raw and dt_bias are [16B].
+ * gate_raw, y and, with KDA_GATE_PER_CHANNEL, f_raw and dt_bias are [16B].  Overlapping codes, scales
+ * and rings return 40003.
  * Unlike kda_decode_fused, a T-token call is not T one-token calls bit for bit: those round the
  * state T times.  A call's outputs do not depend on the other rows of the batch.  With T <= 4 its
  * first keep[n] rows are those of a call of keep[n] tokens, bit for bit; calls of more tokens differ

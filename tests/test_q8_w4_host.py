@@ -145,3 +145,19 @@ def test_pool_format_names(kda):
     p = mixer.StatePoolQ8(3, 4, "cpu", Hk=2, Dv=256, K=3, fmt="e4m3")
     assert p.codes.shape == (3, 4, 256, 128) and p.codes.dtype == torch.float8_e4m3fn
     assert p.scales.shape == (3, 4, 256) and p.ring.shape == (3, 2 * 2 * 128 + 4 * 256, 2)
+
+
+@pytest.mark.parametrize("move", [_store, _load])
+@pytest.mark.parametrize("kw", [
+    dict(ring=FAKE), dict(ring=FAKE + 4 * 2 * 128 * 128 * 4 - 16), dict(ring=FAR),
+    dict(ring=FAR + 8 * 2 * 128 * 128 - 16), dict(ring=2 * FAR), dict(ring_pool=FAKE),
+    dict(ring_pool=FAR + 64), dict(ring_pool=2 * FAR + 8 * 2 * 128 * 4 - 16)])
+def test_rings_apart_from_states_and_codes(kda, move, kw):
+    """The rings overlap no other array of the call: states of 4 rows, codes and scales of 8 slots."""
+    assert move(kda, **{"ring_row": 8, "ring": FAR * 3, "ring_pool": FAR * 4, **kw}) == 40003
+
+
+@pytest.mark.parametrize("kw", [dict(ring=FAR), dict(ring=FAR + 8 * 2 * 128 * 128 - 16),
+                                dict(ring=2 * FAR), dict(ring=2 * FAR - 8 * 768 * 3 * 4 + 16)])
+def test_decode_ring_pool_apart_from_codes_and_scales(kda, kw):
+    assert _decode(kda, **kw) == 40003
