@@ -140,43 +140,43 @@ bool arity(const char* name, Py_ssize_t n, Py_ssize_t want) {
     return false;
 }
 
-// (store, state, codes, scales, state_rows, slots, N, H, Dv, ring, ring_pool, stream)
-PyObject* state_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!arity("state_move", n, 12)) return nullptr;
+// (state, codes, scales, state_rows, slots, N, H, Dv, ring, ring_pool, stream)
+template <bool STORE>
+PyObject* state_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity(STORE ? "state_store_q8" : "state_load_q8", n, 11)) return nullptr;
     Call c;
-    const bool store = a[0] == Py_True;
-    const int64_t N = c.integer(a[6]), H = c.integer(a[7]), Dv = c.integer(a[8]);
+    const int64_t N = c.integer(a[5]), H = c.integer(a[6]), Dv = c.integer(a[7]);
     int format = 0;
     int64_t P = 0, S = 0, ring_row = 0;
-    void* codes = c.pool(a[2], H, Dv, &format, &P);
-    if (const at::Tensor* t = c.tensor(a[1], "state")) {
+    void* codes = c.pool(a[1], H, Dv, &format, &P);
+    if (const at::Tensor* t = c.tensor(a[0], "state")) {
         if (t->dim() != 4 || t->size(1) != H || t->size(2) != Dv || t->size(3) != kHead)
             c.fail(PyExc_ValueError, "state", "expected a [rows, H, Dv, 128] tensor");
         S = t->size(0);
     }
-    void* state = c.take(a[1], "state", ScalarType::Float, -1);
-    void* scales = c.take(a[3], "scales", ScalarType::Float, P * H * Dv);
-    void* rows = c.maybe(a[4], "state rows", ScalarType::Int, N);
-    void* slots = c.maybe(a[5], "slots", ScalarType::Int, N);
+    void* state = c.take(a[0], "state", ScalarType::Float, -1);
+    void* scales = c.take(a[2], "scales", ScalarType::Float, P * H * Dv);
+    void* rows = c.maybe(a[3], "state rows", ScalarType::Int, N);
+    void* slots = c.maybe(a[4], "slots", ScalarType::Int, N);
     void *ring = nullptr, *ring_pool = nullptr;
-    if ((a[9] == Py_None) != (a[10] == Py_None)) {
+    if ((a[8] == Py_None) != (a[9] == Py_None)) {
         c.fail(PyExc_ValueError, "ring, ring_pool", "both or neither");
-    } else if (a[9] != Py_None) {
-        const at::Tensor* r = c.tensor(a[9], "ring");
-        const at::Tensor* p = c.tensor(a[10], "ring_pool");
+    } else if (a[8] != Py_None) {
+        const at::Tensor* r = c.tensor(a[8], "ring");
+        const at::Tensor* p = c.tensor(a[9], "ring_pool");
         if (r != nullptr && p != nullptr) {
             if (r->dim() < 2 || p->dim() < 2 || r->size(0) != S || p->size(0) != P)
                 c.fail(PyExc_ValueError, "ring, ring_pool", "expected one row for each state and slot");
             else
                 ring_row = S > 0 ? r->numel() / S : (P > 0 ? p->numel() / P : 0);
         }
-        ring = c.take(a[9], "ring", ScalarType::Float, S * ring_row);
-        ring_pool = c.take(a[10], "ring_pool", ScalarType::Float, P * ring_row);
+        ring = c.take(a[8], "ring", ScalarType::Float, S * ring_row);
+        ring_pool = c.take(a[9], "ring_pool", ScalarType::Float, P * ring_row);
     }
-    void* stream = c.stream(a[11]);
+    void* stream = c.stream(a[10]);
     if (c.failed) return nullptr;
     return status([&] {
-        return store ? kda_state_store_q8((float*)state, codes, (float*)scales, format, (int*)rows,
+        return STORE ? kda_state_store_q8((float*)state, codes, (float*)scales, format, (int*)rows,
                                           (int*)slots, (int)S, (int)P, (int)N, (int)H, (int)kHead, (int)Dv,
                                           (float*)ring, (float*)ring_pool, ring_row, stream)
                      : kda_state_load_q8(codes, (float*)scales, (float*)state, format, (int*)slots,
@@ -316,7 +316,8 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyMethodDef methods[] = {
-    {"state_move", (PyCFunction)(void (*)(void))guarded<state_move>, METH_FASTCALL, nullptr},
+    {"state_store_q8", (PyCFunction)(void (*)(void))guarded<state_q8<true>>, METH_FASTCALL, nullptr},
+    {"state_load_q8", (PyCFunction)(void (*)(void))guarded<state_q8<false>>, METH_FASTCALL, nullptr},
     {"decode_fused_q8", (PyCFunction)(void (*)(void))guarded<decode_fused_q8>, METH_FASTCALL, nullptr},
     {"proj_w4", (PyCFunction)(void (*)(void))guarded<proj_w4>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

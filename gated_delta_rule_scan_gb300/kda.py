@@ -551,14 +551,14 @@ def kda_state_store_q8(state, codes, scales, *, N, H, src=None, dst=None, Dv=HEA
                        ring_pool=None, stream=None):
     """Rows src[n] of state [S, H, Dv, 128] (and of ring) into pool slots dst[n].  codes: int8 or
     float8_e4m3fn, which names the format; src, dst: int32 device [N] or None (n)."""
-    _native("state_move", codes, stream, True, state, codes, scales, src, dst, N, H, Dv, ring,
+    _native("state_store_q8", codes, stream, state, codes, scales, src, dst, N, H, Dv, ring,
             ring_pool)
 
 
 def kda_state_load_q8(codes, scales, state, *, N, H, src=None, dst=None, Dv=HEAD_DIM,
                       ring_pool=None, ring=None, stream=None):
     """Pool slots src[n] into rows dst[n] of state (and of ring); see kda_state_store_q8."""
-    _native("state_move", codes, stream, False, state, codes, scales, dst, src, N, H, Dv, ring,
+    _native("state_load_q8", codes, stream, state, codes, scales, dst, src, N, H, Dv, ring,
             ring_pool)
 
 

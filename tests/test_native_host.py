@@ -41,7 +41,7 @@ with FakeTensorMode():
     codes, scales, state = cuda(3, 2, 1, 128, 128, dtype=torch.int8), cuda(2, 1, 128), cuda(2, 1, 128, 128)
     for call, t in (
             (lambda x: refused(native.proj_w4, x, [w], [s], None, [o], 32, None, 0), x),
-            (lambda c: refused(native.state_move, True, state, c, scales, None, None, 2, 1, 128, None,
+            (lambda c: refused(native.state_store_q8, state, c, scales, None, None, 2, 1, 128, None,
                                None, 0), codes),
             (lambda x: refused(native.decode_fused_q8, x, *[x] * 8, codes[0], scales, x, x, x, None, None,
                                None, 2, 1, 1, 1, 128, 4, 0, -5.0, 1e-6, 1.0, 1e-6, 0), x)):
@@ -144,3 +144,23 @@ def test_without_torchs_headers_the_library_is_built(scratch_build, monkeypatch)
         assert build.build() == build.LIB_PATH
     assert "libkda.so" in made and os.path.exists(build.LIB_PATH)
     assert not os.path.exists(build.NATIVE_PATH)
+
+
+def test_errors_name_the_entry_that_refused(monkeypatch):
+    import torch
+    from gated_delta_rule_scan_gb300 import kda
+
+    class Refuses:
+        def __getattr__(self, name):
+            return lambda *args: 40005
+    monkeypatch.setattr(kda, "_kda_native", Refuses())
+    t = torch.zeros(1)
+    for name, call in (
+            ("kda_state_store_q8", lambda: kda.kda_state_store_q8(t, t, t, N=1, H=1)),
+            ("kda_state_load_q8", lambda: kda.kda_state_load_q8(t, t, t, N=1, H=1)),
+            ("kda_decode_fused_q8", lambda: kda.kda_decode_fused_q8(*[t] * 14, N=1, T=1, H=1)),
+            ("kda_proj_w4", lambda: kda.kda_proj_w4(t, [t], [t], [t], group=32))):
+        assert name in kda.EXPORTED
+        with pytest.raises(kda.KdaError, match=name + r"\b") as e:
+            call()
+        assert e.value.status == 40005
