@@ -566,7 +566,10 @@ kda_proj_w4_wide_kernel(const __grid_constant__ WideMaps maps, const __grid_cons
                         if (lane == 0 && ok) seen = atomicAdd(count, 1);
                         write = __shfl_sync(0xffffffffu, seen, 0) == others;
                     }
+                    // lane 0 has seen the other parts' counts: its fence and the warp's barrier order
+                    // every lane's reads of them behind that (a shuffle orders no memory)
                     __threadfence();
+                    __syncwarp();
                 }
                 if (write && ok) {
 #pragma unroll 1
