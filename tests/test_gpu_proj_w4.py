@@ -265,3 +265,11 @@ def test_first_calls_of_many_threads():
         _check(c, o)
     for c, o in zip(cases, got):
         assert all(torch.equal(a, b) for a, b in zip(_gpu(c), o))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("x,zeros", [("f32", False), ("f32", True), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("t", [17, 24, 64, 65, 200])
+def test_batches_by_f32_scales(t, x, zeros, group):
+    c = _case(t * 13 + group, t, 384, (130, 1, 77), group, x, "f32", zeros)
+    _check(c, _gpu(c))
