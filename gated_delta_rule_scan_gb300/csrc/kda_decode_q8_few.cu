@@ -12,7 +12,7 @@
 // state are a matrix product, 128 columns x 128 keys by 2 T vectors: its left side are the codes
 // themselves, whole numbers or e4m3 values, exact in f16, the row scale going on afterwards; its
 // right side the vectors A_t k_t and A_t q_t, each times the power of two that brings its largest
-// element (read to 8 bits) to [2^11, 2^13), as f16 hi + lo: an element is held to 2^-22 of itself or
+// element (read to 8 bits) to [2^11, 2^13), as f16 hi + lo: an element is held to 2^-23 of itself or
 // 2^-36 of the vector's largest, whichever is more, and mma.sync sums in f32.  (One power of two for
 // all vectors loses the readout of a state that has faded, where nothing new covers it: relative
 // errors of 2e-2 behind a decay of e^-20, of 1 behind e^-25.)  Decays are at most 1, which keeps the
@@ -27,9 +27,10 @@
 // pieces; the same words are the MMA's left side and, unpacked, the state.  Everything a block reads
 // is asked for at once, before its slots have been looked over; codes and output gates wait in shared
 // memory (in registers: 4 blocks an SM and spills, 45 us at one token and 85 at four, 64 x 64 heads).
-// There it runs 39.5 us at one token, 48 at two, 57 at three and 62 at four, where its bytes need 27 to 32; the
-// other form takes 53, 70 and 100.  What is left is the wait for a block's first bytes, about a third of its
-// life, overlapped by four other blocks only.  (Persistent blocks that fetch the next unit by bulk
+// There it runs 40 us at one token, 48 at two, 60 at three and 66 at four, where its bytes need 27 to 32; the
+// other form takes 53 at one, 70 at two and 118 at five.  (The vectors' own powers of two cost 0.5 us at one
+// token and 3.5 at four, 4 % more instructions.)  What is left is the wait for a block's first bytes, about
+// a third of its life, overlapped by four other blocks only.  (Persistent blocks that fetch the next unit by bulk
 // copies meanwhile: 62 us; issuing some fifteen small copies a unit takes longer than the wait.)
 #include <cuda_fp16.h>
 
@@ -43,8 +44,9 @@ constexpr int kThreads = 128;
 constexpr int kVecBytes = 320;               // one f16 vector: 256 bytes, and 64 against bank conflicts
 constexpr int kDotRow = 136;                 // floats: four lanes' columns land in different banks
 constexpr int kVecExp = 11;                  // exponent of a vector's largest element in f16
-constexpr int kMinBlocks = 5;                // an SM: 39.5 us at one token and 62 at four, 64 x 64 heads
-                                             // (4: 43 and 67, 6: 40 and 71)
+constexpr int kMinBlocks = 5;                // an SM: 64 x 64 heads, with one power of two for all
+                                             // vectors, 39.5 us at one token and 62 at four (4
+                                             // blocks: 43 and 67, 6: 40 and 71)
 
 // Key i is byte e of word m (0 .. 7) of lane c: i = 64 (m / 4) + 16 c + 4 (m % 4) + e.
 __device__ __forceinline__ int key_word(int i) { return ((i >> 6) << 2) | ((i >> 2) & 3); }

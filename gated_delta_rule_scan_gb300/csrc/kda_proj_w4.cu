@@ -17,8 +17,9 @@
 // then loses nothing, and a code needs no more than a logical operation to become a number (taking 8
 // off each code first: 22.8 us against 19.1 at one row x 6144, 64 heads).  hi + lo is x within 2^-23
 // of the element's own magnitude or 2^-27 of the largest of the 128, whichever is more.
-//     5 rows or more of a bf16 x take hi alone (8 bits fit, in any order of magnitude), for half the
-// MMA's columns.  Its sums are rounded, so there the codes have 8 taken off first.
+//     5 rows or more of a bf16 x take hi alone, for half the MMA's columns: its 8 bits are exact down to
+// 2^-31 of the largest of the 128, and smaller elements are off by at most 2^-39 of it.  Its sums are
+// rounded, so there the codes have 8 taken off first.
 //
 // The form for few rows: up to 16, by the rule at its launch.  The weights' bytes are read once and bound the
 // launch, so the kernel is built around their stream: a warp takes 16 weight rows x 128 k (1 KB of
@@ -34,9 +35,9 @@
 // turn; its warps split K, and their partial sums meet in shared memory in warp order.  Where x of
 // all of K does not fit, the CTAs of a cluster split K further and add their sums through
 // distributed shared memory in rank order.  No atomics: results do not depend on timing.
-// At 64 heads x 6144 and groups of 128: one row 17.9 us (4.4 TB/s of codes and scales: the shared
-// loads, MMAs and logical operations of a chunk cost about half its bytes' time again), four rows
-// 20.7, eight bf16 rows 25.0, five f32 rows 28.
+// At 64 heads x 6144 and groups of 128: one row 17.9 to 20.3 us from box to box (4.4 to 3.9 TB/s of
+// codes and scales: the shared loads, MMAs and logical operations of a chunk cost about half its bytes'
+// time again), four rows 20.7 to 22.6, eight bf16 rows 25.0 to 25.8, five f32 rows 28.
 #include <cuda_fp16.h>
 
 #include "kda_device.cuh"
@@ -83,7 +84,8 @@ __host__ __device__ inline W4Smem w4_smem(int chunks, int cols, int group, int t
 
 // Nibbles 0 and 4 (lo) or 1 and 5 (hi) of a word as f16 pairs.  Alone in its place of the mantissa,
 // with no exponent, a code q is the f16 number q 2^-24 or 16 q 2^-24.  CENTRED: q - 8, from 1024 + q
-// and 1024 + 16 q (the code or-ed into the mantissa of 1024); both corrections are exact.
+// and 1024 + 16 q (the code or-ed into the mantissa of 1024: Kim, Henry, Fahim and Awadalla, "Who Says
+// Elephants Can't Run", 2022); both corrections are exact.
 template <bool CENTRED>
 __device__ __forceinline__ uint32_t nib_lo(uint32_t w) {
     if constexpr (!CENTRED) return w & 0x000f000fu;

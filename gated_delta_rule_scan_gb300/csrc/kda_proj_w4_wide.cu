@@ -1,11 +1,13 @@
 // kda_proj_w4_wide.cu -- kda_proj_w4 for batches: the products on the tcgen05 tensor cores.
 //
 // Mathematics.  Codes minus 8 are whole numbers, exact in f16; x is scaled by a power of two per
-// token (its largest magnitude to [2^7, 2^8)) and split into f16 hi + lo (22 significant bits; a
-// bf16 x needs hi only).  The tensor cores sum code * x over one group of G k into f32, and the
+// token (its largest magnitude to [2^7, 2^8)) and split into f16 hi + lo (22 significant bits; of a
+// bf16 x hi alone, whose 8 bits are exact down to 2^-24 of that magnitude; both are off by at most
+// 2^-32 of it below).  The tensor cores sum code * x over one group of G k into f32, and the
 // group's scale multiplies that sum in f32:
 //     acc[r][s] += c[r][g] * D_g[r][s] + (8 - z[r][g]) c[r][g] * xsum_g[s],
-// so neither weights nor scales are ever rounded, whatever their type.
+// so neither weights nor scales are ever rounded, whatever their type.  (The two terms are rounded
+// apart: a group whose codes all equal its zero point leaves their rounding errors, not 0.)
 //
 // What bounds it: the codes' bytes from HBM up to about 48 rows, then the tensor cores (every
 // product is made twice, for hi and lo).  Layout: a tile is 128 weight rows (the MMA's M = TMEM
@@ -27,8 +29,8 @@
 // cut between blocks.  Its parts meet in the workspace, added in block order whoever adds them, so
 // results do not depend on timing: usually the block that holds a tile's first units ends last,
 // finds the other parts there, and adds them to its registers.
-// At 64 heads x 6144 with groups of 128: 16 rows 34 us, 64 rows 45.5 (the tensor pipe active 41 % of
-// the time), 256 rows 116 (60 %).
+// At 64 heads x 6144 with groups of 128: 16 rows 34 us, 64 rows 45 (the tensor pipe active 41 % of
+// the time), 256 rows 117 (60 %); of a bf16 x, half the products, 64 rows 43, 256 rows 101.
 #include <cuda_fp16.h>
 
 #include "kda_chunk_common.cuh"
@@ -204,7 +206,8 @@ __global__ void __launch_bounds__(kSplitThreads) kda_proj_w4_split_kernel(
 
 // ---- the products ---------------------------------------------------------------------------
 
-// 8 codes as four f16 pairs of whole numbers -8 .. 7 (k order 0 4 | 1 5 | 2 6 | 3 7)
+// 8 codes as four f16 pairs of whole numbers -8 .. 7 (k order 0 4 | 1 5 | 2 6 | 3 7), each or-ed into
+// the mantissa of 1024 (the publication named in kda_proj_w4.cu)
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t* o) {
     const __half2 k1032 = __float2half2_rn(1032.0f), k16 = __float2half2_rn(0.0625f),
                   k72 = __float2half2_rn(-72.0f);

@@ -8,8 +8,9 @@
 // 4l .. 4l+3, so a row is one 512-byte access on the f32 side and one 128-byte access on the code
 // side, and the row maximum is one warp-wide integer maximum over magnitude bits.  The warp's 16
 // rows are issued in two batches of 8, so that 4 KB of each warp is in flight.
-// The slots are checked while the loads are in flight: only the stores wait for the answer.
-// 64 sequences x 64 heads: 59.5 us a store, 59.9 us a load, 93 and 92 % of the copy bandwidth.
+// A block looks its row's indices over before its first access; other blocks of the SM stream
+// meanwhile.  64 sequences x 64 heads: 59.5 us a store, 59.9 us a load, 93 and 92 % of the copy
+// bandwidth.
 #include "kda_q8.cuh"
 
 namespace kda {

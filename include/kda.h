@@ -622,8 +622,11 @@ int kda_state_load_q8(const void* codes, const float* scales, float* state, int 
  * and rings return 40003.
  * Unlike kda_decode_fused, a T-token call is not T one-token calls bit for bit: those round the
  * state T times.  A call's outputs do not depend on the other rows of the batch.  With T <= 4 its
- * first keep[n] rows are those of a call of keep[n] tokens, bit for bit; calls of more tokens differ
- * from those in the last bits of f32.
+ * first keep[n] rows are those of a call of keep[n] tokens, bit for bit, and among calls of more than 4
+ * tokens likewise; between the two they differ in the last bits of f32.
+ * Precision: f32 throughout; with T <= 4 (and gate_lb <= 0 or a per-head gate) the decayed k and q rows
+ * enter their products with the incoming state within 2^-23 of an element or 2^-36 of the row's
+ * largest, whatever the decay.
  */
 int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw, int raw_dtype,
                         const float* conv_w, float* ring_pool, const float* f_raw,
@@ -653,7 +656,10 @@ int kda_decode_fused_q8(const void* q_raw, const void* k_raw, const void* v_raw,
  *              may be 0 (then NULL is accepted); 40009 otherwise.  Calls sharing it must not overlap.
  * Precision: codes, scales and zero points enter exactly; x enters within 2^-22 of an element's
  * magnitude plus 2^-25 of the largest of its 128 k (forms for few rows) or 2^-31 of its row's largest
- * (batches); sums are f32.  One token row's result depends on the other rows of the call only
+ * (batches), either taken as 2^-100 where it is smaller; sums are f32.  With zero points the batches'
+ * form adds c (8 - z) sum x to c sum (q - 8) x, each in f32: a group whose codes all equal its zero
+ * point leaves their rounding errors instead of 0.  Batches are calls of more than 16 rows, and of 5 to
+ * 16 where the weights are many.  One token row's result depends on the other rows of the call only
  * through the choice of form for t rows.  A NaN or an infinity in x makes every output of its token
  * row NaN or infinite, and no other row's.
  */
