@@ -120,7 +120,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if native is not None:
         try:
             _link_native(*native.result())
-        except (OSError, RuntimeError) as e:
+        except (ImportError, OSError, RuntimeError) as e:
             # an older one is for other sources or another torch
             for p in (NATIVE_PATH, NATIVE_STAMP):
                 if os.path.exists(p):

@@ -35,7 +35,7 @@
 // turn; its warps split K, and their partial sums meet in shared memory in warp order.  Where x of
 // all of K does not fit, the CTAs of a cluster split K further and add their sums through
 // distributed shared memory in rank order.  No atomics: results do not depend on timing.
-// At 64 heads x 6144 and groups of 128: one row 17.9 to 20.3 us from box to box (4.4 to 3.9 TB/s of
+// At 64 heads x 6144 and groups of 128: one row 17.9 to 20.3 us from machine to machine (4.4 to 3.9 TB/s of
 // codes and scales: the shared loads, MMAs and logical operations of a chunk cost about half its bytes'
 // time again), four rows 20.7 to 22.6, eight bf16 rows 25.0 to 25.8, five f32 rows 28.
 #include <cuda_fp16.h>

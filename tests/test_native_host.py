@@ -134,11 +134,12 @@ def test_a_change_of_torch_rebuilds_the_marshalling(scratch_build, monkeypatch):
     assert made == []
 
 
-def test_without_torchs_headers_the_library_is_built(scratch_build, monkeypatch):
+@pytest.mark.parametrize("error", [RuntimeError, FileNotFoundError, ImportError])
+def test_without_torchs_headers_the_library_is_built(scratch_build, monkeypatch, error):
     build, made = scratch_build
 
     def fails():
-        raise RuntimeError("no headers")
+        raise error("no headers")
     monkeypatch.setattr(build, "_compile_native", fails)
     with pytest.warns(UserWarning, match="no headers"):
         assert build.build() == build.LIB_PATH
