@@ -1073,6 +1073,169 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
     return cuda_status(launch_proj_w4(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype) {
+    const int m = value_subheads(Dk, Dv);
+    if (m == 0 || N < 0 || total_T < 0 || H <= 0 || Hk < 1 || Hk > H) return 0;
+    (void)raw_dtype;
+    return 0;
+}
+
+// Contract checks of the linear attention entries and their argument block.
+static int linattn_build(const void* q, long q_stride, const void* k, long k_stride, const void* v,
+                         long v_stride, int raw_dtype, const float* log_decay, float* o,
+                         const SeqLayout& seq, int H, int Hk, int Dk, int Dv, float scale, LinArgs& a) {
+    const int m = value_subheads(Dk, Dv);
+    if (m == 0) return KDA_ERR_HEAD_DIM;
+    if (seq.N < 0 || seq.N > kMaxGridY || seq.total_rows < 0 || seq.total_rows >= (1L << 31) || H <= 0 ||
+        (long)H * m > kMaxGridY || Hk < 1 || Hk > H)
+        return KDA_ERR_SHAPE;
+    if (raw_dtype != KDA_DTYPE_F32 && raw_dtype != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
+    const long per16 = raw_dtype == KDA_DTYPE_BF16 ? 8 : 4, qk = (long)Hk * kHeadDim, vw = (long)H * Dv;
+    if (q_stride < qk || k_stride < qk || v_stride < vw || q_stride % per16 || k_stride % per16 ||
+        v_stride % per16 || q_stride >= (1L << 31) || k_stride >= (1L << 31) || v_stride >= (1L << 31))
+        return KDA_ERR_SHAPE;
+    if (seq.N > 0 && !log_decay) return KDA_ERR_NULL;
+    if (seq.total_rows > 0) {
+        if (!q || !k || !v || !o) return KDA_ERR_NULL;
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return KDA_ERR_ALIGN;
+    }
+    a.q = q; a.k = k; a.v = v; a.bf16 = raw_dtype == KDA_DTYPE_BF16;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.log_decay = log_decay; a.o = o; a.seq = seq; a.H = H; a.Hk = Hk; a.m = m; a.scale = scale;
+    return KDA_OK;
+}
+
+static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_out,
+                                const int* cu_host, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (a.seq.N == 0) return KDA_OK;
+    if (!state_out) return KDA_ERR_NULL;
+    if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_ALIGN;
+    const size_t sb = (size_t)a.seq.N * a.H * a.m * kHeadDim * kHeadDim * sizeof(float);
+    if (state_in && overlap(state_in, state_out, sb)) return KDA_ERR_STATE_ALIAS;
+    (void)cu_host;
+    (void)workspace;
+    (void)workspace_bytes;
+    if (const int sd = check_stream_device(stream)) return sd;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.err = dev_err_ptr();
+    return cuda_status(launch_linattn_seq(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_linattn_prefill(const void* q, long q_stride, const void* k, long k_stride, const void* v,
+                        long v_stride, int raw_dtype, const float* log_decay, const float* state_in,
+                        float* state_out, float* o, int N, int T, int H, int Hk, int Dk, int Dv,
+                        float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0) return KDA_ERR_SHAPE;
+    LinArgs a{};
+    const int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype, log_decay, o,
+                                 SeqLayout{nullptr, T, N, (long)N * T}, H, Hk, Dk, Dv, scale, a);
+    return rc ? rc : linattn_prefill_impl(a, state_in, state_out, nullptr, workspace, workspace_bytes, stream);
+}
+
+int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long k_stride,
+                               const void* v, long v_stride, int raw_dtype, const float* log_decay,
+                               const float* state_in, float* state_out, float* o,
+                               const int* cu_seqlens, const int* cu_seqlens_host, int N, int total_T,
+                               int H, int Hk, int Dk, int Dv, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    LinArgs a{};
+    int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype, log_decay, o,
+                           SeqLayout{cu_seqlens, 0, N, (long)total_T}, H, Hk, Dk, Dv, scale, a);
+    if (rc) return rc;
+    if (N > 0) {
+        if (cu_seqlens == nullptr) return KDA_ERR_NULL;
+        rc = check_cu(cu_seqlens_host, N, total_T);
+        if (rc) return rc;
+    }
+    return linattn_prefill_impl(a, state_in, state_out, cu_seqlens_host, workspace, workspace_bytes, stream);
+}
+
+int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_stride, const void* v,
+                       long v_stride, int raw_dtype, const float* log_decay, float* pool,
+                       const int* slots, const int* slots_out, const int* keep, float* o, int P, int N,
+                       int T, int H, int Hk, int Dk, int Dv, float scale, void* stream) {
+    if (T < 1 || T > kDecodeMaxT || P < 0) return KDA_ERR_SHAPE;
+    LinArgs a{};
+    const int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype, log_decay, o,
+                                 SeqLayout{nullptr, T, N, (long)N * T}, H, Hk, Dk, Dv, scale, a);
+    if (rc) return rc;
+    if (slots == nullptr && N > P) return KDA_ERR_SHAPE;
+    if (N == 0) return KDA_OK;
+    if (!pool) return KDA_ERR_NULL;
+    if (!aligned16(pool)) return KDA_ERR_ALIGN;
+    if (const int sd = check_stream_device(stream)) return sd;
+    a.state_in = a.state_out = pool;
+    a.slots = slots; a.slots_out = slots_out; a.keep = keep; a.pool_rows = P;
+    a.err = dev_err_ptr();
+    return cuda_status(launch_linattn_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_draft_accept(const void* target, long target_stride, const void* draft, long draft_stride,
+                     int prob_dtype, const int* tokens, const float* u, const float* r,
+                     const int* n_draft, int* keep, int* out_tokens, int N, int T, int V,
+                     void* stream) {
+    if (N < 0 || N > kMaxGridY || T < 1 || T > kDecodeMaxT || V < 1 || target_stride < V ||
+        target_stride >= (1L << 40))
+        return KDA_ERR_SHAPE;
+    if (T == 1) draft = nullptr;
+    if (draft && (draft_stride < V || draft_stride >= (1L << 40))) return KDA_ERR_SHAPE;
+    if (prob_dtype != KDA_DTYPE_F32 && prob_dtype != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
+    if (N == 0) return KDA_OK;
+    if (!target || !r || !keep || !out_tokens || (T > 1 && (!tokens || !u))) return KDA_ERR_NULL;
+    if (const int sd = check_stream_device(stream)) return sd;
+    AcceptArgs a{};
+    a.target = target; a.draft = draft; a.bf16 = prob_dtype == KDA_DTYPE_BF16;
+    a.target_stride = target_stride; a.draft_stride = draft_stride;
+    a.tokens = tokens; a.u = u; a.r = r; a.n_draft = n_draft; a.keep = keep; a.out_tokens = out_tokens;
+    a.N = N; a.T = T; a.V = V;
+    return cuda_status(launch_draft_accept(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_residual_rmsnorm(const void* residual, int residual_dtype, const void* block, int block_dtype,
+                         const float* block_w, const void* gate, int gate_per_row, int gate_act,
+                         float res_scale, float block_scale, const float* norm_w, void* h, void* z,
+                         int z_dtype, long rows, int F, float eps, void* stream) {
+    const int dtypes[3] = {residual_dtype, block_dtype, z_dtype};
+    for (int d : dtypes)
+        if (d != KDA_DTYPE_F32 && d != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
+    if (gate_act < KDA_ACT_NONE || gate_act > KDA_ACT_SILU || gate_per_row < 0 || gate_per_row > 1)
+        return KDA_ERR_ENUM;
+    if (rows < 0 || rows >= (1L << 31) || F < 8 || F > kResNormMaxF || F % 8 != 0) return KDA_ERR_SHAPE;
+    if (rows == 0 || (!h && !z)) return KDA_OK;
+    if (!residual || (z && !norm_w)) return KDA_ERR_NULL;
+    if (!block) block_w = nullptr, gate = nullptr;
+    const void* const ptrs[] = {residual, block, block_w, gate, norm_w, h, z};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return KDA_ERR_ALIGN;
+    const auto size = [](int dtype) { return (size_t)(dtype == KDA_DTYPE_BF16 ? 2 : 4); };
+    const size_t n = (size_t)rows * F, w = (size_t)F * 4;
+    const Span in[] = {{residual, n * size(residual_dtype)},
+                       {block, block ? n * size(block_dtype) : 0},
+                       {gate, !gate ? 0 : gate_per_row ? n * size(block_dtype) : w},
+                       {block_w, block_w ? w : 0},
+                       {norm_w, z ? w : 0}};
+    const Span hs{h, h ? n * size(residual_dtype) : 0}, zs{z, z ? n * size(z_dtype) : 0};
+    for (int i = 0; i < 5; ++i) {
+        const Span with_h[2] = {in[i], hs}, with_z[2] = {in[i], zs};
+        // the very same plane in the same type may be written over: a thread reads its elements first
+        if (any_overlap(with_h) && !(i == 0 && h == residual)) return KDA_ERR_STATE_ALIAS;
+        const bool same = (i == 1 || (i == 2 && gate_per_row)) && in[i].at == z && block_dtype == z_dtype;
+        if (any_overlap(with_z) && !same) return KDA_ERR_STATE_ALIAS;
+    }
+    const Span out[2] = {hs, zs};
+    if (any_overlap(out)) return KDA_ERR_STATE_ALIAS;
+    if (const int sd = check_stream_device(stream)) return sd;
+    ResNormArgs a{};
+    a.residual = residual; a.residual_bf16 = residual_dtype == KDA_DTYPE_BF16;
+    a.block = block; a.block_bf16 = block_dtype == KDA_DTYPE_BF16; a.block_w = block_w;
+    a.gate = gate; a.gate_per_row = gate_per_row; a.gate_act = gate_act;
+    a.res_scale = res_scale; a.block_scale = block_scale; a.norm_w = norm_w;
+    a.h = h; a.z = z; a.z_bf16 = z_dtype == KDA_DTYPE_BF16; a.rows = rows; a.F = F; a.eps = eps;
+    return cuda_status(launch_residual_rmsnorm(a, static_cast<cudaStream_t>(stream)));
+}
+
 int kda_scan_varlen_static(const float* q_hat, const float* k_hat, const float* v_hat,
                            const float* g, int gate_mode, const float* beta,
                            const float* state_in, float* state_out, float* o,

@@ -247,12 +247,54 @@ cudaError_t launch_proj_w4_wide(const ProjW4Args& a, cudaStream_t s);
 // 2-D byte tensor map over [rows, cols] with a [box_rows][64] box in the 64-byte swizzle
 bool make_tensor_map_2d_u8_sw64(CUtensorMap* m, const void* base, long rows, long cols, int box_rows);
 
+// Linear attention with one log-decay a head (kda_linattn.cu: the recurrent form; kda_linattn_chunk.cu:
+// the chunked form on tcgen05).
+struct LinArgs {
+    const void* q; const void* k; const void* v; int bf16;
+    long q_stride, k_stride, v_stride;   // elements between token rows
+    const float* log_decay;              // [H]
+    const float* state_in;               // null: zero (prefill)
+    float* state_out;
+    float* o;
+    SeqLayout seq;
+    int H; int Hk; int m;                // value heads, q/k heads, 128-wide units of a value head
+    float scale;
+    // decode on a pool (state_in == state_out): rows by slot, as in DecodeQ8Args
+    const int* slots; const int* slots_out; const int* keep; int pool_rows;
+    int* err;
+};
+cudaError_t launch_linattn_decode(const LinArgs& a, cudaStream_t s);
+cudaError_t launch_linattn_seq(const LinArgs& a, cudaStream_t s);
+
+// Verification of drafted tokens (kda_accept.cu).
+struct AcceptArgs {
+    const void* target; const void* draft; int bf16;
+    long target_stride, draft_stride;    // elements between probability rows
+    const int* tokens; const float* u; const float* r; const int* n_draft;
+    int* keep; int* out_tokens;
+    int N; int T; int V;
+};
+cudaError_t launch_draft_accept(const AcceptArgs& a, cudaStream_t s);
+
+// The norms around a block with its gate and residual (kda_resnorm.cu).
+constexpr int kResNormMaxF = 16384;      // widest row
+struct ResNormArgs {
+    const void* residual; int residual_bf16;
+    const void* block; int block_bf16;
+    const float* block_w; const void* gate; int gate_per_row; int gate_act;
+    float res_scale, block_scale;
+    const float* norm_w; void* h; void* z; int z_bf16;
+    long rows; int F; float eps;
+};
+cudaError_t launch_residual_rmsnorm(const ResNormArgs& a, cudaStream_t s);
+
 // ---- optional per-kernel timing (kda_timer.cu): a KernelTimer scoped around a launch records a
 // CUDA event before and after it on the launch stream while timing is enabled.
 enum KernelId {
     kKPrep, kKRingRoll, kKScanSeq, kKChunkOffsets, kKChunkIntra, kKChunkInter, kKRmsNorm,
     kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKStateStoreQ8, kKStateLoadQ8, kKDecodeQ8,
-    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKernelCount
+    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKDraftAccept, kKResNorm,
+    kKernelCount
 };
 class KernelTimer {
 public:

@@ -1,5 +1,6 @@
 // kda_native.cpp -- CPython marshalling of the entry points whose host time is a step's latency:
-// the decode on the 8-bit state pool, the pool's store and load, and the 4-bit projections.  One
+// the decode on the 8-bit state pool, the pool's store and load, the 4-bit projections, linear
+// attention, the verification of drafts and the norms around a block.  One
 // token's kernels run a few microseconds; checking and unpacking 17 to 28 tensors attribute by
 // attribute in Python took 9 to 16 us a call, here it takes about one.  Each function checks that
 // every tensor is a contiguous CUDA tensor of the right type and size on one device (ValueError or
@@ -59,6 +60,63 @@ struct Call {
             PyErr_Format(PyExc_ValueError, "%s: expected %lld elements, got %lld", name,
                          (long long)numel, (long long)t->numel());
         }
+        return failed ? nullptr : t->data_ptr();
+    }
+    // a required [rows, width] tensor of `type` whose rows may lie apart; *stride: elements between them
+    void* rows2d(PyObject* o, const char* name, ScalarType type, int64_t rows, int64_t width, long* stride) {
+        const at::Tensor* t = tensor(o, name);
+        if (t == nullptr) return nullptr;
+        *stride = (long)width;
+        if (!t->is_cuda()) {
+            fail(PyExc_ValueError, name, "expected a CUDA tensor");
+        } else if (t->scalar_type() != type) {
+            failed = true;
+            PyErr_Format(PyExc_TypeError, "%s: expected %s, got %s", name, c10::toString(type),
+                         c10::toString(t->scalar_type()));
+        } else if (t->dim() != 2 || t->size(0) != rows || t->size(1) != width) {
+            failed = true;
+            PyErr_Format(PyExc_ValueError, "%s: expected a [%lld, %lld] tensor", name, (long long)rows,
+                         (long long)width);
+        } else if (width > 1 && t->stride(1) != 1) {
+            fail(PyExc_ValueError, name, "expected rows of adjacent elements");
+        } else {
+            if (device == -2) device = t->get_device();
+            if (t->get_device() != device) {
+                failed = true;
+                PyErr_Format(PyExc_ValueError, "%s: expected a tensor on cuda:%d, got cuda:%d", name, device,
+                             (int)t->get_device());
+            }
+            if (rows > 1) *stride = (long)t->stride(0);
+        }
+        return failed ? nullptr : t->data_ptr();
+    }
+    // a required [a, b, width] tensor whose a * b rows lie evenly apart; *stride: elements between them
+    void* rows3d(PyObject* o, const char* name, ScalarType type, int64_t a, int64_t b, int64_t width,
+                 long* stride) {
+        const at::Tensor* t = tensor(o, name);
+        if (t == nullptr) return nullptr;
+        if (t->dim() != 3 || t->size(0) != a || t->size(1) != b || t->size(2) != width) {
+            failed = true;
+            PyErr_Format(PyExc_ValueError, "%s: expected a [%lld, %lld, %lld] tensor", name, (long long)a,
+                         (long long)b, (long long)width);
+            return nullptr;
+        }
+        if (!t->is_cuda()) {
+            fail(PyExc_ValueError, name, "expected a CUDA tensor");
+            return nullptr;
+        }
+        if (device == -2) device = t->get_device();
+        const int64_t row = b > 1 ? t->stride(1) : a > 1 ? t->stride(0) : width;
+        if (t->scalar_type() != type) {
+            failed = true;
+            PyErr_Format(PyExc_TypeError, "%s: expected %s, got %s", name, c10::toString(type),
+                         c10::toString(t->scalar_type()));
+        } else if (t->get_device() != device) {
+            fail(PyExc_ValueError, name, "expected a tensor on the other tensors' device");
+        } else if ((width > 1 && t->stride(2) != 1) || (a > 1 && b > 1 && t->stride(0) != b * row)) {
+            fail(PyExc_ValueError, name, "expected rows of adjacent elements, evenly apart");
+        }
+        *stride = (long)row;
         return failed ? nullptr : t->data_ptr();
     }
     void* maybe(PyObject* o, const char* name, ScalarType type, int64_t numel) {
@@ -298,6 +356,173 @@ PyObject* proj_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// What the linear attention calls share: q, k, v rows and their strides.
+struct LinRows {
+    int dtype = 0;
+    long qs = 0, ks = 0, vs = 0;
+    void *q, *k, *v;
+    LinRows(Call& c, PyObject* const* a, int64_t rows, int64_t H, int64_t Hk, int64_t Dv) {
+        const ScalarType t = c.float_type(a[0], "q", &dtype);
+        q = c.rows2d(a[0], "q", t, rows, Hk * kHead, &qs);
+        k = c.rows2d(a[1], "k", t, rows, Hk * kHead, &ks);
+        v = c.rows2d(a[2], "v", t, rows, H * Dv, &vs);
+    }
+};
+
+// (q, k, v, log_decay, state_in or None, state_out, o, workspace or None, cu_seqlens or None,
+//  cu_seqlens_host or None, N, T, H, Hk, Dv, scale, stream); T: tokens of each sequence without
+// cu_seqlens, ignored with it
+PyObject* linattn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity("linattn_prefill", n, 17)) return nullptr;
+    Call c;
+    int64_t N = c.integer(a[10]), T = c.integer(a[11]);
+    const int64_t H = c.integer(a[12]), Hk = c.integer(a[13]), Dv = c.integer(a[14]);
+    const float scale = c.real(a[15]);
+    const bool varlen = a[8] != Py_None;
+    int64_t rows = N * T;
+    const int* cu_host = nullptr;
+    if (varlen) {
+        const at::Tensor* h = c.tensor(a[9], "cu_seqlens_host");
+        if (h != nullptr && (h->is_cuda() || h->scalar_type() != ScalarType::Int || !h->is_contiguous() ||
+                             h->numel() < 1))
+            c.fail(PyExc_ValueError, "cu_seqlens_host", "expected a contiguous int32 CPU tensor [N + 1]");
+        if (c.failed) return nullptr;
+        cu_host = h->data_ptr<int>();
+        N = h->numel() - 1;
+        rows = cu_host[N];
+        // (before any size follows from them)
+        for (int64_t i = 0; i < N; ++i)
+            if (cu_host[i + 1] < cu_host[i]) return PyLong_FromLong(KDA_ERR_CU_SEQLENS);
+        if (cu_host[0] != 0) return PyLong_FromLong(KDA_ERR_CU_SEQLENS);
+    }
+    const LinRows r(c, a, rows, H, Hk, Dv);
+    void* g = c.take(a[3], "log_decay", ScalarType::Float, H);
+    void* s_in = c.maybe(a[4], "state_in", ScalarType::Float, N * H * Dv * kHead);
+    void* s_out = c.take(a[5], "state_out", ScalarType::Float, N * H * Dv * kHead);
+    void* o = c.take(a[6], "o", ScalarType::Float, rows * H * Dv);
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (a[7] != Py_None) {
+        ws = c.take(a[7], "workspace", ScalarType::Byte, -1);
+        if (ws != nullptr) ws_bytes = (size_t)THPVariable_Unpack(a[7]).numel();
+    }
+    void* cu = varlen ? c.take(a[8], "cu_seqlens", ScalarType::Int, N + 1) : nullptr;
+    void* stream = c.stream(a[16]);
+    if (c.failed) return nullptr;
+    return status([&] {
+        return varlen ? kda_linattn_prefill_varlen(r.q, r.qs, r.k, r.ks, r.v, r.vs, r.dtype, (float*)g,
+                                                   (float*)s_in, (float*)s_out, (float*)o, (int*)cu, cu_host,
+                                                   (int)N, (int)rows, (int)H, (int)Hk, (int)kHead, (int)Dv,
+                                                   scale, ws, ws_bytes, stream)
+                      : kda_linattn_prefill(r.q, r.qs, r.k, r.ks, r.v, r.vs, r.dtype, (float*)g,
+                                            (float*)s_in, (float*)s_out, (float*)o, (int)N, (int)T, (int)H,
+                                            (int)Hk, (int)kHead, (int)Dv, scale, ws, ws_bytes, stream);
+    });
+}
+
+// (q, k, v, log_decay, pool, o, slots, slots_out, keep, N, T, H, Hk, Dv, scale, stream)
+PyObject* linattn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity("linattn_decode", n, 16)) return nullptr;
+    Call c;
+    const int64_t N = c.integer(a[9]), T = c.integer(a[10]), H = c.integer(a[11]), Hk = c.integer(a[12]);
+    const int64_t Dv = c.integer(a[13]);
+    const float scale = c.real(a[14]);
+    const LinRows r(c, a, N * T, H, Hk, Dv);
+    int64_t P = 0;
+    if (const at::Tensor* t = c.tensor(a[4], "pool")) {
+        if (t->dim() != 4 || t->size(1) != H || t->size(2) != Dv || t->size(3) != kHead ||
+            t->size(0) > 0x7fffffff)
+            c.fail(PyExc_ValueError, "pool", "expected a [slots, H, Dv, 128] tensor");
+        else
+            P = t->size(0);
+    }
+    void* g = c.take(a[3], "log_decay", ScalarType::Float, H);
+    void* pool = c.take(a[4], "pool", ScalarType::Float, -1);
+    void* o = c.take(a[5], "o", ScalarType::Float, N * T * H * Dv);
+    void* slots = c.maybe(a[6], "slots", ScalarType::Int, N);
+    void* slots_out = c.maybe(a[7], "slots_out", ScalarType::Int, N);
+    void* keep = c.maybe(a[8], "keep", ScalarType::Int, N);
+    void* stream = c.stream(a[15]);
+    if (c.failed) return nullptr;
+    return status([&] {
+        return kda_linattn_decode(r.q, r.qs, r.k, r.ks, r.v, r.vs, r.dtype, (float*)g, (float*)pool,
+                                  (int*)slots, (int*)slots_out, (int*)keep, (float*)o, (int)P, (int)N,
+                                  (int)T, (int)H, (int)Hk, (int)kHead, (int)Dv, scale, stream);
+    });
+}
+
+// (target, tokens, u, r, keep, out_tokens, draft or None, n_draft or None, stream)
+PyObject* draft_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity("draft_accept", n, 9)) return nullptr;
+    Call c;
+    int dtype = 0;
+    const ScalarType pt = c.float_type(a[0], "target", &dtype);
+    int64_t N = 0, T = 0, V = 0;
+    if (const at::Tensor* t = c.tensor(a[0], "target")) {
+        if (t->dim() != 3 || t->size(0) > (1 << 30) || t->size(1) > (1 << 30) || t->size(2) > 0x7fffffff)
+            c.fail(PyExc_ValueError, "target", "expected a [N, T, V] tensor");
+        else
+            N = t->size(0), T = t->size(1), V = t->size(2);
+    }
+    if (!c.failed && T < 1) c.fail(PyExc_ValueError, "target", "expected at least one row a sequence");
+    if (c.failed) return nullptr;
+    long ts = 0, ds = 0;
+    void* target = c.rows3d(a[0], "target", pt, N, T, V, &ts);
+    void* draft = a[6] == Py_None ? nullptr : c.rows3d(a[6], "draft", pt, N, T - 1, V, &ds);
+    void* tokens = c.take(a[1], "tokens", ScalarType::Int, N * (T - 1));
+    void* u = c.take(a[2], "u", ScalarType::Float, N * (T - 1));
+    void* r = c.take(a[3], "r", ScalarType::Float, N);
+    void* keep = c.take(a[4], "keep", ScalarType::Int, N);
+    void* out = c.take(a[5], "out_tokens", ScalarType::Int, N * T);
+    void* nd = c.maybe(a[7], "n_draft", ScalarType::Int, N);
+    void* stream = c.stream(a[8]);
+    if (c.failed) return nullptr;
+    return status([&] {
+        return kda_draft_accept(target, ts, draft, ds, dtype, (int*)tokens, (float*)u, (float*)r, (int*)nd,
+                                (int*)keep, (int*)out, (int)N, (int)T, (int)V, stream);
+    });
+}
+
+// (residual, block or None, h or None, z or None, norm_w or None, block_w or None, gate or None,
+//  gate_act, res_scale, block_scale, eps, stream)
+PyObject* residual_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!arity("residual_rmsnorm", n, 12)) return nullptr;
+    Call c;
+    int rt = 0, bt = 0, zt = 0, per_row = 0;
+    const ScalarType res_t = c.float_type(a[0], "residual", &rt);
+    const ScalarType blk_t = a[1] == Py_None ? res_t : c.float_type(a[1], "block", &bt);
+    const ScalarType z_t = a[3] == Py_None ? res_t : c.float_type(a[3], "z", &zt);
+    int64_t rows = 0, F = 0;
+    if (const at::Tensor* t = c.tensor(a[0], "residual")) {
+        if (t->dim() != 2 || t->size(0) > 0x7fffffff || t->size(1) > 0x7fffffff)
+            c.fail(PyExc_ValueError, "residual", "expected a [rows, F] tensor");
+        else
+            rows = t->size(0), F = t->size(1);
+    }
+    const int64_t act = c.integer(a[7]);
+    const float rs = c.real(a[8]), bs = c.real(a[9]), eps = c.real(a[10]);
+    const ScalarType f32 = ScalarType::Float;
+    void* res = c.take(a[0], "residual", res_t, -1);
+    void* blk = c.maybe(a[1], "block", blk_t, rows * F);
+    void* h = c.maybe(a[2], "h", res_t, rows * F);
+    void* z = c.maybe(a[3], "z", z_t, rows * F);
+    void* nw = c.maybe(a[4], "norm_w", f32, F);
+    void* bw = c.maybe(a[5], "block_w", f32, F);
+    void* gate = nullptr;
+    if (a[6] != Py_None) {
+        if (const at::Tensor* t = c.tensor(a[6], "gate")) {
+            per_row = t->dim() != 1;
+            gate = c.take(a[6], "gate", per_row ? blk_t : f32, per_row ? rows * F : F);
+        }
+    }
+    void* stream = c.stream(a[11]);
+    if (c.failed) return nullptr;
+    return status([&] {
+        return kda_residual_rmsnorm(res, rt, blk, bt, (float*)bw, gate, per_row, (int)act, rs, bs, (float*)nw,
+                                    h, z, zt, (long)rows, (int)F, eps, stream);
+    });
+}
+
 using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
 
 // No C++ exception passes the interpreter's C frames: that would end the process.
@@ -320,6 +545,10 @@ PyMethodDef methods[] = {
     {"state_load_q8", (PyCFunction)(void (*)(void))guarded<state_q8<false>>, METH_FASTCALL, nullptr},
     {"decode_fused_q8", (PyCFunction)(void (*)(void))guarded<decode_fused_q8>, METH_FASTCALL, nullptr},
     {"proj_w4", (PyCFunction)(void (*)(void))guarded<proj_w4>, METH_FASTCALL, nullptr},
+    {"linattn_prefill", (PyCFunction)(void (*)(void))guarded<linattn_prefill>, METH_FASTCALL, nullptr},
+    {"linattn_decode", (PyCFunction)(void (*)(void))guarded<linattn_decode>, METH_FASTCALL, nullptr},
+    {"draft_accept", (PyCFunction)(void (*)(void))guarded<draft_accept>, METH_FASTCALL, nullptr},
+    {"residual_rmsnorm", (PyCFunction)(void (*)(void))guarded<residual_rmsnorm>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_native", nullptr, -1, methods,

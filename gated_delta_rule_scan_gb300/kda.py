@@ -37,6 +37,7 @@ GATE_EXP = 2  # flag: g holds decay factors exp(log-decay)
 NORM_SILU = 4  # flag (fused entries): the RMSNorm gates with SiLU(z) instead of sigmoid(z)
 ALGO_AUTO, ALGO_SEQ, ALGO_CHUNK = 0, 1, 2
 Q8_INT8, Q8_E4M3 = 0, 1  # 8-bit state formats
+ACT_NONE, ACT_SIGMOID, ACT_SILU = 0, 1, 2  # a block's gate
 HEAD_DIM = 128
 DECODE_MAX_T = 16
 STATIC_SCRATCH_BYTES = 32 << 20  # kda_scan_varlen_static's fixed device scratch
@@ -164,6 +165,22 @@ _lib.kda_proj_w4_workspace_bytes.restype = _Z
 _lib.kda_proj_w4_workspace_bytes.argtypes = [_I, _I]
 _lib.kda_proj_w4.restype = _I
 _lib.kda_proj_w4.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _P]
+_lib.kda_linattn_workspace_bytes.restype = _Z
+_lib.kda_linattn_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I, _I]
+_lib.kda_linattn_prefill.restype = _I
+_lib.kda_linattn_prefill.argtypes = [_P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                     _I, _F, _P, _Z, _P]
+_lib.kda_linattn_prefill_varlen.restype = _I
+_lib.kda_linattn_prefill_varlen.argtypes = [_P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _P, _P, _P, _I,
+                                            _I, _I, _I, _I, _I, _F, _P, _Z, _P]
+_lib.kda_linattn_decode.restype = _I
+_lib.kda_linattn_decode.argtypes = [_P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I,
+                                    _I, _I, _I, _I, _F, _P]
+_lib.kda_draft_accept.restype = _I
+_lib.kda_draft_accept.argtypes = [_P, _L, _P, _L, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P]
+_lib.kda_residual_rmsnorm.restype = _I
+_lib.kda_residual_rmsnorm.argtypes = [_P, _I, _P, _I, _P, _P, _I, _I, _F, _F, _P, _P, _P, _I, _L, _I,
+                                      _F, _P]
 
 # every symbol include/kda.h declares
 EXPORTED = ("kda_abi_version", "kda_status_string", "kda_conv_l2norm_prep",
@@ -180,7 +197,9 @@ EXPORTED = ("kda_abi_version", "kda_status_string", "kda_conv_l2norm_prep",
             "kda_scan_varlen_dv", "kda_prefill_fused_dv", "kda_prefill_fused_varlen_dv",
             "kda_decode_fused_dv", "kda_verify_rollback_dv", "kda_state_store_q8",
             "kda_state_load_q8", "kda_decode_fused_q8", "kda_proj_w4_workspace_bytes",
-            "kda_proj_w4")
+            "kda_proj_w4", "kda_linattn_workspace_bytes", "kda_linattn_prefill",
+            "kda_linattn_prefill_varlen", "kda_linattn_decode", "kda_draft_accept",
+            "kda_residual_rmsnorm")
 
 
 class KdaError(RuntimeError):
@@ -590,6 +609,69 @@ def kda_proj_w4(x, weights, scales, outs, *, group, zeros=None, workspace=None, 
     uint8 [rows_i, in_f/2], scales[i] (and zeros[i]) f32 or bf16 [rows_i, in_f/group], outs[i] f32
     [t, rows_i]."""
     _native("proj_w4", x, stream, x, weights, scales, zeros, outs, group, workspace)
+
+
+def kda_linattn_workspace_bytes(N, total_T, H, Hk=None, Dv=HEAD_DIM, dtype=torch.bfloat16) -> int:
+    return int(_lib.kda_linattn_workspace_bytes(N, total_T, H, H if Hk is None else Hk, HEAD_DIM, Dv,
+                                                DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32))
+
+
+def linattn_workspace(N, total_T, H, device, Hk=None, Dv=HEAD_DIM, dtype=torch.bfloat16):
+    """A device byte buffer large enough for kda_linattn_prefill / _varlen over N sequences of
+    total_T tokens in all, of q, k and v in `dtype` (None when none is needed)."""
+    nbytes = kda_linattn_workspace_bytes(N, total_T, H, Hk, Dv, dtype)
+    return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def kda_linattn_prefill(q, k, v, log_decay, state_in, state_out, o, workspace=None, *, N, T, H,
+                        Hk=None, Dv=HEAD_DIM, scale=None, stream=None):
+    """Linear attention with one log-decay a head over N sequences of T tokens.  q, k [N*T, Hk*128]
+    and v [N*T, H*Dv], f32 or bf16, may be column slices of one tensor; state_in [N, H, Dv, 128] or
+    None (zero); o f32 [N*T, H*Dv]."""
+    _native("linattn_prefill", q, stream, q, k, v, log_decay, state_in, state_out, o, workspace, None,
+            None, N, T, H, H if Hk is None else Hk, Dv,
+            HEAD_DIM ** -0.5 if scale is None else scale)
+
+
+def kda_linattn_prefill_varlen(q, k, v, log_decay, state_in, state_out, o, workspace, cu_seqlens,
+                               cu_seqlens_host, *, H, Hk=None, Dv=HEAD_DIM, scale=None,
+                               stream=None):
+    """kda_linattn_prefill over packed sequences (cu_seqlens: int32 device, cu_seqlens_host: CPU)."""
+    _native("linattn_prefill", q, stream, q, k, v, log_decay, state_in, state_out, o, workspace,
+            cu_seqlens, cu_seqlens_host, 0, 0, H, H if Hk is None else Hk, Dv,
+            HEAD_DIM ** -0.5 if scale is None else scale)
+
+
+def kda_linattn_decode(q, k, v, log_decay, pool, o, *, N, T, H, slots=None, slots_out=None, keep=None,
+                       Hk=None, Dv=HEAD_DIM, scale=None, stream=None):
+    """One decode step or T-token verify on a pool of f32 states [slots, H, Dv, 128]; slots,
+    slots_out and keep as in kda_decode_fused_q8."""
+    _native("linattn_decode", q, stream, q, k, v, log_decay, pool, o, slots, slots_out, keep, N, T, H,
+            H if Hk is None else Hk, Dv, HEAD_DIM ** -0.5 if scale is None else scale)
+
+
+def kda_draft_accept(target, tokens, u, r, keep, out_tokens, *, draft=None, n_draft=None,
+                     stream=None):
+    """Verify drafted tokens [N, T-1] (int32) against the target's probabilities [N, T, V] (f32 or
+    bf16; draft, the drafter's [N, T-1, V], or None for drafts without probabilities) with the random
+    numbers u [N, T-1] and r [N]: keep [N] and out_tokens [N, T] (int32) receive the verify rows that
+    stand and the tokens that follow from them."""
+    _native("draft_accept", target, stream, target, tokens, u, r, keep, out_tokens, draft, n_draft)
+
+
+_ACTS = {None: ACT_NONE, "none": ACT_NONE, "sigmoid": ACT_SIGMOID, "silu": ACT_SILU}
+
+
+def kda_residual_rmsnorm(residual, block, h, z, norm_w, *, block_w=None, gate=None, gate_act=None,
+                         res_scale=1.0, block_scale=1.0, eps=1e-6, stream=None):
+    """h = res_scale * residual + block_scale * act(gate) * rms(block) * block_w and z = rms(h) *
+    norm_w over rows [rows, F] (f32 or bf16 each; h in residual's type).  gate: [F] f32 for all rows or
+    [rows, F] in block's type; gate_act: None, "sigmoid" or "silu".  block, block_w, gate, h or z may
+    be None."""
+    if gate_act not in _ACTS:
+        raise ValueError(gate_act)
+    _native("residual_rmsnorm", residual, stream, residual, block, h, z, norm_w, block_w, gate,
+            _ACTS[gate_act], res_scale, block_scale, eps)
 
 
 def kernel_timing(enable: bool) -> bool:

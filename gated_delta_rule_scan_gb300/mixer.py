@@ -258,6 +258,87 @@ def kda_proj_w4(*, x, weights, scales, group, zeros=None, outs=None, workspace=N
     return outs
 
 
+def kda_linattn_prefill(*, q, k, v, log_decay, H, state_in=None, cu_seqlens=None,
+                        cu_seqlens_host=None, N=None, T=None, Hk=None, Dv=None, scale=None,
+                        state_out=None, o=None, workspace=None, stream=None):
+    """Linear attention with one log-decay a head over (N, T) or packed sequences (cu_seqlens int32
+    device + cu_seqlens_host int32 CPU), from state_in (None: zero).  workspace: from
+    kda.linattn_workspace (allocated here when None).  Returns a dict with o and state_out."""
+    Dv = kda.HEAD_DIM if Dv is None else Dv
+    rows, made = q.shape[0], []
+    varlen = cu_seqlens is not None
+    if not varlen:
+        assert N is not None and T is not None and N * T == rows
+    n_seq = (cu_seqlens_host.numel() - 1) if varlen else N
+    with _on(stream, q.device):
+        if o is None:
+            o = _made(made, _empty((rows, H * Dv), q))
+        if state_out is None:
+            state_out = _made(made, _empty((n_seq, H, Dv, kda.HEAD_DIM), q))
+        if workspace is None:
+            workspace = kda.linattn_workspace(n_seq, rows, H, q.device, Hk=Hk, Dv=Dv, dtype=q.dtype)
+    args = (q, k, v, log_decay, state_in, state_out, o, workspace)
+    common = dict(H=H, Hk=Hk, Dv=Dv, scale=scale, stream=stream)
+    if varlen:
+        kda.kda_linattn_prefill_varlen(*args, cu_seqlens, cu_seqlens_host, **common)
+    else:
+        kda.kda_linattn_prefill(*args, N=N, T=T, **common)
+    _hand_over(stream, *made)
+    return dict(o=o, state_out=state_out)
+
+
+def kda_linattn_decode(*, q, k, v, log_decay, pool, N, T, H, slots=None, slots_out=None, keep=None,
+                       Hk=None, Dv=None, scale=None, o=None, stream=None):
+    """One decode step or T-token verify of linear attention on a pool of f32 states [slots, H, Dv,
+    128]; with keep the rollback of a verify that ran into other slots.  Returns o (zero in rows not
+    computed when it is allocated here)."""
+    Dv, made = kda.HEAD_DIM if Dv is None else Dv, o is None
+    if made:
+        with _on(stream, pool.device):
+            o = torch.zeros(N * T, H * Dv, device=pool.device)
+    kda.kda_linattn_decode(q, k, v, log_decay, pool, o, N=N, T=T, H=H, slots=slots,
+                           slots_out=slots_out, keep=keep, Hk=Hk, Dv=Dv, scale=scale, stream=stream)
+    if made:
+        _hand_over(stream, o)
+    return o
+
+
+def kda_draft_accept(*, target, tokens, u, r, draft=None, n_draft=None, keep=None, out_tokens=None,
+                     stream=None):
+    """Verify drafted tokens against the target's probabilities.  Returns keep [N], the rows of the
+    verify that stand (what kda_verify_rollback, StatePoolQ8.decode and kda_linattn_decode take), and
+    out_tokens [N, T]: the accepted drafts, the new token, then -1."""
+    made = []
+    with _on(stream, target.device):
+        if keep is None:
+            keep = _made(made, torch.empty(target.shape[0], dtype=torch.int32, device=target.device))
+        if out_tokens is None:
+            out_tokens = _made(made, torch.empty(target.shape[:2], dtype=torch.int32,
+                                                 device=target.device))
+    kda.kda_draft_accept(target, tokens, u, r, keep, out_tokens, draft=draft, n_draft=n_draft,
+                         stream=stream)
+    _hand_over(stream, *made)
+    return keep, out_tokens
+
+
+def kda_residual_rmsnorm(*, residual, block=None, norm_w=None, block_w=None, gate=None, gate_act=None,
+                         res_scale=1.0, block_scale=1.0, eps=1e-6, h=None, z=None, z_dtype=None,
+                         stream=None):
+    """The norms after and before a block with its gate, scale and residual.  Returns (h, z), both
+    allocated when not given (z in z_dtype, residual's by default; no z without norm_w)."""
+    made = []
+    with _on(stream, residual.device):
+        if h is None:
+            h = _made(made, torch.empty_like(residual))
+        if z is None and norm_w is not None:
+            z = _made(made, torch.empty_like(residual, dtype=z_dtype))
+    kda.kda_residual_rmsnorm(residual, block, h, z, norm_w, block_w=block_w, gate=gate,
+                             gate_act=gate_act, res_scale=res_scale, block_scale=block_scale, eps=eps,
+                             stream=stream)
+    _hand_over(stream, *made)
+    return h, z
+
+
 class StatePoolQ8:
     """States and conv rings of up to `slots` sequences, the states in 8 bits (include/kda.h, "The
     8-bit state pool"): codes [slots, H, Dv, 128], scales [slots, H, Dv], rings [slots, channels,

@@ -670,6 +670,108 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
                 float* const* out_host, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Linear attention with one decay a head: the recurrence without the delta rule,
+ *     S <- exp(log_decay[h]) S + k_t v_t^T;   o_t = scale S^T q_t
+ * for each sequence and value head h (kda_scan's state layout and grouped queries: value head h reads
+ * q/k head h % Hk; a value head of Dv = 128 * m columns has a state [Dv, 128]).
+ *
+ * kda_linattn_prefill -- N sequences of T tokens; kda_linattn_prefill_varlen -- N packed sequences
+ * (cu_seqlens, cu_seqlens_host as in kda_conv_l2norm_prep_varlen).
+ * q, k         [rows, Hk*128], v [rows, H*Dv] in raw_dtype [16B]; token rows are q_stride, k_stride
+ *              and v_stride elements apart (the planes may be column slices of one projection's
+ *              output): at least the row's width and a multiple of 16 bytes (40005 otherwise).
+ * log_decay    [H] f32, at most 0.
+ * state_in     [N, H, Dv, 128] f32 [16B], or NULL: zero.  state_out the same shape; overlapping
+ *              states return 40003.  An empty sequence's state passes through.
+ * o            [rows, H*Dv] f32 [16B], rows 128-wide heads apart as kda_gated_rmsnorm_out reads them.
+ * workspace    device scratch [16B] of at least kda_linattn_workspace_bytes(...) bytes (40009
+ *              otherwise; where that is 0 NULL is accepted).  Its contents are overwritten: calls that
+ *              share it must not overlap.
+ * Dk = 128, Dv = 128 * m, m = 1..8 (40001).
+ */
+size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype);
+int kda_linattn_prefill(const void* q, long q_stride, const void* k, long k_stride, const void* v,
+                        long v_stride, int raw_dtype, const float* log_decay, const float* state_in,
+                        float* state_out, float* o, int N, int T, int H, int Hk, int Dk, int Dv,
+                        float scale, void* workspace, size_t workspace_bytes, void* stream);
+int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long k_stride,
+                               const void* v, long v_stride, int raw_dtype, const float* log_decay,
+                               const float* state_in, float* state_out, float* o,
+                               const int* cu_seqlens, const int* cu_seqlens_host, int N, int total_T,
+                               int H, int Hk, int Dk, int Dv, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * kda_linattn_decode -- one decode step (T = 1) or T-token verify (T <= 16) of N sequences on a pool
+ * of states [P, H, Dv, 128] f32 [16B]: sequence n's state is read from slot slots[n] and written to
+ * slot slots_out[n] (NULL: in place; slots NULL: slot n, for N <= P, 40005 otherwise).
+ * slots, slots_out, keep   device int32 [N], with the meaning, padding and exclusions they have in
+ *              kda_decode_fused_q8: negative slots are padding; keep[n] (clamped to 0..T) takes only
+ *              the first keep[n] rows, so that a rollback is the verify call again with keep from the
+ *              slots of before the round; a row whose slot lies past the pool, or whose output slot
+ *              another row reads or an earlier row writes, is left out (40013, kda_device_status).
+ * q, k, v, log_decay, o, scale   as in kda_linattn_prefill; sequence n owns rows n*T .. n*T + T-1.  o
+ *              rows of padding, of rows left out and of rows t >= keep[n] are not written.
+ * A T-token call equals T one-token calls bit for bit.
+ */
+int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_stride, const void* v,
+                       long v_stride, int raw_dtype, const float* log_decay, float* pool,
+                       const int* slots, const int* slots_out, const int* keep, float* o, int P, int N,
+                       int T, int H, int Hk, int Dk, int Dv, float scale, void* stream);
+
+/*
+ * kda_draft_accept -- verification of drafted tokens against the target's probabilities: what turns a
+ * T-token verify's outputs into the keep of kda_verify_rollback, kda_decode_fused_q8 and
+ * kda_linattn_decode.  Row 0 of a verify holds the last token of the sequence, rows 1 .. T-1 its
+ * drafts; row t's outputs give the target's distribution of the token after it.  For sequence n, with
+ * p_t = target[n][t], q_t = draft[n][t] and x_t = tokens[n][t] the draft after row t:
+ *   draft t holds while u[n][t] * q_t(x_t) < p_t(x_t), tested in turn for t = 0 .. n_draft[n]-1;
+ *   with a of them holding, one more token is the first index whose running sum of weights passes
+ *   r[n] times their total; the weights are max(p_a - q_a, 0) where draft a was refused (p_a where
+ *   those are all 0) and p_a where none was;
+ *   keep[n] = a + 1 (rows of the verify that stand);
+ *   out_tokens[n] = x_0 .. x_{a-1}, the new token, then -1 up to T entries.
+ * target       [N, T, V], draft [N, T-1, V] in prob_dtype, rows target_stride and draft_stride
+ *              elements apart (at least V, 40005); draft NULL: drafts without probabilities (a
+ *              lookup's), q is 1 at the draft and 0 elsewhere.
+ * tokens       int32 [N, T-1], u [N, T-1] and r [N] f32, random numbers in [0, 1) (r is clamped to it).
+ * n_draft      int32 [N]: drafts of each sequence, at most T-1, or NULL: T-1 of all; a negative entry
+ *              is padding: keep 0, no tokens.
+ * T = 1..16 (1: plain sampling; tokens, u and draft are not read), N <= 65535, V >= 1 (40005).
+ * Nothing needs to be normalised.  A drafted id outside the vocabulary is refused.  A weight that is
+ * negative, NaN or infinite counts as 0; where no weight is left the new token is -1.
+ * Sums are exact to about 2^-46 of the row's total.
+ */
+int kda_draft_accept(const void* target, long target_stride, const void* draft, long draft_stride,
+                     int prob_dtype, const int* tokens, const float* u, const float* r,
+                     const int* n_draft, int* keep, int* out_tokens, int N, int T, int V,
+                     void* stream);
+
+/*
+ * kda_residual_rmsnorm -- the norms after and before a block, with its gate, its scale and the
+ * residual sum, in one pass over [rows, F]:
+ *     h = res_scale * x + block_scale * act(gate) * (rms(y) * block_w),   z = rms(h) * norm_w,
+ * rms(a)_i = a_i / sqrt(mean_i a_i^2 + eps).  z is the next block's input (kda_proj6, kda_proj_w4).
+ * residual     x in residual_dtype;  h the same type, or NULL: not written.  h may be residual itself.
+ * block        y in block_dtype, or NULL: h = res_scale * x (the norm before a first block).
+ * block_w      [F] f32, or NULL: y enters without its norm.
+ * gate         NULL: none; gate_per_row 0: [F] f32, one for all rows; 1: [rows, F] in block_dtype.
+ * gate_act     KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU (40007 otherwise).
+ * norm_w       [F] f32;  z in z_dtype, or NULL: not written (then norm_w may be NULL).  z may be the
+ *              same buffer as y or as a gate per row, in the same type.
+ * F            a multiple of 8, 8 .. 16384; rows 0 .. 2^31-1 (40005).  All pointers [16B].
+ * h is rounded to its type after the second norm has taken it.  Other overlaps of h or z with an
+ * input, or with each other, return 40003.
+ */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SIGMOID 1
+#define KDA_ACT_SILU 2
+int kda_residual_rmsnorm(const void* residual, int residual_dtype, const void* block, int block_dtype,
+                         const float* block_w, const void* gate, int gate_per_row, int gate_act,
+                         float res_scale, float block_scale, const float* norm_w, void* h, void* z,
+                         int z_dtype, long rows, int F, float eps, void* stream);
+
+/*
  * kda_selftest_wait_timeout -- a self-test of failure detection (no counterpart in the pages):
  * launches one kernel whose single thread waits, with the bounded wait every kernel here uses,
  * on a barrier that nothing completes.  The wait gives up after about a second, raises the device
