@@ -1073,6 +1073,9 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
     return cuda_status(launch_proj_w4(a, static_cast<cudaStream_t>(stream)));
 }
 
+// bf16 prompts take the chunked form when the longest has at least this many tokens.
+static constexpr long kLinChunkMinLen = 32;
+
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype) {
     const int m = value_subheads(Dk, Dv);
     if (m == 0 || N < 0 || total_T < 0 || H <= 0 || Hk < 1 || Hk > H) return 0;
@@ -1113,14 +1116,15 @@ static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_
     if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_ALIGN;
     const size_t sb = (size_t)a.seq.N * a.H * a.m * kHeadDim * kHeadDim * sizeof(float);
     if (state_in && overlap(state_in, state_out, sb)) return KDA_ERR_STATE_ALIAS;
-    (void)cu_host;
     (void)workspace;
     (void)workspace_bytes;
     if (const int sd = check_stream_device(stream)) return sd;
     a.state_in = state_in;
     a.state_out = state_out;
     a.err = dev_err_ptr();
-    return cuda_status(launch_linattn_seq(a, static_cast<cudaStream_t>(stream)));
+    const bool chunk = a.bf16 && max_len(a.seq, cu_host) >= kLinChunkMinLen;
+    return cuda_status(chunk ? launch_linattn_chunk(a, static_cast<cudaStream_t>(stream))
+                             : launch_linattn_seq(a, static_cast<cudaStream_t>(stream)));
 }
 
 int kda_linattn_prefill(const void* q, long q_stride, const void* k, long k_stride, const void* v,

@@ -114,17 +114,6 @@ __device__ __forceinline__ void mma3_ss(uint32_t d, uint64_t a_hi, uint64_t a_lo
                       p > 0 || ks > 0);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc]^T, issued by one thread
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                         uint32_t idesc, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
-}
-
 // D = A * B^T, f16 x 2: A in tensor memory split as hi (at a_hi) + lo (at a_lo), 8 columns per
 // K-step of 16; B one f16 image in shared memory; the first product starts the sum
 __device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a_hi, uint32_t a_lo, uint64_t b,

@@ -193,9 +193,10 @@ inline size_t proj_workspace_bytes(int t, int in_f) {
     return 2 * (size_t)proj_t_pad(t) * (size_t)in_f * 2;   // x hi and x lo, bf16
 }
 cudaError_t launch_proj6(const Proj6Args& a, cudaStream_t s);
-// 2-D bf16 tensor map over [rows, cols] with a [box_rows][64] box in the 128-byte swizzle
+// 2-D bf16 tensor map over [rows, cols], rows row_stride elements apart (0: cols), with a [box_rows][64]
+// box in the 128-byte swizzle
 bool make_tensor_map_2d_bf16_sw128(CUtensorMap* m, const void* base, long rows, long cols,
-                                   int box_rows);
+                                   int box_rows, long row_stride = 0);
 cudaError_t launch_gated_rmsnorm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_decode_fused(const DecodeArgs& a, cudaStream_t s);
 
@@ -265,6 +266,7 @@ struct LinArgs {
 };
 cudaError_t launch_linattn_decode(const LinArgs& a, cudaStream_t s);
 cudaError_t launch_linattn_seq(const LinArgs& a, cudaStream_t s);
+cudaError_t launch_linattn_chunk(const LinArgs& a, cudaStream_t s);   // bf16, total_rows > 0
 
 // Verification of drafted tokens (kda_accept.cu).
 struct AcceptArgs {
@@ -293,7 +295,8 @@ cudaError_t launch_residual_rmsnorm(const ResNormArgs& a, cudaStream_t s);
 enum KernelId {
     kKPrep, kKRingRoll, kKScanSeq, kKChunkOffsets, kKChunkIntra, kKChunkInter, kKRmsNorm,
     kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKStateStoreQ8, kKStateLoadQ8, kKDecodeQ8,
-    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKDraftAccept, kKResNorm,
+    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKLinChunk, kKDraftAccept,
+    kKResNorm,
     kKernelCount
 };
 class KernelTimer {

@@ -212,11 +212,11 @@ bool make_tensor_map_blocks_ut(CUtensorMap* m, void* base, long nblocks, size_t 
 }
 
 bool make_tensor_map_2d_bf16_sw128(CUtensorMap* m, const void* base, long rows, long cols,
-                                   int box_rows) {
+                                   int box_rows, long row_stride) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    cuuint64_t strides[1] = {(cuuint64_t)(row_stride > 0 ? row_stride : cols) * 2};
     cuuint32_t box[2] = {64, (cuuint32_t)box_rows};      // 64 bf16 = one 128-byte swizzle row
     cuuint32_t es[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,

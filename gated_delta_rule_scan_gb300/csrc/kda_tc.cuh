@@ -92,6 +92,22 @@ __device__ __forceinline__ uint64_t tc_smem_desc_sw128(uint32_t smem_addr) {
     return d;
 }
 
+// The same for an MN-major tile written by a TMA load in the 128-byte swizzle: k rows of 128 bytes (64
+// elements of M or N), 8-row groups 1024 bytes apart (SBO), the next 64 elements of M or N in a tile
+// `atom` bytes further (LBO).  The K-step ks of 16 rows starts 2048 * ks bytes further.
+__device__ __forceinline__ uint64_t tc_smem_desc_sw128_mn(uint32_t smem_addr, uint32_t atom) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((atom >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Added to an instruction descriptor: A or B is MN-major.
+constexpr uint32_t kTcAMajorMN = 1u << 15, kTcBMajorMN = 1u << 16;
+
 // Instruction descriptor, kind::f16: f16 A and B, f32 accumulator, both K-major, dense.
 __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N) {
     return (1u << 4)                    // D format: f32 (A and B format fields 0: f16)
@@ -118,6 +134,17 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, issued by one thread
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                         uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
