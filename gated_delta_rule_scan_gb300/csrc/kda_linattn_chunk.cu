@@ -4,20 +4,26 @@
 // Mathematics.  Over a chunk of C = 64 tokens with incoming state S (stored [value j][key i]):
 //     O^T = scale * ( V^T P^T + e^{g (t+1)} S Q^T ),   P[t][s] = e^{g (t-s)} q_t . k_s  for s <= t,
 //     S  <- e^{g C} S + V^T Kd,                        Kd[s]   = e^{g (C-1-s)} k_s.
-// Every decay is a power e^{g n} with 0 <= n <= C, at most 1, whatever g is.  q, k and v enter as the
-// bf16 values they are; what is f32 (P, Kd and the state) enters as three bf16 parts, 24 bits in all,
-// so that the result is an f32 one: P = 3 products, S = 3, Kd = 3 beside q k's one.  (Two parts would
-// leave errors of 2^-17 to save 3 of the 10 product passes.)  The state itself stays in f32 registers.
+// Both parts of O are one sum in the tensor cores when its rows share a factor: with everything
+// relative to the middle of the chunk, P[t][s] = e^{g (31-s)} q_t . k_s, the state kept as e^{32 g} S
+// (and Kd 32 further on), a token's output is e^{g (t-31)} times that sum.  These factors stay within
+// e^{32 |g|}, 8e13 at |g| = 1.  Heads that decay faster (g < -1) take the parts one after the other, with
+// the powers as they stand, all of them at most 1, and a slower pipeline: there S Q^T matters to a few tens
+// of tokens at most, but overflow must not.
+// q, k and v enter as the bf16 values they are; what is f32 (P, Kd and the state) enters as bf16 hi + lo,
+// within 2^-18 of an element, as x does in the bf16 projections: outputs and states come within about 1e-6
+// of their scale.  (A third part brought 1e-7 for half as much again in MMAs and splitting, 166 against
+// TODO us at 4096 tokens x 64 heads.)  The state itself stays in f32 registers.
 //
 // One CTA per (sequence, 128-wide value unit), chunk after chunk, the values on the MMA's M = 128 TMEM
 // lanes.  Shared memory carries what the tensor cores read of it at 128 bytes a cycle, so the A
 // operands lie in tensor memory: the state parts, written by the threads that hold the state rows, and
 // v, transposed on the way (from shared memory as an MN-major operand it cost twice its bytes: U 140
 // cycles an MMA against 64).  B operands are q's tile as TMA brings it, P, and Kd transposed to
-// [key][token] while it is formed.  The 512 TMEM columns are full: S parts 3 x 64, V^T Kd 128, the
-// outputs 64 (S Q^T, scaled in place, then V^T P^T on top), q k 64, v 2 x 32.
+// [key][token] while it is formed.  The 512 TMEM columns are full: S parts 2 x 64, V^T Kd 128, the
+// outputs 64, q k 64, v 2 x 32.
 // 64 tokens, not 128: the parts of P and Kd then fit beside two stages of q, k, v.
-// Warps have roles: 8 hold the state (64 f32 a thread), 8 turn k into Kd and q k into P, 8 write o, three
+// Warps have roles: 16 hold the state (32 f32 a thread) and write o, 8 turn k into Kd and q k into P, three
 // issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads, the MMAs and the groups'
 // register work overlap across chunks.  (One issuing warp took 50 to 100 cycles an MMA beside six busy
 // warps on its scheduler, twice the tensor pipe's time.)
@@ -28,51 +34,50 @@ namespace kda {
 namespace {
 
 constexpr int kC = 64;                           // tokens of a chunk
-constexpr int kStages = 2;
+constexpr int kMid = kC / 2;
+constexpr int kParts = 2;
+constexpr int kStages = 3;
 constexpr int kHalf = kC * 128;                  // bytes of 64 tokens x 64 columns, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalf;            // 64 tokens x 128 columns
 constexpr int kKAt = 0, kVAt = kTileBytes, kQAt = 2 * kTileBytes;   // in a stage
 constexpr int kStageBytes = 3 * kTileBytes;
-constexpr int kKdBytes = 3 * kTileBytes;         // Kd: 3 parts, two buffers
+constexpr int kKdBytes = kParts * kTileBytes;    // Kd's parts, two buffers
 constexpr int kKdAt = kStages * kStageBytes;
-constexpr int kPAt = kKdAt + 2 * kKdBytes;       // P: 3 parts of [64 t][64 s]
-constexpr int kTailAt = kPAt + 3 * kHalf;
-constexpr int kStateWarps = 8, kConvWarps = 8, kOutWarps = 8;
+constexpr int kPAt = kKdAt + 2 * kKdBytes;       // P's parts, [64 t][64 s] each
+constexpr int kTailAt = kPAt + kParts * kHalf;
+constexpr int kStateWarps = 16, kConvWarps = 8;
 // The first warpgroup issues the MMAs and the loads; whole warpgroups: registers move between them.
-constexpr int kUWarp = 0, kOiWarp = 1, kOaWarp = 2, kTmaWarp = 3, kStateWarp0 = 4;
-constexpr int kConvWarp0 = kStateWarp0 + kStateWarps, kOutWarp0 = kConvWarp0 + kConvWarps;
-constexpr int kThr = 32 * (kOutWarp0 + kOutWarps);
+constexpr int kUWarp = 0, kOiWarp = 1, kTmaWarp = 3, kStateWarp0 = 4;
+constexpr int kConvWarp0 = kStateWarp0 + kStateWarps;
+constexpr int kThr = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kPWarps = 6;                       // converting warps with a share of P
 constexpr int kLaunchRegs = 72;
-constexpr int kStateRegs = 136, kConvRegs = 64, kOutRegs = 40, kOtherRegs = 24;
-static_assert(32 * (kStateWarps * kStateRegs + kConvWarps * kConvRegs + kOutWarps * kOutRegs +
-                    4 * kOtherRegs) <= kThr * kLaunchRegs, "");
+constexpr int kStateRegs = 88, kConvRegs = 64, kOtherRegs = 24;
+static_assert(32 * (kStateWarps * kStateRegs + kConvWarps * kConvRegs + 4 * kOtherRegs) <= kThr * kLaunchRegs, "");
 
 struct __align__(16) Tail {
-    float pw1[kC];                               // e^{g (n+1)}, n = 0 .. 63
-    float pw[kC + 4];                            // e^{g n}, n = 0 .. 64
+    float pw[kC + kMid + 4];                     // e^{g n}, n = 0 .. 96
+    float down[kC];                              // P's factors: e^{g (31-s)}
+    float up[kC];                                // the outputs': scale * e^{g (t-31)}, or scale * e^{g (t+1)}
     uint64_t kv_full[kStages], kv_free[kStages], q_full[kStages], q_free[kStages];
     uint64_t kd_full[2], kd_free[2];
-    uint64_t sc_full, sc_free, u_full, u_free, sp_full, oi_full, oi_free, p_full, oa_full, oa_free;
+    uint64_t sc_full, sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free[2];
     uint64_t drain[3];
     uint32_t tmem;
 };
 constexpr int kSmemBytes = 1024 + kTailAt + (int)sizeof(Tail);
 
 // TMEM columns
-constexpr uint32_t kTSp = 0, kTU = 192, kTO = 320, kTSc = 384, kTVt = 448;
+constexpr uint32_t kTSp = 0, kTU = 128, kTO = 256, kTSc = 384, kTVt = 448;     // kTO: two buffers
 
-// Two f32 as three bf16x2 words whose sum they are to 24 bits.
-__device__ __forceinline__ void split3(float2 x, uint32_t& a, uint32_t& b, uint32_t& c) {
-    const float2 neg = make_float2(-1.0f, -1.0f);
+// Two f32 as two bf16x2 words, hi and lo.
+__device__ __forceinline__ void split2(float2 x, uint32_t& a, uint32_t& b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
     a = *reinterpret_cast<const uint32_t*>(&h);
-    x = __ffma2_rn(make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)), neg, x);
-    const __nv_bfloat162 m = __floats2bfloat162_rn(x.x, x.y);
-    b = *reinterpret_cast<const uint32_t*>(&m);
-    x = __ffma2_rn(make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), neg, x);
+    x = __ffma2_rn(make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)),
+                   make_float2(-1.0f, -1.0f), x);
     const __nv_bfloat162 l = __floats2bfloat162_rn(x.x, x.y);
-    c = *reinterpret_cast<const uint32_t*>(&l);
+    b = *reinterpret_cast<const uint32_t*>(&l);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -128,6 +133,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
     }
     const int chunks = (len + kC - 1) / kC;
     const float g = a.log_decay[hv];
+    const bool strong = g < -1.0f;
+    const int mid = strong ? 0 : kMid;           // the state is kept as e^{mid g} S
 
     if (warp == kUWarp) {
         tmem_alloc(&sm.tmem, 512);
@@ -150,11 +157,11 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             mbar_init(&sm.u_full, 1);
             mbar_init(&sm.u_free, kStateWarps);
             mbar_init(&sm.sp_full, kStateWarps);
-            mbar_init(&sm.oi_full, 1);
+            mbar_init(&sm.o_full, 1);
             mbar_init(&sm.p_full, kPWarps);
-            mbar_init(&sm.oa_full, 1);
-            mbar_init(&sm.oi_free, kOutWarps);
-            mbar_init(&sm.oa_free, kOutWarps);
+            for (int i = 0; i < 2; ++i) mbar_init(&sm.oa_full[i], 1);
+            mbar_init(&sm.oa_free, kStateWarps);
+            for (int i = 0; i < 2; ++i) mbar_init(&sm.o_free[i], kStateWarps);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             fence_mbar_init();
             prefetch_tensormap(&tq);
@@ -162,10 +169,10 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             prefetch_tensormap(&tv);
         }
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
-        for (int i = lane; i <= kC; i += 32) {
-            const float x = i == 0 ? 1.0f : expf(g * (float)i);
-            sm.pw[i] = x;
-            if (i > 0) sm.pw1[i - 1] = x;
+        for (int i = lane; i <= kC + kMid; i += 32) sm.pw[i] = i == 0 ? 1.0f : expf(g * (float)i);
+        for (int i = lane; i < kC; i += 32) {
+            sm.down[i] = strong || i == kMid - 1 ? 1.0f : expf(g * (float)(kMid - 1 - i));
+            sm.up[i] = a.scale * (strong ? expf(g * (float)(i + 1)) : i == kMid - 1 ? 1.0f : expf(g * (float)(i - kMid + 1)));
         }
     }
     tc_fence_before();
@@ -215,56 +222,16 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         const uint64_t d0 = tc_smem_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(base), 0));
         if (warp == kUWarp) {
             for (int c = 0; c < chunks; ++c) {
-                const uint64_t kd = tc_desc_advance(d0, kKdAt + (c & 1) * kKdBytes);
-                const uint32_t vt = tmem + kTVt + 32 * (c & 1), par = (uint32_t)(c & 1);
-                ok = mbar_wait_bounded(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
-                     (c == 0 || mbar_wait_bounded(&sm.u_free, par ^ 1u, a.err));
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int p = 2; p >= 0; --p)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + kTU, vt + 8 * ks, tc_desc_advance(kd, p * kTileBytes + 32 * ks), id_u,
-                                      p < 2 || ks > 0);
-                    tc_commit(&sm.u_full);
-                    tc_commit(&sm.kd_free[c & 1]);
-                }
-                __syncwarp();
-            }
-        } else if (warp == kOiWarp) {
-            for (int c = 0; c < chunks; ++c) {
                 const int st = c % kStages;
-                const uint64_t q = tc_desc_advance(d0, st * kStageBytes + kQAt);
-                const uint32_t par = (uint32_t)(c & 1);
-                ok = mbar_wait_bounded(&sm.q_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
-                     mbar_wait_bounded(&sm.sp_full, par, a.err) &&
-                     (c == 0 || mbar_wait_bounded(&sm.oa_free, par ^ 1u, a.err));
+                const uint32_t par = (uint32_t)(c & 1), pst = (uint32_t)((c / kStages) & 1);
+                // q_t . k_s, s < 32 with q on the lanes 0 .. 63, s >= 32 with q on 64 .. 127: the threads of
+                // three lane quarters then share the work on P.  (M = 128 covers twice the rows of q's tile,
+                // those behind it, or before it, being whatever lies there: their lanes are never read.)
+                ok = mbar_wait_bounded(&sm.kv_full[st], pst, a.err) && mbar_wait_bounded(&sm.q_full[st], pst, a.err) &&
+                     (c == 0 || mbar_wait_bounded(&sm.sc_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int p = 2; p >= 0; --p)
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ts(tmem + kTO, tmem + kTSp + 64 * p + 8 * ks,
-                                      tc_desc_advance(q, (ks >> 2) * kHalf + (ks & 3) * 32), id_o, p < 2 || ks > 0);
-                    tc_commit(&sm.oi_full);
-                    tc_commit(&sm.q_free[st]);
-                }
-                __syncwarp();
-            }
-            // no arrival of the tensor pipe on a barrier of a CTA that has left: each warp sees its last
-            if (ok && chunks > 0)
-                ok = mbar_wait_bounded(&sm.q_free[(chunks - 1) % kStages],
-                                       (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
-        } else {
-            // q_t . k_s, s < 32 with q on the lanes 0 .. 63, s >= 32 with q on 64 .. 127: the threads of
-            // three lane quarters then share the work on P.  (M = 128 covers twice the rows of q's tile,
-            // those behind it, or before it, being whatever lies there: their lanes are never read.)
-            auto qk = [&](int c) {
-                const uint64_t s = tc_desc_advance(d0, (c % kStages) * kStageBytes);
+                const uint64_t s = tc_desc_advance(d0, st * kStageBytes);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
@@ -275,103 +242,86 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                                   tc_desc_advance(s, kKAt + kHalf / 2 + off), id_sc, ks > 0);
                     }
                     tc_commit(&sm.sc_full);
-                    tc_commit(&sm.kv_free[c % kStages]);
-                    tc_commit(&sm.q_free[c % kStages]);
+                    tc_commit(&sm.kv_free[st]);
+                    tc_commit(&sm.q_free[st]);
                 }
                 __syncwarp();
-            };
-            for (int c = -1; c < chunks; ++c) {
-                if (c + 1 < chunks) {            // the next chunk's q k
-                    const int s1 = (c + 1) % kStages;
-                    const uint32_t p1 = (uint32_t)(((c + 1) / kStages) & 1);
-                    ok = mbar_wait_bounded(&sm.kv_full[s1], p1, a.err) &&
-                         mbar_wait_bounded(&sm.q_full[s1], p1, a.err) &&
-                         (c < 0 || mbar_wait_bounded(&sm.sc_free, (uint32_t)(c & 1), a.err));
-                    if (!ok) break;
-                    tc_fence_after();
-                    qk(c + 1);
-                }
-                if (c < 0) continue;
-                const uint64_t pp = tc_desc_advance(d0, kPAt);
-                const uint32_t vt = tmem + kTVt + 32 * (c & 1), par = (uint32_t)(c & 1);
-                ok = mbar_wait_bounded(&sm.p_full, par, a.err) && mbar_wait_bounded(&sm.oi_free, par, a.err);
+                const uint64_t kd = tc_desc_advance(d0, kKdAt + (c & 1) * kKdBytes);
+                const uint32_t vt = tmem + kTVt + 32 * (c & 1);
+                ok = mbar_wait_bounded(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
+                     (c == 0 || mbar_wait_bounded(&sm.u_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int p = 2; p >= 0; --p)
+                    for (int p = kParts - 1; p >= 0; --p)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + kTO, vt + 8 * ks, tc_desc_advance(pp, p * kHalf + 32 * ks), id_o, true);
-                    tc_commit(&sm.oa_full);
+                            tc_mma_ts(tmem + kTU, vt + 8 * ks, tc_desc_advance(kd, p * kTileBytes + 32 * ks), id_u,
+                                      p < kParts - 1 || ks > 0);
+                    tc_commit(&sm.u_full);
+                    tc_commit(&sm.kd_free[c & 1]);
+                }
+                __syncwarp();
+            }
+            // no arrival of the tensor pipe on a barrier of a CTA that has left: each warp sees its last
+            if (ok && chunks > 0)
+                ok = mbar_wait_bounded(&sm.kv_free[(chunks - 1) % kStages],
+                                       (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
+        } else if (warp == kOiWarp) {
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c % kStages;
+                const uint64_t q = tc_desc_advance(d0, st * kStageBytes + kQAt);
+                const uint32_t par = (uint32_t)(c & 1);
+                ok = mbar_wait_bounded(&sm.q_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
+                     mbar_wait_bounded(&sm.sp_full, par, a.err) &&
+                     mbar_wait_bounded(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
+                     (!strong || mbar_wait_bounded(&sm.oa_free, par, a.err));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int p = kParts - 1; p >= 0; --p)
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc_mma_ts(tmem + kTO + 64 * (c & 1), tmem + kTSp + 64 * p + 8 * ks,
+                                      tc_desc_advance(q, (ks >> 2) * kHalf + (ks & 3) * 32), id_o,
+                                      !strong || p < kParts - 1 || ks > 0);
+                    tc_commit(&sm.o_full);
+                    tc_commit(&sm.q_free[st]);
+                }
+                __syncwarp();
+            }
+            if (ok && chunks > 0)
+                ok = mbar_wait_bounded(&sm.q_free[(chunks - 1) % kStages],
+                                       (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
+        } else {
+            for (int c = 0; c < chunks; ++c) {
+                const uint64_t pp = tc_desc_advance(d0, kPAt);
+                const uint32_t vt = tmem + kTVt + 32 * (c & 1), par = (uint32_t)(c & 1);
+                ok = mbar_wait_bounded(&sm.p_full, par, a.err) &&
+                     (c < 2 || mbar_wait_bounded(&sm.o_free[c & 1], (uint32_t)(((c >> 1) - 1) & 1), a.err));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int p = kParts - 1; p >= 0; --p)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc_mma_ts(tmem + kTO + 64 * (c & 1), vt + 8 * ks, tc_desc_advance(pp, p * kHalf + 32 * ks), id_o,
+                                      p < kParts - 1 || ks > 0);
+                    tc_commit(&sm.oa_full[c & 1]);
                     tc_commit(&sm.kd_free[c & 1]);
                 }
                 __syncwarp();
             }
             if (ok && chunks > 0)
-                ok = mbar_wait_bounded(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err) &&
-                     mbar_wait_bounded(&sm.kv_free[(chunks - 1) % kStages],
-                                       (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
+                ok = mbar_wait_bounded(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err);
         }
         if (!ok) {                               // a wait gave up: whatever still runs ends first
             if (elect_one()) tc_commit(&sm.drain[warp]);
             __syncwarp();
             mbar_wait_bounded(&sm.drain[warp], 0, nullptr);
-        }
-    } else if (warp >= kOutWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
-        // ---- o -------------------------------------------------------------------------------
-        const int j = 32 * (warp & 3) + lane, t0 = 32 * ((warp - kOutWarp0) >> 2);   // value, first token
-        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const long step = (long)units * kHeadDim;
-        float* o = a.o + (begin + t0) * step + (long)unit * kHeadDim;    // the same for the whole warp
-        const float4* pw = reinterpret_cast<const float4*>(sm.pw1 + t0);
-        for (int c = 0; c < chunks; ++c, o += kC * step) {
-            const uint32_t par = (uint32_t)(c & 1);
-            // e^{g (t+1)} S Q^T, back to where V^T P^T is added
-            ok = mbar_wait_bounded(&sm.oi_full, par, a.err);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x[16];
-                tmem_ld16(tl + kTO + t0 + 16 * b, x);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 f = pw[4 * b + i];
-                    const float2 u = __fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y));
-                    const float2 w = __fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
-                    x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = w.x; x[4 * i + 3] = w.y;
-                }
-                tmem_st16(tl + kTO + t0 + 16 * b, x);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&sm.oi_free);
-            ok = mbar_wait_bounded(&sm.oa_full, par, a.err);
-            if (!ok) break;
-            tc_fence_after();
-            const int live = len - c * kC - t0;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x[16];
-                tmem_ld16(tl + kTO + t0 + 16 * b, x);
-                tmem_ld_wait();
-                if (b == 1) {
-                    tc_fence_before();
-                    warp_arrive(&sm.oa_free);
-                }
-                float* ob = o + 16 * b * step + j;
-                if (live >= 32) {
-#pragma unroll
-                    for (int t = 0; t < 16; ++t, ob += step) __stcs(ob, a.scale * x[t]);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < 16; ++t, ob += step)
-                        if (16 * b + t < live) __stcs(ob, a.scale * x[t]);
-                }
-            }
         }
     } else if (warp >= kConvWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
@@ -383,18 +333,16 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         const uint32_t b0 = __shfl_sync(0xffffffffu, smem_u32(base), 0);
         if (cw == 2) {                           // t < 32 <= s: P is 0 there, once and for all
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+            for (int p = 0; p < kParts; ++p)
 #pragma unroll
                 for (int q = 4; q < 8; ++q)
                     *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
                         make_uint4(0u, 0u, 0u, 0u);
         }
-        float f[16];                             // e^{g (t - s)} of its 16 s, -1 where s > t
+        float f[16];                             // P's factors of its 16 s
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int gap = prow - (pcol + i);
-            f[i] = gap >= 0 ? sm.pw[gap] : -1.0f;
-        }
+        for (int i = 0; i < 16; ++i) f[i] = sm.down[pcol + i];
+        const int last = prow - pcol;            // the last of them that t sees
         for (int c = 0; c < chunks; ++c) {
             const int st = c % kStages;
             const uint32_t par = (uint32_t)(c & 1);
@@ -427,8 +375,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             // Kd: tokens 8 cw .., transposed to [key][token]
             {
                 const int t = 8 * cw + 2 * (lane & 3), r = lane & 7;
-                const float2 d = make_float2(t < nt ? sm.pw[nt - 1 - t] : 0.0f,
-                                             t + 1 < nt ? sm.pw[nt - 2 - t] : 0.0f);
+                const float2 d = make_float2(sm.pw[mid + max(nt - 1 - t, 0)], sm.pw[mid + max(nt - 2 - t, 0)]);
                 uint32_t w[4][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -443,15 +390,15 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int ic = 4 * q + (lane >> 3);
-                    uint32_t o[3][4];
+                    uint32_t o[kParts][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 x = make_float2(__uint_as_float(w[q][i] << 16),
                                                      __uint_as_float(w[q][i] & 0xffff0000u));
-                        split3(__fmul2_rn(x, d), o[0][i], o[1][i], o[2][i]);
+                        split2(__fmul2_rn(x, d), o[0][i], o[1][i]);
                     }
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
+                    for (int p = 0; p < kParts; ++p)
                         stsm4(kd + p * kTileBytes + (8 * ic + r) * 128 + ((cw ^ r) * 16), o[p]);
                 }
             }
@@ -468,20 +415,27 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(&sm.sc_free);
-            uint32_t o[2][3][4];
+            uint32_t o[2][kParts][4];
+            if (strong)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] *= i == last ? 1.0f : expf(g * (float)max(last - i, 0));
+            // (where s > t not 0 times q k: it is what it is for tokens to come, and another sequence's behind the
+            // end)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                // (not 0 times q k: q k is what it is for tokens to come, and another sequence's behind the end)
-                const float2 y = make_float2(f[2 * i] < 0.0f ? 0.0f : x[2 * i] * f[2 * i],
-                                             f[2 * i + 1] < 0.0f ? 0.0f : x[2 * i + 1] * f[2 * i + 1]);
-                split3(y, o[i >> 2][0][i & 3], o[i >> 2][1][i & 3], o[i >> 2][2][i & 3]);
+                float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(f[2 * i], f[2 * i + 1]));
+                if (quarter != 1) {
+                    y.x = 2 * i <= last ? y.x : 0.0f;
+                    y.y = 2 * i + 1 <= last ? y.y : 0.0f;
+                }
+                split2(y, o[i >> 2][0][i & 3], o[i >> 2][1][i & 3]);
             }
-            if (c > 0) ok = mbar_wait_bounded(&sm.oa_full, par ^ 1u, a.err);
+            if (c > 0) ok = mbar_wait_bounded(&sm.oa_full[(c & 1) ^ 1], (uint32_t)(((c - 1) >> 1) & 1), a.err);
             if (!ok) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
+                for (int p = 0; p < kParts; ++p)
                     *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + prow * 128 +
                                               (((pcol / 8 + q) ^ (prow & 7)) * 16)) =
                         make_uint4(o[q][p][0], o[q][p][1], o[q][p][2], o[q][p][3]);
@@ -490,40 +444,46 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
-        // ---- the state -----------------------------------------------------------------------
-        const int j = 32 * (warp & 3) + lane, hf = (warp - kStateWarp0) >> 2;     // value row, half of its keys
+        // ---- the state and o -----------------------------------------------------------------
+        // value row j; keys 32 part .. of its state, tokens 16 part .. of its outputs
+        const int j = 32 * (warp & 3) + lane, part = (warp - kStateWarp0) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        float2 S[32];                            // keys 64 hf ..
+        float2 S[16];                            // times e^{mid g}
         if (a.state_in != nullptr) {
+            const float in = chunks > 0 ? sm.pw[mid] : 1.0f;
             const float4* src = reinterpret_cast<const float4*>(
-                a.state_in + (((long)n * units + unit) * kHeadDim + j) * kHeadDim + 64 * hf);
+                a.state_in + (((long)n * units + unit) * kHeadDim + j) * kHeadDim + 32 * part);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float4 x = __ldg(src + i);
-                S[2 * i] = make_float2(x.x, x.y);
-                S[2 * i + 1] = make_float2(x.z, x.w);
+                S[2 * i] = make_float2(x.x * in, x.y * in);
+                S[2 * i + 1] = make_float2(x.z * in, x.w * in);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 16; ++i) S[i] = make_float2(0.0f, 0.0f);
         }
         auto put_state = [&]() {
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {        // 8 keys: 4 columns of each part
-                uint32_t w[3][4];
+            for (int b = 0; b < 4; ++b) {        // 8 keys: 4 columns of each part
+                uint32_t w[kParts][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split3(S[4 * b + i], w[0][i], w[1][i], w[2][i]);
+                for (int i = 0; i < 4; ++i) split2(S[4 * b + i], w[0][i], w[1][i]);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) tmem_st4(tl + kTSp + 64 * p + 32 * hf + 4 * b, w[p]);
+                for (int p = 0; p < kParts; ++p) tmem_st4(tl + kTSp + 64 * p + 16 * part + 4 * b, w[p]);
             }
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&sm.sp_full);
         };
         if (chunks > 0) put_state();
-        for (int c = 0; c < chunks; ++c) {
+        const long step = (long)units * kHeadDim;
+        float* o = a.o + (begin + 16 * part) * step + (long)unit * kHeadDim + j;
+        const float4* up = reinterpret_cast<const float4*>(sm.up + 16 * part);
+        for (int c = 0; c < chunks; ++c, o += kC * step) {
             const uint32_t par = (uint32_t)(c & 1);
-            const int nt = min(kC, len - c * kC);
+            const int nt = min(kC, len - c * kC), live = nt - 16 * part;
+            const uint32_t to = tl + kTO + 64 * (c & 1) + 16 * part;
             // S <- e^{g nt} S + U; above a half as S + (e^{g nt} - 1) S, which keeps a decay next to 1
             const float lam = sm.pw[nt];
             const bool near1 = lam > 0.5f;
@@ -533,32 +493,69 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 float u[16];
-                tmem_ld16(tl + kTU + 64 * hf + 16 * b, u);
+                tmem_ld16(tl + kTU + 32 * part + 16 * b, u);
                 tmem_ld_wait();
-                if (b == 3) {
+                if (b == 1) {
                     tc_fence_before();
                     warp_arrive(&sm.u_free);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float2& x = S[8 * b + i];
-                    x = __ffma2_rn(fa2, x, __ffma2_rn(fd2, x, make_float2(u[2 * i], u[2 * i + 1])));
+                    float2& y = S[8 * b + i];
+                    y = __ffma2_rn(fa2, y, __ffma2_rn(fd2, y, make_float2(u[2 * i], u[2 * i + 1])));
                 }
             }
-            if (c + 1 == chunks) break;
-            ok = mbar_wait_bounded(&sm.oi_full, par, a.err);     // S Q^T has read the parts
+            if (strong) {                        // V^T P^T by itself: stored, and S Q^T added to it below
+                ok = mbar_wait_bounded(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int t = 0; t < 16; t += 4) {
+                    float x[4];
+                    tmem_ld4(to + t, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t + i < live) o[(t + i) * step] = a.scale * x[i];
+                }
+                tc_fence_before();
+                warp_arrive(&sm.oa_free);
+            }
+            ok = mbar_wait_bounded(&sm.o_full, par, a.err);      // O is whole, S Q^T has read the parts
             if (!ok) break;
             tc_fence_after();
-            put_state();
+            if (c + 1 < chunks) put_state();
+            float x[16];
+            tmem_ld16(to, x);
+            tmem_ld_wait();
+            tc_fence_before();
+            warp_arrive(&sm.o_free[c & 1]);
+            float* ob = o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = up[i];
+                const float2 u = __fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y));
+                const float2 w = __fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
+                x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = w.x; x[4 * i + 3] = w.y;
+            }
+            if (live >= 16 && !strong) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t, ob += step) __stcs(ob, x[t]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 16; ++t, ob += step)
+                    if (t < live) *ob = strong ? *ob + x[t] : x[t];
+            }
         }
         if (ok) {
+            const float out = chunks > 0 ? 1.0f / sm.pw[mid] : 1.0f;
             float4* dst = reinterpret_cast<float4*>(
-                a.state_out + (((long)n * units + unit) * kHeadDim + j) * kHeadDim + 64 * hf);
+                a.state_out + (((long)n * units + unit) * kHeadDim + j) * kHeadDim + 32 * part);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                dst[i] = make_float4(S[2 * i].x, S[2 * i].y, S[2 * i + 1].x, S[2 * i + 1].y);
+            for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(S[2 * i].x * out, S[2 * i].y * out, S[2 * i + 1].x * out, S[2 * i + 1].y * out);
         }
     }
     tc_fence_before();
