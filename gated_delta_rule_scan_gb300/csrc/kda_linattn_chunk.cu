@@ -23,8 +23,8 @@
 // [key][token] while it is formed.  The 512 TMEM columns are full: S parts 2 x 64, V^T Kd 128, the
 // outputs 64, q k 64, v 2 x 32.
 // 64 tokens, not 128: the parts of P and Kd then fit beside two stages of q, k, v.
-// Warps have roles: 16 hold the state (32 f32 a thread) and write o, 8 turn k into Kd and q k into P, three
-// issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads, the MMAs and the groups'
+// Warps have roles: 16 hold the state (32 f32 a thread) and write o, 8 turn k into Kd and q k into P (4 of
+// them a chunk, in turn), three issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads, the MMAs and the groups'
 // register work overlap across chunks.  (One issuing warp took 50 to 100 cycles an MMA beside six busy
 // warps on its scheduler, twice the tensor pipe's time.)
 #include "kda_tc.cuh"
@@ -50,9 +50,10 @@ constexpr int kStateWarps = 16, kConvWarps = 8;
 constexpr int kUWarp = 0, kOiWarp = 1, kTmaWarp = 3, kStateWarp0 = 4;
 constexpr int kConvWarp0 = kStateWarp0 + kStateWarps;
 constexpr int kThr = 32 * (kConvWarp0 + kConvWarps);
-constexpr int kPWarps = 6;                       // converting warps with a share of P
+constexpr int kGroupWarps = 4;                   // converting warps of a chunk: two groups in turn
+constexpr int kPWarps = 3;                       // those of them with a share of P
 constexpr int kLaunchRegs = 72;
-constexpr int kStateRegs = 88, kConvRegs = 64, kOtherRegs = 24;
+constexpr int kStateRegs = 80, kConvRegs = 80, kOtherRegs = 24;
 static_assert(32 * (kStateWarps * kStateRegs + kConvWarps * kConvRegs + 4 * kOtherRegs) <= kThr * kLaunchRegs, "");
 
 struct __align__(16) Tail {
@@ -61,7 +62,7 @@ struct __align__(16) Tail {
     float up[kC];                                // the outputs': scale * e^{g (t-31)}, or scale * e^{g (t+1)}
     uint64_t kv_full[kStages], kv_free[kStages], q_full[kStages], q_free[kStages];
     uint64_t kd_full[2], kd_free[2];
-    uint64_t sc_full, sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free[2];
+    uint64_t sc_full[2], sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free[2];
     uint64_t drain[3];
     uint32_t tmem;
 };
@@ -144,15 +145,15 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
                 mbar_init(&sm.kv_full[i], 1);
-                mbar_init(&sm.kv_free[i], kConvWarps + 1);
+                mbar_init(&sm.kv_free[i], kGroupWarps + 1);
                 mbar_init(&sm.q_full[i], 1);
                 mbar_init(&sm.q_free[i], 2);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sm.kd_full[i], kConvWarps);
+                mbar_init(&sm.kd_full[i], kGroupWarps);
                 mbar_init(&sm.kd_free[i], 2);
             }
-            mbar_init(&sm.sc_full, 1);
+            for (int i = 0; i < 2; ++i) mbar_init(&sm.sc_full[i], 1);
             mbar_init(&sm.sc_free, kPWarps);
             mbar_init(&sm.u_full, 1);
             mbar_init(&sm.u_free, kStateWarps);
@@ -174,6 +175,15 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             sm.down[i] = strong || i == kMid - 1 ? 1.0f : expf(g * (float)(kMid - 1 - i));
             sm.up[i] = a.scale * (strong ? expf(g * (float)(i + 1)) : i == kMid - 1 ? 1.0f : expf(g * (float)(i - kMid + 1)));
         }
+    }
+    if (warp == kConvWarp0) {                    // t < 32 <= s: P is 0 there, once and for all
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int q = 4; q < 8; ++q)
+                *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
@@ -241,7 +251,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                         tc_mma_ss(tmem + kTSc + 32, tc_desc_advance(s, kQAt - kHalf + off),
                                   tc_desc_advance(s, kKAt + kHalf / 2 + off), id_sc, ks > 0);
                     }
-                    tc_commit(&sm.sc_full);
+                    tc_commit(&sm.sc_full[c & 1]);
                     tc_commit(&sm.kv_free[st]);
                     tc_commit(&sm.q_free[st]);
                 }
@@ -324,82 +334,71 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             mbar_wait_bounded(&sm.drain[warp], 0, nullptr);
         }
     } else if (warp >= kConvWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         // ---- k into Kd, q k into P -----------------------------------------------------------
-        const int cw = warp - kConvWarp0, quarter = cw & 3;
-        const int prow = (quarter == 0 ? 0 : 32) + lane;              // token t of P
-        const int pcol = (quarter == 3 ? 32 : 0) + 16 * (cw >> 2);    // its tokens s
+        const int quarter = (warp - kConvWarp0) & 3, r = lane & 7;
+        const int prow = 32 * (quarter != 0) + lane;                  // token t of P
+        const int pcol = 32 * (quarter == 3);                         // the first of its 32 tokens s
+        const int last = prow - pcol;                                 // the last of them that t sees
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t b0 = __shfl_sync(0xffffffffu, smem_u32(base), 0);
-        if (cw == 2) {                           // t < 32 <= s: P is 0 there, once and for all
-#pragma unroll
-            for (int p = 0; p < kParts; ++p)
-#pragma unroll
-                for (int q = 4; q < 8; ++q)
-                    *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                        make_uint4(0u, 0u, 0u, 0u);
-        }
-        float f[16];                             // P's factors of its 16 s
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = sm.down[pcol + i];
-        const int last = prow - pcol;            // the last of them that t sees
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = (warp - kConvWarp0) / kGroupWarps; c < chunks; c += 2) {
             const int st = c % kStages;
-            const uint32_t par = (uint32_t)(c & 1);
+            const uint32_t pc = (uint32_t)((c >> 1) & 1);
             const int nt = min(kC, len - c * kC);
             const uint32_t stage = b0 + st * kStageBytes, kd = b0 + kKdAt + (c & 1) * kKdBytes;
-            ok = mbar_wait_bounded(&sm.kv_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
-                 (c < 2 || mbar_wait_bounded(&sm.kd_free[c & 1], (uint32_t)(((c >> 1) - 1) & 1), a.err));
+            // (in this order: the MMAs of chunk c - 2 come after those of c - 3, whose loads were this stage's
+            // last, so that the barrier of its loads is not a phase behind)
+            ok = (c < 2 || mbar_wait_bounded(&sm.kd_free[c & 1], pc ^ 1u, a.err)) &&
+                 mbar_wait_bounded(&sm.kv_full[st], (uint32_t)((c / kStages) & 1), a.err);
             if (!ok) break;
-            // v^T: values of this warp's lane quarter, tokens 32 (cw / 4) ..
-            {
-                const int vs = 32 * (cw >> 2) + 8 * (lane >> 4) + (lane & 7);     // + 16 for the second pair
-                const int ve = 32 * (cw >> 2) + 2 * (lane & 3);                   // of the words it gets
+            // v^T: values of this warp's lane quarter, 16 and 16, tokens 0 .. 31 and 32 ..
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {                                     // 16 values
-                    const int jc = 4 * quarter + 2 * h + ((lane >> 3) & 1);       // 16-byte piece of the row
-                    uint32_t w[8];
+            for (int h = 0; h < 4; ++h) {
+                const int jc = 4 * quarter + 2 * (h & 1) + ((lane >> 3) & 1);     // 16-byte piece of the row
+                const int vs = 32 * (h >> 1) + 8 * (lane >> 4) + r;               // + 16 for the second pair
+                uint32_t w[8];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        ldsm4_t(*reinterpret_cast<uint32_t(*)[4]>(w + 4 * q),
-                                stage + kVAt + (jc >> 3) * kHalf + (vs + 16 * q) * 128 + (((jc ^ vs) & 7) * 16));
-                    if (nt < kC)      // rows past the sequence's end are another's: 0 times a NaN there is not 0
+                for (int q = 0; q < 2; ++q)
+                    ldsm4_t(*reinterpret_cast<uint32_t(*)[4]>(w + 4 * q),
+                            stage + kVAt + (jc >> 3) * kHalf + (vs + 16 * q) * 128 + (((jc ^ vs) & 7) * 16));
+                if (nt < kC)      // rows past the sequence's end are another's: 0 times a NaN there is not 0
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int t = ve + 8 * (i >> 1);
-                            w[i] = t >= nt ? 0u : t + 1 >= nt ? w[i] & 0xffffu : w[i];
-                        }
-                    tmem_st_16x128b_x4(tl + ((uint32_t)(16 * h) << 16) + kTVt + 32 * (c & 1) + 16 * (cw >> 2), w);
-                }
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = 32 * (h >> 1) + 8 * (i >> 1) + 2 * (lane & 3);
+                        w[i] = t >= nt ? 0u : t + 1 >= nt ? w[i] & 0xffffu : w[i];
+                    }
+                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + kTVt + 32 * (c & 1) + 16 * (h >> 1), w);
             }
-            // Kd: tokens 8 cw .., transposed to [key][token]
-            {
-                const int t = 8 * cw + 2 * (lane & 3), r = lane & 7;
-                const float2 d = make_float2(sm.pw[mid + max(nt - 1 - t, 0)], sm.pw[mid + max(nt - 2 - t, 0)]);
-                uint32_t w[4][4];
+            // Kd: tokens 16 quarter .., 8 and 8, transposed to [key][token]
+            uint32_t kw[2][4][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int ic = 4 * q + (lane >> 3);                           // 16-byte piece of k's row
-                    ldsm4_t(w[q], stage + kKAt + (ic >> 3) * kHalf + (8 * cw + r) * 128 + (((ic ^ r) & 7) * 16));
+                    ldsm4_t(kw[h][q], stage + kKAt + (ic >> 3) * kHalf + (16 * quarter + 8 * h + r) * 128 +
+                                          (((ic ^ r) & 7) * 16));
                 }
-                warp_arrive(&sm.kv_free[st]);
-                if (nt < kC)
+            warp_arrive(&sm.kv_free[st]);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i >> 2][i & 3] = t >= nt ? 0u : t + 1 >= nt ? w[i >> 2][i & 3] & 0xffffu : w[i >> 2][i & 3];
+            for (int h = 0; h < 2; ++h) {
+                const int sb = 2 * quarter + h, t = 8 * sb + 2 * (lane & 3);
+                const float2 d = make_float2(sm.pw[mid + max(nt - 1 - t, 0)], sm.pw[mid + max(nt - 2 - t, 0)]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int ic = 4 * q + (lane >> 3);
                     uint32_t o[kParts][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 x = make_float2(__uint_as_float(w[q][i] << 16),
-                                                     __uint_as_float(w[q][i] & 0xffff0000u));
+                        uint32_t w = kw[h][q][i];
+                        if (nt < kC) w = t >= nt ? 0u : t + 1 >= nt ? w & 0xffffu : w;
+                        const float2 x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
                         split2(__fmul2_rn(x, d), o[0][i], o[1][i]);
                     }
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
-                        stsm4(kd + p * kTileBytes + (8 * ic + r) * 128 + ((cw ^ r) * 16), o[p]);
+                        stsm4(kd + p * kTileBytes + (8 * ic + r) * 128 + ((sb ^ r) * 16), o[p]);
                 }
             }
             tmem_st_wait();
@@ -407,23 +406,25 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             fence_proxy_async_smem();
             warp_arrive(&sm.kd_full[c & 1]);
             if (quarter == 2) continue;
-            ok = mbar_wait_bounded(&sm.sc_full, par, a.err);
+            ok = mbar_wait_bounded(&sm.sc_full[c & 1], pc, a.err);
             if (!ok) break;
             tc_fence_after();
-            float x[16];
-            tmem_ld16(tl + kTSc + pcol, x);
+            float x[32];
+            tmem_ld16(tl + kTSc + pcol, *reinterpret_cast<float(*)[16]>(x));
+            tmem_ld16(tl + kTSc + pcol + 16, *reinterpret_cast<float(*)[16]>(x + 16));
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(&sm.sc_free);
-            uint32_t o[2][kParts][4];
             if (strong)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= i == last ? 1.0f : expf(g * (float)max(last - i, 0));
-            // (where s > t not 0 times q k: it is what it is for tokens to come, and another sequence's behind the
-            // end)
+                for (int i = 0; i < 32; ++i) x[i] *= i == last ? 1.0f : expf(g * (float)max(last - i, 0));
+            uint32_t o[4][kParts][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(f[2 * i], f[2 * i + 1]));
+            for (int i = 0; i < 16; ++i) {
+                const float2 f = *reinterpret_cast<const float2*>(sm.down + pcol + 2 * i);
+                float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), f);
+                // (where s > t not 0 times q k: it is what it is for tokens to come, and another sequence's
+                // behind the end)
                 if (quarter != 1) {
                     y.x = 2 * i <= last ? y.x : 0.0f;
                     y.y = 2 * i + 1 <= last ? y.y : 0.0f;
@@ -433,7 +434,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             if (c > 0) ok = mbar_wait_bounded(&sm.oa_full[(c & 1) ^ 1], (uint32_t)(((c - 1) >> 1) & 1), a.err);
             if (!ok) break;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
                     *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + prow * 128 +
