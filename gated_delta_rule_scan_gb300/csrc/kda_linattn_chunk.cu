@@ -11,7 +11,7 @@
 // the powers as they stand, all of them at most 1, and a slower pipeline: there S Q^T matters to a few tens
 // of tokens at most, but overflow must not.
 // q, k and v enter as the bf16 values they are; what is f32 (P, Kd and the state) enters as bf16 hi + lo,
-// within 2^-18 of an element, as x does in the bf16 projections: outputs and states come within about 1e-6
+// within 2^-17 of an element, as x does in the bf16 projections: outputs and states come within about 1e-6
 // of their scale.  (A third part brought 1e-7 for half as much again in MMAs and splitting, 166 against
 // TODO us at 4096 tokens x 64 heads.)  The state itself stays in f32 registers.
 //
@@ -81,6 +81,32 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& a, uint32_t& b) {
     b = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// mbar_wait_bounded for two dozen warps that wait most of the time: the suspended wait is left to the
+// hardware (polling took issue slots from the warps that work), and a clock bounds it.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, int* err) {
+    unsigned long long t0;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (done) return true;
+        unsigned long long t;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+        if (t - t0 > 1000000000ull) break;
+    }
+    if (err) atomicOr(err, kDevErrTimeout);
+    return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
+    return mbar_try_wait(bar, parity) || mbar_wait_long(bar, parity, err);
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -126,8 +152,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
     long begin;
     int len;
     if (a.seq.cu_seqlens != nullptr) {
-        begin = a.seq.cu_seqlens[n];
-        len = a.seq.cu_seqlens[n + 1] - (int)begin;
+        begin = __shfl_sync(0xffffffffu, a.seq.cu_seqlens[n], 0);
+        len = __shfl_sync(0xffffffffu, a.seq.cu_seqlens[n + 1], 0) - (int)begin;
     } else {
         begin = (long)n * a.seq.T_uniform;
         len = a.seq.T_uniform;
@@ -199,7 +225,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             const uint32_t before = (uint32_t)((c / kStages - 1) & 1);
             unsigned char* s = base + st * kStageBytes;
             const int row = (int)(begin + (long)c * kC);
-            if (c >= kStages) ok = mbar_wait_bounded(&sm.kv_free[st], before, a.err);
+            if (c >= kStages) ok = mbar_wait(&sm.kv_free[st], before, a.err);
             if (ok && elect_one()) {
                 mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
                 for (int h = 0; h < 2; ++h) {
@@ -208,7 +234,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 }
             }
             __syncwarp();
-            if (ok && c >= kStages) ok = mbar_wait_bounded(&sm.q_free[st], before, a.err);
+            if (ok && c >= kStages) ok = mbar_wait(&sm.q_free[st], before, a.err);
             if (ok && elect_one()) {
                 mbar_arrive_expect_tx(&sm.q_full[st], kTileBytes);
                 for (int h = 0; h < 2; ++h)
@@ -219,8 +245,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         if (!ok)                                 // no load may land after the CTA has left
             for (int i = 0; i < kStages; ++i)
                 for (uint32_t p = 0; p < 2; ++p) {
-                    mbar_wait_bounded(&sm.kv_full[i], p, nullptr);
-                    mbar_wait_bounded(&sm.q_full[i], p, nullptr);
+                    mbar_wait(&sm.kv_full[i], p, nullptr);
+                    mbar_wait(&sm.q_full[i], p, nullptr);
                 }
     } else if (warp < kTmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -237,8 +263,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 // q_t . k_s, s < 32 with q on the lanes 0 .. 63, s >= 32 with q on 64 .. 127: the threads of
                 // three lane quarters then share the work on P.  (M = 128 covers twice the rows of q's tile,
                 // those behind it, or before it, being whatever lies there: their lanes are never read.)
-                ok = mbar_wait_bounded(&sm.kv_full[st], pst, a.err) && mbar_wait_bounded(&sm.q_full[st], pst, a.err) &&
-                     (c == 0 || mbar_wait_bounded(&sm.sc_free, par ^ 1u, a.err));
+                ok = mbar_wait(&sm.kv_full[st], pst, a.err) && mbar_wait(&sm.q_full[st], pst, a.err) &&
+                     (c == 0 || mbar_wait(&sm.sc_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t s = tc_desc_advance(d0, st * kStageBytes);
@@ -258,8 +284,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 __syncwarp();
                 const uint64_t kd = tc_desc_advance(d0, kKdAt + (c & 1) * kKdBytes);
                 const uint32_t vt = tmem + kTVt + 32 * (c & 1);
-                ok = mbar_wait_bounded(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
-                     (c == 0 || mbar_wait_bounded(&sm.u_free, par ^ 1u, a.err));
+                ok = mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
+                     (c == 0 || mbar_wait(&sm.u_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -276,17 +302,17 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             }
             // no arrival of the tensor pipe on a barrier of a CTA that has left: each warp sees its last
             if (ok && chunks > 0)
-                ok = mbar_wait_bounded(&sm.kv_free[(chunks - 1) % kStages],
+                ok = mbar_wait(&sm.kv_free[(chunks - 1) % kStages],
                                        (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
         } else if (warp == kOiWarp) {
             for (int c = 0; c < chunks; ++c) {
                 const int st = c % kStages;
                 const uint64_t q = tc_desc_advance(d0, st * kStageBytes + kQAt);
                 const uint32_t par = (uint32_t)(c & 1);
-                ok = mbar_wait_bounded(&sm.q_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
-                     mbar_wait_bounded(&sm.sp_full, par, a.err) &&
-                     mbar_wait_bounded(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
-                     (!strong || mbar_wait_bounded(&sm.oa_free, par, a.err));
+                ok = mbar_wait(&sm.q_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
+                     mbar_wait(&sm.sp_full, par, a.err) &&
+                     mbar_wait(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
+                     (!strong || mbar_wait(&sm.oa_free, par, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -303,14 +329,16 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 __syncwarp();
             }
             if (ok && chunks > 0)
-                ok = mbar_wait_bounded(&sm.q_free[(chunks - 1) % kStages],
+                ok = mbar_wait(&sm.q_free[(chunks - 1) % kStages],
                                        (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
         } else {
             for (int c = 0; c < chunks; ++c) {
                 const uint64_t pp = tc_desc_advance(d0, kPAt);
                 const uint32_t vt = tmem + kTVt + 32 * (c & 1), par = (uint32_t)(c & 1);
-                ok = mbar_wait_bounded(&sm.p_full, par, a.err) &&
-                     (c < 2 || mbar_wait_bounded(&sm.o_free[c & 1], (uint32_t)(((c >> 1) - 1) & 1), a.err));
+                // (v's last quarter comes from a warp without a share of P)
+                ok = mbar_wait(&sm.p_full, par, a.err) &&
+                     mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
+                     (c < 2 || mbar_wait(&sm.o_free[c & 1], (uint32_t)(((c >> 1) - 1) & 1), a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -326,12 +354,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 __syncwarp();
             }
             if (ok && chunks > 0)
-                ok = mbar_wait_bounded(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err);
+                ok = mbar_wait(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err);
         }
         if (!ok) {                               // a wait gave up: whatever still runs ends first
             if (elect_one()) tc_commit(&sm.drain[warp]);
             __syncwarp();
-            mbar_wait_bounded(&sm.drain[warp], 0, nullptr);
+            mbar_wait(&sm.drain[warp], 0, nullptr);
         }
     } else if (warp >= kConvWarp0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvRegs));
@@ -349,8 +377,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             const uint32_t stage = b0 + st * kStageBytes, kd = b0 + kKdAt + (c & 1) * kKdBytes;
             // (in this order: the MMAs of chunk c - 2 come after those of c - 3, whose loads were this stage's
             // last, so that the barrier of its loads is not a phase behind)
-            ok = (c < 2 || mbar_wait_bounded(&sm.kd_free[c & 1], pc ^ 1u, a.err)) &&
-                 mbar_wait_bounded(&sm.kv_full[st], (uint32_t)((c / kStages) & 1), a.err);
+            ok = (c < 2 || mbar_wait(&sm.kd_free[c & 1], pc ^ 1u, a.err)) &&
+                 mbar_wait(&sm.kv_full[st], (uint32_t)((c / kStages) & 1), a.err);
             if (!ok) break;
             // v^T: values of this warp's lane quarter, 16 and 16, tokens 0 .. 31 and 32 ..
 #pragma unroll
@@ -406,7 +434,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             fence_proxy_async_smem();
             warp_arrive(&sm.kd_full[c & 1]);
             if (quarter == 2) continue;
-            ok = mbar_wait_bounded(&sm.sc_full[c & 1], pc, a.err);
+            ok = mbar_wait(&sm.sc_full[c & 1], pc, a.err);
             if (!ok) break;
             tc_fence_after();
             float x[32];
@@ -431,7 +459,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 }
                 split2(y, o[i >> 2][0][i & 3], o[i >> 2][1][i & 3]);
             }
-            if (c > 0) ok = mbar_wait_bounded(&sm.oa_full[(c & 1) ^ 1], (uint32_t)(((c - 1) >> 1) & 1), a.err);
+            if (c > 0) ok = mbar_wait(&sm.oa_full[(c & 1) ^ 1], (uint32_t)(((c - 1) >> 1) & 1), a.err);
             if (!ok) break;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -479,7 +507,9 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         };
         if (chunks > 0) put_state();
         const long step = (long)units * kHeadDim;
-        float* o = a.o + (begin + 16 * part) * step + (long)unit * kHeadDim + j;
+        // (rows by 32-bit offsets from an address that the whole warp shares: one addition a store)
+        float* o = a.o + (begin + 16 * part) * step + (long)unit * kHeadDim;
+        const uint32_t step4 = (uint32_t)step * 4;
         const float4* up = reinterpret_cast<const float4*>(sm.up + 16 * part);
         for (int c = 0; c < chunks; ++c, o += kC * step) {
             const uint32_t par = (uint32_t)(c & 1);
@@ -490,7 +520,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             const bool near1 = lam > 0.5f;
             const float fa = near1 ? 1.0f : lam, fd = near1 ? expm1f(g * (float)nt) : 0.0f;
             const float2 fa2 = make_float2(fa, fa), fd2 = make_float2(fd, fd);
-            ok = mbar_wait_bounded(&sm.u_full, par, a.err);
+            ok = mbar_wait(&sm.u_full, par, a.err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -509,7 +539,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 }
             }
             if (strong) {                        // V^T P^T by itself: stored, and S Q^T added to it below
-                ok = mbar_wait_bounded(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err);
+                ok = mbar_wait(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -519,12 +549,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (t + i < live) o[(t + i) * step] = a.scale * x[i];
+                        if (t + i < live) o[(t + i) * step + j] = a.scale * x[i];
                 }
                 tc_fence_before();
                 warp_arrive(&sm.oa_free);
             }
-            ok = mbar_wait_bounded(&sm.o_full, par, a.err);      // O is whole, S Q^T has read the parts
+            ok = mbar_wait(&sm.o_full, par, a.err);      // O is whole, S Q^T has read the parts
             if (!ok) break;
             tc_fence_after();
             if (c + 1 < chunks) put_state();
@@ -533,7 +563,6 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(&sm.o_free[c & 1]);
-            float* ob = o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 f = up[i];
@@ -541,13 +570,18 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 const float2 w = __fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
                 x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = w.x; x[4 * i + 3] = w.y;
             }
+            uint32_t at = (uint32_t)j * 4;
             if (live >= 16 && !strong) {
 #pragma unroll
-                for (int t = 0; t < 16; ++t, ob += step) __stcs(ob, x[t]);
+                for (int t = 0; t < 16; ++t, at += step4)
+                    __stcs(reinterpret_cast<float*>(reinterpret_cast<char*>(o) + at), x[t]);
             } else {
 #pragma unroll
-                for (int t = 0; t < 16; ++t, ob += step)
-                    if (t < live) *ob = strong ? *ob + x[t] : x[t];
+                for (int t = 0; t < 16; ++t, at += step4)
+                    if (t < live) {
+                        float* ob = reinterpret_cast<float*>(reinterpret_cast<char*>(o) + at);
+                        *ob = strong ? *ob + x[t] : x[t];
+                    }
             }
         }
         if (ok) {
