@@ -1079,8 +1079,7 @@ static constexpr long kLinChunkMinLen = 32;
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype) {
     const int m = value_subheads(Dk, Dv);
     if (m == 0 || N < 0 || total_T < 0 || H <= 0 || Hk < 1 || Hk > H) return 0;
-    (void)raw_dtype;
-    return 0;
+    return raw_dtype == KDA_DTYPE_BF16 ? linattn_chunk_workspace_bound(N, total_T, H * m) : 0;
 }
 
 // Contract checks of the linear attention entries and their argument block.
@@ -1116,14 +1115,17 @@ static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_
     if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_ALIGN;
     const size_t sb = (size_t)a.seq.N * a.H * a.m * kHeadDim * kHeadDim * sizeof(float);
     if (state_in && overlap(state_in, state_out, sb)) return KDA_ERR_STATE_ALIAS;
-    (void)workspace;
-    (void)workspace_bytes;
+    const bool chunk = a.bf16 && max_len(a.seq, cu_host) >= kLinChunkMinLen;
+    if (chunk) {
+        const size_t need = linattn_chunk_workspace_bytes(a.seq, cu_host, a.H * a.m);
+        if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return KDA_ERR_ALIGN;
+    }
     if (const int sd = check_stream_device(stream)) return sd;
     a.state_in = state_in;
     a.state_out = state_out;
     a.err = dev_err_ptr();
-    const bool chunk = a.bf16 && max_len(a.seq, cu_host) >= kLinChunkMinLen;
-    return cuda_status(chunk ? launch_linattn_chunk(a, static_cast<cudaStream_t>(stream))
+    return cuda_status(chunk ? launch_linattn_chunk(a, cu_host, workspace, static_cast<cudaStream_t>(stream))
                              : launch_linattn_seq(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -27,7 +27,14 @@
 // them a chunk, in turn), three issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads, the MMAs and the groups'
 // register work overlap across chunks.  (One issuing warp took 50 to 100 cycles an MMA beside six busy
 // warps on its scheduler, twice the tensor pipe's time.)
+//
+// Few sequences and heads leave SMs idle, so long sequences are then cut into segments: a first launch
+// (STATE) forms each segment's own contribution to the state from k and v alone, a second adds them up to
+// the state that each segment starts from, and the third is the kernel above with a CTA a segment.  The cut is
+// chosen by a cost model (plan()).
 #include "kda_tc.cuh"
+
+#include <algorithm>
 
 namespace kda {
 
@@ -66,6 +73,7 @@ struct __align__(16) Tail {
     uint64_t drain[3];
     uint32_t tmem;
 };
+constexpr int kMaxRanked = 32;                   // packed sequences that are taken longest first
 constexpr int kSmemBytes = 1024 + kTailAt + (int)sizeof(Tail);
 
 // TMEM columns
@@ -138,8 +146,27 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  : "memory");
 }
 
+// How the sequences are cut: segments of seg_chunks chunks, at most segs of one sequence; parts: [N][segs - 1]
+// [units][128][128] f32, first the segments' contributions to the state, then the states after them.
+struct Cut {
+    int seg_chunks, segs;
+    float* parts;
+};
+
+__device__ __forceinline__ long seg_state(const Cut& cut, int n, int seg, int units) {
+    return ((long)n * (cut.segs - 1) + seg) * units * (kHeadDim * kHeadDim);
+}
+
+// a + b is e^x: a step S <- e^x S + U is S <- a S + (b S + U).  Above a half a = 1 and b = e^x - 1, which
+// keeps a decay next to 1: rounded itself, e^x would be off by up to 2^-25 at every step.
+__device__ __forceinline__ float2 decay_pair(float x) {
+    const float lam = expf(x);
+    return lam > 0.5f ? make_float2(1.0f, expm1f(x)) : make_float2(lam, 0.0f);
+}
+
+template <bool STATE>
 __global__ void __launch_bounds__(kThr, 1)
-kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq,
+kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__ CUtensorMap tq,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const base = reinterpret_cast<unsigned char*>(
@@ -147,17 +174,33 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
     Tail& sm = *reinterpret_cast<Tail*>(base + kTailAt);
     // (shuffled from lane 0, what is the same in a warp is known to be: it goes to uniform registers)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int unit = blockIdx.x, n = blockIdx.y;
+    const int unit = blockIdx.x, seg = blockIdx.z;
     const int units = a.H * a.m, hv = unit / a.m, hk = hv % a.Hk;
+    int n = blockIdx.y, len;
     long begin;
-    int len;
     if (a.seq.cu_seqlens != nullptr) {
-        begin = __shfl_sync(0xffffffffu, a.seq.cu_seqlens[n], 0);
-        len = __shfl_sync(0xffffffffu, a.seq.cu_seqlens[n + 1], 0) - (int)begin;
+        const int* cu = a.seq.cu_seqlens;
+        if (a.seq.N <= kMaxRanked) {             // the longest sequences first
+            const int mine = lane < a.seq.N ? cu[lane + 1] - cu[lane] : -1;
+            int rank = 0;
+            for (int k = 0; k < a.seq.N; ++k) {
+                const int other = __shfl_sync(0xffffffffu, mine, k);
+                rank += other > mine || (other == mine && k < lane);
+            }
+            n = __ffs(__ballot_sync(0xffffffffu, lane < a.seq.N && rank == n)) - 1;
+        }
+        begin = __shfl_sync(0xffffffffu, cu[n], 0);
+        len = __shfl_sync(0xffffffffu, cu[n + 1], 0) - (int)begin;
     } else {
         begin = (long)n * a.seq.T_uniform;
         len = a.seq.T_uniform;
     }
+    const int seg_len = cut.seg_chunks * kC;
+    if (seg > 0 && seg * (long)seg_len >= len) return;       // (the whole CTA)
+    if (STATE && (seg + 1) * (long)seg_len >= len) return;   // nothing follows this segment
+    const bool ends = (seg + 1) * (long)seg_len >= len;
+    begin += (long)seg * seg_len;
+    len = min(len - seg * seg_len, seg_len);
     const int chunks = (len + kC - 1) / kC;
     const float g = a.log_decay[hv];
     const bool strong = g < -1.0f;
@@ -171,13 +214,13 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
                 mbar_init(&sm.kv_full[i], 1);
-                mbar_init(&sm.kv_free[i], kGroupWarps + 1);
+                mbar_init(&sm.kv_free[i], kGroupWarps + !STATE);
                 mbar_init(&sm.q_full[i], 1);
                 mbar_init(&sm.q_free[i], 2);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sm.kd_full[i], kGroupWarps);
-                mbar_init(&sm.kd_free[i], 2);
+                mbar_init(&sm.kd_free[i], STATE ? 1 : 2);
             }
             for (int i = 0; i < 2; ++i) mbar_init(&sm.sc_full[i], 1);
             mbar_init(&sm.sc_free, kPWarps);
@@ -234,6 +277,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 }
             }
             __syncwarp();
+            if (STATE) continue;
             if (ok && c >= kStages) ok = mbar_wait(&sm.q_free[st], before, a.err);
             if (ok && elect_one()) {
                 mbar_arrive_expect_tx(&sm.q_full[st], kTileBytes);
@@ -246,7 +290,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             for (int i = 0; i < kStages; ++i)
                 for (uint32_t p = 0; p < 2; ++p) {
                     mbar_wait(&sm.kv_full[i], p, nullptr);
-                    mbar_wait(&sm.q_full[i], p, nullptr);
+                    if (!STATE) mbar_wait(&sm.q_full[i], p, nullptr);
                 }
     } else if (warp < kTmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -263,12 +307,14 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                 // q_t . k_s, s < 32 with q on the lanes 0 .. 63, s >= 32 with q on 64 .. 127: the threads of
                 // three lane quarters then share the work on P.  (M = 128 covers twice the rows of q's tile,
                 // those behind it, or before it, being whatever lies there: their lanes are never read.)
-                ok = mbar_wait(&sm.kv_full[st], pst, a.err) && mbar_wait(&sm.q_full[st], pst, a.err) &&
-                     (c == 0 || mbar_wait(&sm.sc_free, par ^ 1u, a.err));
-                if (!ok) break;
-                tc_fence_after();
+                if (!STATE) {
+                    ok = mbar_wait(&sm.kv_full[st], pst, a.err) && mbar_wait(&sm.q_full[st], pst, a.err) &&
+                         (c == 0 || mbar_wait(&sm.sc_free, par ^ 1u, a.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 const uint64_t s = tc_desc_advance(d0, st * kStageBytes);
-                if (elect_one()) {
+                if (!STATE && elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
@@ -302,8 +348,10 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             }
             // no arrival of the tensor pipe on a barrier of a CTA that has left: each warp sees its last
             if (ok && chunks > 0)
-                ok = mbar_wait(&sm.kv_free[(chunks - 1) % kStages],
+                ok = STATE ? mbar_wait(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err)
+                           : mbar_wait(&sm.kv_free[(chunks - 1) % kStages],
                                        (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
+        } else if (STATE) {
         } else if (warp == kOiWarp) {
             for (int c = 0; c < chunks; ++c) {
                 const int st = c % kStages;
@@ -433,7 +481,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             tc_fence_before();
             fence_proxy_async_smem();
             warp_arrive(&sm.kd_full[c & 1]);
-            if (quarter == 2) continue;
+            if (STATE || quarter == 2) continue;
             ok = mbar_wait(&sm.sc_full[c & 1], pc, a.err);
             if (!ok) break;
             tc_fence_after();
@@ -478,19 +526,26 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
         const int j = 32 * (warp & 3) + lane, part = (warp - kStateWarp0) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float2 S[16];                            // times e^{mid g}
-        if (a.state_in != nullptr) {
-            const float in = chunks > 0 ? sm.pw[mid] : 1.0f;
-            const float4* src = reinterpret_cast<const float4*>(
-                a.state_in + (((long)n * units + unit) * kHeadDim + j) * kHeadDim + 32 * part);
+        const long row = ((long)unit * kHeadDim + j) * kHeadDim + 32 * part;    // its state row in a sequence's
+        const long seq_state = (long)units * kHeadDim * kHeadDim;
+        const float* from = STATE ? nullptr : a.state_in;
+        if (!STATE && seg > 0) from = cut.parts + seg_state(cut, n, seg - 1, units) - n * seq_state;
+        if (from != nullptr) {
+            const float4* src = reinterpret_cast<const float4*>(from + n * seq_state + row);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float4 x = __ldg(src + i);
-                S[2 * i] = make_float2(x.x * in, x.y * in);
-                S[2 * i + 1] = make_float2(x.z * in, x.w * in);
+                S[2 * i] = make_float2(x.x, x.y);
+                S[2 * i + 1] = make_float2(x.z, x.w);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = make_float2(0.0f, 0.0f);
+        }
+        if (chunks > 0) {
+            const float2 in = make_float2(sm.pw[mid], sm.pw[mid]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], in);
         }
         auto put_state = [&]() {
 #pragma unroll
@@ -505,7 +560,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             tc_fence_before();
             warp_arrive(&sm.sp_full);
         };
-        if (chunks > 0) put_state();
+        if (!STATE && chunks > 0) put_state();
+        const float2 whole = decay_pair(g * (float)kC);
         const long step = (long)units * kHeadDim;
         // (rows by 32-bit offsets from an address that the whole warp shares: one addition a store)
         float* o = a.o + (begin + 16 * part) * step + (long)unit * kHeadDim;
@@ -515,11 +571,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
             const uint32_t par = (uint32_t)(c & 1);
             const int nt = min(kC, len - c * kC), live = nt - 16 * part;
             const uint32_t to = tl + kTO + 64 * (c & 1) + 16 * part;
-            // S <- e^{g nt} S + U; above a half as S + (e^{g nt} - 1) S, which keeps a decay next to 1
-            const float lam = sm.pw[nt];
-            const bool near1 = lam > 0.5f;
-            const float fa = near1 ? 1.0f : lam, fd = near1 ? expm1f(g * (float)nt) : 0.0f;
-            const float2 fa2 = make_float2(fa, fa), fd2 = make_float2(fd, fd);
+            const float2 f = nt == kC ? whole : decay_pair(g * (float)nt);
+            const float2 fa2 = make_float2(f.x, f.x), fd2 = make_float2(f.y, f.y);
             ok = mbar_wait(&sm.u_full, par, a.err);
             if (!ok) break;
             tc_fence_after();
@@ -538,6 +591,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                     y = __ffma2_rn(fa2, y, __ffma2_rn(fd2, y, make_float2(u[2 * i], u[2 * i + 1])));
                 }
             }
+            if (STATE) continue;
             if (strong) {                        // V^T P^T by itself: stored, and S Q^T added to it below
                 ok = mbar_wait(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err);
                 if (!ok) break;
@@ -584,10 +638,10 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
                     }
             }
         }
-        if (ok) {
+        if (ok && (STATE || ends)) {
             const float out = chunks > 0 ? 1.0f / sm.pw[mid] : 1.0f;
             float4* dst = reinterpret_cast<float4*>(
-                a.state_out + (((long)n * units + unit) * kHeadDim + j) * kHeadDim + 32 * part);
+                (STATE ? cut.parts + seg_state(cut, n, seg, units) : a.state_out + n * seq_state) + row);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 dst[i] = make_float4(S[2 * i].x * out, S[2 * i].y * out, S[2 * i + 1].x * out, S[2 * i + 1].y * out);
@@ -601,21 +655,137 @@ kda_linattn_chunk_kernel(const LinArgs a, const __grid_constant__ CUtensorMap tq
     }
 }
 
+// The contributions of a sequence's segments into the states after them, in place; a thread owns four elements
+// of a unit's state.
+constexpr int kJoinThr = 256;
+constexpr int kJoinAhead = 4;
+
+__global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArgs a, const Cut cut) {
+    constexpr int kPieces = kHeadDim * kHeadDim / 4;
+    const int units = a.H * a.m, n = blockIdx.y;
+    const long piece = (long)blockIdx.x * kJoinThr + threadIdx.x;     // kPieces is a multiple of kJoinThr
+    const int unit = (int)(piece / kPieces);
+    const int len = a.seq.cu_seqlens ? a.seq.cu_seqlens[n + 1] - a.seq.cu_seqlens[n] : a.seq.T_uniform;
+    const int seg_len = cut.seg_chunks * kC;
+    const int parts = (len + seg_len - 1) / seg_len - 1;      // the last segment's is not formed
+    const float2 f = decay_pair(a.log_decay[unit / a.m] * (float)seg_len);
+    const long stride = (long)units * kPieces;
+    float4* at = reinterpret_cast<float4*>(cut.parts + seg_state(cut, n, 0, units)) + piece;
+    float4 S = a.state_in ? __ldg(reinterpret_cast<const float4*>(a.state_in) + (long)n * stride + piece)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = 0; p < parts; p += kJoinAhead) {
+        float4 u[kJoinAhead];
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+            if (p + i < parts) u[i] = at[(p + i) * stride];
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+            if (p + i < parts) {
+                S.x = fmaf(f.x, S.x, fmaf(f.y, S.x, u[i].x));
+                S.y = fmaf(f.x, S.y, fmaf(f.y, S.y, u[i].y));
+                S.z = fmaf(f.x, S.z, fmaf(f.y, S.z, u[i].z));
+                S.w = fmaf(f.x, S.w, fmaf(f.y, S.w, u[i].w));
+                at[(p + i) * stride] = S;
+            }
+    }
+}
+
+// Segments of a call, by the time of their waves of CTAs in us: a chunk of the main kernel 2.05, of the state
+// kernel 0.8, a CTA's start and end 4, the two further launches 7.  (4096 tokens x 64 heads: whole 129 us,
+// 2 segments TODO; 8192 x 8 heads: whole 234, 16 segments TODO.)
+constexpr int kMaxSegs = 32;
+long most_segs(long chains, long chunks, int sms) {
+    return std::max(1L, std::min({(long)kMaxSegs, chunks, 4L * sms / std::max(1L, chains)}));
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+long seq_chunks(const SeqLayout& s, const int* cu_host, int n) {
+    const long len = cu_host ? cu_host[n + 1] - cu_host[n] : s.T_uniform;
+    return (len + kC - 1) / kC;
+}
+
+// Chains of (sequence, unit) that are cut at all: with two on each SM they fill it.
+bool may_cut(long chains, int sms) { return chains < 2L * sms; }
+
+Cut plan(const SeqLayout& s, const int* cu_host, int units) {
+    const int sms = sm_count();
+    long most = 1;
+    for (int n = 0; n < s.N; ++n) most = std::max(most, seq_chunks(s, cu_host, n));
+    Cut best{(int)most, 1, nullptr};
+    if (!may_cut((long)s.N * units, sms)) return best;
+    double least = 0.0;
+    for (long segs = 1; segs <= most_segs((long)s.N * units, most, sms); ++segs) {
+        const long per = (most + segs - 1) / segs;
+        if (segs > 1 && (most + per - 1) / per != segs) continue;
+        long blocks = 0, cut_seqs = 0;
+        for (int n = 0; n < s.N; ++n) {
+            const long k = (seq_chunks(s, cu_host, n) + per - 1) / per;
+            blocks += k;
+            cut_seqs += k > 0;
+        }
+        const auto waves = [&](long b) { return (double)((b * units + sms - 1) / sms); };
+        const double cost = waves(blocks) * (per * 2.05 + 4.0) +
+                            (segs > 1 ? waves(blocks - cut_seqs) * (per * 0.8 + 4.0) + 7.0 : 0.0);
+        if (segs == 1 || cost < least) {
+            least = cost;
+            best = Cut{(int)per, (int)segs, nullptr};
+        }
+    }
+    return best;
+}
+
+template <bool STATE>
+cudaError_t launch(const LinArgs& a, const Cut& cut, const CUtensorMap& tq, const CUtensorMap& tk,
+                   const CUtensorMap& tv, cudaStream_t s) {
+    static PerDevice<int> done;
+    const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE>, kSmemBytes, done);
+    if (e != cudaSuccess) return e;
+    KernelTimer kt(STATE ? kKLinState : kKLinChunk, s);
+    kda_linattn_chunk_kernel<STATE><<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(cut.segs - STATE)),
+                                      kThr, kSmemBytes, s>>>(a, cut, tq, tk, tv);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_linattn_chunk(const LinArgs& a, cudaStream_t s) {
+size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int units) {
+    return (size_t)seq.N * (plan(seq, cu_host, units).segs - 1) * units * kHeadDim * kHeadDim * sizeof(float);
+}
+
+// (more than any cut of total_T tokens into N sequences takes: the cut of the longest possible one)
+size_t linattn_chunk_workspace_bound(int N, long total_T, int units) {
+    const int sms = sm_count();
+    const long chains = (long)N * units;
+    if (!may_cut(chains, sms)) return 0;
+    return (size_t)chains * (most_segs(chains, (total_T + kC - 1) / kC, sms) - 1) * kHeadDim * kHeadDim * sizeof(float);
+}
+
+cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s) {
     const long qk = (long)a.Hk * kHeadDim, vw = (long)a.H * a.m * kHeadDim;
     CUtensorMap tq, tk, tv;
     if (!make_tensor_map_2d_bf16_sw128(&tq, a.q, a.seq.total_rows, qk, kC, a.q_stride) ||
         !make_tensor_map_2d_bf16_sw128(&tk, a.k, a.seq.total_rows, qk, kC, a.k_stride) ||
         !make_tensor_map_2d_bf16_sw128(&tv, a.v, a.seq.total_rows, vw, kC, a.v_stride))
         return cudaErrorInvalidValue;
-    static PerDevice<int> done;
-    const cudaError_t e = set_smem(kda_linattn_chunk_kernel, kSmemBytes, done);
-    if (e != cudaSuccess) return e;
-    KernelTimer kt(kKLinChunk, s);
-    kda_linattn_chunk_kernel<<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N), kThr, kSmemBytes, s>>>(a, tq, tk, tv);
-    return cudaGetLastError();
+    Cut cut = plan(a.seq, cu_host, a.H * a.m);
+    cut.parts = static_cast<float*>(workspace);
+    if (cut.segs > 1) {
+        cudaError_t e = launch<true>(a, cut, tq, tk, tv, s);
+        if (e != cudaSuccess) return e;
+        KernelTimer kt(kKLinJoin, s);
+        const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
+        kda_linattn_join_kernel<<<dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s>>>(a, cut);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return launch<false>(a, cut, tq, tk, tv, s);
 }
 
 }  // namespace kda

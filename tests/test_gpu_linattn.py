@@ -215,3 +215,26 @@ def test_long_memory_keeps_a_decay_next_to_one():
         # the systematic part alone is bounded by 2^-24 of g T
         err = (out["state_out"].double().cpu() / want - 1).abs().max()
         assert float(err) < 20000 * 2.0 ** -26
+
+
+@pytest.mark.parametrize("lengths,H,kind", [([5000], 1, "mixed"), ([3000, 1, 900, 2100], 2, "mixed"),
+                                            ([2500], 3, "strong"), ([4097], 2, "none"),
+                                            ([64 * 40], 5, "mixed")])
+def test_few_long_prompts(lengths, H, kind):
+    """Long prompts of few heads are cut into segments: outputs and states as of the whole."""
+    from gated_delta_rule_scan_gb300 import kda, mixer
+    rows, N = sum(lengths), len(lengths)
+    (q, k, v), (dq, dk, dv) = _inputs(rows, H, H, D, torch.bfloat16, rows)
+    g = _decays(H, kind) if kind != "mixed" else _decays(H, kind) * 0.02
+    S = torch.randn(N, H, D, D, generator=torch.Generator().manual_seed(rows))
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32)
+    assert kda.kda_linattn_workspace_bytes(N, rows, H) > 0
+    out = mixer.kda_linattn_prefill(q=dq, k=dk, v=dv, log_decay=g.cuda(), H=H, state_in=S.cuda(),
+                                    cu_seqlens=cu.cuda(), cu_seqlens_host=cu)
+    torch.cuda.synchronize()
+    assert kda.kda_device_status() == 0
+    for n, L in enumerate(lengths):
+        b, e = int(cu[n]), int(cu[n + 1])
+        (o, last), (om, lm) = ref.both(q[b:e], k[b:e], v[b:e], g, S[n], H, H, D, D ** -0.5)
+        _close(out["o"][b:e], o, om, _tol(L, g), ("o", n))
+        _close(out["state_out"][n], last, lm, _tol(L, g), ("state", n))
