@@ -197,6 +197,8 @@ cudaError_t launch_proj6(const Proj6Args& a, cudaStream_t s);
 // box in the 128-byte swizzle
 bool make_tensor_map_2d_bf16_sw128(CUtensorMap* m, const void* base, long rows, long cols,
                                    int box_rows, long row_stride = 0);
+// 2-D f32 tensor map over [rows, cols] with a [box_rows][32] box in the 128-byte swizzle
+bool make_tensor_map_2d_f32_sw128(CUtensorMap* m, const void* base, long rows, long cols, int box_rows);
 cudaError_t launch_gated_rmsnorm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_decode_fused(const DecodeArgs& a, cudaStream_t s);
 

@@ -35,6 +35,7 @@
 #include "kda_tc.cuh"
 
 #include <algorithm>
+#include <cstring>
 
 namespace kda {
 
@@ -51,6 +52,8 @@ constexpr int kStageBytes = 3 * kTileBytes;
 constexpr int kKdBytes = kParts * kTileBytes;    // Kd's parts, two buffers
 constexpr int kKdAt = kStages * kStageBytes;
 constexpr int kPAt = kKdAt + 2 * kKdBytes;       // P's parts, [64 t][64 s] each
+constexpr int kStTile = kHeadDim * 128;          // 128 state rows x 32 keys, f32
+static_assert(4 * kStTile <= 2 * kKdBytes, "");
 constexpr int kTailAt = kPAt + kParts * kHalf;
 constexpr int kStateWarps = 16, kConvWarps = 8;
 // The first warpgroup issues the MMAs and the loads; whole warpgroups: registers move between them.
@@ -70,6 +73,7 @@ struct __align__(16) Tail {
     uint64_t kv_full[kStages], kv_free[kStages], q_full[kStages], q_free[kStages];
     uint64_t kd_full[2], kd_free[2];
     uint64_t sc_full[2], sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free[2];
+    uint64_t st_full, st_free, st_out[4];        // the state on its way in and out
     uint64_t drain[3];
     uint32_t tmem;
 };
@@ -153,8 +157,15 @@ struct Cut {
     float* parts;
 };
 
+// Tensor maps: q, k, v; the states as rows of 128 keys, one a value: state_in, the parts, and where they go
+// (the parts in the STATE launch, else state_out).
+struct Maps {
+    CUtensorMap q, k, v, in, parts, out;
+};
+
+// the first unit's state of a segment among the parts
 __device__ __forceinline__ long seg_state(const Cut& cut, int n, int seg, int units) {
-    return ((long)n * (cut.segs - 1) + seg) * units * (kHeadDim * kHeadDim);
+    return ((long)n * (cut.segs - 1) + seg) * units;
 }
 
 // a + b is e^x: a step S <- e^x S + U is S <- a S + (b S + U).  Above a half a = 1 and b = e^x - 1, which
@@ -166,8 +177,7 @@ __device__ __forceinline__ float2 decay_pair(float x) {
 
 template <bool STATE>
 __global__ void __launch_bounds__(kThr, 1)
-kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__ CUtensorMap tq,
-                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__ Maps maps) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -206,10 +216,30 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
     const bool strong = g < -1.0f;
     const int mid = strong ? 0 : kMid;           // the state is kept as e^{mid g} S
 
+    // what this CTA starts from; it comes through shared memory, where Kd will be: 4 tiles of 128 rows x 32 keys
+    const bool starts = !STATE && (seg > 0 || a.state_in != nullptr);
+
     if (warp == kUWarp) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
+    const auto load_kv = [&](int c) {            // by one thread
+        unsigned char* s = base + c % kStages * kStageBytes;
+        uint64_t* bar = &sm.kv_full[c % kStages];
+        const int row = (int)(begin + (long)c * kC);
+        mbar_arrive_expect_tx(bar, 2 * kTileBytes);
+        for (int h = 0; h < 2; ++h) {
+            tma_load_2d(s + kKAt + h * kHalf, &maps.k, hk * kHeadDim + 64 * h, row, bar);
+            tma_load_2d(s + kVAt + h * kHalf, &maps.v, unit * kHeadDim + 64 * h, row, bar);
+        }
+    };
+    const auto load_q = [&](int c) {
+        unsigned char* s = base + c % kStages * kStageBytes;
+        uint64_t* bar = &sm.q_full[c % kStages];
+        mbar_arrive_expect_tx(bar, kTileBytes);
+        for (int h = 0; h < 2; ++h)
+            tma_load_2d(s + kQAt + h * kHalf, &maps.q, hk * kHeadDim + 64 * h, (int)(begin + (long)c * kC), bar);
+    };
     if (warp == kTmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
@@ -233,11 +263,23 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             mbar_init(&sm.oa_free, kStateWarps);
             for (int i = 0; i < 2; ++i) mbar_init(&sm.o_free[i], kStateWarps);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
+            mbar_init(&sm.st_full, 1);
+            mbar_init(&sm.st_free, kStateWarps);
+            for (int i = 0; i < 4; ++i) mbar_init(&sm.st_out[i], 4);
             fence_mbar_init();
-            prefetch_tensormap(&tq);
-            prefetch_tensormap(&tk);
-            prefetch_tensormap(&tv);
+            if (starts) {
+                const long st = seg > 0 ? seg_state(cut, n, seg - 1, units) : (long)n * units;
+                mbar_arrive_expect_tx(&sm.st_full, 4 * kStTile);
+                for (int i = 0; i < 4; ++i)
+                    tma_load_2d(base + kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
+                                (int)(st + unit) * kHeadDim, &sm.st_full);
+            }
+            for (int c = 0; c < kStages && c < chunks; ++c) {
+                load_kv(c);
+                if (!STATE) load_q(c);
+            }
         }
+        __syncwarp();
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
         for (int i = lane; i <= kC + kMid; i += 32) sm.pw[i] = i == 0 ? 1.0f : expf(g * (float)i);
         for (int i = lane; i < kC; i += 32) {
@@ -263,27 +305,15 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
     if (warp == kTmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // ---- loads ---------------------------------------------------------------------------
-        for (int c = 0; c < chunks && ok; ++c) {
+        for (int c = kStages; c < chunks && ok; ++c) {
             const int st = c % kStages;
             const uint32_t before = (uint32_t)((c / kStages - 1) & 1);
-            unsigned char* s = base + st * kStageBytes;
-            const int row = (int)(begin + (long)c * kC);
-            if (c >= kStages) ok = mbar_wait(&sm.kv_free[st], before, a.err);
-            if (ok && elect_one()) {
-                mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
-                for (int h = 0; h < 2; ++h) {
-                    tma_load_2d(s + kKAt + h * kHalf, &tk, hk * kHeadDim + 64 * h, row, &sm.kv_full[st]);
-                    tma_load_2d(s + kVAt + h * kHalf, &tv, unit * kHeadDim + 64 * h, row, &sm.kv_full[st]);
-                }
-            }
+            ok = mbar_wait(&sm.kv_free[st], before, a.err);
+            if (ok && elect_one()) load_kv(c);
             __syncwarp();
             if (STATE) continue;
-            if (ok && c >= kStages) ok = mbar_wait(&sm.q_free[st], before, a.err);
-            if (ok && elect_one()) {
-                mbar_arrive_expect_tx(&sm.q_full[st], kTileBytes);
-                for (int h = 0; h < 2; ++h)
-                    tma_load_2d(s + kQAt + h * kHalf, &tq, hk * kHeadDim + 64 * h, row, &sm.q_full[st]);
-            }
+            ok = ok && mbar_wait(&sm.q_free[st], before, a.err);
+            if (ok && elect_one()) load_q(c);
             __syncwarp();
         }
         if (!ok)                                 // no load may land after the CTA has left
@@ -291,6 +321,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 for (uint32_t p = 0; p < 2; ++p) {
                     mbar_wait(&sm.kv_full[i], p, nullptr);
                     if (!STATE) mbar_wait(&sm.q_full[i], p, nullptr);
+                    if (starts) mbar_wait(&sm.st_full, 0, nullptr);
                 }
     } else if (warp < kTmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -425,7 +456,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             const uint32_t stage = b0 + st * kStageBytes, kd = b0 + kKdAt + (c & 1) * kKdBytes;
             // (in this order: the MMAs of chunk c - 2 come after those of c - 3, whose loads were this stage's
             // last, so that the barrier of its loads is not a phase behind)
-            ok = (c < 2 || mbar_wait(&sm.kd_free[c & 1], pc ^ 1u, a.err)) &&
+            ok = (c >= 2 ? mbar_wait(&sm.kd_free[c & 1], pc ^ 1u, a.err)
+                         : !starts || mbar_wait(&sm.st_free, 0, a.err)) &&
                  mbar_wait(&sm.kv_full[st], (uint32_t)((c / kStages) & 1), a.err);
             if (!ok) break;
             // v^T: values of this warp's lane quarter, 16 and 16, tokens 0 .. 31 and 32 ..
@@ -526,26 +558,20 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const int j = 32 * (warp & 3) + lane, part = (warp - kStateWarp0) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float2 S[16];                            // times e^{mid g}
-        const long row = ((long)unit * kHeadDim + j) * kHeadDim + 32 * part;    // its state row in a sequence's
-        const long seq_state = (long)units * kHeadDim * kHeadDim;
-        const float* from = STATE ? nullptr : a.state_in;
-        if (!STATE && seg > 0) from = cut.parts + seg_state(cut, n, seg - 1, units) - n * seq_state;
-        if (from != nullptr) {
-            const float4* src = reinterpret_cast<const float4*>(from + n * seq_state + row);
+        unsigned char* const tile = base + kKdAt + part * kStTile + j * 128;
+        if (starts) {
+            ok = mbar_wait(&sm.st_full, 0, a.err);
+            const float in = chunks > 0 ? sm.pw[mid] : 1.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float4 x = __ldg(src + i);
-                S[2 * i] = make_float2(x.x, x.y);
-                S[2 * i + 1] = make_float2(x.z, x.w);
+                const float4 x = *reinterpret_cast<const float4*>(tile + ((i ^ (j & 7)) * 16));
+                S[2 * i] = make_float2(x.x * in, x.y * in);
+                S[2 * i + 1] = make_float2(x.z * in, x.w * in);
             }
+            warp_arrive(&sm.st_free);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = make_float2(0.0f, 0.0f);
-        }
-        if (chunks > 0) {
-            const float2 in = make_float2(sm.pw[mid], sm.pw[mid]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], in);
         }
         auto put_state = [&]() {
 #pragma unroll
@@ -560,14 +586,14 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             tc_fence_before();
             warp_arrive(&sm.sp_full);
         };
-        if (!STATE && chunks > 0) put_state();
+        if (!STATE && chunks > 0 && ok) put_state();
         const float2 whole = decay_pair(g * (float)kC);
         const long step = (long)units * kHeadDim;
         // (rows by 32-bit offsets from an address that the whole warp shares: one addition a store)
         float* o = a.o + (begin + 16 * part) * step + (long)unit * kHeadDim;
         const uint32_t step4 = (uint32_t)step * 4;
         const float4* up = reinterpret_cast<const float4*>(sm.up + 16 * part);
-        for (int c = 0; c < chunks; ++c, o += kC * step) {
+        for (int c = 0; c < chunks && ok; ++c, o += kC * step) {
             const uint32_t par = (uint32_t)(c & 1);
             const int nt = min(kC, len - c * kC), live = nt - 16 * part;
             const uint32_t to = tl + kTO + 64 * (c & 1) + 16 * part;
@@ -640,11 +666,18 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         }
         if (ok && (STATE || ends)) {
             const float out = chunks > 0 ? 1.0f / sm.pw[mid] : 1.0f;
-            float4* dst = reinterpret_cast<float4*>(
-                (STATE ? cut.parts + seg_state(cut, n, seg, units) : a.state_out + n * seq_state) + row);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(S[2 * i].x * out, S[2 * i].y * out, S[2 * i + 1].x * out, S[2 * i + 1].y * out);
+                *reinterpret_cast<float4*>(tile + ((i ^ (j & 7)) * 16)) =
+                    make_float4(S[2 * i].x * out, S[2 * i].y * out, S[2 * i + 1].x * out, S[2 * i + 1].y * out);
+            fence_proxy_async_smem();
+            warp_arrive(&sm.st_out[part]);       // one of the tile's four warps
+            if ((warp & 3) == 0 && mbar_wait(&sm.st_out[part], 0, a.err) && elect_one()) {
+                const long st = STATE ? seg_state(cut, n, seg, units) : (long)n * units;
+                tma_store_2d(&maps.out, base + kKdAt + part * kStTile, 32 * part, (int)(st + unit) * kHeadDim);
+                bulk_commit();
+                bulk_wait_read0();
+            }
         }
     }
     tc_fence_before();
@@ -670,7 +703,7 @@ __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArg
     const int parts = (len + seg_len - 1) / seg_len - 1;      // the last segment's is not formed
     const float2 f = decay_pair(a.log_decay[unit / a.m] * (float)seg_len);
     const long stride = (long)units * kPieces;
-    float4* at = reinterpret_cast<float4*>(cut.parts + seg_state(cut, n, 0, units)) + piece;
+    float4* at = reinterpret_cast<float4*>(cut.parts) + seg_state(cut, n, 0, units) * kPieces + piece;
     float4 S = a.state_in ? __ldg(reinterpret_cast<const float4*>(a.state_in) + (long)n * stride + piece)
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int p = 0; p < parts; p += kJoinAhead) {
@@ -742,14 +775,13 @@ Cut plan(const SeqLayout& s, const int* cu_host, int units) {
 }
 
 template <bool STATE>
-cudaError_t launch(const LinArgs& a, const Cut& cut, const CUtensorMap& tq, const CUtensorMap& tk,
-                   const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, cudaStream_t s) {
     static PerDevice<int> done;
     const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE>, kSmemBytes, done);
     if (e != cudaSuccess) return e;
     KernelTimer kt(STATE ? kKLinState : kKLinChunk, s);
     kda_linattn_chunk_kernel<STATE><<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(cut.segs - STATE)),
-                                      kThr, kSmemBytes, s>>>(a, cut, tq, tk, tv);
+                                      kThr, kSmemBytes, s>>>(a, cut, maps);
     return cudaGetLastError();
 }
 
@@ -769,23 +801,32 @@ size_t linattn_chunk_workspace_bound(int N, long total_T, int units) {
 
 cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s) {
     const long qk = (long)a.Hk * kHeadDim, vw = (long)a.H * a.m * kHeadDim;
-    CUtensorMap tq, tk, tv;
-    if (!make_tensor_map_2d_bf16_sw128(&tq, a.q, a.seq.total_rows, qk, kC, a.q_stride) ||
-        !make_tensor_map_2d_bf16_sw128(&tk, a.k, a.seq.total_rows, qk, kC, a.k_stride) ||
-        !make_tensor_map_2d_bf16_sw128(&tv, a.v, a.seq.total_rows, vw, kC, a.v_stride))
-        return cudaErrorInvalidValue;
-    Cut cut = plan(a.seq, cu_host, a.H * a.m);
+    const int units = a.H * a.m;
+    Cut cut = plan(a.seq, cu_host, units);
     cut.parts = static_cast<float*>(workspace);
+    Maps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const auto states = [&](CUtensorMap* m, const float* base, long seqs) {
+        return make_tensor_map_2d_f32_sw128(m, base, seqs * units * kHeadDim, kHeadDim, kHeadDim);
+    };
+    if (!make_tensor_map_2d_bf16_sw128(&maps.q, a.q, a.seq.total_rows, qk, kC, a.q_stride) ||
+        !make_tensor_map_2d_bf16_sw128(&maps.k, a.k, a.seq.total_rows, qk, kC, a.k_stride) ||
+        !make_tensor_map_2d_bf16_sw128(&maps.v, a.v, a.seq.total_rows, vw, kC, a.v_stride) ||
+        (a.state_in != nullptr && !states(&maps.in, a.state_in, a.seq.N)))
+        return cudaErrorInvalidValue;
     if (cut.segs > 1) {
-        cudaError_t e = launch<true>(a, cut, tq, tk, tv, s);
+        if (!states(&maps.parts, cut.parts, (long)a.seq.N * (cut.segs - 1))) return cudaErrorInvalidValue;
+        maps.out = maps.parts;
+        cudaError_t e = launch<true>(a, cut, maps, s);
         if (e != cudaSuccess) return e;
         KernelTimer kt(kKLinJoin, s);
-        const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
+        const unsigned blocks = (unsigned)((long)units * kHeadDim * kHeadDim / 4 / kJoinThr);
         kda_linattn_join_kernel<<<dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s>>>(a, cut);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    return launch<false>(a, cut, tq, tk, tv, s);
+    if (!states(&maps.out, a.state_out, a.seq.N)) return cudaErrorInvalidValue;
+    return launch<false>(a, cut, maps, s);
 }
 
 }  // namespace kda
