@@ -9,21 +9,23 @@
 // the tile that holds the drawn index, and only that tile is read again (from L2).
 //
 // Which index is drawn must not hang on the order of summation: next to a border an f32 running sum
-// over a flat row is off by several indices.  A lane sums its weights as an exact f32 pair (value and
-// error of each addition and of p - q), about 2^-46 of the sum, and everything above a lane is in f64.
-// (f64 throughout would be 4 operations a weight at a rate far below HBM's.)
+// over a flat row is off by several indices.  All sums are of f32 pairs (a value and what its rounding left,
+// the exact error of p - q among it), about 2^-45 of the sum.  (f64 has the same bits, but its additions took
+// some 600 cycles each here: 10 us of a call's 12.)
 #include "kda_device.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kThr = 256;
+constexpr int kThr = 512;
 constexpr int kWarps = kThr / 32;
-constexpr int kTileElems = 1024;                 // weights of a tile: 32 a lane
+constexpr int kTileElems = 512;                  // weights of a tile
+constexpr int kPerLane = kTileElems / 32;
 constexpr int kMaxTiles = 1024;                  // tiles whose sums a CTA keeps; longer rows: more a sum
 
-struct Pair {                                    // hi + lo
+// An unevaluated sum hi + lo; "whole" when hi is that sum rounded, which comparisons and products need.
+struct Pair {
     float hi = 0.0f, lo = 0.0f;
     __device__ __forceinline__ void add(float x, float xe) {
         const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
@@ -31,16 +33,62 @@ struct Pair {                                    // hi + lo
         hi = s;
         lo = __fadd_rn(lo, __fadd_rn(e, xe));
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ Pair whole() const {
+        Pair r;
+        r.hi = __fadd_rn(hi, lo);
+        r.lo = __fsub_rn(lo, __fsub_rn(r.hi, hi));
+        return r;
+    }
 };
 
-template <bool BF16>
-__device__ __forceinline__ float prob(const void* row, long i) {
-    return load_raw<BF16>(row, i);
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    a.add(b.hi, b.lo);
+    return a.whole();
+}
+__device__ __forceinline__ bool operator>(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ Pair operator*(float r, Pair a) {
+    Pair p;
+    p.hi = __fmul_rn(r, a.hi);
+    p.lo = fmaf(r, a.lo, fmaf(r, a.hi, -p.hi));
+    return p.whole();
+}
+
+__device__ __forceinline__ Pair shfl(Pair x, int from) {
+    x.hi = __shfl_sync(0xffffffffu, x.hi, from);
+    x.lo = __shfl_sync(0xffffffffu, x.lo, from);
+    return x;
+}
+
+// the sum over the warp, the same in every lane
+__device__ __forceinline__ Pair warp_pair_sum(Pair x) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, x.hi, m), l = __shfl_xor_sync(0xffffffffu, x.lo, m);
+        x.add(h, l);
+    }
+    // (the lanes may differ in the last bits of lo: all take lane 0's, and so the same branches)
+    return shfl(x.whole(), 0);
+}
+
+// the sums over the lanes up to each, and (before) those up to the one before it
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane, Pair& before) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        Pair y;
+        y.hi = __shfl_up_sync(0xffffffffu, x.hi, m);
+        y.lo = __shfl_up_sync(0xffffffffu, x.lo, m);
+        const Pair z = y + x;
+        if (lane >= m) x = z;
+    }
+    before.hi = __shfl_up_sync(0xffffffffu, x.hi, 1);
+    before.lo = __shfl_up_sync(0xffffffffu, x.lo, 1);
+    if (lane == 0) before = Pair();
+    return x;
 }
 
 // One weight and its rounding error: p - q where positive, else 0 (so is a NaN or an infinity).
 __device__ __forceinline__ void weight(float p, float q, float& w, float& e) {
+    q = q > 0.0f ? q : 0.0f;
     const float d = __fsub_rn(p, q);
     const bool on = d > 0.0f && d < __int_as_float(0x7f800000);
     w = on ? d : 0.0f;
@@ -51,19 +99,22 @@ struct Row {                                     // what a sequence draws from
     const void* p;
     const void* q;                               // or null
     int skip;                                    // index that weighs nothing, or -1
+    // tiles begin `lead` elements before the row, where p's address is a multiple of 4 elements; q_vec: so
+    // is q's
+    int lead;
+    bool q_vec;
+    template <bool BF16>
+    __device__ __forceinline__ void align() {
+        constexpr int kElem = BF16 ? 2 : 4;
+        lead = (int)(reinterpret_cast<uintptr_t>(p) / kElem % 4);
+        q_vec = q == nullptr || (int)(reinterpret_cast<uintptr_t>(q) / kElem % 4) == lead;
+    }
 };
 
 template <bool BF16>
-__device__ __forceinline__ float q_at(const Row& row, long i) {
-    const float q = row.q ? prob<BF16>(row.q, i) : 0.0f;
-    return q > 0.0f ? q : 0.0f;
-}
-
-template <bool BF16>
-__device__ __forceinline__ double weight_at(const Row& row, long i) {
-    float w, e;
-    weight(prob<BF16>(row.p, i), q_at<BF16>(row, i), w, e);
-    return i == row.skip ? 0.0 : (double)w + (double)e;
+__device__ __forceinline__ void weight_at(const Row& row, long i, long V, float& w, float& e) {
+    const bool in = i >= 0 && i < V && i != row.skip;
+    weight(in ? load_raw<BF16>(row.p, i) : 0.0f, in && row.q ? load_raw<BF16>(row.q, i) : 0.0f, w, e);
 }
 
 // 4 consecutive probabilities, their address a multiple of 4 elements
@@ -78,66 +129,62 @@ __device__ __forceinline__ float4 prob4(const void* row, long i) {
     }
 }
 
-// The sum of weights b .. e - 1 (at most kTileElems), by one warp; every lane returns it.
+// A lane's share of the weights b .. b + kTileElems - 1: with `runs` its 16 are consecutive, else 4 times 4 at
+// distances of 128.  Their sum.
 template <bool BF16>
-__device__ __forceinline__ double tile_sum(const Row& row, long b, long e, bool vec, int lane) {
+__device__ __forceinline__ Pair lane_sum(const Row& row, long b, long V, int lane, bool runs) {
     Pair acc;
-    if (vec && e - b == kTileElems) {
-        float4 p[8], q[8];
+    const int at = runs ? kPerLane * lane : 4 * lane, step = runs ? 4 : 128;
+    if (b >= 0 && b + kTileElems <= V) {
+        float4 p[kPerLane / 4], q[kPerLane / 4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = prob4<BF16>(row.p, b + 128 * i + 4 * lane);
+        for (int i = 0; i < kPerLane / 4; ++i) p[i] = prob4<BF16>(row.p, b + at + step * i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q[i] = row.q ? prob4<BF16>(row.q, b + 128 * i + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kPerLane / 4; ++i) {
+            const long x = b + at + step * i;
+            q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row.q != nullptr) {
+                if (row.q_vec) q[i] = prob4<BF16>(row.q, x);
+                else q[i] = make_float4(load_raw<BF16>(row.q, x), load_raw<BF16>(row.q, x + 1),
+                                        load_raw<BF16>(row.q, x + 2), load_raw<BF16>(row.q, x + 3));
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kPerLane / 4; ++i) {
             const float pp[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
             const float qq[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            const int skip = (int)(row.skip - (b + at + step * i));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float w, we;
-                weight(pp[j], qq[j] > 0.0f ? qq[j] : 0.0f, w, we);
-                const bool skip = b + 128 * i + 4 * lane + j == row.skip;
-                acc.add(skip ? 0.0f : w, skip ? 0.0f : we);
+                float w, e;
+                weight(j == skip ? 0.0f : pp[j], qq[j], w, e);
+                acc.add(w, e);
             }
         }
     } else {
-        for (long i0 = b + lane; i0 < e; i0 += 32 * 8) {
-            float p[8], q[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const long i = i0 + 32 * j;
-                p[j] = i < e ? prob<BF16>(row.p, i) : 0.0f;
-                q[j] = i < e ? q_at<BF16>(row, i) : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float w, we;
-                weight(p[j], q[j], w, we);
-                const bool skip = i0 + 32 * j == row.skip;
-                acc.add(skip ? 0.0f : w, skip ? 0.0f : we);
-            }
+#pragma unroll 4
+        for (int i = 0; i < kPerLane; ++i) {
+            float w, e;
+            weight_at<BF16>(row, b + (runs ? kPerLane * lane + i : 32 * i + lane), V, w, e);
+            acc.add(w, e);
         }
     }
-    double x = acc.value();
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
+    return acc;
 }
 
-__device__ __forceinline__ double ld_cluster_f64(const double* local, uint32_t rank) {
+__device__ __forceinline__ Pair ld_cluster_pair(const Pair* local, uint32_t rank) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote) : "memory");
+    Pair v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(remote) : "memory");
     return v;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThr) kda_draft_accept_kernel(const AcceptArgs a) {
-    __shared__ double tiles[kMaxTiles];
-    __shared__ double total[2];                  // of this CTA, by attempt
-    __shared__ int s_taken, s_count;
+__global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptArgs a) {
+    __shared__ __align__(8) Pair tiles[kMaxTiles];
+    __shared__ __align__(8) Pair total[2];       // of this CTA, by attempt
+    __shared__ int s_taken, s_count, s_token;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;   // the cluster is the x extent
     const int drafts = a.T - 1;
@@ -148,6 +195,7 @@ __global__ void __launch_bounds__(kThr) kda_draft_accept_kernel(const AcceptArgs
                                                (size_t)n * drafts * a.draft_stride * kElem
                                          : nullptr;
 
+    const float r = a.r[n];
     // how many drafts hold: lane i tests draft i
     if (warp == 0) {
         int count = a.n_draft ? a.n_draft[n] : drafts;
@@ -158,10 +206,11 @@ __global__ void __launch_bounds__(kThr) kda_draft_accept_kernel(const AcceptArgs
         if (lane < count) {
             tok = a.tokens[(long)n * drafts + lane];
             if (tok >= 0 && tok < a.V) {
-                const float p = prob<BF16>(target + (size_t)lane * a.target_stride * kElem, tok);
-                const float q = draft ? prob<BF16>(draft + (size_t)lane * a.draft_stride * kElem, tok) : 1.0f;
-                // the product of two f32 is exact in f64
-                good = (double)a.u[(long)n * drafts + lane] * (double)q < (double)p;
+                const float p = load_raw<BF16>(target + (size_t)lane * a.target_stride * kElem, tok);
+                const float q = draft ? load_raw<BF16>(draft + (size_t)lane * a.draft_stride * kElem, tok) : 1.0f;
+                // u q < p exactly: where the rounded product equals p its error decides
+                const float u = a.u[(long)n * drafts + lane], x = __fmul_rn(u, q);
+                good = x < p || (x == p && fmaf(u, q, -x) < 0.0f);
             }
         }
         const unsigned refused = ~__ballot_sync(0xffffffffu, good);
@@ -170,6 +219,7 @@ __global__ void __launch_bounds__(kThr) kda_draft_accept_kernel(const AcceptArgs
             s_taken = taken;
             s_count = count;
         }
+        if (lane == taken) s_token = tok;        // the refused one
         if (rank == 0) {
             if (lane == 0) a.keep[n] = taken + 1;
             if (lane < a.T && lane != taken)
@@ -182,109 +232,108 @@ __global__ void __launch_bounds__(kThr) kda_draft_accept_kernel(const AcceptArgs
     const bool refused = taken < s_count;
 
     const void* p_row = target + (size_t)taken * a.target_stride * kElem;
-    Row row{p_row, nullptr, -1};
+    Row row{p_row, nullptr, -1, 0, true};
     if (refused) {
         if (draft) row.q = draft + (size_t)taken * a.draft_stride * kElem;
-        else row.skip = a.tokens[(long)n * drafts + taken];
+        else row.skip = s_token;
     }
+    row.template align<BF16>();
     // this CTA's slice, in spans of whole tiles; a span's sum is one entry of tiles[]
-    const long all_tiles = (a.V + kTileElems - 1) / kTileElems;
+    const long all_tiles = ((long)a.V + row.lead + kTileElems - 1) / kTileElems;
     const long per_cta = (all_tiles + ranks - 1) / ranks;
     const long tile0 = min(all_tiles, rank * per_cta), tile1 = min(all_tiles, tile0 + per_cta);
     const long group = (per_cta + kMaxTiles - 1) / kMaxTiles;         // tiles of a span
     const int spans = (int)((tile1 - tile0 + group - 1) / group);
 
-    double before = 0.0, mine = 0.0, sum = 0.0;
+    Pair before, mine, sum;
     for (int attempt = 0; attempt < 2; ++attempt) {
-        const bool vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) &
-                          (4 * kElem - 1)) == 0;
         for (int sp = warp; sp < spans; sp += kWarps) {
-            double x = 0.0;
+            Pair x;
             for (long t = tile0 + sp * group; t < min(tile1, tile0 + (sp + 1) * group); ++t)
-                x += tile_sum<BF16>(row, t * kTileElems, min((long)a.V, (t + 1) * kTileElems), vec, lane);
+                x = x + lane_sum<BF16>(row, t * kTileElems - row.lead, a.V, lane, false);
+            x = warp_pair_sum(x);
             if (lane == 0) tiles[sp] = x;
         }
         __syncthreads();
         if (warp == 0) {
-            double x = 0.0;
-            for (int sp = lane; sp < spans; sp += 32) x += tiles[sp];
-#pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+            Pair x;
+            for (int sp = lane; sp < spans; sp += 32) x = x + tiles[sp];
+            x = warp_pair_sum(x);
             if (lane == 0) total[attempt] = x;
         }
+        __syncwarp();
         cluster_sync_all();
-        before = mine = sum = 0.0;
-        for (int k = 0; k < ranks; ++k) {
+        Pair of[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < ranks) of[k] = ld_cluster_pair(&total[attempt], k);
+        before = mine = sum = Pair();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
             if (k == rank) before = sum;
-            sum += ld_cluster_f64(&total[attempt], k);
+            if (k < ranks) sum = sum + of[k];
             if (k == rank) mine = sum;           // the running sum past this CTA
         }
-        if (sum > 0.0 || (row.q == nullptr && row.skip < 0)) break;
-        row = Row{p_row, nullptr, -1};           // nothing is left of p - q: p itself
+        if (sum.hi > 0.0f || (row.q == nullptr && row.skip < 0)) break;
+        row.q = nullptr;                         // nothing is left of p - q: p itself
+        row.skip = -1;
+        row.q_vec = true;
     }
     // r in [0, 1): the whole sum is passed at the last weight at the latest
-    const double aim = (double)fminf(fmaxf(a.r[n], 0.0f), 0x1.fffffep-1f) * sum;
-    if (!(sum > 0.0)) {
+    const Pair aim = fminf(fmaxf(r, 0.0f), 0x1.fffffep-1f) * sum;
+    if (!(sum.hi > 0.0f)) {
         if (rank == 0 && tid == 0) a.out_tokens[(long)n * a.T + taken] = -1;
-    } else if (aim >= before && aim < mine && warp == 0) {
-        // the span, then the tile, then the lane's 32 weights in which the running sum passes aim
-        double run = before;
+    } else if (!(before > aim) && mine > aim && warp == 0) {
+        // the span, the tile, the lane's 16 weights and the one of them at which the running sum passes aim.
+        // (Where rounding between two ways of summing leaves aim past a piece, its last part is taken.)
+        Pair run = before, below;
         int sp = 0;
-        for (; sp < spans - 1; ++sp) {
-            if (run + tiles[sp] > aim) break;
-            run += tiles[sp];
+        for (;; sp += 32) {
+            const Pair x = sp + lane < spans ? tiles[sp + lane] : Pair();
+            const Pair upto = run + warp_scan(x, lane, below);
+            const unsigned past = __ballot_sync(0xffffffffu, upto > aim);
+            const bool done = past != 0 || sp + 32 >= spans;
+            const int at = past != 0 ? __ffs(past) - 1 : done ? spans - 1 - sp : 31;
+            const Pair at_below = run + shfl(below, at);
+            run = done ? at_below : shfl(upto, at);
+            if (done) {
+                sp += at;
+                break;
+            }
         }
-        const bool vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) &
-                          (4 * kElem - 1)) == 0;
         long t = tile0 + sp * group;
         const long t_end = min(tile1, t + group);
         for (; t < t_end - 1; ++t) {
-            const double x = tile_sum<BF16>(row, t * kTileElems, (t + 1) * kTileElems, vec, lane);
-            if (run + x > aim) break;
-            run += x;
+            const Pair x = run + warp_pair_sum(lane_sum<BF16>(row, t * kTileElems - row.lead, a.V, lane, false));
+            if (x > aim) break;
+            run = x;
         }
-        const long b = t * kTileElems, e = min((long)a.V, b + kTileElems);
-        const long lb = b + 32 * lane, le = min(e, lb + 32);
-        double x = 0.0;
-        int last = -1;
-        for (long i = lb; i < le; ++i) {
-            const double w = weight_at<BF16>(row, i);
-            x += w;
-            if (w > 0.0) last = (int)i;
-        }
-        double upto = x;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, upto, m);
-            if (lane >= m) upto += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, run + upto > aim);
-        int pick = -1;
-        if (past != 0) {
-            if (lane == __ffs(past) - 1) {
-                double at = run + (upto - x);
-                for (long i = lb; i < le; ++i) {
-                    const double w = weight_at<BF16>(row, i);
-                    at += w;
-                    if (w > 0.0) pick = (int)i;
-                    if (at > aim && w > 0.0) break;
-                }
-            }
-        }
-        // (rounding between the two ways of summing may leave aim past the tile: its last weight)
-        pick = __reduce_max_sync(0xffffffffu, past != 0 ? pick : last);
-        if (lane == 0) a.out_tokens[(long)n * a.T + taken] = pick;
+        const long b = t * kTileElems - row.lead;
+        const Pair of_lane = lane_sum<BF16>(row, b, a.V, lane, true).whole();
+        const Pair upto = run + warp_scan(of_lane, lane, below);
+        unsigned past = __ballot_sync(0xffffffffu, upto > aim);
+        const unsigned any = __ballot_sync(0xffffffffu, of_lane.hi > 0.0f);
+        const int pick_lane = past != 0 ? __ffs(past) - 1 : any != 0 ? 31 - __clz(any) : 31;
+        run = run + shfl(below, pick_lane);
+        Pair w;
+        weight_at<BF16>(row, lane < kPerLane ? b + kPerLane * pick_lane + lane : -1, a.V, w.hi, w.lo);
+        const Pair at_lane = run + warp_scan(w, lane, below);        // (every lane takes part)
+        past = __ballot_sync(0xffffffffu, w.hi > 0.0f && at_lane > aim);
+        const unsigned on = __ballot_sync(0xffffffffu, w.hi > 0.0f);
+        const int at = past != 0 ? __ffs(past) - 1 : on != 0 ? 31 - __clz(on) : 0;
+        if (lane == 0) a.out_tokens[(long)n * a.T + taken] = (int)(b + kPerLane * pick_lane + at);
     }
+    __syncwarp();
     cluster_sync_all();                          // no CTA leaves while another reads its total
 }
 
 template <bool BF16>
 cudaError_t launch(const AcceptArgs& a, cudaStream_t s) {
-    // CTAs a sequence: up to 8 tiles each stay one warp's work apiece; more sequences than SMs need
-    // no sharing
+    // CTAs a sequence: of at least a tile a warp, and as many as run at once (two on an SM; clusters of 8 leave
+    // some of the 152 SMs out)
     const long tiles = ((long)a.V + kTileElems - 1) / kTileElems;
     int ranks = 1;
-    while (ranks < 8 && (long)a.N * ranks < 1216 && tiles > (long)ranks * kWarps) ranks *= 2;
+    while (ranks < 8 && 2L * a.N * ranks <= 256 && tiles > (long)ranks * kWarps) ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ranks, (unsigned)a.N);
     cfg.blockDim = dim3(kThr);

@@ -15,28 +15,34 @@ struct V8 {
     float x[8];
 };
 
+// Eight elements as they lie in memory: 16 bytes of bf16, 32 of f32.
 template <bool BF16>
-__device__ __forceinline__ V8 load8(const void* base, long i) {
-    V8 v;
-    if constexpr (BF16) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v.x[2 * j] = __uint_as_float(u[j] << 16);
-            v.x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-        }
-    } else {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-        const float4 a = __ldcs(p), b = __ldcs(p + 1);
-        v = V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+struct Raw8 {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void* base, long i) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + i * (BF16 ? 2 : 4));
+        w[0] = __ldcs(p);
+        if constexpr (!BF16) w[1] = __ldcs(p + 1);
     }
-    return v;
-}
+    __device__ __forceinline__ V8 get() const {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        V8 v;
+        if constexpr (BF16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v.x[2 * j] = __uint_as_float(u[j] << 16);
+                v.x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v.x[j] = __uint_as_float(u[j]);
+        }
+        return v;
+    }
+};
 
-template <bool BF16>
-__device__ __forceinline__ void store8(void* base, long i, const V8& v) {
-    if constexpr (BF16) {
+__device__ __forceinline__ void store8(void* base, long i, const V8& v, bool bf16) {
+    if (bf16) {
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -54,14 +60,6 @@ __device__ __forceinline__ void store8(void* base, long i, const V8& v) {
 __device__ __forceinline__ V8 load_w(const float* w, int i) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(w + i)), b = __ldg(reinterpret_cast<const float4*>(w + i + 4));
     return V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-
-__device__ __forceinline__ V8 load8_any(const void* base, long i, bool bf16) {
-    return bf16 ? load8<true>(base, i) : load8<false>(base, i);
-}
-__device__ __forceinline__ void store8_any(void* base, long i, const V8& v, bool bf16) {
-    if (bf16) store8<true>(base, i, v);
-    else store8<false>(base, i, v);
 }
 
 // The sum over a row's threads; every one of them gets it.  part: one float a warp.
@@ -82,49 +80,60 @@ __device__ __forceinline__ float row_sum(float x, float* part) {
 // elements each.
 constexpr int kThrNarrow = 128;
 
-template <int THR, int STEPS>
-__global__ void __launch_bounds__(THR == 32 ? kThrNarrow : THR) kda_residual_rmsnorm_kernel(const ResNormArgs a) {
+template <int THR, int STEPS, bool XB, bool RB>
+__global__ void __launch_bounds__(THR == 32 ? kThrNarrow : THR, THR == 256 && STEPS <= 3 && XB && RB ? 4 : 1)
+kda_residual_rmsnorm_kernel(const ResNormArgs a) {
     __shared__ float part[2][THR / 32];
     const int t = THR == 32 ? threadIdx.x & 31 : threadIdx.x;
     const long row = THR == 32 ? (long)blockIdx.x * (kThrNarrow / 32) + (threadIdx.x >> 5) : (long)blockIdx.x;
     if (row >= a.rows) return;                   // (THR = 32: whole warps; else never)
     const long base = row * a.F;
-    V8 h[STEPS];
-    if (a.block != nullptr) {
-        V8 y[STEPS];
+    // everything a row needs is on its way before the first sum
+    Raw8<XB> y[STEPS], gate[STEPS];
+    Raw8<RB> x[STEPS];
+    const bool row_gate = a.gate != nullptr && a.gate_per_row;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int i = (s * THR + t) * 8;
-            if (i < a.F) {
-                y[s] = load8_any(a.block, base + i, a.block_bf16);
-                h[s] = load8_any(a.residual, base + i, a.residual_bf16);
+    for (int s = 0; s < STEPS; ++s) {
+        const int i = (s * THR + t) * 8;
+        if (i < a.F) {
+            if (a.block != nullptr) y[s].load(a.block, base + i);
+            x[s].load(a.residual, base + i);
+            if (row_gate) gate[s].load(a.gate, base + i);
+        }
+    }
+    float inv = a.block_scale;
+    if (a.block_w != nullptr) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            if ((s * THR + t) * 8 < a.F) {
+                const V8 v = y[s].get();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(v.x[j], v.x[j], ss);
             }
-        }
-        float inv = a.block_scale;
-        if (a.block_w != nullptr) {
-            float ss = 0.0f;
+        ss = row_sum<THR>(ss, part[0]);
+        inv = a.block_scale * rsqrtf(ss / (float)a.F + a.eps);
+    }
+    V8 h[STEPS];
+    float ss = 0.0f;
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s)
-                if ((s * THR + t) * 8 < a.F)
+    for (int s = 0; s < STEPS; ++s) {
+        const int i = (s * THR + t) * 8;
+        if (i >= a.F) continue;
+        h[s] = x[s].get();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(y[s].x[j], y[s].x[j], ss);
-            ss = row_sum<THR>(ss, part[0]);
-            inv = a.block_scale * rsqrtf(ss / (float)a.F + a.eps);
-        }
+        for (int j = 0; j < 8; ++j) h[s].x[j] *= a.res_scale;
+        if (a.block != nullptr) {
+            V8 v = y[s].get();
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int i = (s * THR + t) * 8;
-            if (i >= a.F) continue;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[s].x[j] *= inv;
+            for (int j = 0; j < 8; ++j) v.x[j] *= inv;
             if (a.block_w != nullptr) {
                 const V8 w = load_w(a.block_w, i);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[s].x[j] *= w.x[j];
+                for (int j = 0; j < 8; ++j) v.x[j] *= w.x[j];
             }
             if (a.gate != nullptr) {
-                V8 g = a.gate_per_row ? load8_any(a.gate, base + i, a.block_bf16)
-                                      : load_w(static_cast<const float*>(a.gate), i);
+                V8 g = row_gate ? gate[s].get() : load_w(static_cast<const float*>(a.gate), i);
                 if (a.gate_act != 0)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -132,36 +141,18 @@ __global__ void __launch_bounds__(THR == 32 ? kThrNarrow : THR) kda_residual_rms
                         g.x[j] = a.gate_act == 2 ? g.x[j] * sg : sg;
                     }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[s].x[j] *= g.x[j];
+                for (int j = 0; j < 8; ++j) v.x[j] *= g.x[j];
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[s].x[j] = fmaf(a.res_scale, h[s].x[j], y[s].x[j]);
+            for (int j = 0; j < 8; ++j) h[s].x[j] += v.x[j];
         }
-    } else {
+        if (a.h != nullptr) store8(a.h, base + i, h[s], RB);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int i = (s * THR + t) * 8;
-            if (i >= a.F) continue;
-            h[s] = load8_any(a.residual, base + i, a.residual_bf16);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[s].x[j] *= a.res_scale;
-        }
+        for (int j = 0; j < 8; ++j) ss = fmaf(h[s].x[j], h[s].x[j], ss);
     }
-    if (a.h != nullptr)
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int i = (s * THR + t) * 8;
-            if (i < a.F) store8_any(a.h, base + i, h[s], a.residual_bf16);
-        }
     if (a.z == nullptr) return;
-    float ss = 0.0f;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-        if ((s * THR + t) * 8 < a.F)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(h[s].x[j], h[s].x[j], ss);
     ss = row_sum<THR>(ss, part[1]);
-    const float inv = rsqrtf(ss / (float)a.F + a.eps);
+    inv = rsqrtf(ss / (float)a.F + a.eps);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
         const int i = (s * THR + t) * 8;
@@ -170,16 +161,20 @@ __global__ void __launch_bounds__(THR == 32 ? kThrNarrow : THR) kda_residual_rms
         V8 z;
 #pragma unroll
         for (int j = 0; j < 8; ++j) z.x[j] = h[s].x[j] * inv * w.x[j];
-        store8_any(a.z, base + i, z, a.z_bf16);
+        store8(a.z, base + i, z, a.z_bf16);
     }
 }
 
 template <int THR, int STEPS>
 cudaError_t launch(const ResNormArgs& a, cudaStream_t s) {
     constexpr int rows_per = THR == 32 ? kThrNarrow / 32 : 1;
+    const unsigned blocks = (unsigned)((a.rows + rows_per - 1) / rows_per);
+    const int thr = THR == 32 ? kThrNarrow : THR;
     KernelTimer kt(kKResNorm, s);
-    kda_residual_rmsnorm_kernel<THR, STEPS>
-        <<<(unsigned)((a.rows + rows_per - 1) / rows_per), THR == 32 ? kThrNarrow : THR, 0, s>>>(a);
+    if (a.block_bf16 && a.residual_bf16) kda_residual_rmsnorm_kernel<THR, STEPS, true, true><<<blocks, thr, 0, s>>>(a);
+    else if (a.block_bf16) kda_residual_rmsnorm_kernel<THR, STEPS, true, false><<<blocks, thr, 0, s>>>(a);
+    else if (a.residual_bf16) kda_residual_rmsnorm_kernel<THR, STEPS, false, true><<<blocks, thr, 0, s>>>(a);
+    else kda_residual_rmsnorm_kernel<THR, STEPS, false, false><<<blocks, thr, 0, s>>>(a);
     return cudaGetLastError();
 }
 
