@@ -1073,13 +1073,13 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
     return cuda_status(launch_proj_w4(a, static_cast<cudaStream_t>(stream)));
 }
 
-// bf16 prompts take the chunked form when the longest has at least this many tokens.
+// Prompts take the chunked form when the longest has at least this many tokens.
 static constexpr long kLinChunkMinLen = 32;
 
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype) {
     const int m = value_subheads(Dk, Dv);
     if (m == 0 || N < 0 || total_T < 0 || H <= 0 || Hk < 1 || Hk > H) return 0;
-    return raw_dtype == KDA_DTYPE_BF16 ? linattn_chunk_workspace_bound(N, total_T, H * m) : 0;
+    return linattn_chunk_workspace_bound(N, total_T, Hk, H * m, raw_dtype == KDA_DTYPE_BF16);
 }
 
 // Contract checks of the linear attention entries and their argument block.
@@ -1115,9 +1115,9 @@ static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_
     if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_ALIGN;
     const size_t sb = (size_t)a.seq.N * a.H * a.m * kHeadDim * kHeadDim * sizeof(float);
     if (state_in && overlap(state_in, state_out, sb)) return KDA_ERR_STATE_ALIAS;
-    const bool chunk = a.bf16 && max_len(a.seq, cu_host) >= kLinChunkMinLen;
+    const bool chunk = max_len(a.seq, cu_host) >= kLinChunkMinLen;
     if (chunk) {
-        const size_t need = linattn_chunk_workspace_bytes(a.seq, cu_host, a.H * a.m);
+        const size_t need = linattn_chunk_workspace_bytes(a.seq, cu_host, a.Hk, a.H * a.m, a.bf16 != 0);
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return KDA_ERR_ALIGN;
     }

@@ -268,11 +268,11 @@ struct LinArgs {
 };
 cudaError_t launch_linattn_decode(const LinArgs& a, cudaStream_t s);
 cudaError_t launch_linattn_seq(const LinArgs& a, cudaStream_t s);
-// bf16, total_rows > 0; workspace: linattn_chunk_workspace_bytes for these lengths, which the bound covers
-// for any lengths of total_T tokens in all
+// total_rows > 0; workspace: linattn_chunk_workspace_bytes for these lengths, which the bound covers for any
+// lengths of total_T tokens in all
 cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s);
-size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int units);
-size_t linattn_chunk_workspace_bound(int N, long total_T, int units);
+size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int Hk, int units, bool bf16);
+size_t linattn_chunk_workspace_bound(int N, long total_T, int Hk, int units, bool bf16);
 
 // Verification of drafted tokens (kda_accept.cu).
 struct AcceptArgs {
@@ -301,7 +301,7 @@ cudaError_t launch_residual_rmsnorm(const ResNormArgs& a, cudaStream_t s);
 enum KernelId {
     kKPrep, kKRingRoll, kKScanSeq, kKChunkOffsets, kKChunkIntra, kKChunkInter, kKRmsNorm,
     kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKStateStoreQ8, kKStateLoadQ8, kKDecodeQ8,
-    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKLinState, kKLinJoin, kKLinChunk, kKDraftAccept,
+    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKLinSplit, kKLinState, kKLinJoin, kKLinChunk, kKDraftAccept,
     kKResNorm,
     kKernelCount
 };

@@ -44,17 +44,36 @@ namespace {
 constexpr int kC = 64;                           // tokens of a chunk
 constexpr int kMid = kC / 2;
 constexpr int kParts = 2;
-constexpr int kStages = 3;
 constexpr int kHalf = kC * 128;                  // bytes of 64 tokens x 64 columns, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalf;            // 64 tokens x 128 columns
-constexpr int kKAt = 0, kVAt = kTileBytes, kQAt = 2 * kTileBytes;   // in a stage
-constexpr int kStageBytes = 3 * kTileBytes;
 constexpr int kKdBytes = kParts * kTileBytes;    // Kd's parts, two buffers
-constexpr int kKdAt = kStages * kStageBytes;
-constexpr int kPAt = kKdAt + 2 * kKdBytes;       // P's parts, [64 t][64 s] each
 constexpr int kStTile = kHeadDim * 128;          // 128 state rows x 32 keys, f32
 static_assert(4 * kStTile <= 2 * kKdBytes, "");
-constexpr int kTailAt = kPAt + kParts * kHalf;
+
+// Shared memory and tensor memory by the inputs' type.  F32: q, k and v are bf16 hi + lo themselves (split by a
+// launch before), every product three of them (hi hi, hi lo, lo hi); the loads have fewer stages and the
+// outputs one buffer.
+template <bool F32>
+struct Lay {
+    static constexpr int kIn = F32 ? 2 : 1;                          // parts of q, k, v
+    static constexpr int kKvStages = F32 ? 1 : 3, kQStages = F32 ? 2 : 3;
+    // barriers of k and v: a chunk's comes two chunks later again at the earliest, since its group of warps knows
+    // only of its own chunks that they have passed
+    static constexpr int kKvBars = F32 ? 2 : 3;
+    static constexpr int kKvBytes = 2 * kIn * kTileBytes;            // k's parts, v's parts
+    static constexpr int kQBytes = kIn * kTileBytes;
+    static constexpr int kVAt = kIn * kTileBytes;                    // in a stage
+    static constexpr int kQAt = kKvStages * kKvBytes;
+    static constexpr int kKdAt = kQAt + kQStages * kQBytes;
+    static constexpr int kPAt = kKdAt + 2 * kKdBytes;                // P's parts, [64 t][64 s] each
+    static constexpr int kTailAt = kPAt + kParts * kHalf;
+    // TMEM columns
+    static constexpr uint32_t kTSp = 0, kTU = 128, kTO = 256, kTSc = F32 ? 320 : 384, kTVt = F32 ? 384 : 448;
+    static constexpr int kOBufs = F32 ? 1 : 2;
+    static constexpr uint32_t kVtCols = 32 * kIn;                    // of one of v's two buffers
+    __device__ static constexpr uint32_t o_at(int c) { return kTO + 64 * (c % kOBufs); }
+};
+
 constexpr int kStateWarps = 16, kConvWarps = 8;
 // The first warpgroup issues the MMAs and the loads; whole warpgroups: registers move between them.
 constexpr int kUWarp = 0, kOiWarp = 1, kTmaWarp = 3, kStateWarp0 = 4;
@@ -70,7 +89,7 @@ struct __align__(16) Tail {
     float pw[kC + kMid + 4];                     // e^{g n}, n = 0 .. 96
     float down[kC];                              // P's factors: e^{g (31-s)}
     float up[kC];                                // the outputs': scale * e^{g (t-31)}, or scale * e^{g (t+1)}
-    uint64_t kv_full[kStages], kv_free[kStages], q_full[kStages], q_free[kStages];
+    uint64_t kv_full[3], kv_free[3], q_full[3], q_free[3];
     uint64_t kd_full[2], kd_free[2];
     uint64_t sc_full[2], sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free[2];
     uint64_t st_full, st_free, st_out[4];        // the state on its way in and out
@@ -78,10 +97,9 @@ struct __align__(16) Tail {
     uint32_t tmem;
 };
 constexpr int kMaxRanked = 32;                   // packed sequences that are taken longest first
-constexpr int kSmemBytes = 1024 + kTailAt + (int)sizeof(Tail);
-
-// TMEM columns
-constexpr uint32_t kTSp = 0, kTU = 128, kTO = 256, kTSc = 384, kTVt = 448;     // kTO: two buffers
+template <bool F32>
+constexpr int smem_bytes() { return 1024 + Lay<F32>::kTailAt + (int)sizeof(Tail); }
+static_assert(smem_bytes<false>() <= kMaxBlockSmem && smem_bytes<true>() <= kMaxBlockSmem, "");
 
 // Two f32 as two bf16x2 words, hi and lo.
 __device__ __forceinline__ void split2(float2 x, uint32_t& a, uint32_t& b) {
@@ -157,10 +175,10 @@ struct Cut {
     float* parts;
 };
 
-// Tensor maps: q, k, v; the states as rows of 128 keys, one a value: state_in, the parts, and where they go
+// Tensor maps: q, k, v (hi and lo of f32); the states as rows of 128 keys, one a value: state_in, the parts, and where they go
 // (the parts in the STATE launch, else state_out).
 struct Maps {
-    CUtensorMap q, k, v, in, parts, out;
+    CUtensorMap q[2], k[2], v[2], in, parts, out;
 };
 
 // the first unit's state of a segment among the parts
@@ -175,13 +193,14 @@ __device__ __forceinline__ float2 decay_pair(float x) {
     return lam > 0.5f ? make_float2(1.0f, expm1f(x)) : make_float2(lam, 0.0f);
 }
 
-template <bool STATE>
+template <bool STATE, bool F32>
 __global__ void __launch_bounds__(kThr, 1)
 kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__ Maps maps) {
+    using L = Lay<F32>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tail& sm = *reinterpret_cast<Tail*>(base + kTailAt);
+    Tail& sm = *reinterpret_cast<Tail*>(base + L::kTailAt);
     // (shuffled from lane 0, what is the same in a warp is known to be: it goes to uniform registers)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int unit = blockIdx.x, seg = blockIdx.z;
@@ -224,25 +243,29 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         tmem_relinquish();
     }
     const auto load_kv = [&](int c) {            // by one thread
-        unsigned char* s = base + c % kStages * kStageBytes;
-        uint64_t* bar = &sm.kv_full[c % kStages];
+        unsigned char* s = base + c % L::kKvStages * L::kKvBytes;
+        uint64_t* bar = &sm.kv_full[c % L::kKvBars];
         const int row = (int)(begin + (long)c * kC);
-        mbar_arrive_expect_tx(bar, 2 * kTileBytes);
-        for (int h = 0; h < 2; ++h) {
-            tma_load_2d(s + kKAt + h * kHalf, &maps.k, hk * kHeadDim + 64 * h, row, bar);
-            tma_load_2d(s + kVAt + h * kHalf, &maps.v, unit * kHeadDim + 64 * h, row, bar);
-        }
+        mbar_arrive_expect_tx(bar, L::kKvBytes);
+        for (int p = 0; p < L::kIn; ++p)
+            for (int h = 0; h < 2; ++h) {
+                const int at = p * kTileBytes + h * kHalf;
+                tma_load_2d(s + at, &maps.k[p], hk * kHeadDim + 64 * h, row, bar);
+                tma_load_2d(s + L::kVAt + at, &maps.v[p], unit * kHeadDim + 64 * h, row, bar);
+            }
     };
     const auto load_q = [&](int c) {
-        unsigned char* s = base + c % kStages * kStageBytes;
-        uint64_t* bar = &sm.q_full[c % kStages];
-        mbar_arrive_expect_tx(bar, kTileBytes);
-        for (int h = 0; h < 2; ++h)
-            tma_load_2d(s + kQAt + h * kHalf, &maps.q, hk * kHeadDim + 64 * h, (int)(begin + (long)c * kC), bar);
+        unsigned char* s = base + L::kQAt + c % L::kQStages * L::kQBytes;
+        uint64_t* bar = &sm.q_full[c % L::kQStages];
+        mbar_arrive_expect_tx(bar, L::kQBytes);
+        for (int p = 0; p < L::kIn; ++p)
+            for (int h = 0; h < 2; ++h)
+                tma_load_2d(s + p * kTileBytes + h * kHalf, &maps.q[p], hk * kHeadDim + 64 * h,
+                            (int)(begin + (long)c * kC), bar);
     };
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            for (int i = 0; i < kStages; ++i) {
+            for (int i = 0; i < 3; ++i) {
                 mbar_init(&sm.kv_full[i], 1);
                 mbar_init(&sm.kv_free[i], kGroupWarps + !STATE);
                 mbar_init(&sm.q_full[i], 1);
@@ -271,13 +294,11 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 const long st = seg > 0 ? seg_state(cut, n, seg - 1, units) : (long)n * units;
                 mbar_arrive_expect_tx(&sm.st_full, 4 * kStTile);
                 for (int i = 0; i < 4; ++i)
-                    tma_load_2d(base + kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
+                    tma_load_2d(base + L::kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
                                 (int)(st + unit) * kHeadDim, &sm.st_full);
             }
-            for (int c = 0; c < kStages && c < chunks; ++c) {
-                load_kv(c);
-                if (!STATE) load_q(c);
-            }
+            for (int c = 0; c < L::kKvStages && c < chunks; ++c) load_kv(c);
+            for (int c = 0; !STATE && c < L::kQStages && c < chunks; ++c) load_q(c);
         }
         __syncwarp();
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
@@ -292,7 +313,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         for (int p = 0; p < kParts; ++p)
 #pragma unroll
             for (int q = 4; q < 8; ++q)
-                *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                *reinterpret_cast<uint4*>(base + L::kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
                     make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -305,24 +326,25 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
     if (warp == kTmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // ---- loads ---------------------------------------------------------------------------
-        for (int c = kStages; c < chunks && ok; ++c) {
-            const int st = c % kStages;
-            const uint32_t before = (uint32_t)((c / kStages - 1) & 1);
-            ok = mbar_wait(&sm.kv_free[st], before, a.err);
-            if (ok && elect_one()) load_kv(c);
-            __syncwarp();
-            if (STATE) continue;
-            ok = ok && mbar_wait(&sm.q_free[st], before, a.err);
+        // (in the order in which the stages come free: k and v are done with a product earlier than q)
+        for (int c = L::kKvStages; c < chunks && ok; ++c) {
+            {
+                const int was = c - L::kKvStages;
+                ok = mbar_wait(&sm.kv_free[was % L::kKvBars], (uint32_t)((was / L::kKvBars) & 1), a.err);
+                if (ok && elect_one()) load_kv(c);
+                __syncwarp();
+            }
+            if (STATE || c < L::kQStages) continue;
+            ok = ok && mbar_wait(&sm.q_free[c % L::kQStages], (uint32_t)((c / L::kQStages - 1) & 1), a.err);
             if (ok && elect_one()) load_q(c);
             __syncwarp();
         }
         if (!ok)                                 // no load may land after the CTA has left
-            for (int i = 0; i < kStages; ++i)
-                for (uint32_t p = 0; p < 2; ++p) {
-                    mbar_wait(&sm.kv_full[i], p, nullptr);
-                    if (!STATE) mbar_wait(&sm.q_full[i], p, nullptr);
-                    if (starts) mbar_wait(&sm.st_full, 0, nullptr);
-                }
+            for (uint32_t p = 0; p < 2; ++p) {
+                for (int i = 0; i < L::kKvBars; ++i) mbar_wait(&sm.kv_full[i], p, nullptr);
+                for (int i = 0; !STATE && i < L::kQStages; ++i) mbar_wait(&sm.q_full[i], p, nullptr);
+                if (starts) mbar_wait(&sm.st_full, 0, nullptr);
+            }
     } else if (warp < kTmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // ---- MMAs: V^T Kd by one warp, S Q^T by the next, q k and V^T P^T by the third -------
@@ -333,45 +355,54 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const uint64_t d0 = tc_smem_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(base), 0));
         if (warp == kUWarp) {
             for (int c = 0; c < chunks; ++c) {
-                const int st = c % kStages;
-                const uint32_t par = (uint32_t)(c & 1), pst = (uint32_t)((c / kStages) & 1);
+                const int skv = c % L::kKvStages, bkv = c % L::kKvBars, sq = c % L::kQStages;
+                const uint32_t par = (uint32_t)(c & 1);
                 // q_t . k_s, s < 32 with q on the lanes 0 .. 63, s >= 32 with q on 64 .. 127: the threads of
                 // three lane quarters then share the work on P.  (M = 128 covers twice the rows of q's tile,
                 // those behind it, or before it, being whatever lies there: their lanes are never read.)
                 if (!STATE) {
-                    ok = mbar_wait(&sm.kv_full[st], pst, a.err) && mbar_wait(&sm.q_full[st], pst, a.err) &&
+                    ok = mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / L::kKvBars) & 1), a.err) &&
+                         mbar_wait(&sm.q_full[sq], (uint32_t)((c / L::kQStages) & 1), a.err) &&
                          (c == 0 || mbar_wait(&sm.sc_free, par ^ 1u, a.err));
                     if (!ok) break;
                     tc_fence_after();
                 }
-                const uint64_t s = tc_desc_advance(d0, st * kStageBytes);
+                const uint64_t k0 = tc_desc_advance(d0, skv * L::kKvBytes);
+                const uint64_t q0 = tc_desc_advance(d0, L::kQAt + sq * L::kQBytes);
                 if (!STATE && elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                        tc_mma_ss(tmem + kTSc, tc_desc_advance(s, kQAt + off), tc_desc_advance(s, kKAt + off), id_sc,
-                                  ks > 0);
-                        tc_mma_ss(tmem + kTSc + 32, tc_desc_advance(s, kQAt - kHalf + off),
-                                  tc_desc_advance(s, kKAt + kHalf / 2 + off), id_sc, ks > 0);
+                    for (int x = 0; x < 2 * L::kIn - 1; ++x) {       // hi lo, lo hi, hi hi
+                        const int kp = F32 && x == 0, qp = F32 && x == 1;
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks) {
+                            const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+                            const uint64_t q = tc_desc_advance(q0, qp * kTileBytes + off);
+                            const uint64_t k = tc_desc_advance(k0, kp * kTileBytes + off);
+                            tc_mma_ss(tmem + L::kTSc, q, k, id_sc, x > 0 || ks > 0);
+                            tc_mma_ss(tmem + L::kTSc + 32, q - (kHalf >> 4), tc_desc_advance(k, kHalf / 2), id_sc,
+                                      x > 0 || ks > 0);
+                        }
                     }
                     tc_commit(&sm.sc_full[c & 1]);
-                    tc_commit(&sm.kv_free[st]);
-                    tc_commit(&sm.q_free[st]);
+                    tc_commit(&sm.kv_free[bkv]);
+                    tc_commit(&sm.q_free[sq]);
                 }
                 __syncwarp();
-                const uint64_t kd = tc_desc_advance(d0, kKdAt + (c & 1) * kKdBytes);
-                const uint32_t vt = tmem + kTVt + 32 * (c & 1);
+                const uint64_t kd = tc_desc_advance(d0, L::kKdAt + (c & 1) * kKdBytes);
+                const uint32_t vt = tmem + L::kTVt + L::kVtCols * (c & 1);
                 ok = mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
                      (c == 0 || mbar_wait(&sm.u_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int p = kParts - 1; p >= 0; --p)
+                    for (int x = 0; x < L::kIn + 1; ++x) {           // (lo hi,) hi lo, hi hi
+                        const int vp = F32 && x == 0, p = x == L::kIn - 1;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + kTU, vt + 8 * ks, tc_desc_advance(kd, p * kTileBytes + 32 * ks), id_u,
-                                      p < kParts - 1 || ks > 0);
+                            tc_mma_ts(tmem + L::kTU, vt + 32 * vp + 8 * ks, tc_desc_advance(kd, p * kTileBytes + 32 * ks),
+                                      id_u, x > 0 || ks > 0);
+                    }
                     tc_commit(&sm.u_full);
                     tc_commit(&sm.kd_free[c & 1]);
                 }
@@ -380,15 +411,15 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             // no arrival of the tensor pipe on a barrier of a CTA that has left: each warp sees its last
             if (ok && chunks > 0)
                 ok = STATE ? mbar_wait(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err)
-                           : mbar_wait(&sm.kv_free[(chunks - 1) % kStages],
-                                       (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
+                           : mbar_wait(&sm.kv_free[(chunks - 1) % L::kKvBars],
+                                       (uint32_t)(((chunks - 1) / L::kKvBars) & 1), a.err);
         } else if (STATE) {
         } else if (warp == kOiWarp) {
             for (int c = 0; c < chunks; ++c) {
-                const int st = c % kStages;
-                const uint64_t q = tc_desc_advance(d0, st * kStageBytes + kQAt);
+                const int st = c % L::kQStages;
+                const uint64_t q = tc_desc_advance(d0, L::kQAt + st * L::kQBytes);
                 const uint32_t par = (uint32_t)(c & 1);
-                ok = mbar_wait(&sm.q_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
+                ok = mbar_wait(&sm.q_full[st], (uint32_t)((c / L::kQStages) & 1), a.err) &&
                      mbar_wait(&sm.sp_full, par, a.err) &&
                      mbar_wait(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
                      (!strong || mbar_wait(&sm.oa_free, par, a.err));
@@ -396,37 +427,41 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int p = kParts - 1; p >= 0; --p)
+                    for (int x = 0; x < L::kIn + 1; ++x) {           // (hi lo,) lo hi, hi hi
+                        const int qp = F32 && x == 0, p = x == L::kIn - 1;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ts(tmem + kTO + 64 * (c & 1), tmem + kTSp + 64 * p + 8 * ks,
-                                      tc_desc_advance(q, (ks >> 2) * kHalf + (ks & 3) * 32), id_o,
-                                      !strong || p < kParts - 1 || ks > 0);
+                            tc_mma_ts(tmem + L::o_at(c), tmem + L::kTSp + 64 * p + 8 * ks,
+                                      tc_desc_advance(q, qp * kTileBytes + (ks >> 2) * kHalf + (ks & 3) * 32), id_o,
+                                      !strong || x > 0 || ks > 0);
+                    }
                     tc_commit(&sm.o_full);
                     tc_commit(&sm.q_free[st]);
                 }
                 __syncwarp();
             }
             if (ok && chunks > 0)
-                ok = mbar_wait(&sm.q_free[(chunks - 1) % kStages],
-                                       (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
+                ok = mbar_wait(&sm.q_free[(chunks - 1) % L::kQStages],
+                               (uint32_t)(((chunks - 1) / L::kQStages) & 1), a.err);
         } else {
             for (int c = 0; c < chunks; ++c) {
-                const uint64_t pp = tc_desc_advance(d0, kPAt);
-                const uint32_t vt = tmem + kTVt + 32 * (c & 1), par = (uint32_t)(c & 1);
+                const uint64_t pp = tc_desc_advance(d0, L::kPAt);
+                const uint32_t vt = tmem + L::kTVt + L::kVtCols * (c & 1), par = (uint32_t)(c & 1);
                 // (v's last quarter comes from a warp without a share of P)
                 ok = mbar_wait(&sm.p_full, par, a.err) &&
                      mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
-                     (c < 2 || mbar_wait(&sm.o_free[c & 1], (uint32_t)(((c >> 1) - 1) & 1), a.err));
+                     (c < L::kOBufs || mbar_wait(&sm.o_free[c % L::kOBufs], (uint32_t)((c / L::kOBufs - 1) & 1), a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int p = kParts - 1; p >= 0; --p)
+                    for (int x = 0; x < L::kIn + 1; ++x) {           // (lo hi,) hi lo, hi hi
+                        const int vp = F32 && x == 0, p = x == L::kIn - 1;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + kTO + 64 * (c & 1), vt + 8 * ks, tc_desc_advance(pp, p * kHalf + 32 * ks), id_o,
-                                      p < kParts - 1 || ks > 0);
+                            tc_mma_ts(tmem + L::o_at(c), vt + 32 * vp + 8 * ks, tc_desc_advance(pp, p * kHalf + 32 * ks),
+                                      id_o, x > 0 || ks > 0);
+                    }
                     tc_commit(&sm.oa_full[c & 1]);
                     tc_commit(&sm.kd_free[c & 1]);
                 }
@@ -450,45 +485,51 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t b0 = __shfl_sync(0xffffffffu, smem_u32(base), 0);
         for (int c = (warp - kConvWarp0) / kGroupWarps; c < chunks; c += 2) {
-            const int st = c % kStages;
+            const int st = c % L::kKvStages, bkv = c % L::kKvBars;
             const uint32_t pc = (uint32_t)((c >> 1) & 1);
             const int nt = min(kC, len - c * kC);
-            const uint32_t stage = b0 + st * kStageBytes, kd = b0 + kKdAt + (c & 1) * kKdBytes;
-            // (in this order: the MMAs of chunk c - 2 come after those of c - 3, whose loads were this stage's
-            // last, so that the barrier of its loads is not a phase behind)
+            const uint32_t stage = b0 + st * L::kKvBytes, kd = b0 + L::kKdAt + (c & 1) * kKdBytes;
+            // (in this order: the MMAs of chunk c - 2, and with them those of c - 3, are done, so that the barrier of
+            // the loads is not a phase behind)
             ok = (c >= 2 ? mbar_wait(&sm.kd_free[c & 1], pc ^ 1u, a.err)
                          : !starts || mbar_wait(&sm.st_free, 0, a.err)) &&
-                 mbar_wait(&sm.kv_full[st], (uint32_t)((c / kStages) & 1), a.err);
+                 mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / L::kKvBars) & 1), a.err);
             if (!ok) break;
             // v^T: values of this warp's lane quarter, 16 and 16, tokens 0 .. 31 and 32 ..
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < 4 * L::kIn; ++h) {
+                const int vp = h >> 2, half = (h >> 1) & 1;
                 const int jc = 4 * quarter + 2 * (h & 1) + ((lane >> 3) & 1);     // 16-byte piece of the row
-                const int vs = 32 * (h >> 1) + 8 * (lane >> 4) + r;               // + 16 for the second pair
+                const int vs = 32 * half + 8 * (lane >> 4) + r;                   // + 16 for the second pair
                 uint32_t w[8];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     ldsm4_t(*reinterpret_cast<uint32_t(*)[4]>(w + 4 * q),
-                            stage + kVAt + (jc >> 3) * kHalf + (vs + 16 * q) * 128 + (((jc ^ vs) & 7) * 16));
+                            stage + L::kVAt + vp * kTileBytes + (jc >> 3) * kHalf + (vs + 16 * q) * 128 +
+                                (((jc ^ vs) & 7) * 16));
                 if (nt < kC)      // rows past the sequence's end are another's: 0 times a NaN there is not 0
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int t = 32 * (h >> 1) + 8 * (i >> 1) + 2 * (lane & 3);
+                        const int t = 32 * half + 8 * (i >> 1) + 2 * (lane & 3);
                         w[i] = t >= nt ? 0u : t + 1 >= nt ? w[i] & 0xffffu : w[i];
                     }
-                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + kTVt + 32 * (c & 1) + 16 * (h >> 1), w);
+                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + L::kTVt + L::kVtCols * (c & 1) + 32 * vp +
+                                       16 * half, w);
             }
             // Kd: tokens 16 quarter .., 8 and 8, transposed to [key][token]
-            uint32_t kw[2][4][4];
+            const auto k_words = [&](uint32_t (&w)[4], int h, int q, int p) {
+                const int ic = 4 * q + (lane >> 3);                               // 16-byte piece of k's row
+                ldsm4_t(w, stage + p * kTileBytes + (ic >> 3) * kHalf + (16 * quarter + 8 * h + r) * 128 +
+                               (((ic ^ r) & 7) * 16));
+            };
+            uint32_t kw[F32 ? 1 : 2][F32 ? 1 : 4][4];
+            if constexpr (!F32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int ic = 4 * q + (lane >> 3);                           // 16-byte piece of k's row
-                    ldsm4_t(kw[h][q], stage + kKAt + (ic >> 3) * kHalf + (16 * quarter + 8 * h + r) * 128 +
-                                          (((ic ^ r) & 7) * 16));
-                }
-            warp_arrive(&sm.kv_free[st]);
+                    for (int q = 0; q < 4; ++q) k_words(kw[h][q], h, q, 0);
+                warp_arrive(&sm.kv_free[bkv]);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int sb = 2 * quarter + h, t = 8 * sb + 2 * (lane & 3);
@@ -496,12 +537,22 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int ic = 4 * q + (lane >> 3);
-                    uint32_t o[kParts][4];
+                    uint32_t o[kParts][4], wl[4];
+                    if constexpr (F32) {
+                        k_words(kw[0][0], h, q, 0);
+                        k_words(wl, h, q, 1);
+                        if (h == 1 && q == 3) warp_arrive(&sm.kv_free[bkv]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t w = kw[h][q][i];
+                        uint32_t w = kw[F32 ? 0 : h][F32 ? 0 : q][i];
                         if (nt < kC) w = t >= nt ? 0u : t + 1 >= nt ? w & 0xffffu : w;
-                        const float2 x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                        float2 x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                        if constexpr (F32) {
+                            uint32_t l = wl[i];
+                            if (nt < kC) l = t >= nt ? 0u : t + 1 >= nt ? l & 0xffffu : l;
+                            x = __fadd2_rn(x, make_float2(__uint_as_float(l << 16), __uint_as_float(l & 0xffff0000u)));
+                        }
                         split2(__fmul2_rn(x, d), o[0][i], o[1][i]);
                     }
 #pragma unroll
@@ -518,8 +569,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             if (!ok) break;
             tc_fence_after();
             float x[32];
-            tmem_ld16(tl + kTSc + pcol, *reinterpret_cast<float(*)[16]>(x));
-            tmem_ld16(tl + kTSc + pcol + 16, *reinterpret_cast<float(*)[16]>(x + 16));
+            tmem_ld16(tl + L::kTSc + pcol, *reinterpret_cast<float(*)[16]>(x));
+            tmem_ld16(tl + L::kTSc + pcol + 16, *reinterpret_cast<float(*)[16]>(x + 16));
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(&sm.sc_free);
@@ -545,7 +596,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
-                    *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + prow * 128 +
+                    *reinterpret_cast<uint4*>(base + L::kPAt + p * kHalf + prow * 128 +
                                               (((pcol / 8 + q) ^ (prow & 7)) * 16)) =
                         make_uint4(o[q][p][0], o[q][p][1], o[q][p][2], o[q][p][3]);
             fence_proxy_async_smem();
@@ -558,7 +609,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const int j = 32 * (warp & 3) + lane, part = (warp - kStateWarp0) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float2 S[16];                            // times e^{mid g}
-        unsigned char* const tile = base + kKdAt + part * kStTile + j * 128;
+        unsigned char* const tile = base + L::kKdAt + part * kStTile + j * 128;
         if (starts) {
             ok = mbar_wait(&sm.st_full, 0, a.err);
             const float in = chunks > 0 ? sm.pw[mid] : 1.0f;
@@ -580,7 +631,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split2(S[4 * b + i], w[0][i], w[1][i]);
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) tmem_st4(tl + kTSp + 64 * p + 16 * part + 4 * b, w[p]);
+                for (int p = 0; p < kParts; ++p) tmem_st4(tl + L::kTSp + 64 * p + 16 * part + 4 * b, w[p]);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -596,7 +647,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         for (int c = 0; c < chunks && ok; ++c, o += kC * step) {
             const uint32_t par = (uint32_t)(c & 1);
             const int nt = min(kC, len - c * kC), live = nt - 16 * part;
-            const uint32_t to = tl + kTO + 64 * (c & 1) + 16 * part;
+            const uint32_t to = tl + L::o_at(c) + 16 * part;
             const float2 f = nt == kC ? whole : decay_pair(g * (float)nt);
             const float2 fa2 = make_float2(f.x, f.x), fd2 = make_float2(f.y, f.y);
             ok = mbar_wait(&sm.u_full, par, a.err);
@@ -605,7 +656,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float u[16];
-                tmem_ld16(tl + kTU + 32 * part + 16 * b, u);
+                tmem_ld16(tl + L::kTU + 32 * part + 16 * b, u);
                 tmem_ld_wait();
                 if (b == 1) {
                     tc_fence_before();
@@ -642,7 +693,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             tmem_ld16(to, x);
             tmem_ld_wait();
             tc_fence_before();
-            warp_arrive(&sm.o_free[c & 1]);
+            warp_arrive(&sm.o_free[c % L::kOBufs]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 f = up[i];
@@ -674,7 +725,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             warp_arrive(&sm.st_out[part]);       // one of the tile's four warps
             if ((warp & 3) == 0 && mbar_wait(&sm.st_out[part], 0, a.err) && elect_one()) {
                 const long st = STATE ? seg_state(cut, n, seg, units) : (long)n * units;
-                tma_store_2d(&maps.out, base + kKdAt + part * kStTile, 32 * part, (int)(st + unit) * kHeadDim);
+                tma_store_2d(&maps.out, base + L::kKdAt + part * kStTile, 32 * part, (int)(st + unit) * kHeadDim);
                 bulk_commit();
                 bulk_wait_read0();
             }
@@ -723,9 +774,35 @@ __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArg
     }
 }
 
-// Segments of a call, by the time of their waves of CTAs in us: a chunk of the main kernel 2.05, of the state
+// f32 rows as bf16 hi and lo, packed: a plane's hi [rows][cols], then its lo.
+constexpr int kSplitThr = 256;
+
+struct SplitPlane {
+    const float* src; uint32_t* hi; uint32_t* lo;
+    long stride; int quads;                      // elements between rows; groups of 4 in a row
+};
+struct SplitArgs {
+    SplitPlane p[3];
+    long rows;
+};
+
+__global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const SplitArgs a) {
+    const SplitPlane p = a.p[blockIdx.y];
+    const long n = a.rows * p.quads, step = (long)gridDim.x * kSplitThr;
+    for (long i = (long)blockIdx.x * kSplitThr + threadIdx.x; i < n; i += step) {
+        const long row = i / p.quads;
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(p.src + row * p.stride) + (i - row * p.quads));
+        uint2 hi, lo;
+        split2(make_float2(x.x, x.y), hi.x, lo.x);
+        split2(make_float2(x.z, x.w), hi.y, lo.y);
+        reinterpret_cast<uint2*>(p.hi)[i] = hi;
+        reinterpret_cast<uint2*>(p.lo)[i] = lo;
+    }
+}
+
+// Segments of a call, by the time of their waves of CTAs in us: a chunk of the main kernel 2.05 (f32: TODO), of the state
 // kernel 0.8, a CTA's start and end 4, the two further launches 7.  (4096 tokens x 64 heads: whole 129 us,
-// 2 segments TODO; 8192 x 8 heads: whole 234, 16 segments TODO.)
+// 2 segments 110; 8192 x 8 heads: whole 234, 16 segments 46.)
 constexpr int kMaxSegs = 32;
 long most_segs(long chains, long chunks, int sms) {
     return std::max(1L, std::min({(long)kMaxSegs, chunks, 4L * sms / std::max(1L, chains)}));
@@ -774,59 +851,100 @@ Cut plan(const SeqLayout& s, const int* cu_host, int units) {
     return best;
 }
 
-template <bool STATE>
+template <bool STATE, bool F32>
 cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, cudaStream_t s) {
     static PerDevice<int> done;
-    const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE>, kSmemBytes, done);
+    const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE, F32>, smem_bytes<F32>(), done);
     if (e != cudaSuccess) return e;
     KernelTimer kt(STATE ? kKLinState : kKLinChunk, s);
-    kda_linattn_chunk_kernel<STATE><<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(cut.segs - STATE)),
-                                      kThr, kSmemBytes, s>>>(a, cut, maps);
+    kda_linattn_chunk_kernel<STATE, F32>
+        <<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(cut.segs - STATE)), kThr, smem_bytes<F32>(), s>>>(
+            a, cut, maps);
     return cudaGetLastError();
 }
 
-}  // namespace
-
-size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int units) {
-    return (size_t)seq.N * (plan(seq, cu_host, units).segs - 1) * units * kHeadDim * kHeadDim * sizeof(float);
-}
-
-// (more than any cut of total_T tokens into N sequences takes: the cut of the longest possible one)
-size_t linattn_chunk_workspace_bound(int N, long total_T, int units) {
-    const int sms = sm_count();
-    const long chains = (long)N * units;
-    if (!may_cut(chains, sms)) return 0;
-    return (size_t)chains * (most_segs(chains, (total_T + kC - 1) / kC, sms) - 1) * kHeadDim * kHeadDim * sizeof(float);
-}
-
-cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s) {
-    const long qk = (long)a.Hk * kHeadDim, vw = (long)a.H * a.m * kHeadDim;
-    const int units = a.H * a.m;
-    Cut cut = plan(a.seq, cu_host, units);
-    cut.parts = static_cast<float*>(workspace);
-    Maps maps;
-    std::memset(&maps, 0, sizeof(maps));
-    const auto states = [&](CUtensorMap* m, const float* base, long seqs) {
-        return make_tensor_map_2d_f32_sw128(m, base, seqs * units * kHeadDim, kHeadDim, kHeadDim);
-    };
-    if (!make_tensor_map_2d_bf16_sw128(&maps.q, a.q, a.seq.total_rows, qk, kC, a.q_stride) ||
-        !make_tensor_map_2d_bf16_sw128(&maps.k, a.k, a.seq.total_rows, qk, kC, a.k_stride) ||
-        !make_tensor_map_2d_bf16_sw128(&maps.v, a.v, a.seq.total_rows, vw, kC, a.v_stride) ||
-        (a.state_in != nullptr && !states(&maps.in, a.state_in, a.seq.N)))
-        return cudaErrorInvalidValue;
+template <bool F32>
+cudaError_t launch_all(const LinArgs& a, const Cut& cut, Maps& maps, const CUtensorMap& out, cudaStream_t s) {
     if (cut.segs > 1) {
-        if (!states(&maps.parts, cut.parts, (long)a.seq.N * (cut.segs - 1))) return cudaErrorInvalidValue;
         maps.out = maps.parts;
-        cudaError_t e = launch<true>(a, cut, maps, s);
+        cudaError_t e = launch<true, F32>(a, cut, maps, s);
         if (e != cudaSuccess) return e;
         KernelTimer kt(kKLinJoin, s);
-        const unsigned blocks = (unsigned)((long)units * kHeadDim * kHeadDim / 4 / kJoinThr);
+        const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
         kda_linattn_join_kernel<<<dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s>>>(a, cut);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (!states(&maps.out, a.state_out, a.seq.N)) return cudaErrorInvalidValue;
-    return launch<false>(a, cut, maps, s);
+    maps.out = out;
+    return launch<false, F32>(a, cut, maps, s);
+}
+
+// bytes of q, k and v as bf16 hi and lo
+size_t split_bytes(long rows, int Hk, int units, bool bf16) {
+    return bf16 ? 0 : (size_t)rows * (2L * Hk + units) * kHeadDim * 4;
+}
+
+}  // namespace
+
+// The workspace: q, k and v split (f32), then the segments' states.
+size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int Hk, int units, bool bf16) {
+    return split_bytes(seq.total_rows, Hk, units, bf16) +
+           (size_t)seq.N * (plan(seq, cu_host, units).segs - 1) * units * kHeadDim * kHeadDim * sizeof(float);
+}
+
+// (more than any cut of total_T tokens into N sequences takes: the cut of the longest possible one)
+size_t linattn_chunk_workspace_bound(int N, long total_T, int Hk, int units, bool bf16) {
+    const int sms = sm_count();
+    const long chains = (long)N * units;
+    const size_t split = split_bytes(total_T, Hk, units, bf16);
+    if (!may_cut(chains, sms)) return split;
+    return split + (size_t)chains * (most_segs(chains, (total_T + kC - 1) / kC, sms) - 1) * kHeadDim * kHeadDim *
+                       sizeof(float);
+}
+
+cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s) {
+    const int units = a.H * a.m;
+    const long rows = a.seq.total_rows, width[3] = {(long)a.Hk * kHeadDim, (long)a.Hk * kHeadDim, (long)units * kHeadDim};
+    const void* const in[3] = {a.q, a.k, a.v};
+    const long stride[3] = {a.q_stride, a.k_stride, a.v_stride};
+    Cut cut = plan(a.seq, cu_host, units);
+    cut.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + split_bytes(rows, a.Hk, units, a.bf16));
+    Maps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    CUtensorMap* const to[3] = {maps.q, maps.k, maps.v};
+    SplitArgs sp;
+    sp.rows = rows;
+    unsigned char* at = static_cast<unsigned char*>(workspace);
+    for (int i = 0; i < 3; ++i) {
+        if (a.bf16) {
+            if (!make_tensor_map_2d_bf16_sw128(&to[i][0], in[i], rows, width[i], kC, stride[i]))
+                return cudaErrorInvalidValue;
+            continue;
+        }
+        unsigned char* const lo = at + (size_t)rows * width[i] * 2;
+        if (!make_tensor_map_2d_bf16_sw128(&to[i][0], at, rows, width[i], kC) ||
+            !make_tensor_map_2d_bf16_sw128(&to[i][1], lo, rows, width[i], kC))
+            return cudaErrorInvalidValue;
+        sp.p[i] = SplitPlane{static_cast<const float*>(in[i]), reinterpret_cast<uint32_t*>(at),
+                             reinterpret_cast<uint32_t*>(lo), stride[i], (int)(width[i] / 4)};
+        at = lo + (size_t)rows * width[i] * 2;
+    }
+    const auto states = [&](CUtensorMap* m, const float* base, long seqs) {
+        return make_tensor_map_2d_f32_sw128(m, base, seqs * units * kHeadDim, kHeadDim, kHeadDim);
+    };
+    CUtensorMap out;
+    if ((a.state_in != nullptr && !states(&maps.in, a.state_in, a.seq.N)) || !states(&out, a.state_out, a.seq.N) ||
+        (cut.segs > 1 && !states(&maps.parts, cut.parts, (long)a.seq.N * (cut.segs - 1))))
+        return cudaErrorInvalidValue;
+    if (a.bf16) return launch_all<false>(a, cut, maps, out, s);
+    {
+        KernelTimer kt(kKLinSplit, s);
+        const long blocks = (rows * width[2] / 4 + kSplitThr - 1) / kSplitThr;
+        kda_linattn_split_kernel<<<dim3((unsigned)std::min(blocks, 152L * 8), 3), kSplitThr, 0, s>>>(sp);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return launch_all<true>(a, cut, maps, out, s);
 }
 
 }  // namespace kda

@@ -3,10 +3,13 @@ pool of states, against the recurrence in 64 bits.
 
 Tolerance.  Relative to the same sums of magnitudes, an output of the recurrent form carries at most 3
 roundings a token still remembered, 16 + 8 in the readout's sum and a few for the scale; the chunked
-form at most one split (2^-24) and one rounding for each of about 60 accumulation steps, which the
-tensor cores may truncate (2^-23).  With at most 16 / 24 bits' worth remembered below, 64 * 2^-23 +
-3 * min(T, 1 / (1 - lambda)) * 2^-24 covers both; log_decay enters e^(g n) with n g rounded, an error of
-x 2^-24 e^-x <= 2^-25 more."""
+form of bf16 at most one split to 17 bits (2^-17 = 64 * 2^-23) where its 60 or so accumulation steps, which
+the tensor cores may truncate (2^-23 each), and the split are not at their largest together.  With at most
+16 / 24 bits' worth remembered below, 64 * 2^-23 + 3 * min(T, 1 / (1 - lambda)) * 2^-24 covers both;
+log_decay enters e^(g n) with n g rounded, an error of x 2^-24 e^-x <= 2^-25 more.
+The chunked form of f32 (32 tokens and more) splits q, k and v themselves: on the way through the state k,
+its decayed form, v, the state and q are each off by 2^-17, and the two products leave out lo * lo, at most
+2^-8 * 2^-8 = 2 * 2^-17 each: 9 * 2^-17 in all (within a chunk q, k, v, P and two products: 8)."""
 
 import pytest
 import torch
@@ -27,7 +30,9 @@ def _decays(H, kind="mixed"):
     return (-torch.exp2(-8.0 * h / H)).float()
 
 
-def _tol(T, g):
+def _tol(T, g, dtype=torch.bfloat16, longest=None):
+    if dtype == torch.float32 and (T if longest is None else longest) >= 32:
+        return _tol(T, g) + 9 * 2.0 ** -17
     lam = torch.exp(g.double())
     horizon = torch.minimum(torch.tensor(float(max(T, 1)), dtype=torch.float64), 1 / (1 - lam).clamp(min=1e-9))
     return 64 * 2.0 ** -23 + 3 * float(horizon.max()) * 2.0 ** -24
@@ -82,8 +87,8 @@ def test_prefill(lengths, H, Hk, Dv, kind, dtype, state, fused):
     for n, L in enumerate(lengths):
         b, e = int(cu[n]), int(cu[n + 1])
         (o, last), (om, lm) = ref.both(q[b:e], k[b:e], v[b:e], g, S[n], H, Hk, Dv, D ** -0.5)
-        _close(out["o"][b:e], o, om, _tol(L, g), ("o", n))
-        _close(out["state_out"][n], last, lm, _tol(L, g), ("state", n))
+        _close(out["o"][b:e], o, om, _tol(L, g, dtype, max(lengths)), ("o", n))
+        _close(out["state_out"][n], last, lm, _tol(L, g, dtype, max(lengths)), ("state", n))
 
 
 @pytest.mark.parametrize("N,T", [(1, 64), (2, 100), (3, 1)])
@@ -217,18 +222,19 @@ def test_long_memory_keeps_a_decay_next_to_one():
         assert float(err) < 20000 * 2.0 ** -26
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("lengths,H,kind", [([5000], 1, "mixed"), ([3000, 1, 900, 2100], 2, "mixed"),
                                             ([2500], 3, "strong"), ([4097], 2, "none"),
                                             ([64 * 40], 5, "mixed")])
-def test_few_long_prompts(lengths, H, kind):
+def test_few_long_prompts(lengths, H, kind, dtype):
     """Long prompts of few heads are cut into segments: outputs and states as of the whole."""
     from gated_delta_rule_scan_gb300 import kda, mixer
     rows, N = sum(lengths), len(lengths)
-    (q, k, v), (dq, dk, dv) = _inputs(rows, H, H, D, torch.bfloat16, rows)
+    (q, k, v), (dq, dk, dv) = _inputs(rows, H, H, D, dtype, rows)
     g = _decays(H, kind) if kind != "mixed" else _decays(H, kind) * 0.02
     S = torch.randn(N, H, D, D, generator=torch.Generator().manual_seed(rows))
     cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32)
-    assert kda.kda_linattn_workspace_bytes(N, rows, H) > 0
+    assert kda.kda_linattn_workspace_bytes(N, rows, H, dtype=dtype) > 0
     out = mixer.kda_linattn_prefill(q=dq, k=dk, v=dv, log_decay=g.cuda(), H=H, state_in=S.cuda(),
                                     cu_seqlens=cu.cuda(), cu_seqlens_host=cu)
     torch.cuda.synchronize()
@@ -236,5 +242,5 @@ def test_few_long_prompts(lengths, H, kind):
     for n, L in enumerate(lengths):
         b, e = int(cu[n]), int(cu[n + 1])
         (o, last), (om, lm) = ref.both(q[b:e], k[b:e], v[b:e], g, S[n], H, H, D, D ** -0.5)
-        _close(out["o"][b:e], o, om, _tol(L, g), ("o", n))
-        _close(out["state_out"][n], last, lm, _tol(L, g), ("state", n))
+        _close(out["o"][b:e], o, om, _tol(L, g, dtype, max(lengths)), ("o", n))
+        _close(out["state_out"][n], last, lm, _tol(L, g, dtype, max(lengths)), ("state", n))
