@@ -15,6 +15,10 @@
 // of their scale.  (A third part brought 1e-7 for half as much again in MMAs and splitting, 166 against
 // TODO us at 4096 tokens x 64 heads.)  The state itself stays in f32 registers.
 //
+// A NaN or an infinity at one token does not reach the tokens before it: where q k is not seen P is 0 by
+// selection, and in v, whose products with P = 0 would be NaN, it is replaced by 0 and its value column made
+// NaN from that token on.
+//
 // One CTA per (sequence, 128-wide value unit), chunk after chunk, the values on the MMA's M = 128 TMEM
 // lanes.  Shared memory carries what the tensor cores read of it at 128 bytes a cycle, so the A
 // operands lie in tensor memory: the state parts, written by the threads that hold the state rows, and
@@ -95,6 +99,7 @@ struct __align__(16) Tail {
     uint64_t st_full, st_free, st_out[4];        // the state on its way in and out
     uint64_t drain[3];
     uint32_t tmem;
+    int bad[kHeadDim];                           // by value: the first token whose v is no number
 };
 constexpr int kMaxRanked = 32;                   // packed sequences that are taken longest first
 template <bool F32>
@@ -308,6 +313,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             sm.up[i] = a.scale * (strong ? expf(g * (float)(i + 1)) : i == kMid - 1 ? 1.0f : expf(g * (float)(i - kMid + 1)));
         }
     }
+    if (warp >= kConvWarp0 && warp < kConvWarp0 + 4) sm.bad[32 * (warp - kConvWarp0) + lane] = 0x7fffffff;
     if (warp == kConvWarp0) {                    // t < 32 <= s: P is 0 there, once and for all
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
@@ -496,12 +502,10 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                  mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / L::kKvBars) & 1), a.err);
             if (!ok) break;
             // v^T: values of this warp's lane quarter, 16 and 16, tokens 0 .. 31 and 32 ..
-#pragma unroll
-            for (int h = 0; h < 4 * L::kIn; ++h) {
+            const auto v_words = [&](uint32_t (&w)[8], int h) {
                 const int vp = h >> 2, half = (h >> 1) & 1;
                 const int jc = 4 * quarter + 2 * (h & 1) + ((lane >> 3) & 1);     // 16-byte piece of the row
                 const int vs = 32 * half + 8 * (lane >> 4) + r;                   // + 16 for the second pair
-                uint32_t w[8];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     ldsm4_t(*reinterpret_cast<uint32_t(*)[4]>(w + 4 * q),
@@ -513,8 +517,37 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                         const int t = 32 * half + 8 * (i >> 1) + 2 * (lane & 3);
                         w[i] = t >= nt ? 0u : t + 1 >= nt ? w[i] & 0xffffu : w[i];
                     }
-                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + L::kTVt + L::kVtCols * (c & 1) + 32 * vp +
-                                       16 * half, w);
+            };
+            const auto v_store = [&](const uint32_t (&w)[8], int h) {
+                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + L::kTVt + L::kVtCols * (c & 1) +
+                                       32 * (h >> 2) + 16 * ((h >> 1) & 1), w);
+            };
+            const __nv_bfloat162 zero2 = __floats2bfloat162_rn(0.0f, 0.0f);
+            __nv_bfloat162 odd[2] = {zero2, zero2};          // 0 times v, summed: 0 unless one is no number
+#pragma unroll
+            for (int h = 0; h < 4 * L::kIn; ++h) {
+                uint32_t w[8];
+                v_words(w, h);
+                v_store(w, h);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    odd[i & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(w + i), zero2, odd[i & 1]);
+            }
+            const uint32_t odd_bits = *reinterpret_cast<const uint32_t*>(odd) | *reinterpret_cast<const uint32_t*>(odd + 1);
+            if (__any_sync(0xffffffffu, (odd_bits & 0x7fff7fffu) != 0)) {
+#pragma unroll 1
+                for (int h = 0; h < 4 * L::kIn; ++h) {
+                    uint32_t w[8];
+                    v_words(w, h);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        int* bad = &sm.bad[32 * quarter + 16 * (h & 1) + 8 * (i & 1) + (lane >> 2)];
+                        const int t = c * kC + 32 * ((h >> 1) & 1) + 8 * (i >> 1) + 2 * (lane & 3);
+                        if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0xffffu; atomicMin(bad, t + 1); }
+                        if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; atomicMin(bad, t); }
+                    }
+                    v_store(w, h);
+                }
             }
             // Kd: tokens 16 quarter .., 8 and 8, transposed to [key][token]
             const auto k_words = [&](uint32_t (&w)[4], int h, int q, int p) {
@@ -668,6 +701,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                     y = __ffma2_rn(fa2, y, __ffma2_rn(fd2, y, make_float2(u[2 * i], u[2 * i + 1])));
                 }
             }
+            const int bad = sm.bad[j];
+            if (bad < (c + 1) * kC) {
+                const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[i] = make_float2(nan, nan);
+            }
             if (STATE) continue;
             if (strong) {                        // V^T P^T by itself: stored, and S Q^T added to it below
                 ok = mbar_wait(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err);
@@ -701,6 +740,10 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 const float2 w = __fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
                 x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = w.x; x[4 * i + 3] = w.y;
             }
+            if (bad < (c + 1) * kC)
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    if (c * kC + 16 * part + t >= bad) x[t] = __int_as_float(0x7fffffff);
             uint32_t at = (uint32_t)j * 4;
             if (live >= 16 && !strong) {
 #pragma unroll

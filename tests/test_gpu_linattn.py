@@ -244,3 +244,61 @@ def test_few_long_prompts(lengths, H, kind, dtype):
         (o, last), (om, lm) = ref.both(q[b:e], k[b:e], v[b:e], g, S[n], H, H, D, D ** -0.5)
         _close(out["o"][b:e], o, om, _tol(L, g, dtype, max(lengths)), ("o", n))
         _close(out["state_out"][n], last, lm, _tol(L, g, dtype, max(lengths)), ("state", n))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,decay", [(10, -0.1), (200, -0.1), (200, -5.0), (3000, -0.01)])
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+def test_no_number_reaches_earlier_tokens(what, T, decay, dtype):
+    """A NaN or an infinity in one token's row leaves the tokens before it, the other sequences and (in v) the
+    other value columns as they are, bit for bit, and is seen where it counts."""
+    from gated_delta_rule_scan_gb300 import mixer
+    H, at, col = 2, 2 * T // 3, 17
+    _, dev = _inputs(3 * T, H, H, D, dtype, T)
+    x = dict(zip("qkv", (d.clone() for d in dev)))
+    g = torch.full((H,), decay, device="cuda")
+
+    def run():
+        return mixer.kda_linattn_prefill(**x, log_decay=g, H=H, N=3, T=T)
+    clean = run()
+    for value in (float("nan"), float("inf"), float("-inf")):
+        x[what][T + at, D + col] = value                   # sequence 1, head 1
+        out = run()
+        x[what][T + at, D + col] = dev["qkv".index(what)][T + at, D + col]
+        o, o0 = (r["o"].view(3, T, H, D) for r in (out, clean))
+        s, s0 = (r["state_out"] for r in (out, clean))
+        same = torch.ones(3, T, H, D, dtype=torch.bool, device="cuda")
+        if what == "q":
+            same[1, at, 1] = False
+        else:
+            same[1, at:, 1, col if what == "v" else slice(None)] = False
+        assert torch.equal(o[same], o0[same])
+        assert not bool(torch.isfinite(o[1, at, 1, col]))
+        live = torch.ones(3, H, D, D, dtype=torch.bool, device="cuda")
+        if what == "v":
+            live[1, 1, col] = False
+        elif what == "k":
+            live[1, 1, :, col] = False
+        assert torch.equal(s[live], s0[live])
+        if what != "q":
+            assert not bool(torch.isfinite(s[1, 1, col, col]))
+
+
+def test_neighbours_that_are_no_numbers():
+    """Packed sequences of odd lengths: one of NaN throughout leaves the others as they are."""
+    from gated_delta_rule_scan_gb300 import mixer
+    H, lengths = 2, [70, 33, 90, 1, 64]
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32)
+    for dtype in (torch.float32, torch.bfloat16):
+        _, (q, k, v) = _inputs(sum(lengths), H, H, D, dtype, 1)
+        g = _decays(H).cuda()
+        kw = dict(log_decay=g, H=H, cu_seqlens=cu.cuda(), cu_seqlens_host=cu)
+        clean = mixer.kda_linattn_prefill(q=q, k=k, v=v, **kw)
+        for x in (q, k, v):
+            x[int(cu[1]):int(cu[2])] = float("nan")
+        out = mixer.kda_linattn_prefill(q=q, k=k, v=v, **kw)
+        for n in (0, 2, 3, 4):
+            at = slice(int(cu[n]), int(cu[n + 1]))
+            assert torch.equal(out["o"][at], clean["o"][at])
+            assert torch.equal(out["state_out"][n], clean["state_out"][n])
+        assert bool(torch.isnan(out["o"][int(cu[1]):int(cu[2])]).all())
