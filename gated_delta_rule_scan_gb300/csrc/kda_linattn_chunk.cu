@@ -702,10 +702,11 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 }
             }
             const int bad = sm.bad[j];
-            if (bad < (c + 1) * kC) {
-                const float nan = __int_as_float(0x7fffffff);
+            const bool any_bad = __any_sync(0xffffffffu, bad < (c + 1) * kC);
+            if (any_bad) {
+                const float nan = bad < (c + 1) * kC ? __int_as_float(0x7fffffff) : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[i] = make_float2(nan, nan);
+                for (int i = 0; i < 16; ++i) S[i] = make_float2(S[i].x + nan, S[i].y + nan);
             }
             if (STATE) continue;
             if (strong) {                        // V^T P^T by itself: stored, and S Q^T added to it below
@@ -740,7 +741,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 const float2 w = __fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
                 x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = w.x; x[4 * i + 3] = w.y;
             }
-            if (bad < (c + 1) * kC)
+            if (any_bad)
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     if (c * kC + 16 * part + t >= bad) x[t] = __int_as_float(0x7fffffff);
