@@ -680,14 +680,23 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
  * q, k         [rows, Hk*128], v [rows, H*Dv] in raw_dtype [16B]; token rows are q_stride, k_stride
  *              and v_stride elements apart (the planes may be column slices of one projection's
  *              output): at least the row's width and a multiple of 16 bytes (40005 otherwise).
- * log_decay    [H] f32, at most 0.
- * state_in     [N, H, Dv, 128] f32 [16B], or NULL: zero.  state_out the same shape; overlapping
- *              states return 40003.  An empty sequence's state passes through.
- * o            [rows, H*Dv] f32 [16B], rows 128-wide heads apart as kda_gated_rmsnorm_out reads them.
- * workspace    device scratch [16B] of at least kda_linattn_workspace_bytes(...) bytes (40009
- *              otherwise; where that is 0 NULL is accepted).  Its contents are overwritten: calls that
- *              share it must not overlap.
- * Dk = 128, Dv = 128 * m, m = 1..8 (40001).
+ * log_decay    [H] f32, at most 0; -infinity forgets everything at each token.
+ * state_in     [N, H, Dv, 128] f32 [16B], or NULL: zero.  state_out the same shape.  An empty
+ *              sequence's state passes through.
+ * o            [rows, H*Dv] f32 [16B], packed, as kda_gated_rmsnorm_out reads it.
+ * workspace    device scratch [16B] of at least kda_linattn_workspace_bytes(...) bytes (asked for with the
+ *              device current that runs the call; 40009 otherwise; where it is 0 NULL is accepted).  Its
+ *              contents are overwritten: calls that share it must not overlap.
+ * Dk = 128, Dv = 128 * m, m = 1..8 (40001).  o and state_out overlap nothing else of the call (40003).
+ * Short prompts (bf16 below 20 tokens, f32 below 48, by the longest sequence) run the recurrence itself, in
+ * f32, and equal chained kda_linattn_decode calls bit for bit; longer ones run in chunks of 64 tokens on
+ * the tensor cores, few long ones cut into segments.
+ * Precision of the chunks: bf16 q, k and v enter exactly, f32 ones as bf16 hi + lo, within 2^-17 of an
+ * element; decayed scores and keys and the state likewise enter their products within 2^-17; the state
+ * itself and all sums are f32.  Against the sums of the terms' magnitudes the results are off by a few
+ * 1e-6.
+ * Products q k v and states must stay below 1e24 in magnitude.  A NaN or an infinity at a token reaches no
+ * earlier token and no other sequence, one in v no other value column.
  */
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype);
 int kda_linattn_prefill(const void* q, long q_stride, const void* k, long k_stride, const void* v,
@@ -712,7 +721,7 @@ int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long
  *              another row reads or an earlier row writes, is left out (40013, kda_device_status).
  * q, k, v, log_decay, o, scale   as in kda_linattn_prefill; sequence n owns rows n*T .. n*T + T-1.  o
  *              rows of padding, of rows left out and of rows t >= keep[n] are not written.
- * A T-token call equals T one-token calls bit for bit.
+ * A T-token call equals T one-token calls bit for bit.  o overlaps nothing else of the call (40003).
  */
 int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_stride, const void* v,
                        long v_stride, int raw_dtype, const float* log_decay, float* pool,
@@ -740,7 +749,7 @@ int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_strid
  * T = 1..16 (1: plain sampling; tokens, u and draft are not read), N <= 65535, V >= 1 (40005).
  * Nothing needs to be normalised.  A drafted id outside the vocabulary is refused.  A weight that is
  * negative, NaN or infinite counts as 0; where no weight is left the new token is -1.
- * Sums are exact to about 2^-46 of the row's total.
+ * Sums are exact to about 2^-45 of the row's total.  keep and out_tokens overlap nothing else (40003).
  */
 int kda_draft_accept(const void* target, long target_stride, const void* draft, long draft_stride,
                      int prob_dtype, const int* tokens, const float* u, const float* r,
