@@ -47,36 +47,41 @@ namespace {
 
 constexpr int kC = 64;                           // tokens of a chunk
 constexpr int kMid = kC / 2;
-constexpr int kParts = 2;
 constexpr int kHalf = kC * 128;                  // bytes of 64 tokens x 64 columns, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalf;            // 64 tokens x 128 columns
-constexpr int kKdBytes = kParts * kTileBytes;    // Kd's parts, two buffers
 constexpr int kStTile = kHeadDim * 128;          // 128 state rows x 32 keys, f32
-static_assert(4 * kStTile <= 2 * kKdBytes, "");
 
 // Shared memory and tensor memory by the inputs' type.  F32: q, k and v are bf16 hi + lo themselves (split by a
-// launch before), every product three of them (hi hi, hi lo, lo hi); the loads have fewer stages and the
-// outputs one buffer.
+// launch before), and what they are multiplied by has two parts, so that every product is three MMAs here too (lo hi,
+// hi lo, hi hi); k and v have one stage.
 template <bool F32>
 struct Lay {
     static constexpr int kIn = F32 ? 2 : 1;                          // parts of q, k, v
-    static constexpr int kKvStages = F32 ? 1 : 3, kQStages = F32 ? 2 : 3;
+    static constexpr int kParts = F32 ? 2 : 3;                       // of P, Kd and the state
+    static constexpr int kKvStages = F32 ? 1 : 2, kQStages = 2;
     // barriers of k and v: a chunk's comes two chunks later again at the earliest, since its group of warps knows
     // only of its own chunks that they have passed
-    static constexpr int kKvBars = F32 ? 2 : 3;
+    static constexpr int kKvBars = 2;
     static constexpr int kKvBytes = 2 * kIn * kTileBytes;            // k's parts, v's parts
     static constexpr int kQBytes = kIn * kTileBytes;
     static constexpr int kVAt = kIn * kTileBytes;                    // in a stage
     static constexpr int kQAt = kKvStages * kKvBytes;
+    static constexpr int kKdBytes = kParts * kTileBytes;             // Kd's parts, two buffers
     static constexpr int kKdAt = kQAt + kQStages * kQBytes;
     static constexpr int kPAt = kKdAt + 2 * kKdBytes;                // P's parts, [64 t][64 s] each
     static constexpr int kTailAt = kPAt + kParts * kHalf;
     // TMEM columns
-    static constexpr uint32_t kTSp = 0, kTU = 128, kTO = 256, kTSc = F32 ? 320 : 384, kTVt = F32 ? 384 : 448;
-    static constexpr int kOBufs = F32 ? 1 : 2;
+    static constexpr uint32_t kTSp = 0, kTU = 64 * kParts, kTO = kTU + 128, kTSc = kTO + 64, kTVt = kTSc + 64;
     static constexpr uint32_t kVtCols = 32 * kIn;                    // of one of v's two buffers
-    __device__ static constexpr uint32_t o_at(int c) { return kTO + 64 * (c % kOBufs); }
+    static_assert(kTVt + 2 * kVtCols <= 512, "");
+    static_assert(4 * kStTile <= 2 * kKdBytes, "");
 };
+constexpr int kTerms = 3;                        // MMAs of a product, its smallest term first
+// the part of q, k or v and that of the other factor in term x
+template <bool F32>
+__device__ constexpr int in_part(int x) { return F32 && x == 0; }
+template <bool F32>
+__device__ constexpr int other_part(int x) { return F32 ? x == 1 : 2 - x; }
 
 constexpr int kStateWarps = 16, kConvWarps = 8;
 // The first warpgroup issues the MMAs and the loads; whole warpgroups: registers move between them.
@@ -93,27 +98,30 @@ struct __align__(16) Tail {
     float pw[kC + kMid + 4];                     // e^{g n}, n = 0 .. 96
     float down[kC];                              // P's factors: e^{g (31-s)}
     float up[kC];                                // the outputs': scale * e^{g (t-31)}, or scale * e^{g (t+1)}
-    uint64_t kv_full[3], kv_free[3], q_full[3], q_free[3];
+    uint64_t kv_full[2], kv_free[2], q_full[2], q_free[2];
     uint64_t kd_full[2], kd_free[2];
-    uint64_t sc_full[2], sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free[2];
+    uint64_t sc_full[2], sc_free, u_full, u_free, sp_full, p_full, oa_full[2], oa_free, o_full, o_free;
     uint64_t st_full, st_free, st_out[4];        // the state on its way in and out
     uint64_t drain[3];
     uint32_t tmem;
     int bad[kHeadDim];                           // by value: the first token whose v is no number
 };
+constexpr int kAhead = 4;                        // chunks that are on their way into L2 or further
 constexpr int kMaxRanked = 32;                   // packed sequences that are taken longest first
 template <bool F32>
 constexpr int smem_bytes() { return 1024 + Lay<F32>::kTailAt + (int)sizeof(Tail); }
 static_assert(smem_bytes<false>() <= kMaxBlockSmem && smem_bytes<true>() <= kMaxBlockSmem, "");
 
-// Two f32 as two bf16x2 words, hi and lo.
-__device__ __forceinline__ void split2(float2 x, uint32_t& a, uint32_t& b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-    a = *reinterpret_cast<const uint32_t*>(&h);
-    x = __ffma2_rn(make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)),
-                   make_float2(-1.0f, -1.0f), x);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x.x, x.y);
-    b = *reinterpret_cast<const uint32_t*>(&l);
+// Two f32 as bf16x2 words, each the rest of those before it rounded.
+template <int PARTS>
+__device__ __forceinline__ void split(float2 x, uint32_t (&w)[PARTS]) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        w[p] = *reinterpret_cast<const uint32_t*>(&h);
+        if (p + 1 < PARTS) x = __ffma2_rn(make_float2(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u)),
+                           make_float2(-1.0f, -1.0f), x);
+    }
 }
 
 // mbar_wait_bounded for two dozen warps that wait most of the time: the suspended wait is left to the
@@ -140,6 +148,11 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, i
 }
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
     return mbar_try_wait(bar, parity) || mbar_wait_long(bar, parity, err);
+}
+
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
+                 : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -202,6 +215,7 @@ template <bool STATE, bool F32>
 __global__ void __launch_bounds__(kThr, 1)
 kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__ Maps maps) {
     using L = Lay<F32>;
+    constexpr int kParts = L::kParts, kKdBytes = L::kKdBytes;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -268,9 +282,18 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 tma_load_2d(s + p * kTileBytes + h * kHalf, &maps.q[p], hk * kHeadDim + 64 * h,
                             (int)(begin + (long)c * kC), bar);
     };
+    const auto prefetch = [&](int c) {           // into L2
+        const int row = (int)(begin + (long)c * kC);
+        for (int p = 0; p < L::kIn; ++p)
+            for (int h = 0; h < 2; ++h) {
+                tma_prefetch_2d(&maps.k[p], hk * kHeadDim + 64 * h, row);
+                tma_prefetch_2d(&maps.v[p], unit * kHeadDim + 64 * h, row);
+                if (!STATE) tma_prefetch_2d(&maps.q[p], hk * kHeadDim + 64 * h, row);
+            }
+    };
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 mbar_init(&sm.kv_full[i], 1);
                 mbar_init(&sm.kv_free[i], kGroupWarps + !STATE);
                 mbar_init(&sm.q_full[i], 1);
@@ -289,7 +312,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             mbar_init(&sm.p_full, kPWarps);
             for (int i = 0; i < 2; ++i) mbar_init(&sm.oa_full[i], 1);
             mbar_init(&sm.oa_free, kStateWarps);
-            for (int i = 0; i < 2; ++i) mbar_init(&sm.o_free[i], kStateWarps);
+            mbar_init(&sm.o_free, kStateWarps);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             mbar_init(&sm.st_full, 1);
             mbar_init(&sm.st_free, kStateWarps);
@@ -304,6 +327,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             }
             for (int c = 0; c < L::kKvStages && c < chunks; ++c) load_kv(c);
             for (int c = 0; !STATE && c < L::kQStages && c < chunks; ++c) load_q(c);
+            for (int c = L::kKvStages; c < kAhead && c < chunks; ++c) prefetch(c);
         }
         __syncwarp();
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
@@ -334,12 +358,14 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         // ---- loads ---------------------------------------------------------------------------
         // (in the order in which the stages come free: k and v are done with a product earlier than q)
         for (int c = L::kKvStages; c < chunks && ok; ++c) {
-            {
-                const int was = c - L::kKvStages;
-                ok = mbar_wait(&sm.kv_free[was % L::kKvBars], (uint32_t)((was / L::kKvBars) & 1), a.err);
-                if (ok && elect_one()) load_kv(c);
-                __syncwarp();
+            const int was = c - L::kKvStages;
+            ok = mbar_wait(&sm.kv_free[was % L::kKvBars], (uint32_t)((was / L::kKvBars) & 1), a.err);
+            if (ok && elect_one()) {
+                load_kv(c);
+                const int ahead = c - L::kKvStages + kAhead;
+                if (ahead < chunks) prefetch(ahead);
             }
+            __syncwarp();
             if (STATE || c < L::kQStages) continue;
             ok = ok && mbar_wait(&sm.q_free[c % L::kQStages], (uint32_t)((c / L::kQStages - 1) & 1), a.err);
             if (ok && elect_one()) load_q(c);
@@ -376,17 +402,17 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 const uint64_t k0 = tc_desc_advance(d0, skv * L::kKvBytes);
                 const uint64_t q0 = tc_desc_advance(d0, L::kQAt + sq * L::kQBytes);
                 if (!STATE && elect_one()) {
+#pragma unroll 1
+                    for (int x = 0; x < 2 * (2 * L::kIn - 1); ++x) {  // hi lo, lo hi, hi hi; 64 keys each time
+                        const int kp = F32 && x < 2, qp = F32 && (x >> 1) == 1;
+                        const uint64_t q = tc_desc_advance(q0, qp * kTileBytes + (x & 1) * kHalf);
+                        const uint64_t k = tc_desc_advance(k0, kp * kTileBytes + (x & 1) * kHalf);
 #pragma unroll
-                    for (int x = 0; x < 2 * L::kIn - 1; ++x) {       // hi lo, lo hi, hi hi
-                        const int kp = F32 && x == 0, qp = F32 && x == 1;
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) {
-                            const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                            const uint64_t q = tc_desc_advance(q0, qp * kTileBytes + off);
-                            const uint64_t k = tc_desc_advance(k0, kp * kTileBytes + off);
-                            tc_mma_ss(tmem + L::kTSc, q, k, id_sc, x > 0 || ks > 0);
-                            tc_mma_ss(tmem + L::kTSc + 32, q - (kHalf >> 4), tc_desc_advance(k, kHalf / 2), id_sc,
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc_mma_ss(tmem + L::kTSc, tc_desc_advance(q, 32 * ks), tc_desc_advance(k, 32 * ks), id_sc,
                                       x > 0 || ks > 0);
+                            tc_mma_ss(tmem + L::kTSc + 32, tc_desc_advance(q, 32 * ks) - (kHalf >> 4),
+                                      tc_desc_advance(k, kHalf / 2 + 32 * ks), id_sc, x > 0 || ks > 0);
                         }
                     }
                     tc_commit(&sm.sc_full[c & 1]);
@@ -401,13 +427,13 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < L::kIn + 1; ++x) {           // (lo hi,) hi lo, hi hi
-                        const int vp = F32 && x == 0, p = x == L::kIn - 1;
+#pragma unroll 1
+                    for (int x = 0; x < kTerms; ++x) {
+                        const int vp = in_part<F32>(x), p = other_part<F32>(x);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + L::kTU, vt + 32 * vp + 8 * ks, tc_desc_advance(kd, p * kTileBytes + 32 * ks),
-                                      id_u, x > 0 || ks > 0);
+                            tc_mma_ts(tmem + L::kTU, vt + 32 * vp + 8 * ks,
+                                      tc_desc_advance(kd, p * kTileBytes + 32 * ks), id_u, x > 0 || ks > 0);
                     }
                     tc_commit(&sm.u_full);
                     tc_commit(&sm.kd_free[c & 1]);
@@ -432,12 +458,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < L::kIn + 1; ++x) {           // (hi lo,) lo hi, hi hi
-                        const int qp = F32 && x == 0, p = x == L::kIn - 1;
+#pragma unroll 1
+                    for (int x = 0; x < kTerms; ++x) {
+                        const int qp = in_part<F32>(x), p = other_part<F32>(x);
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ts(tmem + L::o_at(c), tmem + L::kTSp + 64 * p + 8 * ks,
+                            tc_mma_ts(tmem + L::kTO, tmem + L::kTSp + 64 * p + 8 * ks,
                                       tc_desc_advance(q, qp * kTileBytes + (ks >> 2) * kHalf + (ks & 3) * 32), id_o,
                                       !strong || x > 0 || ks > 0);
                     }
@@ -456,17 +482,17 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 // (v's last quarter comes from a warp without a share of P)
                 ok = mbar_wait(&sm.p_full, par, a.err) &&
                      mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
-                     (c < L::kOBufs || mbar_wait(&sm.o_free[c % L::kOBufs], (uint32_t)((c / L::kOBufs - 1) & 1), a.err));
+                     (c == 0 || mbar_wait(&sm.o_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < L::kIn + 1; ++x) {           // (lo hi,) hi lo, hi hi
-                        const int vp = F32 && x == 0, p = x == L::kIn - 1;
+#pragma unroll 1
+                    for (int x = 0; x < kTerms; ++x) {
+                        const int vp = in_part<F32>(x), p = other_part<F32>(x);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + L::o_at(c), vt + 32 * vp + 8 * ks, tc_desc_advance(pp, p * kHalf + 32 * ks),
-                                      id_o, x > 0 || ks > 0);
+                            tc_mma_ts(tmem + L::kTO, vt + 32 * vp + 8 * ks,
+                                      tc_desc_advance(pp, p * kHalf + 32 * ks), id_o, x > 0 || ks > 0);
                     }
                     tc_commit(&sm.oa_full[c & 1]);
                     tc_commit(&sm.kd_free[c & 1]);
@@ -555,42 +581,35 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 ldsm4_t(w, stage + p * kTileBytes + (ic >> 3) * kHalf + (16 * quarter + 8 * h + r) * 128 +
                                (((ic ^ r) & 7) * 16));
             };
-            uint32_t kw[F32 ? 1 : 2][F32 ? 1 : 4][4];
-            if constexpr (!F32) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) k_words(kw[h][q], h, q, 0);
-                warp_arrive(&sm.kv_free[bkv]);
-            }
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 const int sb = 2 * quarter + h, t = 8 * sb + 2 * (lane & 3);
                 const float2 d = make_float2(sm.pw[mid + max(nt - 1 - t, 0)], sm.pw[mid + max(nt - 2 - t, 0)]);
+                const uint32_t live = t + 1 < nt ? 0xffffffffu : t < nt ? 0xffffu : 0u;
+                uint32_t kw[L::kIn][4][4];
+#pragma unroll
+                for (int p = 0; p < L::kIn; ++p)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) k_words(kw[p][q], h, q, p);
+                if (h == 1) warp_arrive(&sm.kv_free[bkv]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int ic = 4 * q + (lane >> 3);
-                    uint32_t o[kParts][4], wl[4];
-                    if constexpr (F32) {
-                        k_words(kw[0][0], h, q, 0);
-                        k_words(wl, h, q, 1);
-                        if (h == 1 && q == 3) warp_arrive(&sm.kv_free[bkv]);
-                    }
+                    uint32_t o[4][kParts];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t w = kw[F32 ? 0 : h][F32 ? 0 : q][i];
-                        if (nt < kC) w = t >= nt ? 0u : t + 1 >= nt ? w & 0xffffu : w;
+                        const uint32_t w = kw[0][q][i] & live;
                         float2 x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
                         if constexpr (F32) {
-                            uint32_t l = wl[i];
-                            if (nt < kC) l = t >= nt ? 0u : t + 1 >= nt ? l & 0xffffu : l;
+                            const uint32_t l = kw[1][q][i] & live;
                             x = __fadd2_rn(x, make_float2(__uint_as_float(l << 16), __uint_as_float(l & 0xffff0000u)));
                         }
-                        split2(__fmul2_rn(x, d), o[0][i], o[1][i]);
+                        split(__fmul2_rn(x, d), o[i]);
                     }
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
-                        stsm4(kd + p * kTileBytes + (8 * ic + r) * 128 + ((sb ^ r) * 16), o[p]);
+                        stsm4(kd + p * kTileBytes + (8 * ic + r) * 128 + ((sb ^ r) * 16),
+                              {o[0][p], o[1][p], o[2][p], o[3][p]});
                 }
             }
             tmem_st_wait();
@@ -601,37 +620,37 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             ok = mbar_wait(&sm.sc_full[c & 1], pc, a.err);
             if (!ok) break;
             tc_fence_after();
-            float x[32];
-            tmem_ld16(tl + L::kTSc + pcol, *reinterpret_cast<float(*)[16]>(x));
-            tmem_ld16(tl + L::kTSc + pcol + 16, *reinterpret_cast<float(*)[16]>(x + 16));
-            tmem_ld_wait();
-            tc_fence_before();
-            warp_arrive(&sm.sc_free);
-            if (strong)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= i == last ? 1.0f : expf(g * (float)max(last - i, 0));
-            uint32_t o[4][kParts][4];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 f = *reinterpret_cast<const float2*>(sm.down + pcol + 2 * i);
-                float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), f);
-                // (where s > t not 0 times q k: it is what it is for tokens to come, and another sequence's
-                // behind the end)
-                if (quarter != 1) {
-                    y.x = 2 * i <= last ? y.x : 0.0f;
-                    y.y = 2 * i + 1 <= last ? y.y : 0.0f;
-                }
-                split2(y, o[i >> 2][0][i & 3], o[i >> 2][1][i & 3]);
-            }
             if (c > 0) ok = mbar_wait(&sm.oa_full[(c & 1) ^ 1], (uint32_t)(((c - 1) >> 1) & 1), a.err);
             if (!ok) break;
+#pragma unroll 1
+            for (int b = 0; b < 32; b += 16) {
+                float x[16];
+                tmem_ld16(tl + L::kTSc + pcol + b, x);
+                tmem_ld_wait();
+                if (strong)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+                    for (int i = 0; i < 16; ++i) x[i] *= b + i == last ? 1.0f : expf(g * (float)max(last - b - i, 0));
+                uint32_t o[8][kParts];
 #pragma unroll
-                for (int p = 0; p < kParts; ++p)
-                    *reinterpret_cast<uint4*>(base + L::kPAt + p * kHalf + prow * 128 +
-                                              (((pcol / 8 + q) ^ (prow & 7)) * 16)) =
-                        make_uint4(o[q][p][0], o[q][p][1], o[q][p][2], o[q][p][3]);
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = *reinterpret_cast<const float2*>(sm.down + pcol + b + 2 * i);
+                    float2 y = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), f);
+                    // (where s > t not 0 times q k: it is what it is for tokens to come, and another sequence's
+                    // behind the end)
+                    y.x = quarter == 1 || b + 2 * i <= last ? y.x : 0.0f;
+                    y.y = quarter == 1 || b + 2 * i + 1 <= last ? y.y : 0.0f;
+                    split(y, o[i]);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+                        *reinterpret_cast<uint4*>(base + L::kPAt + p * kHalf + prow * 128 +
+                                                  ((((pcol + b) / 8 + q) ^ (prow & 7)) * 16)) =
+                            make_uint4(o[4 * q][p], o[4 * q + 1][p], o[4 * q + 2][p], o[4 * q + 3][p]);
+            }
+            tc_fence_before();
+            warp_arrive(&sm.sc_free);
             fence_proxy_async_smem();
             warp_arrive(&sm.p_full);
         }
@@ -660,11 +679,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         auto put_state = [&]() {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {        // 8 keys: 4 columns of each part
-                uint32_t w[kParts][4];
+                uint32_t w[4][kParts];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split2(S[4 * b + i], w[0][i], w[1][i]);
+                for (int i = 0; i < 4; ++i) split(S[4 * b + i], w[i]);
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) tmem_st4(tl + L::kTSp + 64 * p + 16 * part + 4 * b, w[p]);
+                for (int p = 0; p < kParts; ++p)
+                    tmem_st4(tl + L::kTSp + 64 * p + 16 * part + 4 * b, {w[0][p], w[1][p], w[2][p], w[3][p]});
             }
             tmem_st_wait();
             tc_fence_before();
@@ -680,7 +700,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         for (int c = 0; c < chunks && ok; ++c, o += kC * step) {
             const uint32_t par = (uint32_t)(c & 1);
             const int nt = min(kC, len - c * kC), live = nt - 16 * part;
-            const uint32_t to = tl + L::o_at(c) + 16 * part;
+            const uint32_t to = tl + L::kTO + 16 * part;
             const float2 f = nt == kC ? whole : decay_pair(g * (float)nt);
             const float2 fa2 = make_float2(f.x, f.x), fd2 = make_float2(f.y, f.y);
             ok = mbar_wait(&sm.u_full, par, a.err);
@@ -728,12 +748,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             ok = mbar_wait(&sm.o_full, par, a.err);      // O is whole, S Q^T has read the parts
             if (!ok) break;
             tc_fence_after();
-            if (c + 1 < chunks) put_state();
-            float x[16];
+            float x[16];                         // (first, so that V^T P^T of the next chunk may start)
             tmem_ld16(to, x);
             tmem_ld_wait();
             tc_fence_before();
-            warp_arrive(&sm.o_free[c % L::kOBufs]);
+            warp_arrive(&sm.o_free);
+            if (c + 1 < chunks) put_state();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 f = up[i];
@@ -822,25 +842,39 @@ __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArg
 constexpr int kSplitThr = 256;
 
 struct SplitPlane {
-    const float* src; uint32_t* hi; uint32_t* lo;
-    long stride; int quads;                      // elements between rows; groups of 4 in a row
+    const float* src; uint2* hi; uint2* lo;
+    long stride; int heads;                      // elements between rows; groups of 128 in a row
 };
 struct SplitArgs {
     SplitPlane p[3];
     long rows;
 };
 
-__global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const SplitArgs a) {
-    const SplitPlane p = a.p[blockIdx.y];
-    const long n = a.rows * p.quads, step = (long)gridDim.x * kSplitThr;
-    for (long i = (long)blockIdx.x * kSplitThr + threadIdx.x; i < n; i += step) {
-        const long row = i / p.quads;
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(p.src + row * p.stride) + (i - row * p.quads));
-        uint2 hi, lo;
-        split2(make_float2(x.x, x.y), hi.x, lo.x);
-        split2(make_float2(x.z, x.w), hi.y, lo.y);
-        reinterpret_cast<uint2*>(p.hi)[i] = hi;
-        reinterpret_cast<uint2*>(p.lo)[i] = lo;
+// A warp takes kSplitAhead heads at a time, their loads ahead of their stores.
+constexpr int kSplitAhead = 4;
+
+__global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const __grid_constant__ SplitArgs a) {
+    const SplitPlane& p = a.p[blockIdx.y];
+    const int lane = threadIdx.x & 31, heads = p.heads;
+    const long n = a.rows * heads, step = (long)gridDim.x * (kSplitThr / 32) * kSplitAhead;
+    for (long i = ((long)blockIdx.x * (kSplitThr / 32) + (threadIdx.x >> 5)) * kSplitAhead; i < n; i += step) {
+        long row = i / heads;
+        int head = (int)(i - row * heads);
+        float4 x[kSplitAhead];
+#pragma unroll
+        for (int u = 0; u < kSplitAhead; ++u) {
+            if (i + u < n) x[u] = __ldcs(reinterpret_cast<const float4*>(p.src + row * p.stride) + head * 32 + lane);
+            if (++head == heads) { head = 0; ++row; }
+        }
+#pragma unroll
+        for (int u = 0; u < kSplitAhead; ++u) {
+            if (i + u >= n) break;
+            uint32_t w[2][2];
+            split(make_float2(x[u].x, x[u].y), w[0]);
+            split(make_float2(x[u].z, x[u].w), w[1]);
+            p.hi[(i + u) * 32 + lane] = make_uint2(w[0][0], w[1][0]);
+            p.lo[(i + u) * 32 + lane] = make_uint2(w[0][1], w[1][1]);
+        }
     }
 }
 
@@ -969,8 +1003,8 @@ cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* wor
         if (!make_tensor_map_2d_bf16_sw128(&to[i][0], at, rows, width[i], kC) ||
             !make_tensor_map_2d_bf16_sw128(&to[i][1], lo, rows, width[i], kC))
             return cudaErrorInvalidValue;
-        sp.p[i] = SplitPlane{static_cast<const float*>(in[i]), reinterpret_cast<uint32_t*>(at),
-                             reinterpret_cast<uint32_t*>(lo), stride[i], (int)(width[i] / 4)};
+        sp.p[i] = SplitPlane{static_cast<const float*>(in[i]), reinterpret_cast<uint2*>(at),
+                             reinterpret_cast<uint2*>(lo), stride[i], (int)(width[i] / kHeadDim)};
         at = lo + (size_t)rows * width[i] * 2;
     }
     const auto states = [&](CUtensorMap* m, const float* base, long seqs) {
@@ -983,7 +1017,7 @@ cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* wor
     if (a.bf16) return launch_all<false>(a, cut, maps, out, s);
     {
         KernelTimer kt(kKLinSplit, s);
-        const long blocks = (rows * width[2] / 4 + kSplitThr - 1) / kSplitThr;
+        const long blocks = (rows * units + kSplitThr / 32 * kSplitAhead - 1) / (kSplitThr / 32 * kSplitAhead);
         kda_linattn_split_kernel<<<dim3((unsigned)std::min(blocks, 152L * 8), 3), kSplitThr, 0, s>>>(sp);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
