@@ -106,7 +106,6 @@ struct __align__(16) Tail {
     uint32_t tmem;
     int bad[kHeadDim];                           // by value: the first token whose v is no number
 };
-constexpr int kAhead = 4;                        // chunks that are on their way into L2 or further
 constexpr int kMaxRanked = 32;                   // packed sequences that are taken longest first
 template <bool F32>
 constexpr int smem_bytes() { return 1024 + Lay<F32>::kTailAt + (int)sizeof(Tail); }
@@ -186,11 +185,13 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  : "memory");
 }
 
-// How the sequences are cut: segments of seg_chunks chunks, at most segs of one sequence; parts: [N][segs - 1]
-// [units][128][128] f32, first the segments' contributions to the state, then the states after them.
+// How the sequences are cut: segments of seg_chunks chunks, at most segs of one sequence, each in subs pieces for the
+// STATE launch; parts: [N][(segs - 1) subs][units][128][128] f32, first the pieces' contributions to the state, then
+// the states after them.
 struct Cut {
-    int seg_chunks, segs;
+    int seg_chunks, segs, subs;
     float* parts;
+    __host__ __device__ int pieces() const { return (segs - 1) * subs; }
 };
 
 // Tensor maps: q, k, v (hi and lo of f32); the states as rows of 128 keys, one a value: state_in, the parts, and where they go
@@ -199,9 +200,9 @@ struct Maps {
     CUtensorMap q[2], k[2], v[2], in, parts, out;
 };
 
-// the first unit's state of a segment among the parts
-__device__ __forceinline__ long seg_state(const Cut& cut, int n, int seg, int units) {
-    return ((long)n * (cut.segs - 1) + seg) * units;
+// the first unit's state of a piece among the parts
+__device__ __forceinline__ long piece_state(const Cut& cut, int n, int piece, int units) {
+    return ((long)n * cut.pieces() + piece) * units;
 }
 
 // a + b is e^x: a step S <- e^x S + U is S <- a S + (b S + U).  Above a half a = 1 and b = e^x - 1, which
@@ -243,9 +244,9 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         begin = (long)n * a.seq.T_uniform;
         len = a.seq.T_uniform;
     }
-    const int seg_len = cut.seg_chunks * kC;
+    const int whole_len = cut.seg_chunks * kC, seg_len = STATE ? whole_len / cut.subs : whole_len;
     if (seg > 0 && seg * (long)seg_len >= len) return;       // (the whole CTA)
-    if (STATE && (seg + 1) * (long)seg_len >= len) return;   // nothing follows this segment
+    if (STATE && (seg / cut.subs + 1) * (long)whole_len >= len) return;   // nothing follows this piece's segment
     const bool ends = (seg + 1) * (long)seg_len >= len;
     begin += (long)seg * seg_len;
     len = min(len - seg * seg_len, seg_len);
@@ -282,12 +283,16 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 tma_load_2d(s + p * kTileBytes + h * kHalf, &maps.q[p], hk * kHeadDim + 64 * h,
                             (int)(begin + (long)c * kC), bar);
     };
-    const auto prefetch = [&](int c) {           // into L2
+    // Into L2: what chunk c has no stage for yet.  (Further ahead it only pushed other CTAs' out: 4 chunks cost 1% at
+    // bf16, 6% at f32.)
+    const auto prefetch = [&](int c) {
         const int row = (int)(begin + (long)c * kC);
         for (int p = 0; p < L::kIn; ++p)
             for (int h = 0; h < 2; ++h) {
-                tma_prefetch_2d(&maps.k[p], hk * kHeadDim + 64 * h, row);
-                tma_prefetch_2d(&maps.v[p], unit * kHeadDim + 64 * h, row);
+                if (F32) {
+                    tma_prefetch_2d(&maps.k[p], hk * kHeadDim + 64 * h, row);
+                    tma_prefetch_2d(&maps.v[p], unit * kHeadDim + 64 * h, row);
+                }
                 if (!STATE) tma_prefetch_2d(&maps.q[p], hk * kHeadDim + 64 * h, row);
             }
     };
@@ -319,7 +324,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             for (int i = 0; i < 4; ++i) mbar_init(&sm.st_out[i], 4);
             fence_mbar_init();
             if (starts) {
-                const long st = seg > 0 ? seg_state(cut, n, seg - 1, units) : (long)n * units;
+                const long st = seg > 0 ? piece_state(cut, n, seg * cut.subs - 1, units) : (long)n * units;
                 mbar_arrive_expect_tx(&sm.st_full, 4 * kStTile);
                 for (int i = 0; i < 4; ++i)
                     tma_load_2d(base + L::kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
@@ -327,7 +332,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             }
             for (int c = 0; c < L::kKvStages && c < chunks; ++c) load_kv(c);
             for (int c = 0; !STATE && c < L::kQStages && c < chunks; ++c) load_q(c);
-            for (int c = L::kKvStages; c < kAhead && c < chunks; ++c) prefetch(c);
+            if (chunks > L::kKvStages) prefetch(L::kKvStages);
         }
         __syncwarp();
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
@@ -362,8 +367,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             ok = mbar_wait(&sm.kv_free[was % L::kKvBars], (uint32_t)((was / L::kKvBars) & 1), a.err);
             if (ok && elect_one()) {
                 load_kv(c);
-                const int ahead = c - L::kKvStages + kAhead;
-                if (ahead < chunks) prefetch(ahead);
+                if (c + 1 < chunks) prefetch(c + 1);
             }
             __syncwarp();
             if (STATE || c < L::kQStages) continue;
@@ -550,7 +554,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             };
             const __nv_bfloat162 zero2 = __floats2bfloat162_rn(0.0f, 0.0f);
             __nv_bfloat162 odd[2] = {zero2, zero2};          // 0 times v, summed: 0 unless one is no number
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 4 * L::kIn; ++h) {
                 uint32_t w[8];
                 v_words(w, h);
@@ -629,7 +633,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 tmem_ld_wait();
                 if (strong)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] *= b + i == last ? 1.0f : expf(g * (float)max(last - b - i, 0));
+                    for (int i = 0; i < 16; ++i) x[i] *= sm.pw[max(last - b - i, 0)];
                 uint32_t o[8][kParts];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -788,7 +792,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             fence_proxy_async_smem();
             warp_arrive(&sm.st_out[part]);       // one of the tile's four warps
             if ((warp & 3) == 0 && mbar_wait(&sm.st_out[part], 0, a.err) && elect_one()) {
-                const long st = STATE ? seg_state(cut, n, seg, units) : (long)n * units;
+                const long st = STATE ? piece_state(cut, n, seg, units) : (long)n * units;
                 tma_store_2d(&maps.out, base + L::kKdAt + part * kStTile, 32 * part, (int)(st + unit) * kHeadDim);
                 bulk_commit();
                 bulk_wait_read0();
@@ -803,7 +807,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
     }
 }
 
-// The contributions of a sequence's segments into the states after them, in place; a thread owns four elements
+// The contributions of a sequence's pieces into the states after them, in place; a thread owns four elements
 // of a unit's state.
 constexpr int kJoinThr = 256;
 constexpr int kJoinAhead = 4;
@@ -815,10 +819,10 @@ __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArg
     const int unit = (int)(piece / kPieces);
     const int len = a.seq.cu_seqlens ? a.seq.cu_seqlens[n + 1] - a.seq.cu_seqlens[n] : a.seq.T_uniform;
     const int seg_len = cut.seg_chunks * kC;
-    const int parts = (len + seg_len - 1) / seg_len - 1;      // the last segment's is not formed
-    const float2 f = decay_pair(a.log_decay[unit / a.m] * (float)seg_len);
+    const int parts = ((len + seg_len - 1) / seg_len - 1) * cut.subs;      // the last segment's are not formed
+    const float2 f = decay_pair(a.log_decay[unit / a.m] * (float)(seg_len / cut.subs));
     const long stride = (long)units * kPieces;
-    float4* at = reinterpret_cast<float4*>(cut.parts) + seg_state(cut, n, 0, units) * kPieces + piece;
+    float4* at = reinterpret_cast<float4*>(cut.parts) + piece_state(cut, n, 0, units) * kPieces + piece;
     float4 S = a.state_in ? __ldg(reinterpret_cast<const float4*>(a.state_in) + (long)n * stride + piece)
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int p = 0; p < parts; p += kJoinAhead) {
@@ -878,9 +882,9 @@ __global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const __gr
     }
 }
 
-// Segments of a call, by the time of their waves of CTAs in us: a chunk of the main kernel 2.05 (f32: TODO), of the state
-// kernel 0.8, a CTA's start and end 4, the two further launches 7.  (4096 tokens x 64 heads: whole 129 us,
-// 2 segments 110; 8192 x 8 heads: whole 234, 16 segments 46.)
+// Segments of a call and their pieces, by the time of their waves of CTAs in us: a chunk of the main kernel 2.3 (f32:
+// 3.4), of the state kernel 1.1 (f32: 1.9), a CTA's start and end 6, the two further launches 7.  (bf16, 4096 tokens
+// x 64 heads: whole 145 us, 2 segments 127; 8192 x 8 heads: whole 276, 16 segments 50.)
 constexpr int kMaxSegs = 32;
 long most_segs(long chains, long chunks, int sms) {
     return std::max(1L, std::min({(long)kMaxSegs, chunks, 4L * sms / std::max(1L, chains)}));
@@ -902,30 +906,33 @@ long seq_chunks(const SeqLayout& s, const int* cu_host, int n) {
 // Chains of (sequence, unit) that are cut at all: with two on each SM they fill it.
 bool may_cut(long chains, int sms) { return chains < 2L * sms; }
 
-Cut plan(const SeqLayout& s, const int* cu_host, int units) {
+Cut plan(const SeqLayout& s, const int* cu_host, int units, bool bf16) {
+    const double main_us = bf16 ? 2.3 : 3.4, state_us = bf16 ? 1.1 : 1.9, ends_us = 6.0, launches_us = 7.0;
     const int sms = sm_count();
     long most = 1;
     for (int n = 0; n < s.N; ++n) most = std::max(most, seq_chunks(s, cu_host, n));
-    Cut best{(int)most, 1, nullptr};
+    Cut best{(int)most, 1, 1, nullptr};
     if (!may_cut((long)s.N * units, sms)) return best;
     double least = 0.0;
-    for (long segs = 1; segs <= most_segs((long)s.N * units, most, sms); ++segs) {
-        const long per = (most + segs - 1) / segs;
-        if (segs > 1 && (most + per - 1) / per != segs) continue;
-        long blocks = 0, cut_seqs = 0;
-        for (int n = 0; n < s.N; ++n) {
-            const long k = (seq_chunks(s, cu_host, n) + per - 1) / per;
-            blocks += k;
-            cut_seqs += k > 0;
-        }
-        const auto waves = [&](long b) { return (double)((b * units + sms - 1) / sms); };
-        const double cost = waves(blocks) * (per * 2.05 + 4.0) +
-                            (segs > 1 ? waves(blocks - cut_seqs) * (per * 0.8 + 4.0) + 7.0 : 0.0);
-        if (segs == 1 || cost < least) {
+    const long limit = most_segs((long)s.N * units, most, sms);
+    for (long segs = 1; segs <= limit; ++segs)
+        for (long subs = 1; segs * subs <= limit && (segs > 1 || subs == 1); ++subs) {
+            const long per = ((most + segs - 1) / segs + subs - 1) / subs * subs;
+            if (segs > 1 && (most + per - 1) / per != segs) continue;
+            long blocks = 0, cut_seqs = 0;
+            for (int n = 0; n < s.N; ++n) {
+                const long k = (seq_chunks(s, cu_host, n) + per - 1) / per;
+                blocks += k;
+                cut_seqs += k > 0;
+            }
+            const auto waves = [&](long b) { return (double)((b * units + sms - 1) / sms); };
+            const double cost = waves(blocks) * (per * main_us + ends_us) +
+                                (segs > 1 ? waves((blocks - cut_seqs) * subs) * (per / subs * state_us + ends_us) +
+                                                launches_us : 0.0);
+            if (segs > 1 && cost >= least) continue;
             least = cost;
-            best = Cut{(int)per, (int)segs, nullptr};
+            best = Cut{(int)per, (int)segs, (int)subs, nullptr};
         }
-    }
     return best;
 }
 
@@ -936,7 +943,7 @@ cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, cudaStrea
     if (e != cudaSuccess) return e;
     KernelTimer kt(STATE ? kKLinState : kKLinChunk, s);
     kda_linattn_chunk_kernel<STATE, F32>
-        <<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(cut.segs - STATE)), kThr, smem_bytes<F32>(), s>>>(
+        <<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(STATE ? cut.pieces() : cut.segs)), kThr, smem_bytes<F32>(), s>>>(
             a, cut, maps);
     return cudaGetLastError();
 }
@@ -967,7 +974,7 @@ size_t split_bytes(long rows, int Hk, int units, bool bf16) {
 // The workspace: q, k and v split (f32), then the segments' states.
 size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int Hk, int units, bool bf16) {
     return split_bytes(seq.total_rows, Hk, units, bf16) +
-           (size_t)seq.N * (plan(seq, cu_host, units).segs - 1) * units * kHeadDim * kHeadDim * sizeof(float);
+           (size_t)seq.N * plan(seq, cu_host, units, bf16).pieces() * units * kHeadDim * kHeadDim * sizeof(float);
 }
 
 // (more than any cut of total_T tokens into N sequences takes: the cut of the longest possible one)
@@ -985,7 +992,7 @@ cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* wor
     const long rows = a.seq.total_rows, width[3] = {(long)a.Hk * kHeadDim, (long)a.Hk * kHeadDim, (long)units * kHeadDim};
     const void* const in[3] = {a.q, a.k, a.v};
     const long stride[3] = {a.q_stride, a.k_stride, a.v_stride};
-    Cut cut = plan(a.seq, cu_host, units);
+    Cut cut = plan(a.seq, cu_host, units, a.bf16);
     cut.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + split_bytes(rows, a.Hk, units, a.bf16));
     Maps maps;
     std::memset(&maps, 0, sizeof(maps));
@@ -1012,7 +1019,7 @@ cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* wor
     };
     CUtensorMap out;
     if ((a.state_in != nullptr && !states(&maps.in, a.state_in, a.seq.N)) || !states(&out, a.state_out, a.seq.N) ||
-        (cut.segs > 1 && !states(&maps.parts, cut.parts, (long)a.seq.N * (cut.segs - 1))))
+        (cut.segs > 1 && !states(&maps.parts, cut.parts, (long)a.seq.N * cut.pieces())))
         return cudaErrorInvalidValue;
     if (a.bf16) return launch_all<false>(a, cut, maps, out, s);
     {

@@ -3,9 +3,8 @@ pool of states, against the recurrence in 64 bits.
 
 Tolerance.  Relative to the same sums of magnitudes, an output of the recurrent form carries at most 3
 roundings a token still remembered, 16 + 8 in the readout's sum and a few for the scale; the chunked
-form of bf16 at most one split to 17 bits (2^-17 = 64 * 2^-23) where its 60 or so accumulation steps, which
-the tensor cores may truncate (2^-23 each), and the split are not at their largest together.  With at most
-16 / 24 bits' worth remembered below, 64 * 2^-23 + 3 * min(T, 1 / (1 - lambda)) * 2^-24 covers both;
+form of bf16 60 or so accumulation steps, which the tensor cores may truncate (2^-23 each), and splits to
+24 bits.  64 * 2^-23 + 3 * min(T, 1 / (1 - lambda)) * 2^-24 covers both;
 log_decay enters e^(g n) with n g rounded, an error of x 2^-24 e^-x <= 2^-25 more.
 The chunked form of f32 (32 tokens and more) splits q, k and v themselves: on the way through the state k,
 its decayed form, v, the state and q are each off by 2^-17, and the two products leave out lo * lo, at most
@@ -244,6 +243,33 @@ def test_few_long_prompts(lengths, H, kind, dtype):
         (o, last), (om, lm) = ref.both(q[b:e], k[b:e], v[b:e], g, S[n], H, H, D, D ** -0.5)
         _close(out["o"][b:e], o, om, _tol(L, g, dtype, max(lengths)), ("o", n))
         _close(out["state_out"][n], last, lm, _tol(L, g, dtype, max(lengths)), ("state", n))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lengths,H,kind", [([1700], 52, "mixed"), ([1300, 1700, 0], 26, "none"),
+                                            ([2111], 60, "strong")])
+def test_many_heads_long_prompts(lengths, H, kind, dtype):
+    """Heads enough for few segments, whose states are then formed in pieces; of the heads, which are
+    independent, some are looked at."""
+    from gated_delta_rule_scan_gb300 import kda, mixer
+    rows, N = sum(lengths), len(lengths)
+    (q, k, v), (dq, dk, dv) = _inputs(rows, H, H, D, dtype, 31)
+    g = _decays(H, kind)
+    S = torch.randn(N, H, D, D, generator=torch.Generator().manual_seed(6))
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32)
+    out = mixer.kda_linattn_prefill(q=dq, k=dk, v=dv, log_decay=g.cuda(), H=H, state_in=S.cuda(),
+                                    cu_seqlens=cu.cuda(), cu_seqlens_host=cu)
+    torch.cuda.synchronize()
+    assert kda.kda_device_status() == 0
+    some = [0, H // 2, H - 1]
+    pick = lambda x: x.reshape(rows, H, D)[:, some].reshape(rows, -1)
+    for n in range(N):
+        b, e = int(cu[n]), int(cu[n + 1])
+        (o, last), (om, lm) = ref.both(pick(q)[b:e], pick(k)[b:e], pick(v)[b:e], g[some], S[n, some], 3, 3,
+                                       D, D ** -0.5)
+        tol = _tol(e - b, g[some], dtype, max(lengths))
+        _close(pick(out["o"].cpu())[b:e], o, om, tol, ("o", n))
+        _close(out["state_out"][n, some], last, lm, tol, ("state", n))
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
