@@ -5,13 +5,15 @@
 //
 // The work is the one row (two with the draft's) that a sequence draws from; everything before it is a
 // few dependent reads.  A cluster of CTAs shares a sequence's row, so that one user's 131072 weights
-// are read by 8 SMs.  The row is read once: each warp sums tiles of 1024 weights, the tile sums give
+// are read by 8 SMs.  The row is read once: each warp sums tiles of 512 weights, the tile sums give
 // the tile that holds the drawn index, and only that tile is read again (from L2).
 //
 // Which index is drawn must not hang on the order of summation: next to a border an f32 running sum
 // over a flat row is off by several indices.  All sums are of f32 pairs (a value and what its rounding left,
 // the exact error of p - q among it), about 2^-45 of the sum.  (f64 has the same bits, but its additions took
 // some 600 cycles each here: 10 us of a call's 12.)
+// Measured, vocabulary 131072: one sequence 10.3 us in a stream of calls (three dependent reads, a reduction over
+// the cluster, a tile's read), 64 sequences x 4 drafts 22.5 us, 2.6 TB/s.
 #include "kda_device.cuh"
 
 namespace kda {
@@ -206,9 +208,14 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
         if (lane < count) {
             tok = a.tokens[(long)n * drafts + lane];
             if (tok >= 0 && tok < a.V) {
-                const float p = load_raw<BF16>(target + (size_t)lane * a.target_stride * kElem, tok);
-                const float q = draft ? load_raw<BF16>(draft + (size_t)lane * a.draft_stride * kElem, tok) : 1.0f;
-                // u q < p exactly: where the rounded product equals p its error decides
+                float p = load_raw<BF16>(target + (size_t)lane * a.target_stride * kElem, tok);
+                float q = draft ? load_raw<BF16>(draft + (size_t)lane * a.draft_stride * kElem, tok) : 1.0f;
+                // u q < p exactly: where the rounded product equals p its error decides (small ones are taken
+                // times 2^100, or that error would be lost among denormals)
+                if (fmaxf(p, q) < 0x1p-60f) {
+                    p *= 0x1p100f;
+                    q *= 0x1p100f;
+                }
                 const float u = a.u[(long)n * drafts + lane], x = __fmul_rn(u, q);
                 good = x < p || (x == p && fmaf(u, q, -x) < 0.0f);
             }
@@ -279,11 +286,19 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
         row.skip = -1;
         row.q_vec = true;
     }
-    // r in [0, 1): the whole sum is passed at the last weight at the latest
-    const Pair aim = fminf(fmaxf(r, 0.0f), 0x1.fffffep-1f) * sum;
+    // r in [0, 1): the whole sum is passed at the last weight at the latest.  (Small sums, exact among denormals, are
+    // compared times 2^100: r times them is not.)
+    const float up = sum.hi < 0x1p-60f ? 0x1p100f : 1.0f;
+    const auto scaled = [&](Pair x) {
+        x.hi *= up;
+        x.lo *= up;
+        return x;
+    };
+    const Pair aim = fminf(fmaxf(r, 0.0f), 0x1.fffffep-1f) * scaled(sum);
+    const auto passes = [&](const Pair& x) { return scaled(x) > aim; };
     if (!(sum.hi > 0.0f)) {
         if (rank == 0 && tid == 0) a.out_tokens[(long)n * a.T + taken] = -1;
-    } else if (!(before > aim) && mine > aim && warp == 0) {
+    } else if (!passes(before) && passes(mine) && warp == 0) {
         // the span, the tile, the lane's 16 weights and the one of them at which the running sum passes aim.
         // (Where rounding between two ways of summing leaves aim past a piece, its last part is taken.)
         Pair run = before, below;
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
         for (;; sp += 32) {
             const Pair x = sp + lane < spans ? tiles[sp + lane] : Pair();
             const Pair upto = run + warp_scan(x, lane, below);
-            const unsigned past = __ballot_sync(0xffffffffu, upto > aim);
+            const unsigned past = __ballot_sync(0xffffffffu, passes(upto));
             const bool done = past != 0 || sp + 32 >= spans;
             const int at = past != 0 ? __ffs(past) - 1 : done ? spans - 1 - sp : 31;
             const Pair at_below = run + shfl(below, at);
@@ -305,20 +320,20 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
         const long t_end = min(tile1, t + group);
         for (; t < t_end - 1; ++t) {
             const Pair x = run + warp_pair_sum(lane_sum<BF16>(row, t * kTileElems - row.lead, a.V, lane, false));
-            if (x > aim) break;
+            if (passes(x)) break;
             run = x;
         }
         const long b = t * kTileElems - row.lead;
         const Pair of_lane = lane_sum<BF16>(row, b, a.V, lane, true).whole();
         const Pair upto = run + warp_scan(of_lane, lane, below);
-        unsigned past = __ballot_sync(0xffffffffu, upto > aim);
+        unsigned past = __ballot_sync(0xffffffffu, passes(upto));
         const unsigned any = __ballot_sync(0xffffffffu, of_lane.hi > 0.0f);
         const int pick_lane = past != 0 ? __ffs(past) - 1 : any != 0 ? 31 - __clz(any) : 31;
         run = run + shfl(below, pick_lane);
         Pair w;
         weight_at<BF16>(row, lane < kPerLane ? b + kPerLane * pick_lane + lane : -1, a.V, w.hi, w.lo);
         const Pair at_lane = run + warp_scan(w, lane, below);        // (every lane takes part)
-        past = __ballot_sync(0xffffffffu, w.hi > 0.0f && at_lane > aim);
+        past = __ballot_sync(0xffffffffu, w.hi > 0.0f && passes(at_lane));
         const unsigned on = __ballot_sync(0xffffffffu, w.hi > 0.0f);
         const int at = past != 0 ? __ffs(past) - 1 : on != 0 ? 31 - __clz(on) : 0;
         if (lane == 0) a.out_tokens[(long)n * a.T + taken] = (int)(b + kPerLane * pick_lane + at);

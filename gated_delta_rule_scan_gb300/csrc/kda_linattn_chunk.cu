@@ -1,5 +1,5 @@
-// kda_linattn_chunk.cu -- linear attention with one log-decay g a head, the chunked form for bf16
-// prompts, on the tcgen05 tensor cores.
+// kda_linattn_chunk.cu -- linear attention with one log-decay g a head, the chunked form for prompts, on the
+// tcgen05 tensor cores.
 //
 // Mathematics.  Over a chunk of C = 64 tokens with incoming state S (stored [value j][key i]):
 //     O^T = scale * ( V^T P^T + e^{g (t+1)} S Q^T ),   P[t][s] = e^{g (t-s)} q_t . k_s  for s <= t,
@@ -10,10 +10,11 @@
 // e^{32 |g|}, 8e13 at |g| = 1.  Heads that decay faster (g < -1) take the parts one after the other, with
 // the powers as they stand, all of them at most 1, and a slower pipeline: there S Q^T matters to a few tens
 // of tokens at most, but overflow must not.
-// q, k and v enter as the bf16 values they are; what is f32 (P, Kd and the state) enters as bf16 hi + lo,
-// within 2^-17 of an element, as x does in the bf16 projections: outputs and states come within about 1e-6
-// of their scale.  (A third part brought 1e-7 for half as much again in MMAs and splitting, 166 against
-// TODO us at 4096 tokens x 64 heads.)  The state itself stays in f32 registers.
+// bf16 q, k and v enter as they are; what is f32 (P, Kd and the state) enters as three bf16 parts, 24 bits of
+// it: errors of 6e-7 (two parts: 3e-6).  f32 q, k and v are
+// split into bf16 hi + lo, within 2^-17, by a launch before, and so are P, Kd and the state, every product three of
+// four terms: errors of 7e-6.  (Three parts of all six do not fit tensor memory.)  The state itself stays in f32
+// registers.
 //
 // A NaN or an infinity at one token does not reach the tokens before it: where q k is not seen P is 0 by
 // selection, and in v, whose products with P = 0 would be NaN, it is replaced by 0 and its value column made
@@ -24,18 +25,26 @@
 // operands lie in tensor memory: the state parts, written by the threads that hold the state rows, and
 // v, transposed on the way (from shared memory as an MN-major operand it cost twice its bytes: U 140
 // cycles an MMA against 64).  B operands are q's tile as TMA brings it, P, and Kd transposed to
-// [key][token] while it is formed.  The 512 TMEM columns are full: S parts 2 x 64, V^T Kd 128, the
-// outputs 64, q k 64, v 2 x 32.
+// [key][token] while it is formed.  The 512 TMEM columns are full: S parts 3 x 64, V^T Kd 128, the
+// outputs 64, q k 64, v 2 x 32 (f32: S 2 x 64, v 2 x 64).
 // 64 tokens, not 128: the parts of P and Kd then fit beside two stages of q, k, v.
 // Warps have roles: 16 hold the state (32 f32 a thread) and write o, 8 turn k into Kd and q k into P (4 of
-// them a chunk, in turn), three issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads, the MMAs and the groups'
-// register work overlap across chunks.  (One issuing warp took 50 to 100 cycles an MMA beside six busy
-// warps on its scheduler, twice the tensor pipe's time.)
+// them a chunk, in turn), three issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads,
+// the MMAs and the groups' register work overlap across chunks.  (One issuing warp took 50 to 100 cycles an
+// MMA beside six busy warps on its scheduler, twice the tensor pipe's time.)
+// The roles' loops run at once, so their code has to share the instruction caches: unrolled, every fourth
+// stall was for an instruction, the worse the more SMs were busy (152 heads x 4096 tokens: 210 us; with the
+// loops over terms, halves and columns rolled up 164).
+//
+// Measured: 152 heads x 4096 tokens (a CTA an SM) 164 us, 4.9 TB/s of what it reads and writes; 16 ragged
+// prompts, 64 heads, 73722 tokens: 1222 us, 5.1 TB/s, 75% of a copy's rate.  Issue slots are 64% taken, the
+// tensor pipe 56%: a chunk takes 2.3 to 2.5 us where the MMAs take 1.3, bound by the round from o to the state's
+// parts to S Q^T and by the split's instructions in it.
 //
 // Few sequences and heads leave SMs idle, so long sequences are then cut into segments: a first launch
-// (STATE) forms each segment's own contribution to the state from k and v alone, a second adds them up to
-// the state that each segment starts from, and the third is the kernel above with a CTA a segment.  The cut is
-// chosen by a cost model (plan()).
+// (STATE) forms each segment's own contribution to the state from k and v alone, in pieces where that leaves SMs
+// idle, a second adds them up to the state that each segment starts from, and the third is the kernel above with
+// a CTA a segment.  The cut is chosen by a cost model (plan()).
 #include "kda_tc.cuh"
 
 #include <algorithm>
@@ -194,8 +203,8 @@ struct Cut {
     __host__ __device__ int pieces() const { return (segs - 1) * subs; }
 };
 
-// Tensor maps: q, k, v (hi and lo of f32); the states as rows of 128 keys, one a value: state_in, the parts, and where they go
-// (the parts in the STATE launch, else state_out).
+// Tensor maps: q, k, v (hi and lo of f32); the states as rows of 128 keys, one a value: state_in, the parts, and
+// where they go (the parts in the STATE launch, else state_out).
 struct Maps {
     CUtensorMap q[2], k[2], v[2], in, parts, out;
 };
@@ -339,7 +348,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         for (int i = lane; i <= kC + kMid; i += 32) sm.pw[i] = i == 0 ? 1.0f : expf(g * (float)i);
         for (int i = lane; i < kC; i += 32) {
             sm.down[i] = strong || i == kMid - 1 ? 1.0f : expf(g * (float)(kMid - 1 - i));
-            sm.up[i] = a.scale * (strong ? expf(g * (float)(i + 1)) : i == kMid - 1 ? 1.0f : expf(g * (float)(i - kMid + 1)));
+            const int n = strong ? i + 1 : i - kMid + 1;
+            sm.up[i] = a.scale * (n == 0 ? 1.0f : expf(g * (float)n));
         }
     }
     if (warp >= kConvWarp0 && warp < kConvWarp0 + 4) sm.bad[32 * (warp - kConvWarp0) + lane] = 0x7fffffff;
@@ -563,7 +573,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 for (int i = 0; i < 8; ++i)
                     odd[i & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(w + i), zero2, odd[i & 1]);
             }
-            const uint32_t odd_bits = *reinterpret_cast<const uint32_t*>(odd) | *reinterpret_cast<const uint32_t*>(odd + 1);
+            const uint32_t odd_bits =
+                *reinterpret_cast<const uint32_t*>(odd) | *reinterpret_cast<const uint32_t*>(odd + 1);
             if (__any_sync(0xffffffffu, (odd_bits & 0x7fff7fffu) != 0)) {
 #pragma unroll 1
                 for (int h = 0; h < 4 * L::kIn; ++h) {
@@ -942,9 +953,8 @@ cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, cudaStrea
     const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE, F32>, smem_bytes<F32>(), done);
     if (e != cudaSuccess) return e;
     KernelTimer kt(STATE ? kKLinState : kKLinChunk, s);
-    kda_linattn_chunk_kernel<STATE, F32>
-        <<<dim3((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(STATE ? cut.pieces() : cut.segs)), kThr, smem_bytes<F32>(), s>>>(
-            a, cut, maps);
+    const dim3 grid((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(STATE ? cut.pieces() : cut.segs));
+    kda_linattn_chunk_kernel<STATE, F32><<<grid, kThr, smem_bytes<F32>(), s>>>(a, cut, maps);
     return cudaGetLastError();
 }
 
@@ -989,11 +999,12 @@ size_t linattn_chunk_workspace_bound(int N, long total_T, int Hk, int units, boo
 
 cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s) {
     const int units = a.H * a.m;
-    const long rows = a.seq.total_rows, width[3] = {(long)a.Hk * kHeadDim, (long)a.Hk * kHeadDim, (long)units * kHeadDim};
+    const long rows = a.seq.total_rows, qk = (long)a.Hk * kHeadDim, width[3] = {qk, qk, (long)units * kHeadDim};
     const void* const in[3] = {a.q, a.k, a.v};
     const long stride[3] = {a.q_stride, a.k_stride, a.v_stride};
     Cut cut = plan(a.seq, cu_host, units, a.bf16);
-    cut.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + split_bytes(rows, a.Hk, units, a.bf16));
+    cut.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                         split_bytes(rows, a.Hk, units, a.bf16));
     Maps maps;
     std::memset(&maps, 0, sizeof(maps));
     CUtensorMap* const to[3] = {maps.q, maps.k, maps.v};

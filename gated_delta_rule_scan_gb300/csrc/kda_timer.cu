@@ -49,7 +49,9 @@ const char* const kNames[kKernelCount] = {
     "kda_proj_split_kernel",  "kda_proj6_kernel",       "kda_state_store_q8_kernel",
     "kda_state_load_q8_kernel", "kda_decode_q8_kernel", "kda_ring_roll_q8_kernel",
     "kda_proj_w4_kernel",     "kda_proj_w4_split_kernel", "kda_proj_w4_wide_kernel",
-    "kda_linattn_step_kernel", "kda_linattn_split_kernel",  "kda_linattn_state_kernel", "kda_linattn_join_kernel",  "kda_linattn_chunk_kernel", "kda_draft_accept_kernel", "kda_residual_rmsnorm_kernel"};
+    "kda_linattn_step_kernel", "kda_linattn_split_kernel", "kda_linattn_state_kernel",
+    "kda_linattn_join_kernel", "kda_linattn_chunk_kernel", "kda_draft_accept_kernel",
+    "kda_residual_rmsnorm_kernel"};
 
 }  // namespace
 

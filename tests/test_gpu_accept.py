@@ -118,6 +118,28 @@ def test_edges():
     assert got[1][4, 0] == -1 and got[0][4] == 1
 
 
+def test_denormal_probabilities():
+    """Weights of a few times 2^-149: r times their sum may round to the sum, u q to p."""
+    tiny = 2.0 ** -149
+    V, cases = 9, [[1], [1, 1], [0, 3, 2], [5, 0, 0, 1], [0, 0, 0, 0, 0, 0, 0, 0, 1]]
+    N = 4 * len(cases)
+    target = torch.zeros(N, 2, V)
+    for i in range(N):
+        row = cases[i // 4]
+        target[i, :, :len(row)] = torch.tensor(row, dtype=torch.float64).mul(tiny).float()
+    r = torch.tensor([1 - 2.0 ** -24, 0.6, 0.4, 0.0]).repeat(len(cases))
+    empty = torch.zeros(N, 0)
+    want = plain(target[:, :1], empty.int(), empty, r, None, None)
+    got = _run(target[:, :1].contiguous(), empty.int(), empty, r, None)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    draft = target[:, :1].clone()
+    tokens = torch.tensor([row.index(max(row)) for row in cases], dtype=torch.int32).repeat_interleave(4)[:, None]
+    u = torch.tensor([1 - 2.0 ** -24, 0.9, 0.5, 0.0]).repeat(len(cases))[:, None]
+    want = plain(target, tokens, u, r, draft, None)
+    got = _run(target, tokens, u, r, draft)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_rows_of_a_padded_vocabulary():
     """target and draft as slices of wider rows."""
     N, T, V, W = 3, 4, 1500, 1537
