@@ -305,6 +305,13 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 if (!STATE) tma_prefetch_2d(&maps.q[p], hk * kHeadDim + 64 * h, row);
             }
     };
+    const auto first_loads = [&]() {
+        for (int c = 0; c < L::kKvStages && c < chunks; ++c) load_kv(c);
+        for (int c = 0; !STATE && c < L::kQStages && c < chunks; ++c) load_q(c);
+        if (chunks > L::kKvStages) prefetch(L::kKvStages);
+    };
+    // the next launch may be set up meanwhile; it waits for the end of this one before it reads what this one writes
+    if (STATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kTmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < 2; ++i) {
@@ -332,16 +339,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             mbar_init(&sm.st_free, kStateWarps);
             for (int i = 0; i < 4; ++i) mbar_init(&sm.st_out[i], 4);
             fence_mbar_init();
-            if (starts) {
-                const long st = seg > 0 ? piece_state(cut, n, seg * cut.subs - 1, units) : (long)n * units;
-                mbar_arrive_expect_tx(&sm.st_full, 4 * kStTile);
-                for (int i = 0; i < 4; ++i)
-                    tma_load_2d(base + L::kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
-                                (int)(st + unit) * kHeadDim, &sm.st_full);
-            }
-            for (int c = 0; c < L::kKvStages && c < chunks; ++c) load_kv(c);
-            for (int c = 0; !STATE && c < L::kQStages && c < chunks; ++c) load_q(c);
-            if (chunks > L::kKvStages) prefetch(L::kKvStages);
+            if (!F32) first_loads();
         }
         __syncwarp();
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
@@ -351,6 +349,19 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             const int n = strong ? i + 1 : i - kMid + 1;
             sm.up[i] = a.scale * (n == 0 ? 1.0f : expf(g * (float)n));
         }
+        if (lane == 0) {
+            // the launch before has written these: f32 q, k and v split, the state that a segment starts from
+            if (F32 || seg > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (F32) first_loads();
+            if (starts) {
+                const long st = seg > 0 ? piece_state(cut, n, seg * cut.subs - 1, units) : (long)n * units;
+                mbar_arrive_expect_tx(&sm.st_full, 4 * kStTile);
+                for (int i = 0; i < 4; ++i)
+                    tma_load_2d(base + L::kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
+                                (int)(st + unit) * kHeadDim, &sm.st_full);
+            }
+        }
+        __syncwarp();
     }
     if (warp >= kConvWarp0 && warp < kConvWarp0 + 4) sm.bad[32 * (warp - kConvWarp0) + lane] = 0x7fffffff;
     if (warp == kConvWarp0) {                    // t < 32 <= s: P is 0 there, once and for all
@@ -825,12 +836,15 @@ constexpr int kJoinAhead = 4;
 
 __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArgs a, const Cut cut) {
     constexpr int kPieces = kHeadDim * kHeadDim / 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int units = a.H * a.m, n = blockIdx.y;
     const long piece = (long)blockIdx.x * kJoinThr + threadIdx.x;     // kPieces is a multiple of kJoinThr
     const int unit = (int)(piece / kPieces);
     const int len = a.seq.cu_seqlens ? a.seq.cu_seqlens[n + 1] - a.seq.cu_seqlens[n] : a.seq.T_uniform;
     const int seg_len = cut.seg_chunks * kC;
     const int parts = ((len + seg_len - 1) / seg_len - 1) * cut.subs;      // the last segment's are not formed
+    if (parts <= 0) return;
     const float2 f = decay_pair(a.log_decay[unit / a.m] * (float)(seg_len / cut.subs));
     const long stride = (long)units * kPieces;
     float4* at = reinterpret_cast<float4*>(cut.parts) + piece_state(cut, n, 0, units) * kPieces + piece;
@@ -869,6 +883,7 @@ struct SplitArgs {
 constexpr int kSplitAhead = 4;
 
 __global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const __grid_constant__ SplitArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const SplitPlane& p = a.p[blockIdx.y];
     const int lane = threadIdx.x & 31, heads = p.heads;
     const long n = a.rows * heads, step = (long)gridDim.x * (kSplitThr / 32) * kSplitAhead;
@@ -947,31 +962,46 @@ Cut plan(const SeqLayout& s, const int* cu_host, int units, bool bf16) {
     return best;
 }
 
+// `after`: as the programmatic dependent of the launch before, a launch of this file that it waits for itself.
+template <typename... P, typename... A>
+cudaError_t launch_as(int id, bool after, void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s,
+                      const A&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    KernelTimer kt(id, s);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <bool STATE, bool F32>
-cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, cudaStream_t s) {
+cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, bool after, cudaStream_t s) {
     static PerDevice<int> done;
     const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE, F32>, smem_bytes<F32>(), done);
     if (e != cudaSuccess) return e;
-    KernelTimer kt(STATE ? kKLinState : kKLinChunk, s);
     const dim3 grid((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(STATE ? cut.pieces() : cut.segs));
-    kda_linattn_chunk_kernel<STATE, F32><<<grid, kThr, smem_bytes<F32>(), s>>>(a, cut, maps);
-    return cudaGetLastError();
+    return launch_as(STATE ? kKLinState : kKLinChunk, after, kda_linattn_chunk_kernel<STATE, F32>, grid, kThr,
+                     smem_bytes<F32>(), s, a, cut, maps);
 }
 
 template <bool F32>
 cudaError_t launch_all(const LinArgs& a, const Cut& cut, Maps& maps, const CUtensorMap& out, cudaStream_t s) {
     if (cut.segs > 1) {
         maps.out = maps.parts;
-        cudaError_t e = launch<true, F32>(a, cut, maps, s);
+        cudaError_t e = launch<true, F32>(a, cut, maps, F32, s);
         if (e != cudaSuccess) return e;
-        KernelTimer kt(kKLinJoin, s);
         const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
-        kda_linattn_join_kernel<<<dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s>>>(a, cut);
-        e = cudaGetLastError();
+        e = launch_as(kKLinJoin, true, kda_linattn_join_kernel, dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s, a, cut);
         if (e != cudaSuccess) return e;
     }
     maps.out = out;
-    return launch<false, F32>(a, cut, maps, s);
+    return launch<false, F32>(a, cut, maps, F32 || cut.segs > 1, s);
 }
 
 // bytes of q, k and v as bf16 hi and lo
