@@ -200,25 +200,28 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
     const float r = a.r[n];
     // how many drafts hold: lane i tests draft i
     if (warp == 0) {
+        // (two rounds of reads, not four: what a draft beyond the count would need is read too)
         int count = a.n_draft ? a.n_draft[n] : drafts;
+        const int tok = lane < drafts ? a.tokens[(long)n * drafts + lane] : -1;
+        const float u = lane < drafts ? a.u[(long)n * drafts + lane] : 0.0f;
+        float p = 0.0f, q = 1.0f;
+        const bool known = tok >= 0 && tok < a.V;
+        if (known) {
+            p = load_raw<BF16>(target + (size_t)lane * a.target_stride * kElem, tok);
+            if (draft) q = load_raw<BF16>(draft + (size_t)lane * a.draft_stride * kElem, tok);
+        }
         const bool live = count >= 0;
         count = min(max(count, 0), drafts);
         bool good = false;
-        int tok = -1;
-        if (lane < count) {
-            tok = a.tokens[(long)n * drafts + lane];
-            if (tok >= 0 && tok < a.V) {
-                float p = load_raw<BF16>(target + (size_t)lane * a.target_stride * kElem, tok);
-                float q = draft ? load_raw<BF16>(draft + (size_t)lane * a.draft_stride * kElem, tok) : 1.0f;
-                // u q < p exactly: where the rounded product equals p its error decides (small ones are taken
-                // times 2^100, or that error would be lost among denormals)
-                if (fmaxf(p, q) < 0x1p-60f) {
-                    p *= 0x1p100f;
-                    q *= 0x1p100f;
-                }
-                const float u = a.u[(long)n * drafts + lane], x = __fmul_rn(u, q);
-                good = x < p || (x == p && fmaf(u, q, -x) < 0.0f);
+        if (known && lane < count) {
+            // u q < p exactly: where the rounded product equals p its error decides (small ones are taken times
+            // 2^100, or that error would be lost among denormals)
+            if (fmaxf(p, q) < 0x1p-60f) {
+                p *= 0x1p100f;
+                q *= 0x1p100f;
             }
+            const float x = __fmul_rn(u, q);
+            good = x < p || (x == p && fmaf(u, q, -x) < 0.0f);
         }
         const unsigned refused = ~__ballot_sync(0xffffffffu, good);
         const int taken = live ? min(__ffs(refused) - 1, count) : -1;

@@ -843,7 +843,8 @@ __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArg
     const int unit = (int)(piece / kPieces);
     const int len = a.seq.cu_seqlens ? a.seq.cu_seqlens[n + 1] - a.seq.cu_seqlens[n] : a.seq.T_uniform;
     const int seg_len = cut.seg_chunks * kC;
-    const int parts = ((len + seg_len - 1) / seg_len - 1) * cut.subs;      // the last segment's are not formed
+    // (the last segment's are not formed)
+    const int parts = min(((len + seg_len - 1) / seg_len - 1) * cut.subs, cut.pieces());
     if (parts <= 0) return;
     const float2 f = decay_pair(a.log_decay[unit / a.m] * (float)(seg_len / cut.subs));
     const long stride = (long)units * kPieces;

@@ -688,13 +688,13 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
  *              device current that runs the call; 40009 otherwise; where it is 0 NULL is accepted).  Its
  *              contents are overwritten: calls that share it must not overlap.
  * Dk = 128, Dv = 128 * m, m = 1..8 (40001).  o and state_out overlap nothing else of the call (40003).
- * Short prompts (bf16 below 20 tokens, f32 below 48, by the longest sequence) run the recurrence itself, in
+ * Short prompts (bf16 below 20 tokens, f32 below 32, by the longest sequence) run the recurrence itself, in
  * f32, and equal chained kda_linattn_decode calls bit for bit; longer ones run in chunks of 64 tokens on
  * the tensor cores, few long ones cut into segments.
- * Precision of the chunks: bf16 q, k and v enter exactly, f32 ones as bf16 hi + lo, within 2^-17 of an
- * element; decayed scores and keys and the state likewise enter their products within 2^-17; the state
- * itself and all sums are f32.  Against the sums of the terms' magnitudes the results are off by a few
- * 1e-6.
+ * Precision of the chunks: bf16 q, k and v enter exactly, decayed scores and keys and the state within
+ * 2^-25 of an element; the results are off by 6e-7, relative to their norm.  f32 q, k and v enter as
+ * bf16 hi + lo, and so do scores, keys and the state: within 2^-17 of an element, the results off by
+ * 7e-6.  The state itself and all sums are f32.
  * Products q k v and states must stay below 1e24 in magnitude.  A NaN or an infinity at a token reaches no
  * earlier token and no other sequence, one in v no other value column.
  */
