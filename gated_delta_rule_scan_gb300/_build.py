@@ -125,7 +125,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             for p in (NATIVE_PATH, NATIVE_STAMP):
                 if os.path.exists(p):
                     os.remove(p)
-            warnings.warn(f"_kda_native.so was not built, the low-bit calls will raise: {e}")
+            warnings.warn(f"_kda_native.so was not built, the low-bit and linear attention calls will raise: {e}")
     return LIB_PATH
 
 

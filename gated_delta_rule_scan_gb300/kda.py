@@ -24,7 +24,7 @@ if not os.path.exists(LIB_PATH):
         f"libkda.so not found at {LIB_PATH}; build it first "
         "(python -c 'import __graft_entry__ as g; g.build()')")
 _lib = ctypes.CDLL(LIB_PATH)
-try:  # built beside libkda.so, which it calls; only the low-bit calls need it
+try:  # built beside libkda.so, which it calls; the low-bit and linear attention calls need it
     if not _build.native_matches():
         raise ImportError("_kda_native.so is missing or was built for another Python or torch")
     from . import _kda_native  # noqa: E402
