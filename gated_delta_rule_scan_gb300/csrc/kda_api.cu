@@ -1103,20 +1103,24 @@ static int linattn_build(const void* q, long q_stride, const void* k, long k_str
         if (!q || !k || !v || !o) return KDA_ERR_NULL;
         if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return KDA_ERR_ALIGN;
     }
-    // what a call writes is apart from what it reads
-    const auto rows_bytes = [&](long stride, long width) {
-        return seq.total_rows == 0 ? 0 : (size_t)((seq.total_rows - 1) * stride + width) * (16 / per16);
-    };
-    const Span reads[3] = {{q, rows_bytes(q_stride, qk)}, {k, rows_bytes(k_stride, qk)}, {v, rows_bytes(v_stride, vw)}};
-    const Span writes{o, (size_t)seq.total_rows * vw * 4};
-    for (const Span& x : reads) {
-        const Span pair[2] = {x, writes};
-        if (any_overlap(pair)) return KDA_ERR_STATE_ALIAS;
-    }
     a.q = q; a.k = k; a.v = v; a.bf16 = raw_dtype == KDA_DTYPE_BF16;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.log_decay = log_decay; a.o = o; a.seq = seq; a.H = H; a.Hk = Hk; a.m = m; a.scale = scale;
     return KDA_OK;
+}
+
+// What a call writes is apart from what it reads: is `w` from q, k and v?
+static bool linattn_apart(const LinArgs& a, const Span& w) {
+    const long rows = a.seq.total_rows, qk = (long)a.Hk * kHeadDim, vw = (long)a.H * a.m * kHeadDim;
+    const auto bytes = [&](long stride, long width) {
+        return rows == 0 ? 0 : (size_t)((rows - 1) * stride + width) * (a.bf16 ? 2 : 4);
+    };
+    for (const Span& x : {Span{a.q, bytes(a.q_stride, qk)}, Span{a.k, bytes(a.k_stride, qk)},
+                          Span{a.v, bytes(a.v_stride, vw)}}) {
+        const Span pair[2] = {x, w};
+        if (any_overlap(pair)) return false;
+    }
+    return true;
 }
 
 static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_out,
@@ -1126,13 +1130,16 @@ static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_
     if (!state_out) return KDA_ERR_NULL;
     if (!aligned16(state_in) || !aligned16(state_out)) return KDA_ERR_ALIGN;
     const size_t sb = (size_t)a.seq.N * a.H * a.m * kHeadDim * kHeadDim * sizeof(float);
-    const Span states[3] = {{state_in, state_in ? sb : 0}, {state_out, sb}, {a.o, (size_t)a.seq.total_rows * a.H * a.m * kHeadDim * 4}};
-    if (any_overlap(states)) return KDA_ERR_STATE_ALIAS;
+    Span spans[4] = {{state_in, state_in ? sb : 0}, {state_out, sb},
+                     {a.o, (size_t)a.seq.total_rows * a.H * a.m * kHeadDim * 4}, {workspace, 0}};
+    if (any_overlap(spans) || !linattn_apart(a, spans[1]) || !linattn_apart(a, spans[2])) return KDA_ERR_STATE_ALIAS;
     const bool chunk = max_len(a.seq, cu_host) >= (a.bf16 ? kLinChunkMinLen : kLinChunkMinLenF32);
     if (chunk) {
         const size_t need = linattn_chunk_workspace_bytes(a.seq, cu_host, a.Hk, a.H * a.m, a.bf16 != 0);
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return KDA_ERR_ALIGN;
+        spans[3].bytes = need;
+        if (any_overlap(spans) || !linattn_apart(a, spans[3])) return KDA_ERR_STATE_ALIAS;
     }
     if (const int sd = check_stream_device(stream)) return sd;
     a.state_in = state_in;
@@ -1185,7 +1192,7 @@ int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_strid
     if (!pool) return KDA_ERR_NULL;
     if (!aligned16(pool)) return KDA_ERR_ALIGN;
     const Span spans[2] = {{pool, (size_t)P * H * Dv * kHeadDim * 4}, {o, (size_t)N * T * H * Dv * 4}};
-    if (any_overlap(spans)) return KDA_ERR_STATE_ALIAS;
+    if (any_overlap(spans) || !linattn_apart(a, spans[0]) || !linattn_apart(a, spans[1])) return KDA_ERR_STATE_ALIAS;
     if (const int sd = check_stream_device(stream)) return sd;
     a.state_in = a.state_out = pool;
     a.slots = slots; a.slots_out = slots_out; a.keep = keep; a.pool_rows = P;
@@ -1205,8 +1212,12 @@ int kda_draft_accept(const void* target, long target_stride, const void* draft, 
     if (prob_dtype != KDA_DTYPE_F32 && prob_dtype != KDA_DTYPE_BF16) return KDA_ERR_ENUM;
     if (N == 0) return KDA_OK;
     if (!target || !r || !keep || !out_tokens || (T > 1 && (!tokens || !u))) return KDA_ERR_NULL;
-    const size_t n4 = (size_t)N * 4, drafts4 = n4 * (T - 1);
-    const Span reads[] = {{tokens, drafts4}, {u, drafts4}, {r, n4}, {n_draft, n_draft ? n4 : 0}};
+    const size_t n4 = (size_t)N * 4, drafts4 = n4 * (T - 1), elem = prob_dtype == KDA_DTYPE_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(target) % elem || reinterpret_cast<uintptr_t>(draft) % elem) return KDA_ERR_ALIGN;
+    const size_t target_bytes = (((size_t)N * T - 1) * target_stride + V) * elem;
+    const size_t draft_bytes = draft ? (((size_t)N * (T - 1) - 1) * draft_stride + V) * elem : 0;
+    const Span reads[] = {{tokens, drafts4}, {u, drafts4}, {r, n4}, {n_draft, n_draft ? n4 : 0},
+                          {target, target_bytes}, {draft, draft_bytes}};
     const Span writes[2] = {{keep, n4}, {out_tokens, n4 * T}};
     if (any_overlap(writes)) return KDA_ERR_STATE_ALIAS;
     for (const Span& x : reads)

@@ -687,7 +687,8 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
  * workspace    device scratch [16B] of at least kda_linattn_workspace_bytes(...) bytes (asked for with the
  *              device current that runs the call; 40009 otherwise; where it is 0 NULL is accepted).  Its
  *              contents are overwritten: calls that share it must not overlap.
- * Dk = 128, Dv = 128 * m, m = 1..8 (40001).  o and state_out overlap nothing else of the call (40003).
+ * Dk = 128, Dv = 128 * m, m = 1..8 (40001).  o, state_out and the workspace overlap
+ * nothing else of the call (40003).
  * Short prompts (bf16 below 20 tokens, f32 below 32, by the longest sequence) run the recurrence itself, in
  * f32, and equal chained kda_linattn_decode calls bit for bit; longer ones run in chunks of 64 tokens on
  * the tensor cores, few long ones cut into segments.
@@ -721,7 +722,8 @@ int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long
  *              another row reads or an earlier row writes, is left out (40013, kda_device_status).
  * q, k, v, log_decay, o, scale   as in kda_linattn_prefill; sequence n owns rows n*T .. n*T + T-1.  o
  *              rows of padding, of rows left out and of rows t >= keep[n] are not written.
- * A T-token call equals T one-token calls bit for bit.  o overlaps nothing else of the call (40003).
+ * A T-token call equals T one-token calls bit for bit.  o and the pool overlap nothing else
+ * of the call (40003).
  */
 int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_stride, const void* v,
                        long v_stride, int raw_dtype, const float* log_decay, float* pool,

@@ -45,7 +45,8 @@ def _prefill(kda, varlen, **kw):
     (dict(si=4 * FAR + 8), 40010), (dict(so=4 * FAR + 64), 40003), (dict(o=FAR), 40003),
     (dict(o=3 * FAR + 128 * 1024 - 16), 40003), (dict(v=6 * FAR + 2048), 40003), (dict(o=5 * FAR), 40003),
     (dict(si=6 * FAR + 16), 40003), (dict(raw=0, ws=None), 40009), (dict(raw=0, wb=16), 40009),
-    (dict(raw=0, ws=7 * FAR + 8), 40010), (dict(N=0, cu_host=[0]), 0)])
+    (dict(raw=0, ws=7 * FAR + 8), 40010), (dict(k=5 * FAR + 64), 40003), (dict(raw=0, ws=FAR), 40003),
+    (dict(raw=0, ws=6 * FAR - 4096), 40003), (dict(raw=0, ws=4 * FAR), 40003), (dict(N=0, cu_host=[0]), 0)])
 def test_prefill_contract(kda, varlen, kw, status):
     if varlen and kw.get("N", 2) * kw.get("T", 64) != 128 and status == 40005:
         kw = dict(kw, cu_host=None)
@@ -82,7 +83,7 @@ def _decode(kda, **kw):
     (dict(qs=128), 40005), (dict(ks=258), 40005), (dict(raw=5), 40007), (dict(g=None), 40004),
     (dict(pool=None), 40004), (dict(o=None), 40004), (dict(v=None), 40004), (dict(pool=4 * FAR + 4), 40010),
     (dict(k=2 * FAR + 4), 40010), (dict(o=4 * FAR + 8 * 2 * 256 * 512 - 16), 40003), (dict(o=FAR + 16), 40003),
-    (dict(N=0), 0)])
+    (dict(v=4 * FAR + 4096), 40003), (dict(N=0), 0)])
 def test_decode_contract(kda, kw, status):
     assert _decode(kda, **kw) == status
 
@@ -100,7 +101,8 @@ def _accept(kda, **kw):
     (dict(ts=999), 40005), (dict(ds=999), 40005), (dict(ts=1 << 40), 40005), (dict(dt=2), 40007),
     (dict(t=None), 40004), (dict(tok=None), 40004), (dict(u=None), 40004), (dict(r=None), 40004),
     (dict(keep=None), 40004), (dict(out=None), 40004), (dict(out=3 * FAR + 8), 40003), (dict(out=FAKE), 40003),
-    (dict(keep=FAKE + 8192), 40003), (dict(nd=3 * FAR), 40003), (dict(N=0), 0)])
+    (dict(keep=FAKE + 8192), 40003), (dict(nd=3 * FAR), 40003), (dict(out=FAR + 4000), 40003), (dict(keep=2 * FAR), 40003),
+    (dict(t=FAR + 2), 40010), (dict(d=2 * FAR + 1, dt=1), 40010), (dict(N=0), 0)])
 def test_accept_contract(kda, kw, status):
     assert _accept(kda, **kw) == status
 
