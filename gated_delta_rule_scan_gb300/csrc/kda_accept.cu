@@ -132,12 +132,14 @@ __device__ __forceinline__ float4 prob4(const void* row, long i) {
 }
 
 // A lane's share of the weights b .. b + kTileElems - 1: with `runs` its 16 are consecutive, else 4 times 4 at
-// distances of 128.  Their sum.
+// distances of 128.  Their sum.  By the whole warp.  Whole tiles go two weights an instruction (64 sequences x
+// 131072: 22.9 -> 20.3 us), with max(p, max(q, 0)) - max(q, 0) for the weight, which a NaN leaves 0; a tile
+// with an infinity is summed again one by one.
 template <bool BF16>
 __device__ __forceinline__ Pair lane_sum(const Row& row, long b, long V, int lane, bool runs) {
     Pair acc;
     const int at = runs ? kPerLane * lane : 4 * lane, step = runs ? 4 : 128;
-    if (b >= 0 && b + kTileElems <= V) {
+    if (b >= 0 && b + kTileElems <= V && !(row.skip >= b && row.skip < b + kTileElems)) {
         float4 p[kPerLane / 4], q[kPerLane / 4];
 #pragma unroll
         for (int i = 0; i < kPerLane / 4; ++i) p[i] = prob4<BF16>(row.p, b + at + step * i);
@@ -151,25 +153,32 @@ __device__ __forceinline__ Pair lane_sum(const Row& row, long b, long V, int lan
                                         load_raw<BF16>(row.q, x + 2), load_raw<BF16>(row.q, x + 3));
             }
         }
+        const float2 neg = make_float2(-1.0f, -1.0f);
+        const auto sub = [&](float2 x, float2 y) { return __ffma2_rn(y, neg, x); };
+        float2 hi = make_float2(0.f, 0.f), lo = hi;
 #pragma unroll
-        for (int i = 0; i < kPerLane / 4; ++i) {
-            const float pp[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
-            const float qq[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-            const int skip = (int)(row.skip - (b + at + step * i));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float w, e;
-                weight(j == skip ? 0.0f : pp[j], qq[j], w, e);
-                acc.add(w, e);
-            }
+        for (int i = 0; i < kPerLane / 2; ++i) {
+            const float4 p4 = p[i / 2], q4 = q[i / 2];
+            float2 pp = i % 2 ? make_float2(p4.z, p4.w) : make_float2(p4.x, p4.y);
+            float2 qq = i % 2 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+            qq = make_float2(fmaxf(qq.x, 0.0f), fmaxf(qq.y, 0.0f));
+            pp = make_float2(fmaxf(pp.x, qq.x), fmaxf(pp.y, qq.y));
+            const float2 d = sub(pp, qq), de = sub(sub(pp, d), qq);
+            const float2 s = __fadd2_rn(hi, d), t = sub(s, hi);
+            lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(sub(hi, sub(s, t)), sub(d, t)), de));
+            hi = s;
         }
-    } else {
+        acc.hi = hi.x;
+        acc.lo = lo.x;
+        acc.add(hi.y, lo.y);
+        if (!__any_sync(0xffffffffu, !(acc.hi < __int_as_float(0x7f800000)))) return acc;
+        acc = Pair();
+    }
 #pragma unroll 4
-        for (int i = 0; i < kPerLane; ++i) {
-            float w, e;
-            weight_at<BF16>(row, b + (runs ? kPerLane * lane + i : 32 * i + lane), V, w, e);
-            acc.add(w, e);
-        }
+    for (int i = 0; i < kPerLane; ++i) {
+        float w, e;
+        weight_at<BF16>(row, b + (runs ? kPerLane * lane + i : 32 * i + lane), V, w, e);
+        acc.add(w, e);
     }
     return acc;
 }

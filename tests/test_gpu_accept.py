@@ -118,6 +118,25 @@ def test_edges():
     assert got[1][4, 0] == -1 and got[0][4] == 1
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lookup", [False, True])
+def test_no_numbers_in_long_rows(dtype, lookup):
+    """NaN, infinities and negative entries in rows of many whole tiles, in either side."""
+    N, T, V = 12, 2, 5120
+    target, draft, tokens, u, r, g = _case(N, T, V, dtype, 77)
+    u[:] = 1 - 2.0 ** -24
+    for i, bad in enumerate([float("nan"), float("inf"), -float("inf"), -0.5]):
+        target[:, :, 500 + 700 * i] = bad
+        draft[:, :, 600 + 700 * i] = bad
+        target[1::2, :, 900 + 700 * i] = bad         # in both
+        draft[1::2, :, 900 + 700 * i] = bad
+    tokens[:] = torch.randint(0, V, (N, 1), generator=g, dtype=torch.int32)
+    draft = None if lookup else draft
+    want = plain(target, tokens, u, r, draft, None)
+    got = _run(target, tokens, u, r, draft)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_denormal_probabilities():
     """Weights of a few times 2^-149: r times their sum may round to the sum, u q to p."""
     tiny = 2.0 ** -149
