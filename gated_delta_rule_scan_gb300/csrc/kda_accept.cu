@@ -13,7 +13,7 @@
 // the exact error of p - q among it), about 2^-45 of the sum.  (f64 has the same bits, but its additions took
 // some 600 cycles each here: 10 us of a call's 12.)
 // Measured, vocabulary 131072: one sequence 10.3 us in a stream of calls (three dependent reads, a reduction over
-// the cluster, a tile's read), 64 sequences x 4 drafts 22.5 us, 2.6 TB/s.
+// the cluster, a tile's read), 64 sequences x 4 drafts 20.3 us, 2.9 TB/s.
 #include "kda_device.cuh"
 
 namespace kda {

@@ -4,7 +4,9 @@
 // with rms(a) = a / sqrt(mean a^2 + eps) along a row.  Both sums run over a row that stays in registers
 // (8 elements a thread and step), so a row is read once and written once; h enters the second norm
 // before its rounding to the stream's type.  Bound by HBM for many rows, by the two dependent
-// reductions for one.  Measured: 4096 rows x 6144 with a gate 49.3 us, 5.1 TB/s; one row of f32 6.1 us.
+// reductions for one.  Measured: 4096 rows x 6144 with a gate 49.2 us, 5.1 TB/s (16384
+// rows: 158 us, 6.4 TB/s); one row of f32 6.1 us.  Persistent CTAs with bulk copies three rows ahead and the
+// weights in registers took 70 us: two of them on an SM do not hide a row's sums and its gate's exponentials.
 #include "kda_device.cuh"
 
 namespace kda {
