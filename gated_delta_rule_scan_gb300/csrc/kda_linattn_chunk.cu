@@ -10,11 +10,10 @@
 // e^{32 |g|}, 8e13 at |g| = 1.  Heads that decay faster (g < -1) take the parts one after the other, with
 // the powers as they stand, all of them at most 1, and a slower pipeline: there S Q^T matters to a few tens
 // of tokens at most, but overflow must not.
-// bf16 q, k and v enter as they are; what is f32 (P, Kd and the state) enters as three bf16 parts, 24 bits of
-// it: errors of 6e-7 (two parts: 3e-6).  f32 q, k and v are
-// split into bf16 hi + lo, within 2^-17, by a launch before, and so are P, Kd and the state, every product three of
-// four terms: errors of 7e-6.  (Three parts of all six do not fit tensor memory.)  The state itself stays in f32
-// registers.
+// bf16 q, k and v enter as they are; what is f32 (P, Kd and the state) enters as three bf16 parts, 24 bits of it:
+// errors of 6e-7 (two parts: 3e-6).  f32 q, k and v are split into bf16 hi + lo, within 2^-17, by a launch before,
+// and so are P, Kd and the state, every product three of four terms: errors of 7e-6.  (Three parts of all six do
+// not fit tensor memory.)  The state itself stays in f32 registers.
 //
 // A NaN or an infinity at one token does not reach the tokens before it: where q k is not seen P is 0 by
 // selection, and in v, whose products with P = 0 would be NaN, it is replaced by 0 and its value column made
@@ -38,8 +37,8 @@
 //
 // Measured: 152 heads x 4096 tokens (a CTA an SM) 164 us, 4.9 TB/s of what it reads and writes; 16 ragged
 // prompts, 64 heads, 73722 tokens: 1222 us, 5.1 TB/s, 75% of a copy's rate.  Issue slots are 64% taken, the
-// tensor pipe 56%: a chunk takes 2.3 to 2.5 us where the MMAs take 1.3, bound by the round from o to the state's
-// parts to S Q^T and by the split's instructions in it.
+// tensor pipe 56%: a chunk takes 2.0 to 2.4 us where the MMAs take 1.3, bound by the state's warps, which are
+// busy throughout: 870 cycles for V^T Kd, 1360 for the state's parts, 1540 for o.
 //
 // Few sequences and heads leave SMs idle, so long sequences are then cut into segments: a first launch
 // (STATE) forms each segment's own contribution to the state from k and v alone, in pieces where that leaves SMs
@@ -910,8 +909,8 @@ __global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const __gr
 }
 
 // Segments of a call and their pieces, by the time of their waves of CTAs in us: a chunk of the main kernel 2.3 (f32:
-// 3.4), of the state kernel 1.1 (f32: 1.9), a CTA's start and end 6, the two further launches 7.  (bf16, 4096 tokens
-// x 64 heads: whole 145 us, 2 segments 127; 8192 x 8 heads: whole 276, 16 segments 50.)
+// 3.4), of the state kernel 1.1 (f32: 1.9), a CTA's start and end 6, the two further launches 4.5.  (bf16, 4096 tokens
+// x 64 heads: whole 145 us, 2 segments of 2 pieces 113; 8192 x 8 heads: whole 272, 19 segments 47.)
 constexpr int kMaxSegs = 32;
 long most_segs(long chains, long chunks, int sms) {
     return std::max(1L, std::min({(long)kMaxSegs, chunks, 4L * sms / std::max(1L, chains)}));
@@ -934,7 +933,7 @@ long seq_chunks(const SeqLayout& s, const int* cu_host, int n) {
 bool may_cut(long chains, int sms) { return chains < 2L * sms; }
 
 Cut plan(const SeqLayout& s, const int* cu_host, int units, bool bf16) {
-    const double main_us = bf16 ? 2.3 : 3.4, state_us = bf16 ? 1.1 : 1.9, ends_us = 6.0, launches_us = 7.0;
+    const double main_us = bf16 ? 2.3 : 3.4, state_us = bf16 ? 1.1 : 1.9, ends_us = 6.0, launches_us = 4.5;
     const int sms = sm_count();
     long most = 1;
     for (int n = 0; n < s.N; ++n) most = std::max(most, seq_chunks(s, cu_host, n));
@@ -998,7 +997,8 @@ cudaError_t launch_all(const LinArgs& a, const Cut& cut, Maps& maps, const CUten
         cudaError_t e = launch<true, F32>(a, cut, maps, F32, s);
         if (e != cudaSuccess) return e;
         const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
-        e = launch_as(kKLinJoin, true, kda_linattn_join_kernel, dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s, a, cut);
+        e = launch_as(kKLinJoin, true, kda_linattn_join_kernel, dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s, a,
+                      cut);
         if (e != cudaSuccess) return e;
     }
     maps.out = out;
