@@ -105,6 +105,7 @@ struct Row {                                     // what a sequence draws from
     // is q's
     int lead;
     bool q_vec;
+    float unit;                                  // weights are taken times this power of two
     template <bool BF16>
     __device__ __forceinline__ void align() {
         constexpr int kElem = BF16 ? 2 : 4;
@@ -116,7 +117,8 @@ struct Row {                                     // what a sequence draws from
 template <bool BF16>
 __device__ __forceinline__ void weight_at(const Row& row, long i, long V, float& w, float& e) {
     const bool in = i >= 0 && i < V && i != row.skip;
-    weight(in ? load_raw<BF16>(row.p, i) : 0.0f, in && row.q ? load_raw<BF16>(row.q, i) : 0.0f, w, e);
+    weight(in ? load_raw<BF16>(row.p, i) * row.unit : 0.0f, in && row.q ? load_raw<BF16>(row.q, i) * row.unit : 0.0f,
+           w, e);
 }
 
 // 4 consecutive probabilities, their address a multiple of 4 elements
@@ -134,12 +136,12 @@ __device__ __forceinline__ float4 prob4(const void* row, long i) {
 // A lane's share of the weights b .. b + kTileElems - 1: with `runs` its 16 are consecutive, else 4 times 4 at
 // distances of 128.  Their sum.  By the whole warp.  Whole tiles go two weights an instruction (64 sequences x
 // 131072: 22.9 -> 20.3 us), with max(p, max(q, 0)) - max(q, 0) for the weight, which a NaN leaves 0; a tile
-// with an infinity is summed again one by one.
+// with an infinity is summed again one by one, and so is a row in another unit.
 template <bool BF16>
 __device__ __forceinline__ Pair lane_sum(const Row& row, long b, long V, int lane, bool runs) {
     Pair acc;
     const int at = runs ? kPerLane * lane : 4 * lane, step = runs ? 4 : 128;
-    if (b >= 0 && b + kTileElems <= V && !(row.skip >= b && row.skip < b + kTileElems)) {
+    if (b >= 0 && b + kTileElems <= V && !(row.skip >= b && row.skip < b + kTileElems) && row.unit == 1.0f) {
         float4 p[kPerLane / 4], q[kPerLane / 4];
 #pragma unroll
         for (int i = 0; i < kPerLane / 4; ++i) p[i] = prob4<BF16>(row.p, b + at + step * i);
@@ -194,7 +196,7 @@ __device__ __forceinline__ Pair ld_cluster_pair(const Pair* local, uint32_t rank
 template <bool BF16>
 __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptArgs a) {
     __shared__ __align__(8) Pair tiles[kMaxTiles];
-    __shared__ __align__(8) Pair total[2];       // of this CTA, by attempt
+    __shared__ __align__(8) Pair total[3];       // of this CTA, by attempt
     __shared__ int s_taken, s_count, s_token;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;   // the cluster is the x extent
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
     const bool refused = taken < s_count;
 
     const void* p_row = target + (size_t)taken * a.target_stride * kElem;
-    Row row{p_row, nullptr, -1, 0, true};
+    Row row{p_row, nullptr, -1, 0, true, 1.0f};
     if (refused) {
         if (draft) row.q = draft + (size_t)taken * a.draft_stride * kElem;
         else row.skip = s_token;
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
     const int spans = (int)((tile1 - tile0 + group - 1) / group);
 
     Pair before, mine, sum;
-    for (int attempt = 0; attempt < 2; ++attempt) {
+    for (int attempt = 0; attempt < 3; ++attempt) {
         for (int sp = warp; sp < spans; sp += kWarps) {
             Pair x;
             for (long t = tile0 + sp * group; t < min(tile1, tile0 + (sp + 1) * group); ++t)
@@ -292,6 +294,12 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
             if (k == rank) before = sum;
             if (k < ranks) sum = sum + of[k];
             if (k == rank) mine = sum;           // the running sum past this CTA
+        }
+        if (!(sum.hi < __int_as_float(0x7f800000))) {
+            // the total is past f32: again in a unit in which that of 2^31 weights is not (what the smallest of them
+            // lose is below 2^-180 of it)
+            row.unit = 0x1p-40f;
+            continue;
         }
         if (sum.hi > 0.0f || (row.q == nullptr && row.skip < 0)) break;
         row.q = nullptr;                         // nothing is left of p - q: p itself
