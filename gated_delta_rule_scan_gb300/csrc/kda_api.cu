@@ -1109,14 +1109,17 @@ static int linattn_build(const void* q, long q_stride, const void* k, long k_str
     return KDA_OK;
 }
 
-// What a call writes is apart from what it reads: is `w` from q, k and v?
+// What a call writes is apart from what it reads: is `w` from q, k, v, the decays, lengths, slots and counts?
 static bool linattn_apart(const LinArgs& a, const Span& w) {
     const long rows = a.seq.total_rows, qk = (long)a.Hk * kHeadDim, vw = (long)a.H * a.m * kHeadDim;
     const auto bytes = [&](long stride, long width) {
         return rows == 0 ? 0 : (size_t)((rows - 1) * stride + width) * (a.bf16 ? 2 : 4);
     };
+    const auto ints = [&](const int* p, int n) { return Span{p, p ? (size_t)n * 4 : 0}; };
     for (const Span& x : {Span{a.q, bytes(a.q_stride, qk)}, Span{a.k, bytes(a.k_stride, qk)},
-                          Span{a.v, bytes(a.v_stride, vw)}}) {
+                          Span{a.v, bytes(a.v_stride, vw)}, Span{a.log_decay, (size_t)a.H * 4},
+                          ints(a.seq.cu_seqlens, a.seq.N + 1), ints(a.slots, a.seq.N),
+                          ints(a.slots_out, a.seq.N), ints(a.keep, a.seq.N)}) {
         const Span pair[2] = {x, w};
         if (any_overlap(pair)) return false;
     }
@@ -1191,11 +1194,11 @@ int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_strid
     if (N == 0) return KDA_OK;
     if (!pool) return KDA_ERR_NULL;
     if (!aligned16(pool)) return KDA_ERR_ALIGN;
+    a.slots = slots; a.slots_out = slots_out; a.keep = keep; a.pool_rows = P;
     const Span spans[2] = {{pool, (size_t)P * H * Dv * kHeadDim * 4}, {o, (size_t)N * T * H * Dv * 4}};
     if (any_overlap(spans) || !linattn_apart(a, spans[0]) || !linattn_apart(a, spans[1])) return KDA_ERR_STATE_ALIAS;
     if (const int sd = check_stream_device(stream)) return sd;
     a.state_in = a.state_out = pool;
-    a.slots = slots; a.slots_out = slots_out; a.keep = keep; a.pool_rows = P;
     a.err = dev_err_ptr();
     return cuda_status(launch_linattn_decode(a, static_cast<cudaStream_t>(stream)));
 }
