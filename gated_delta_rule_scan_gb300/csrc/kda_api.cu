@@ -1080,7 +1080,7 @@ static constexpr long kLinChunkMinLen = 20, kLinChunkMinLenF32 = 32;
 
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype) {
     const int m = value_subheads(Dk, Dv);
-    if (m == 0 || N < 0 || total_T < 0 || H <= 0 || Hk < 1 || Hk > H) return 0;
+    if (m == 0 || N < 0 || total_T < 0 || H <= 0 || Hk < 1 || Hk > H || (raw_dtype & KDA_LINATTN_SEQ)) return 0;
     return linattn_chunk_workspace_bound(N, total_T, Hk, H * m, raw_dtype == KDA_DTYPE_BF16);
 }
 
@@ -1126,7 +1126,7 @@ static bool linattn_apart(const LinArgs& a, const Span& w) {
     return true;
 }
 
-static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_out,
+static int linattn_prefill_impl(LinArgs& a, bool seq, const float* state_in, float* state_out,
                                 const int* cu_host, void* workspace, size_t workspace_bytes,
                                 void* stream) {
     if (a.seq.N == 0) return KDA_OK;
@@ -1136,7 +1136,7 @@ static int linattn_prefill_impl(LinArgs& a, const float* state_in, float* state_
     Span spans[4] = {{state_in, state_in ? sb : 0}, {state_out, sb},
                      {a.o, (size_t)a.seq.total_rows * a.H * a.m * kHeadDim * 4}, {workspace, 0}};
     if (any_overlap(spans) || !linattn_apart(a, spans[1]) || !linattn_apart(a, spans[2])) return KDA_ERR_STATE_ALIAS;
-    const bool chunk = max_len(a.seq, cu_host) >= (a.bf16 ? kLinChunkMinLen : kLinChunkMinLenF32);
+    const bool chunk = !seq && max_len(a.seq, cu_host) >= (a.bf16 ? kLinChunkMinLen : kLinChunkMinLenF32);
     if (chunk) {
         const size_t need = linattn_chunk_workspace_bytes(a.seq, cu_host, a.Hk, a.H * a.m, a.bf16 != 0);
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
@@ -1158,9 +1158,10 @@ int kda_linattn_prefill(const void* q, long q_stride, const void* k, long k_stri
                         float scale, void* workspace, size_t workspace_bytes, void* stream) {
     if (T < 0) return KDA_ERR_SHAPE;
     LinArgs a{};
-    const int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype, log_decay, o,
+    const int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype & ~KDA_LINATTN_SEQ, log_decay, o,
                                  SeqLayout{nullptr, T, N, (long)N * T}, H, Hk, Dk, Dv, scale, a);
-    return rc ? rc : linattn_prefill_impl(a, state_in, state_out, nullptr, workspace, workspace_bytes, stream);
+    return rc ? rc : linattn_prefill_impl(a, (raw_dtype & KDA_LINATTN_SEQ) != 0, state_in, state_out, nullptr,
+                                          workspace, workspace_bytes, stream);
 }
 
 int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long k_stride,
@@ -1170,7 +1171,7 @@ int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long
                                int H, int Hk, int Dk, int Dv, float scale, void* workspace,
                                size_t workspace_bytes, void* stream) {
     LinArgs a{};
-    int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype, log_decay, o,
+    int rc = linattn_build(q, q_stride, k, k_stride, v, v_stride, raw_dtype & ~KDA_LINATTN_SEQ, log_decay, o,
                            SeqLayout{cu_seqlens, 0, N, (long)total_T}, H, Hk, Dk, Dv, scale, a);
     if (rc) return rc;
     if (N > 0) {
@@ -1178,7 +1179,8 @@ int kda_linattn_prefill_varlen(const void* q, long q_stride, const void* k, long
         rc = check_cu(cu_seqlens_host, N, total_T);
         if (rc) return rc;
     }
-    return linattn_prefill_impl(a, state_in, state_out, cu_seqlens_host, workspace, workspace_bytes, stream);
+    return linattn_prefill_impl(a, (raw_dtype & KDA_LINATTN_SEQ) != 0, state_in, state_out, cu_seqlens_host,
+                                workspace, workspace_bytes, stream);
 }
 
 int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_stride, const void* v,

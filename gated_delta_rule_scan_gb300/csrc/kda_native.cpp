@@ -370,14 +370,16 @@ struct LinRows {
 };
 
 // (q, k, v, log_decay, state_in or None, state_out, o, workspace or None, cu_seqlens or None,
-//  cu_seqlens_host or None, N, T, H, Hk, Dv, scale, stream); T: tokens of each sequence without
-// cu_seqlens, ignored with it
+//  cu_seqlens_host or None, N, T, H, Hk, Dv, scale, algo, stream); T: tokens of each sequence without
+// cu_seqlens, ignored with it; algo: KDA_ALGO_AUTO or KDA_ALGO_SEQ
 PyObject* linattn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!arity("linattn_prefill", n, 17)) return nullptr;
+    if (!arity("linattn_prefill", n, 18)) return nullptr;
     Call c;
     int64_t N = c.integer(a[10]), T = c.integer(a[11]);
     const int64_t H = c.integer(a[12]), Hk = c.integer(a[13]), Dv = c.integer(a[14]);
     const float scale = c.real(a[15]);
+    const int64_t algo = c.integer(a[16]);
+    if (!c.failed && algo != KDA_ALGO_AUTO && algo != KDA_ALGO_SEQ) return PyLong_FromLong(KDA_ERR_ENUM);
     const bool varlen = a[8] != Py_None;
     int64_t rows = N * T;
     const int* cu_host = nullptr;
@@ -407,14 +409,15 @@ PyObject* linattn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (ws != nullptr) ws_bytes = (size_t)THPVariable_Unpack(a[7]).numel();
     }
     void* cu = varlen ? c.take(a[8], "cu_seqlens", ScalarType::Int, N + 1) : nullptr;
-    void* stream = c.stream(a[16]);
+    void* stream = c.stream(a[17]);
     if (c.failed) return nullptr;
+    const int dtype = algo == KDA_ALGO_SEQ ? r.dtype | KDA_LINATTN_SEQ : r.dtype;
     return status([&] {
-        return varlen ? kda_linattn_prefill_varlen(r.q, r.qs, r.k, r.ks, r.v, r.vs, r.dtype, (float*)g,
+        return varlen ? kda_linattn_prefill_varlen(r.q, r.qs, r.k, r.ks, r.v, r.vs, dtype, (float*)g,
                                                    (float*)s_in, (float*)s_out, (float*)o, (int*)cu, cu_host,
                                                    (int)N, (int)rows, (int)H, (int)Hk, (int)kHead, (int)Dv,
                                                    scale, ws, ws_bytes, stream)
-                      : kda_linattn_prefill(r.q, r.qs, r.k, r.ks, r.v, r.vs, r.dtype, (float*)g,
+                      : kda_linattn_prefill(r.q, r.qs, r.k, r.ks, r.v, r.vs, dtype, (float*)g,
                                             (float*)s_in, (float*)s_out, (float*)o, (int)N, (int)T, (int)H,
                                             (int)Hk, (int)kHead, (int)Dv, scale, ws, ws_bytes, stream);
     });

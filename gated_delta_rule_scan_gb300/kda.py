@@ -36,6 +36,7 @@ GATE_PER_CHANNEL, GATE_PER_HEAD = 0, 1
 GATE_EXP = 2  # flag: g holds decay factors exp(log-decay)
 NORM_SILU = 4  # flag (fused entries): the RMSNorm gates with SiLU(z) instead of sigmoid(z)
 ALGO_AUTO, ALGO_SEQ, ALGO_CHUNK = 0, 1, 2
+LINATTN_SEQ = 8  # flag of the C entries' raw_dtype: what algo=ALGO_SEQ is to kda_linattn_prefill
 Q8_INT8, Q8_E4M3 = 0, 1  # 8-bit state formats
 ACT_NONE, ACT_SIGMOID, ACT_SILU = 0, 1, 2  # a block's gate
 HEAD_DIM = 128
@@ -611,35 +612,39 @@ def kda_proj_w4(x, weights, scales, outs, *, group, zeros=None, workspace=None, 
     _native("proj_w4", x, stream, x, weights, scales, zeros, outs, group, workspace)
 
 
-def kda_linattn_workspace_bytes(N, total_T, H, Hk=None, Dv=HEAD_DIM, dtype=torch.bfloat16) -> int:
+def kda_linattn_workspace_bytes(N, total_T, H, Hk=None, Dv=HEAD_DIM, dtype=torch.bfloat16,
+                                algo=ALGO_AUTO) -> int:
+    raw = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
     return int(_lib.kda_linattn_workspace_bytes(N, total_T, H, H if Hk is None else Hk, HEAD_DIM, Dv,
-                                                DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32))
+                                                raw | LINATTN_SEQ if algo == ALGO_SEQ else raw))
 
 
-def linattn_workspace(N, total_T, H, device, Hk=None, Dv=HEAD_DIM, dtype=torch.bfloat16):
+def linattn_workspace(N, total_T, H, device, Hk=None, Dv=HEAD_DIM, dtype=torch.bfloat16,
+                      algo=ALGO_AUTO):
     """A device byte buffer large enough for kda_linattn_prefill / _varlen over N sequences of
     total_T tokens in all, of q, k and v in `dtype` (None when none is needed)."""
-    nbytes = kda_linattn_workspace_bytes(N, total_T, H, Hk, Dv, dtype)
+    nbytes = kda_linattn_workspace_bytes(N, total_T, H, Hk, Dv, dtype, algo)
     return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def kda_linattn_prefill(q, k, v, log_decay, state_in, state_out, o, workspace=None, *, N, T, H,
-                        Hk=None, Dv=HEAD_DIM, scale=None, stream=None):
+                        Hk=None, Dv=HEAD_DIM, scale=None, algo=ALGO_AUTO, stream=None):
     """Linear attention with one log-decay a head over N sequences of T tokens.  q, k [N*T, Hk*128]
     and v [N*T, H*Dv], f32 or bf16, may be column slices of one tensor; state_in [N, H, Dv, 128] or
-    None (zero); o f32 [N*T, H*Dv]."""
+    None (zero); o f32 [N*T, H*Dv].  algo: ALGO_AUTO, or ALGO_SEQ for the recurrence in f32 at any
+    length, which needs no workspace."""
     _native("linattn_prefill", q, stream, q, k, v, log_decay, state_in, state_out, o, workspace, None,
             None, N, T, H, H if Hk is None else Hk, Dv,
-            HEAD_DIM ** -0.5 if scale is None else scale)
+            HEAD_DIM ** -0.5 if scale is None else scale, algo)
 
 
 def kda_linattn_prefill_varlen(q, k, v, log_decay, state_in, state_out, o, workspace, cu_seqlens,
                                cu_seqlens_host, *, H, Hk=None, Dv=HEAD_DIM, scale=None,
-                               stream=None):
+                               algo=ALGO_AUTO, stream=None):
     """kda_linattn_prefill over packed sequences (cu_seqlens: int32 device, cu_seqlens_host: CPU)."""
     _native("linattn_prefill", q, stream, q, k, v, log_decay, state_in, state_out, o, workspace,
             cu_seqlens, cu_seqlens_host, 0, 0, H, H if Hk is None else Hk, Dv,
-            HEAD_DIM ** -0.5 if scale is None else scale)
+            HEAD_DIM ** -0.5 if scale is None else scale, algo)
 
 
 def kda_linattn_decode(q, k, v, log_decay, pool, o, *, N, T, H, slots=None, slots_out=None, keep=None,

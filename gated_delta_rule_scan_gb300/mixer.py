@@ -260,9 +260,10 @@ def kda_proj_w4(*, x, weights, scales, group, zeros=None, outs=None, workspace=N
 
 def kda_linattn_prefill(*, q, k, v, log_decay, H, state_in=None, cu_seqlens=None,
                         cu_seqlens_host=None, N=None, T=None, Hk=None, Dv=None, scale=None,
-                        state_out=None, o=None, workspace=None, stream=None):
+                        algo=kda.ALGO_AUTO, state_out=None, o=None, workspace=None, stream=None):
     """Linear attention with one log-decay a head over (N, T) or packed sequences (cu_seqlens int32
-    device + cu_seqlens_host int32 CPU), from state_in (None: zero).  workspace: from
+    device + cu_seqlens_host int32 CPU), from state_in (None: zero).  algo: kda.ALGO_AUTO (long
+    prompts in chunks on the tensor cores) or kda.ALGO_SEQ (the recurrence in f32).  workspace: from
     kda.linattn_workspace (allocated here when None).  Returns a dict with o and state_out."""
     Dv = kda.HEAD_DIM if Dv is None else Dv
     rows, made = q.shape[0], []
@@ -276,9 +277,9 @@ def kda_linattn_prefill(*, q, k, v, log_decay, H, state_in=None, cu_seqlens=None
         if state_out is None:
             state_out = _made(made, _empty((n_seq, H, Dv, kda.HEAD_DIM), q))
         if workspace is None:
-            workspace = kda.linattn_workspace(n_seq, rows, H, q.device, Hk=Hk, Dv=Dv, dtype=q.dtype)
+            workspace = kda.linattn_workspace(n_seq, rows, H, q.device, Hk=Hk, Dv=Dv, dtype=q.dtype, algo=algo)
     args = (q, k, v, log_decay, state_in, state_out, o, workspace)
-    common = dict(H=H, Hk=Hk, Dv=Dv, scale=scale, stream=stream)
+    common = dict(H=H, Hk=Hk, Dv=Dv, scale=scale, algo=algo, stream=stream)
     if varlen:
         kda.kda_linattn_prefill_varlen(*args, cu_seqlens, cu_seqlens_host, **common)
     else:
