@@ -105,7 +105,6 @@ struct Row {                                     // what a sequence draws from
     // is q's
     int lead;
     bool q_vec;
-    float unit;                                  // weights are taken times this power of two
     template <bool BF16>
     __device__ __forceinline__ void align() {
         constexpr int kElem = BF16 ? 2 : 4;
@@ -117,8 +116,7 @@ struct Row {                                     // what a sequence draws from
 template <bool BF16>
 __device__ __forceinline__ void weight_at(const Row& row, long i, long V, float& w, float& e) {
     const bool in = i >= 0 && i < V && i != row.skip;
-    weight(in ? load_raw<BF16>(row.p, i) * row.unit : 0.0f, in && row.q ? load_raw<BF16>(row.q, i) * row.unit : 0.0f,
-           w, e);
+    weight(in ? load_raw<BF16>(row.p, i) : 0.0f, in && row.q ? load_raw<BF16>(row.q, i) : 0.0f, w, e);
 }
 
 // 4 consecutive probabilities, their address a multiple of 4 elements
@@ -136,12 +134,12 @@ __device__ __forceinline__ float4 prob4(const void* row, long i) {
 // A lane's share of the weights b .. b + kTileElems - 1: with `runs` its 16 are consecutive, else 4 times 4 at
 // distances of 128.  Their sum.  By the whole warp.  Whole tiles go two weights an instruction (64 sequences x
 // 131072: 22.9 -> 20.3 us), with max(p, max(q, 0)) - max(q, 0) for the weight, which a NaN leaves 0; a tile
-// with an infinity is summed again one by one, and so is a row in another unit.
+// with an infinity is summed again one by one.
 template <bool BF16>
 __device__ __forceinline__ Pair lane_sum(const Row& row, long b, long V, int lane, bool runs) {
     Pair acc;
     const int at = runs ? kPerLane * lane : 4 * lane, step = runs ? 4 : 128;
-    if (b >= 0 && b + kTileElems <= V && !(row.skip >= b && row.skip < b + kTileElems) && row.unit == 1.0f) {
+    if (b >= 0 && b + kTileElems <= V && !(row.skip >= b && row.skip < b + kTileElems)) {
         float4 p[kPerLane / 4], q[kPerLane / 4];
 #pragma unroll
         for (int i = 0; i < kPerLane / 4; ++i) p[i] = prob4<BF16>(row.p, b + at + step * i);
@@ -185,6 +183,45 @@ __device__ __forceinline__ Pair lane_sum(const Row& row, long b, long V, int lan
     return acc;
 }
 
+// The index that a row's weights give whose sum is past f32, by one warp: with all of them times 2^-40, in which unit the
+// sum of 2^31 is not (what the smallest of them lose is below 2^-180 of it).
+template <bool BF16>
+__device__ __noinline__ int draw_scaled(const Row row, long V, float r, int lane) {
+    const auto at = [&](long i) {
+        const bool in = i < V && i != row.skip;
+        Pair w;
+        weight(in ? load_raw<BF16>(row.p, i) * 0x1p-40f : 0.0f,
+               in && row.q ? load_raw<BF16>(row.q, i) * 0x1p-40f : 0.0f, w.hi, w.lo);
+        return w;
+    };
+    const auto tile_sum = [&](long b) {
+        Pair x;
+        for (int i = 0; i < kPerLane; ++i) {
+            const Pair w = at(b + 32 * i + lane);
+            x.add(w.hi, w.lo);
+        }
+        return warp_pair_sum(x);
+    };
+    Pair sum, run;
+    for (long b = 0; b < V; b += kTileElems) sum = sum + tile_sum(b);
+    const Pair aim = r * sum;
+    long b = 0;
+    for (;; b += kTileElems) {
+        const Pair x = run + tile_sum(b);
+        if (x > aim || b + kTileElems >= V) break;
+        run = x;
+    }
+    int last = -1;
+    for (long i = b; i < min(V, b + kTileElems); ++i) {
+        const Pair w = at(i);
+        if (!(w.hi > 0.0f)) continue;
+        last = (int)i;
+        run = run + w;
+        if (run > aim) break;
+    }
+    return last;
+}
+
 __device__ __forceinline__ Pair ld_cluster_pair(const Pair* local, uint32_t rank) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
@@ -196,7 +233,7 @@ __device__ __forceinline__ Pair ld_cluster_pair(const Pair* local, uint32_t rank
 template <bool BF16>
 __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptArgs a) {
     __shared__ __align__(8) Pair tiles[kMaxTiles];
-    __shared__ __align__(8) Pair total[3];       // of this CTA, by attempt
+    __shared__ __align__(8) Pair total[2];       // of this CTA, by attempt
     __shared__ int s_taken, s_count, s_token;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;   // the cluster is the x extent
@@ -253,7 +290,7 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
     const bool refused = taken < s_count;
 
     const void* p_row = target + (size_t)taken * a.target_stride * kElem;
-    Row row{p_row, nullptr, -1, 0, true, 1.0f};
+    Row row{p_row, nullptr, -1, 0, true};
     if (refused) {
         if (draft) row.q = draft + (size_t)taken * a.draft_stride * kElem;
         else row.skip = s_token;
@@ -267,7 +304,7 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
     const int spans = (int)((tile1 - tile0 + group - 1) / group);
 
     Pair before, mine, sum;
-    for (int attempt = 0; attempt < 3; ++attempt) {
+    for (int attempt = 0; attempt < 2; ++attempt) {
         for (int sp = warp; sp < spans; sp += kWarps) {
             Pair x;
             for (long t = tile0 + sp * group; t < min(tile1, tile0 + (sp + 1) * group); ++t)
@@ -295,13 +332,7 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
             if (k < ranks) sum = sum + of[k];
             if (k == rank) mine = sum;           // the running sum past this CTA
         }
-        if (!(sum.hi < __int_as_float(0x7f800000))) {
-            // the total is past f32: again in a unit in which that of 2^31 weights is not (what the smallest of them
-            // lose is below 2^-180 of it)
-            row.unit = 0x1p-40f;
-            continue;
-        }
-        if (sum.hi > 0.0f || (row.q == nullptr && row.skip < 0)) break;
+        if (!(sum.hi == 0.0f) || (row.q == nullptr && row.skip < 0)) break;
         row.q = nullptr;                         // nothing is left of p - q: p itself
         row.skip = -1;
         row.q_vec = true;
@@ -314,10 +345,14 @@ __global__ void __launch_bounds__(kThr, 2) kda_draft_accept_kernel(const AcceptA
         x.lo *= up;
         return x;
     };
-    const Pair aim = fminf(fmaxf(r, 0.0f), 0x1.fffffep-1f) * scaled(sum);
+    const float r01 = fminf(fmaxf(r, 0.0f), 0x1.fffffep-1f);
+    const Pair aim = r01 * scaled(sum);
     const auto passes = [&](const Pair& x) { return scaled(x) > aim; };
-    if (!(sum.hi > 0.0f)) {
-        if (rank == 0 && tid == 0) a.out_tokens[(long)n * a.T + taken] = -1;
+    if (!(sum.hi > 0.0f && sum.hi < __int_as_float(0x7f800000))) {       // nothing, or more than f32 holds
+        if (rank == 0 && warp == 0) {
+            const int token = sum.hi == 0.0f ? -1 : draw_scaled<BF16>(row, a.V, r01, lane);
+            if (lane == 0) a.out_tokens[(long)n * a.T + taken] = token;
+        }
     } else if (!passes(before) && passes(mine) && warp == 0) {
         // the span, the tile, the lane's 16 weights and the one of them at which the running sum passes aim.
         // (Where rounding between two ways of summing leaves aim past a piece, its last part is taken.)
