@@ -2,7 +2,8 @@
 // and value head, token by token,
 //     S <- e^g S + k_t v_t^T,    o_t = scale * S^T q_t
 // (the state is stored [value][key]).  One kernel serves the decode / verify step on a pool of states
-// and prompts of f32 or of few tokens, so that a T-token call equals T one-token calls bit for bit.
+// and prompts of few tokens (bf16 below 20, f32 below 32) or of callers who ask for it, so that a T-token call
+// equals T one-token calls bit for bit.
 //
 // A value column's recurrence needs only its own 128 state elements, so a state is cut into blocks of
 // kRows columns, one CTA each: 8 lanes own a column (16 keys a lane, four runs of 4), 4 columns a warp

@@ -1,5 +1,5 @@
-// kda_linattn_chunk.cu -- linear attention with one log-decay g a head, the chunked form for prompts, on the
-// tcgen05 tensor cores.
+// kda_linattn_chunk.cu -- linear attention with one log-decay g a head, the chunked form for bf16 prompts, on the
+// tcgen05 tensor cores; and how prompts of either type are cut (kda_linattn_chunk_f32.cu has f32's form).
 //
 // Mathematics.  Over a chunk of C = 64 tokens with incoming state S (stored [value j][key i]):
 //     O^T = scale * ( V^T P^T + e^{g (t+1)} S Q^T ),   P[t][s] = e^{g (t-s)} q_t . k_s  for s <= t,
@@ -10,14 +10,13 @@
 // e^{32 |g|}, 8e13 at |g| = 1.  Heads that decay faster (g < -1) take the parts one after the other, with
 // the powers as they stand, all of them at most 1, and a slower pipeline: there S Q^T matters to a few tens
 // of tokens at most, but overflow must not.
-// bf16 q, k and v enter as they are; what is f32 (P, Kd and the state) enters as three bf16 parts, 24 bits of it:
-// errors of 6e-7 (two parts: 3e-6).  f32 q, k and v are split into bf16 hi + lo, within 2^-17, by a launch before,
-// and so are P, Kd and the state, every product three of four terms: errors of 7e-6.  (Three parts of all six do
-// not fit tensor memory.)  The state itself stays in f32 registers.
+// q, k and v enter as they are; what is f32 (P, Kd and the state) enters as three bf16 parts, 24 bits of it: o is off
+// by 4e-7 to 8e-7 of a head's norm, most of it the tensor cores' truncated sums (two parts: 3e-6).  The state itself
+// stays in f32 registers.
 //
 // A NaN or an infinity at one token does not reach the tokens before it: where q k is not seen P is 0 by
 // selection, and in v, whose products with P = 0 would be NaN, it is replaced by 0 and its value column made
-// NaN from that token on.
+// NaN from that token on (by an infinity too).
 //
 // One CTA per (sequence, 128-wide value unit), chunk after chunk, the values on the MMA's M = 128 TMEM
 // lanes.  Shared memory carries what the tensor cores read of it at 128 bytes a cycle, so the A
@@ -25,7 +24,7 @@
 // v, transposed on the way (from shared memory as an MN-major operand it cost twice its bytes: U 140
 // cycles an MMA against 64).  B operands are q's tile as TMA brings it, P, and Kd transposed to
 // [key][token] while it is formed.  The 512 TMEM columns are full: S parts 3 x 64, V^T Kd 128, the
-// outputs 64, q k 64, v 2 x 32 (f32: S 2 x 64, v 2 x 64).
+// outputs 64, q k 64, v 2 x 32.
 // 64 tokens, not 128: the parts of P and Kd then fit beside two stages of q, k, v.
 // Warps have roles: 16 hold the state (32 f32 a thread) and write o, 8 turn k into Kd and q k into P (4 of
 // them a chunk, in turn), three issue MMAs, one the TMA loads; they meet on mbarriers only, so the loads,
@@ -44,63 +43,33 @@
 // (STATE) forms each segment's own contribution to the state from k and v alone, in pieces where that leaves SMs
 // idle, a second adds them up to the state that each segment starts from, and the third is the kernel above with
 // a CTA a segment.  The cut is chosen by a cost model (plan()).
-#include "kda_tc.cuh"
+#include "kda_linattn_chunk.cuh"
 
 #include <algorithm>
 #include <cstring>
 
 namespace kda {
 
+using namespace linattn;
+
 namespace {
 
-constexpr int kC = 64;                           // tokens of a chunk
-constexpr int kMid = kC / 2;
-constexpr int kHalf = kC * 128;                  // bytes of 64 tokens x 64 columns, 128-byte swizzle
-constexpr int kTileBytes = 2 * kHalf;            // 64 tokens x 128 columns
-constexpr int kStTile = kHeadDim * 128;          // 128 state rows x 32 keys, f32
-
-// Shared memory and tensor memory by the inputs' type.  F32: q, k and v are bf16 hi + lo themselves (split by a
-// launch before), and what they are multiplied by has two parts, so that every product is three MMAs here too (lo hi,
-// hi lo, hi hi); k and v have one stage.
-template <bool F32>
-struct Lay {
-    static constexpr int kIn = F32 ? 2 : 1;                          // parts of q, k, v
-    static constexpr int kParts = F32 ? 2 : 3;                       // of P, Kd and the state
-    static constexpr int kKvStages = F32 ? 1 : 2, kQStages = 2;
-    // barriers of k and v: a chunk's comes two chunks later again at the earliest, since its group of warps knows
-    // only of its own chunks that they have passed
-    static constexpr int kKvBars = 2;
-    static constexpr int kKvBytes = 2 * kIn * kTileBytes;            // k's parts, v's parts
-    static constexpr int kQBytes = kIn * kTileBytes;
-    static constexpr int kVAt = kIn * kTileBytes;                    // in a stage
-    static constexpr int kQAt = kKvStages * kKvBytes;
-    static constexpr int kKdBytes = kParts * kTileBytes;             // Kd's parts, two buffers
-    static constexpr int kKdAt = kQAt + kQStages * kQBytes;
-    static constexpr int kPAt = kKdAt + 2 * kKdBytes;                // P's parts, [64 t][64 s] each
-    static constexpr int kTailAt = kPAt + kParts * kHalf;
-    // TMEM columns
-    static constexpr uint32_t kTSp = 0, kTU = 64 * kParts, kTO = kTU + 128, kTSc = kTO + 64, kTVt = kTSc + 64;
-    static constexpr uint32_t kVtCols = 32 * kIn;                    // of one of v's two buffers
-    static_assert(kTVt + 2 * kVtCols <= 512, "");
-    static_assert(4 * kStTile <= 2 * kKdBytes, "");
-};
-constexpr int kTerms = 3;                        // MMAs of a product, its smallest term first
-// the part of q, k or v and that of the other factor in term x
-template <bool F32>
-__device__ constexpr int in_part(int x) { return F32 && x == 0; }
-template <bool F32>
-__device__ constexpr int other_part(int x) { return F32 ? x == 1 : 2 - x; }
-
-constexpr int kStateWarps = 16, kConvWarps = 8;
-// The first warpgroup issues the MMAs and the loads; whole warpgroups: registers move between them.
-constexpr int kUWarp = 0, kOiWarp = 1, kTmaWarp = 3, kStateWarp0 = 4;
-constexpr int kConvWarp0 = kStateWarp0 + kStateWarps;
-constexpr int kThr = 32 * (kConvWarp0 + kConvWarps);
-constexpr int kGroupWarps = 4;                   // converting warps of a chunk: two groups in turn
-constexpr int kPWarps = 3;                       // those of them with a share of P
-constexpr int kLaunchRegs = 72;
-constexpr int kStateRegs = 80, kConvRegs = 80, kOtherRegs = 24;
-static_assert(32 * (kStateWarps * kStateRegs + kConvWarps * kConvRegs + 4 * kOtherRegs) <= kThr * kLaunchRegs, "");
+constexpr int kStages = 2;
+constexpr int kPWarps = 3;                       // of the converting warps of a chunk, those with a share of P
+constexpr int kStateRegs = 80, kConvRegs = 80;
+static_assert(regs_fit(kStateRegs, kConvRegs), "");
+// barriers of k and v: a chunk's comes two chunks later again at the earliest, since its group of warps knows
+// only of its own chunks that they have passed
+constexpr int kBars = 2;
+constexpr int kKvBytes = 2 * kTileBytes, kVAt = kTileBytes;      // a stage: k, v
+constexpr int kQAt = kStages * kKvBytes;
+constexpr int kKdBytes = kParts * kTileBytes;                    // Kd's parts, two buffers
+constexpr int kKdAt = kQAt + kStages * kTileBytes;
+constexpr int kPAt = kKdAt + 2 * kKdBytes;                       // P's parts, [64 t][64 s] each
+constexpr int kTailAt = kPAt + kParts * kHalf;
+// TMEM columns; v has two buffers
+constexpr uint32_t kTSp = 0, kTU = 64 * kParts, kTO = kTU + 128, kTSc = kTO + 64, kTVt = kTSc + 64, kVtCols = 32;
+static_assert(kTVt + 2 * kVtCols <= 512 && 4 * kStTile <= 2 * kKdBytes, "");
 
 struct __align__(16) Tail {
     float pw[kC + kMid + 4];                     // e^{g n}, n = 0 .. 96
@@ -114,63 +83,8 @@ struct __align__(16) Tail {
     uint32_t tmem;
     int bad[kHeadDim];                           // by value: the first token whose v is no number
 };
-constexpr int kMaxRanked = 32;                   // packed sequences that are taken longest first
-template <bool F32>
-constexpr int smem_bytes() { return 1024 + Lay<F32>::kTailAt + (int)sizeof(Tail); }
-static_assert(smem_bytes<false>() <= kMaxBlockSmem && smem_bytes<true>() <= kMaxBlockSmem, "");
-
-// Two f32 as bf16x2 words, each the rest of those before it rounded.
-template <int PARTS>
-__device__ __forceinline__ void split(float2 x, uint32_t (&w)[PARTS]) {
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-        w[p] = *reinterpret_cast<const uint32_t*>(&h);
-        if (p + 1 < PARTS) x = __ffma2_rn(make_float2(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u)),
-                           make_float2(-1.0f, -1.0f), x);
-    }
-}
-
-// mbar_wait_bounded for two dozen warps that wait most of the time: the suspended wait is left to the
-// hardware (polling took issue slots from the warps that work), and a clock bounds it.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, int* err) {
-    unsigned long long t0;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-    for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-            : "memory");
-        if (done) return true;
-        unsigned long long t;
-        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-        if (t - t0 > 1000000000ull) break;
-    }
-    if (err) atomicOr(err, kDevErrTimeout);
-    return false;
-}
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
-    return mbar_try_wait(bar, parity) || mbar_wait_long(bar, parity, err);
-}
-
-__device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// A warp's arrival: its lanes' TMEM and shared memory accesses before it are done.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
+constexpr int kSmemBytes = 1024 + kTailAt + (int)sizeof(Tail);
+static_assert(kSmemBytes <= kMaxBlockSmem, "");
 
 // Four 8 x 8 blocks of bf16 from shared memory, transposed: lane l gets elements (2 (l % 4), l / 4) and
 // the one below of each, 8 lanes giving the addresses of a block's rows.
@@ -178,11 +92,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 // 16 lanes x 16 columns of TMEM: lane l's words 2 i and 2 i + 1 go to lanes l / 4 and l / 4 + 8, column
@@ -193,71 +102,26 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  : "memory");
 }
 
-// How the sequences are cut: segments of seg_chunks chunks, at most segs of one sequence, each in subs pieces for the
-// STATE launch; parts: [N][(segs - 1) subs][units][128][128] f32, first the pieces' contributions to the state, then
-// the states after them.
-struct Cut {
-    int seg_chunks, segs, subs;
-    float* parts;
-    __host__ __device__ int pieces() const { return (segs - 1) * subs; }
-};
-
-// Tensor maps: q, k, v (hi and lo of f32); the states as rows of 128 keys, one a value: state_in, the parts, and
-// where they go (the parts in the STATE launch, else state_out).
 struct Maps {
-    CUtensorMap q[2], k[2], v[2], in, parts, out;
+    CUtensorMap q, k, v, in, parts, out;         // out: the parts in the STATE launch, else state_out
 };
 
-// the first unit's state of a piece among the parts
-__device__ __forceinline__ long piece_state(const Cut& cut, int n, int piece, int units) {
-    return ((long)n * cut.pieces() + piece) * units;
-}
-
-// a + b is e^x: a step S <- e^x S + U is S <- a S + (b S + U).  Above a half a = 1 and b = e^x - 1, which
-// keeps a decay next to 1: rounded itself, e^x would be off by up to 2^-25 at every step.
-__device__ __forceinline__ float2 decay_pair(float x) {
-    const float lam = expf(x);
-    return lam > 0.5f ? make_float2(1.0f, expm1f(x)) : make_float2(lam, 0.0f);
-}
-
-template <bool STATE, bool F32>
+template <bool STATE>
 __global__ void __launch_bounds__(kThr, 1)
 kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__ Maps maps) {
-    using L = Lay<F32>;
-    constexpr int kParts = L::kParts, kKdBytes = L::kKdBytes;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tail& sm = *reinterpret_cast<Tail*>(base + L::kTailAt);
+    Tail& sm = *reinterpret_cast<Tail*>(base + kTailAt);
     // (shuffled from lane 0, what is the same in a warp is known to be: it goes to uniform registers)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int unit = blockIdx.x, seg = blockIdx.z;
     const int units = a.H * a.m, hv = unit / a.m, hk = hv % a.Hk;
-    int n = blockIdx.y, len;
-    long begin;
-    if (a.seq.cu_seqlens != nullptr) {
-        const int* cu = a.seq.cu_seqlens;
-        if (a.seq.N <= kMaxRanked) {             // the longest sequences first
-            const int mine = lane < a.seq.N ? cu[lane + 1] - cu[lane] : -1;
-            int rank = 0;
-            for (int k = 0; k < a.seq.N; ++k) {
-                const int other = __shfl_sync(0xffffffffu, mine, k);
-                rank += other > mine || (other == mine && k < lane);
-            }
-            n = __ffs(__ballot_sync(0xffffffffu, lane < a.seq.N && rank == n)) - 1;
-        }
-        begin = __shfl_sync(0xffffffffu, cu[n], 0);
-        len = __shfl_sync(0xffffffffu, cu[n + 1], 0) - (int)begin;
-    } else {
-        begin = (long)n * a.seq.T_uniform;
-        len = a.seq.T_uniform;
-    }
-    const int whole_len = cut.seg_chunks * kC, seg_len = STATE ? whole_len / cut.subs : whole_len;
-    if (seg > 0 && seg * (long)seg_len >= len) return;       // (the whole CTA)
-    if (STATE && (seg / cut.subs + 1) * (long)whole_len >= len) return;   // nothing follows this piece's segment
-    const bool ends = (seg + 1) * (long)seg_len >= len;
-    begin += (long)seg * seg_len;
-    len = min(len - seg * seg_len, seg_len);
+    const Part at = locate<STATE>(a.seq, cut, lane);
+    if (at.len < 0) return;                      // (the whole CTA)
+    const int n = at.n, len = at.len;
+    const long begin = at.begin;
+    const bool ends = at.ends;
     const int chunks = (len + kC - 1) / kC;
     const float g = a.log_decay[hv];
     const bool strong = g < -1.0f;
@@ -271,43 +135,31 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         tmem_relinquish();
     }
     const auto load_kv = [&](int c) {            // by one thread
-        unsigned char* s = base + c % L::kKvStages * L::kKvBytes;
-        uint64_t* bar = &sm.kv_full[c % L::kKvBars];
+        unsigned char* s = base + c % kStages * kKvBytes;
+        uint64_t* bar = &sm.kv_full[c % kBars];
         const int row = (int)(begin + (long)c * kC);
-        mbar_arrive_expect_tx(bar, L::kKvBytes);
-        for (int p = 0; p < L::kIn; ++p)
-            for (int h = 0; h < 2; ++h) {
-                const int at = p * kTileBytes + h * kHalf;
-                tma_load_2d(s + at, &maps.k[p], hk * kHeadDim + 64 * h, row, bar);
-                tma_load_2d(s + L::kVAt + at, &maps.v[p], unit * kHeadDim + 64 * h, row, bar);
-            }
+        mbar_arrive_expect_tx(bar, kKvBytes);
+        for (int h = 0; h < 2; ++h) {
+            tma_load_2d(s + h * kHalf, &maps.k, hk * kHeadDim + 64 * h, row, bar);
+            tma_load_2d(s + kVAt + h * kHalf, &maps.v, unit * kHeadDim + 64 * h, row, bar);
+        }
     };
     const auto load_q = [&](int c) {
-        unsigned char* s = base + L::kQAt + c % L::kQStages * L::kQBytes;
-        uint64_t* bar = &sm.q_full[c % L::kQStages];
-        mbar_arrive_expect_tx(bar, L::kQBytes);
-        for (int p = 0; p < L::kIn; ++p)
-            for (int h = 0; h < 2; ++h)
-                tma_load_2d(s + p * kTileBytes + h * kHalf, &maps.q[p], hk * kHeadDim + 64 * h,
-                            (int)(begin + (long)c * kC), bar);
+        unsigned char* s = base + kQAt + c % kStages * kTileBytes;
+        uint64_t* bar = &sm.q_full[c % kStages];
+        mbar_arrive_expect_tx(bar, kTileBytes);
+        for (int h = 0; h < 2; ++h)
+            tma_load_2d(s + h * kHalf, &maps.q, hk * kHeadDim + 64 * h, (int)(begin + (long)c * kC), bar);
     };
-    // Into L2: what chunk c has no stage for yet.  (Further ahead it only pushed other CTAs' out: 4 chunks cost 1% at
-    // bf16, 6% at f32.)
+    // Into L2: what chunk c has no stage for yet.  (Further ahead it only pushed other CTAs' out: 4 chunks cost 1%.)
     const auto prefetch = [&](int c) {
-        const int row = (int)(begin + (long)c * kC);
-        for (int p = 0; p < L::kIn; ++p)
-            for (int h = 0; h < 2; ++h) {
-                if (F32) {
-                    tma_prefetch_2d(&maps.k[p], hk * kHeadDim + 64 * h, row);
-                    tma_prefetch_2d(&maps.v[p], unit * kHeadDim + 64 * h, row);
-                }
-                if (!STATE) tma_prefetch_2d(&maps.q[p], hk * kHeadDim + 64 * h, row);
-            }
+        for (int h = 0; h < 2; ++h)
+            if (!STATE) tma_prefetch_2d(&maps.q, hk * kHeadDim + 64 * h, (int)(begin + (long)c * kC));
     };
     const auto first_loads = [&]() {
-        for (int c = 0; c < L::kKvStages && c < chunks; ++c) load_kv(c);
-        for (int c = 0; !STATE && c < L::kQStages && c < chunks; ++c) load_q(c);
-        if (chunks > L::kKvStages) prefetch(L::kKvStages);
+        for (int c = 0; c < kStages && c < chunks; ++c) load_kv(c);
+        for (int c = 0; !STATE && c < kStages && c < chunks; ++c) load_q(c);
+        if (chunks > kStages) prefetch(kStages);
     };
     // the next launch may be set up meanwhile; it waits for the end of this one before it reads what this one writes
     if (STATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -338,7 +190,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             mbar_init(&sm.st_free, kStateWarps);
             for (int i = 0; i < 4; ++i) mbar_init(&sm.st_out[i], 4);
             fence_mbar_init();
-            if (!F32) first_loads();
+            first_loads();
         }
         __syncwarp();
         // e^{g n}; n = 0 apart, so that a log-decay of -infinity is a plain reset
@@ -349,14 +201,13 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             sm.up[i] = a.scale * (n == 0 ? 1.0f : expf(g * (float)n));
         }
         if (lane == 0) {
-            // the launch before has written these: f32 q, k and v split, the state that a segment starts from
-            if (F32 || seg > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-            if (F32) first_loads();
+            // the launch before has written the state that a segment starts from
+            if (seg > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
             if (starts) {
                 const long st = seg > 0 ? piece_state(cut, n, seg * cut.subs - 1, units) : (long)n * units;
                 mbar_arrive_expect_tx(&sm.st_full, 4 * kStTile);
                 for (int i = 0; i < 4; ++i)
-                    tma_load_2d(base + L::kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
+                    tma_load_2d(base + kKdAt + i * kStTile, seg > 0 ? &maps.parts : &maps.in, 32 * i,
                                 (int)(st + unit) * kHeadDim, &sm.st_full);
             }
         }
@@ -368,7 +219,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         for (int p = 0; p < kParts; ++p)
 #pragma unroll
             for (int q = 4; q < 8; ++q)
-                *reinterpret_cast<uint4*>(base + L::kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + lane * 128 + ((q ^ (lane & 7)) * 16)) =
                     make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -382,23 +233,23 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // ---- loads ---------------------------------------------------------------------------
         // (in the order in which the stages come free: k and v are done with a product earlier than q)
-        for (int c = L::kKvStages; c < chunks && ok; ++c) {
-            const int was = c - L::kKvStages;
-            ok = mbar_wait(&sm.kv_free[was % L::kKvBars], (uint32_t)((was / L::kKvBars) & 1), a.err);
+        for (int c = kStages; c < chunks && ok; ++c) {
+            const int was = c - kStages;
+            ok = mbar_wait(&sm.kv_free[was % kBars], (uint32_t)((was / kBars) & 1), a.err);
             if (ok && elect_one()) {
                 load_kv(c);
                 if (c + 1 < chunks) prefetch(c + 1);
             }
             __syncwarp();
-            if (STATE || c < L::kQStages) continue;
-            ok = ok && mbar_wait(&sm.q_free[c % L::kQStages], (uint32_t)((c / L::kQStages - 1) & 1), a.err);
+            if (STATE || c < kStages) continue;
+            ok = ok && mbar_wait(&sm.q_free[c % kStages], (uint32_t)((c / kStages - 1) & 1), a.err);
             if (ok && elect_one()) load_q(c);
             __syncwarp();
         }
         if (!ok)                                 // no load may land after the CTA has left
             for (uint32_t p = 0; p < 2; ++p) {
-                for (int i = 0; i < L::kKvBars; ++i) mbar_wait(&sm.kv_full[i], p, nullptr);
-                for (int i = 0; !STATE && i < L::kQStages; ++i) mbar_wait(&sm.q_full[i], p, nullptr);
+                for (int i = 0; i < kBars; ++i) mbar_wait(&sm.kv_full[i], p, nullptr);
+                for (int i = 0; !STATE && i < kStages; ++i) mbar_wait(&sm.q_full[i], p, nullptr);
                 if (starts) mbar_wait(&sm.st_full, 0, nullptr);
             }
     } else if (warp < kTmaWarp) {
@@ -411,31 +262,29 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const uint64_t d0 = tc_smem_desc_sw128(__shfl_sync(0xffffffffu, smem_u32(base), 0));
         if (warp == kUWarp) {
             for (int c = 0; c < chunks; ++c) {
-                const int skv = c % L::kKvStages, bkv = c % L::kKvBars, sq = c % L::kQStages;
+                const int skv = c % kStages, bkv = c % kBars, sq = c % kStages;
                 const uint32_t par = (uint32_t)(c & 1);
                 // q_t . k_s, s < 32 with q on the lanes 0 .. 63, s >= 32 with q on 64 .. 127: the threads of
                 // three lane quarters then share the work on P.  (M = 128 covers twice the rows of q's tile,
                 // those behind it, or before it, being whatever lies there: their lanes are never read.)
                 if (!STATE) {
-                    ok = mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / L::kKvBars) & 1), a.err) &&
-                         mbar_wait(&sm.q_full[sq], (uint32_t)((c / L::kQStages) & 1), a.err) &&
+                    ok = mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / kBars) & 1), a.err) &&
+                         mbar_wait(&sm.q_full[sq], (uint32_t)((c / kStages) & 1), a.err) &&
                          (c == 0 || mbar_wait(&sm.sc_free, par ^ 1u, a.err));
                     if (!ok) break;
                     tc_fence_after();
                 }
-                const uint64_t k0 = tc_desc_advance(d0, skv * L::kKvBytes);
-                const uint64_t q0 = tc_desc_advance(d0, L::kQAt + sq * L::kQBytes);
+                const uint64_t k0 = tc_desc_advance(d0, skv * kKvBytes);
+                const uint64_t q0 = tc_desc_advance(d0, kQAt + sq * kTileBytes);
                 if (!STATE && elect_one()) {
 #pragma unroll 1
-                    for (int x = 0; x < 2 * (2 * L::kIn - 1); ++x) {  // hi lo, lo hi, hi hi; 64 keys each time
-                        const int kp = F32 && x < 2, qp = F32 && (x >> 1) == 1;
-                        const uint64_t q = tc_desc_advance(q0, qp * kTileBytes + (x & 1) * kHalf);
-                        const uint64_t k = tc_desc_advance(k0, kp * kTileBytes + (x & 1) * kHalf);
+                    for (int x = 0; x < 2; ++x) {         // 64 keys each time
+                        const uint64_t q = tc_desc_advance(q0, x * kHalf), k = tc_desc_advance(k0, x * kHalf);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
-                            tc_mma_ss(tmem + L::kTSc, tc_desc_advance(q, 32 * ks), tc_desc_advance(k, 32 * ks), id_sc,
+                            tc_mma_ss(tmem + kTSc, tc_desc_advance(q, 32 * ks), tc_desc_advance(k, 32 * ks), id_sc,
                                       x > 0 || ks > 0);
-                            tc_mma_ss(tmem + L::kTSc + 32, tc_desc_advance(q, 32 * ks) - (kHalf >> 4),
+                            tc_mma_ss(tmem + kTSc + 32, tc_desc_advance(q, 32 * ks) - (kHalf >> 4),
                                       tc_desc_advance(k, kHalf / 2 + 32 * ks), id_sc, x > 0 || ks > 0);
                         }
                     }
@@ -444,19 +293,19 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                     tc_commit(&sm.q_free[sq]);
                 }
                 __syncwarp();
-                const uint64_t kd = tc_desc_advance(d0, L::kKdAt + (c & 1) * kKdBytes);
-                const uint32_t vt = tmem + L::kTVt + L::kVtCols * (c & 1);
+                const uint64_t kd = tc_desc_advance(d0, kKdAt + (c & 1) * kKdBytes);
+                const uint32_t vt = tmem + kTVt + kVtCols * (c & 1);
                 ok = mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
                      (c == 0 || mbar_wait(&sm.u_free, par ^ 1u, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int x = 0; x < kTerms; ++x) {
-                        const int vp = in_part<F32>(x), p = other_part<F32>(x);
+                    for (int x = 0; x < kParts; ++x) {
+                        const int p = kParts - 1 - x;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + L::kTU, vt + 32 * vp + 8 * ks,
+                            tc_mma_ts(tmem + kTU, vt + 8 * ks,
                                       tc_desc_advance(kd, p * kTileBytes + 32 * ks), id_u, x > 0 || ks > 0);
                     }
                     tc_commit(&sm.u_full);
@@ -467,15 +316,15 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             // no arrival of the tensor pipe on a barrier of a CTA that has left: each warp sees its last
             if (ok && chunks > 0)
                 ok = STATE ? mbar_wait(&sm.kd_free[(chunks - 1) & 1], (uint32_t)(((chunks - 1) >> 1) & 1), a.err)
-                           : mbar_wait(&sm.kv_free[(chunks - 1) % L::kKvBars],
-                                       (uint32_t)(((chunks - 1) / L::kKvBars) & 1), a.err);
+                           : mbar_wait(&sm.kv_free[(chunks - 1) % kBars],
+                                       (uint32_t)(((chunks - 1) / kBars) & 1), a.err);
         } else if (STATE) {
         } else if (warp == kOiWarp) {
             for (int c = 0; c < chunks; ++c) {
-                const int st = c % L::kQStages;
-                const uint64_t q = tc_desc_advance(d0, L::kQAt + st * L::kQBytes);
+                const int st = c % kStages;
+                const uint64_t q = tc_desc_advance(d0, kQAt + st * kTileBytes);
                 const uint32_t par = (uint32_t)(c & 1);
-                ok = mbar_wait(&sm.q_full[st], (uint32_t)((c / L::kQStages) & 1), a.err) &&
+                ok = mbar_wait(&sm.q_full[st], (uint32_t)((c / kStages) & 1), a.err) &&
                      mbar_wait(&sm.sp_full, par, a.err) &&
                      mbar_wait(&sm.oa_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
                      (!strong || mbar_wait(&sm.oa_free, par, a.err));
@@ -483,12 +332,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int x = 0; x < kTerms; ++x) {
-                        const int qp = in_part<F32>(x), p = other_part<F32>(x);
+                    for (int x = 0; x < kParts; ++x) {
+                        const int p = kParts - 1 - x;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ts(tmem + L::kTO, tmem + L::kTSp + 64 * p + 8 * ks,
-                                      tc_desc_advance(q, qp * kTileBytes + (ks >> 2) * kHalf + (ks & 3) * 32), id_o,
+                            tc_mma_ts(tmem + kTO, tmem + kTSp + 64 * p + 8 * ks,
+                                      tc_desc_advance(q, (ks >> 2) * kHalf + (ks & 3) * 32), id_o,
                                       !strong || x > 0 || ks > 0);
                     }
                     tc_commit(&sm.o_full);
@@ -497,12 +346,12 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 __syncwarp();
             }
             if (ok && chunks > 0)
-                ok = mbar_wait(&sm.q_free[(chunks - 1) % L::kQStages],
-                               (uint32_t)(((chunks - 1) / L::kQStages) & 1), a.err);
+                ok = mbar_wait(&sm.q_free[(chunks - 1) % kStages],
+                               (uint32_t)(((chunks - 1) / kStages) & 1), a.err);
         } else {
             for (int c = 0; c < chunks; ++c) {
-                const uint64_t pp = tc_desc_advance(d0, L::kPAt);
-                const uint32_t vt = tmem + L::kTVt + L::kVtCols * (c & 1), par = (uint32_t)(c & 1);
+                const uint64_t pp = tc_desc_advance(d0, kPAt);
+                const uint32_t vt = tmem + kTVt + kVtCols * (c & 1), par = (uint32_t)(c & 1);
                 // (v's last quarter comes from a warp without a share of P)
                 ok = mbar_wait(&sm.p_full, par, a.err) &&
                      mbar_wait(&sm.kd_full[c & 1], (uint32_t)((c >> 1) & 1), a.err) &&
@@ -511,11 +360,11 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int x = 0; x < kTerms; ++x) {
-                        const int vp = in_part<F32>(x), p = other_part<F32>(x);
+                    for (int x = 0; x < kParts; ++x) {
+                        const int p = kParts - 1 - x;
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_ts(tmem + L::kTO, vt + 32 * vp + 8 * ks,
+                            tc_mma_ts(tmem + kTO, vt + 8 * ks,
                                       tc_desc_advance(pp, p * kHalf + 32 * ks), id_o, x > 0 || ks > 0);
                     }
                     tc_commit(&sm.oa_full[c & 1]);
@@ -541,25 +390,25 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t b0 = __shfl_sync(0xffffffffu, smem_u32(base), 0);
         for (int c = (warp - kConvWarp0) / kGroupWarps; c < chunks; c += 2) {
-            const int st = c % L::kKvStages, bkv = c % L::kKvBars;
+            const int st = c % kStages, bkv = c % kBars;
             const uint32_t pc = (uint32_t)((c >> 1) & 1);
             const int nt = min(kC, len - c * kC);
-            const uint32_t stage = b0 + st * L::kKvBytes, kd = b0 + L::kKdAt + (c & 1) * kKdBytes;
+            const uint32_t stage = b0 + st * kKvBytes, kd = b0 + kKdAt + (c & 1) * kKdBytes;
             // (in this order: the MMAs of chunk c - 2, and with them those of c - 3, are done, so that the barrier of
             // the loads is not a phase behind)
             ok = (c >= 2 ? mbar_wait(&sm.kd_free[c & 1], pc ^ 1u, a.err)
                          : !starts || mbar_wait(&sm.st_free, 0, a.err)) &&
-                 mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / L::kKvBars) & 1), a.err);
+                 mbar_wait(&sm.kv_full[bkv], (uint32_t)((c / kBars) & 1), a.err);
             if (!ok) break;
             // v^T: values of this warp's lane quarter, 16 and 16, tokens 0 .. 31 and 32 ..
             const auto v_words = [&](uint32_t (&w)[8], int h) {
-                const int vp = h >> 2, half = (h >> 1) & 1;
+                const int half = (h >> 1) & 1;
                 const int jc = 4 * quarter + 2 * (h & 1) + ((lane >> 3) & 1);     // 16-byte piece of the row
                 const int vs = 32 * half + 8 * (lane >> 4) + r;                   // + 16 for the second pair
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     ldsm4_t(*reinterpret_cast<uint32_t(*)[4]>(w + 4 * q),
-                            stage + L::kVAt + vp * kTileBytes + (jc >> 3) * kHalf + (vs + 16 * q) * 128 +
+                            stage + kVAt + (jc >> 3) * kHalf + (vs + 16 * q) * 128 +
                                 (((jc ^ vs) & 7) * 16));
                 if (nt < kC)      // rows past the sequence's end are another's: 0 times a NaN there is not 0
 #pragma unroll
@@ -569,13 +418,13 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                     }
             };
             const auto v_store = [&](const uint32_t (&w)[8], int h) {
-                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + L::kTVt + L::kVtCols * (c & 1) +
-                                       32 * (h >> 2) + 16 * ((h >> 1) & 1), w);
+                tmem_st_16x128b_x4(tl + ((uint32_t)(16 * (h & 1)) << 16) + kTVt + kVtCols * (c & 1) +
+                                       16 * ((h >> 1) & 1), w);
             };
             const __nv_bfloat162 zero2 = __floats2bfloat162_rn(0.0f, 0.0f);
             __nv_bfloat162 odd[2] = {zero2, zero2};          // 0 times v, summed: 0 unless one is no number
 #pragma unroll 1
-            for (int h = 0; h < 4 * L::kIn; ++h) {
+            for (int h = 0; h < 4; ++h) {
                 uint32_t w[8];
                 v_words(w, h);
                 v_store(w, h);
@@ -587,7 +436,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 *reinterpret_cast<const uint32_t*>(odd) | *reinterpret_cast<const uint32_t*>(odd + 1);
             if (__any_sync(0xffffffffu, (odd_bits & 0x7fff7fffu) != 0)) {
 #pragma unroll 1
-                for (int h = 0; h < 4 * L::kIn; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     uint32_t w[8];
                     v_words(w, h);
 #pragma unroll
@@ -601,9 +450,9 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 }
             }
             // Kd: tokens 16 quarter .., 8 and 8, transposed to [key][token]
-            const auto k_words = [&](uint32_t (&w)[4], int h, int q, int p) {
+            const auto k_words = [&](uint32_t (&w)[4], int h, int q) {
                 const int ic = 4 * q + (lane >> 3);                               // 16-byte piece of k's row
-                ldsm4_t(w, stage + p * kTileBytes + (ic >> 3) * kHalf + (16 * quarter + 8 * h + r) * 128 +
+                ldsm4_t(w, stage + (ic >> 3) * kHalf + (16 * quarter + 8 * h + r) * 128 +
                                (((ic ^ r) & 7) * 16));
             };
 #pragma unroll 1
@@ -611,11 +460,9 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 const int sb = 2 * quarter + h, t = 8 * sb + 2 * (lane & 3);
                 const float2 d = make_float2(sm.pw[mid + max(nt - 1 - t, 0)], sm.pw[mid + max(nt - 2 - t, 0)]);
                 const uint32_t live = t + 1 < nt ? 0xffffffffu : t < nt ? 0xffffu : 0u;
-                uint32_t kw[L::kIn][4][4];
+                uint32_t kw[4][4];
 #pragma unroll
-                for (int p = 0; p < L::kIn; ++p)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) k_words(kw[p][q], h, q, p);
+                for (int q = 0; q < 4; ++q) k_words(kw[q], h, q);
                 if (h == 1) warp_arrive(&sm.kv_free[bkv]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -623,12 +470,8 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                     uint32_t o[4][kParts];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = kw[0][q][i] & live;
-                        float2 x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-                        if constexpr (F32) {
-                            const uint32_t l = kw[1][q][i] & live;
-                            x = __fadd2_rn(x, make_float2(__uint_as_float(l << 16), __uint_as_float(l & 0xffff0000u)));
-                        }
+                        const uint32_t w = kw[q][i] & live;
+                        const float2 x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
                         split(__fmul2_rn(x, d), o[i]);
                     }
 #pragma unroll
@@ -650,7 +493,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
 #pragma unroll 1
             for (int b = 0; b < 32; b += 16) {
                 float x[16];
-                tmem_ld16(tl + L::kTSc + pcol + b, x);
+                tmem_ld16(tl + kTSc + pcol + b, x);
                 tmem_ld_wait();
                 if (strong)
 #pragma unroll
@@ -670,7 +513,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
-                        *reinterpret_cast<uint4*>(base + L::kPAt + p * kHalf + prow * 128 +
+                        *reinterpret_cast<uint4*>(base + kPAt + p * kHalf + prow * 128 +
                                                   ((((pcol + b) / 8 + q) ^ (prow & 7)) * 16)) =
                             make_uint4(o[4 * q][p], o[4 * q + 1][p], o[4 * q + 2][p], o[4 * q + 3][p]);
             }
@@ -686,7 +529,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         const int j = 32 * (warp & 3) + lane, part = (warp - kStateWarp0) >> 2;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float2 S[16];                            // times e^{mid g}
-        unsigned char* const tile = base + L::kKdAt + part * kStTile + j * 128;
+        unsigned char* const tile = base + kKdAt + part * kStTile + j * 128;
         if (starts) {
             ok = mbar_wait(&sm.st_full, 0, a.err);
             const float in = chunks > 0 ? sm.pw[mid] : 1.0f;
@@ -709,7 +552,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
                 for (int i = 0; i < 4; ++i) split(S[4 * b + i], w[i]);
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
-                    tmem_st4(tl + L::kTSp + 64 * p + 16 * part + 4 * b, {w[0][p], w[1][p], w[2][p], w[3][p]});
+                    tmem_st4(tl + kTSp + 64 * p + 16 * part + 4 * b, {w[0][p], w[1][p], w[2][p], w[3][p]});
             }
             tmem_st_wait();
             tc_fence_before();
@@ -725,7 +568,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
         for (int c = 0; c < chunks && ok; ++c, o += kC * step) {
             const uint32_t par = (uint32_t)(c & 1);
             const int nt = min(kC, len - c * kC), live = nt - 16 * part;
-            const uint32_t to = tl + L::kTO + 16 * part;
+            const uint32_t to = tl + kTO + 16 * part;
             const float2 f = nt == kC ? whole : decay_pair(g * (float)nt);
             const float2 fa2 = make_float2(f.x, f.x), fd2 = make_float2(f.y, f.y);
             ok = mbar_wait(&sm.u_full, par, a.err);
@@ -734,7 +577,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float u[16];
-                tmem_ld16(tl + L::kTU + 32 * part + 16 * b, u);
+                tmem_ld16(tl + kTU + 32 * part + 16 * b, u);
                 tmem_ld_wait();
                 if (b == 1) {
                     tc_fence_before();
@@ -814,7 +657,7 @@ kda_linattn_chunk_kernel(const LinArgs a, const Cut cut, const __grid_constant__
             warp_arrive(&sm.st_out[part]);       // one of the tile's four warps
             if ((warp & 3) == 0 && mbar_wait(&sm.st_out[part], 0, a.err) && elect_one()) {
                 const long st = STATE ? piece_state(cut, n, seg, units) : (long)n * units;
-                tma_store_2d(&maps.out, base + L::kKdAt + part * kStTile, 32 * part, (int)(st + unit) * kHeadDim);
+                tma_store_2d(&maps.out, base + kKdAt + part * kStTile, 32 * part, (int)(st + unit) * kHeadDim);
                 bulk_commit();
                 bulk_wait_read0();
             }
@@ -867,49 +710,8 @@ __global__ void __launch_bounds__(kJoinThr) kda_linattn_join_kernel(const LinArg
     }
 }
 
-// f32 rows as bf16 hi and lo, packed: a plane's hi [rows][cols], then its lo.
-constexpr int kSplitThr = 256;
-
-struct SplitPlane {
-    const float* src; uint2* hi; uint2* lo;
-    long stride; int heads;                      // elements between rows; groups of 128 in a row
-};
-struct SplitArgs {
-    SplitPlane p[3];
-    long rows;
-};
-
-// A warp takes kSplitAhead heads at a time, their loads ahead of their stores.
-constexpr int kSplitAhead = 4;
-
-__global__ void __launch_bounds__(kSplitThr) kda_linattn_split_kernel(const __grid_constant__ SplitArgs a) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const SplitPlane& p = a.p[blockIdx.y];
-    const int lane = threadIdx.x & 31, heads = p.heads;
-    const long n = a.rows * heads, step = (long)gridDim.x * (kSplitThr / 32) * kSplitAhead;
-    for (long i = ((long)blockIdx.x * (kSplitThr / 32) + (threadIdx.x >> 5)) * kSplitAhead; i < n; i += step) {
-        long row = i / heads;
-        int head = (int)(i - row * heads);
-        float4 x[kSplitAhead];
-#pragma unroll
-        for (int u = 0; u < kSplitAhead; ++u) {
-            if (i + u < n) x[u] = __ldcs(reinterpret_cast<const float4*>(p.src + row * p.stride) + head * 32 + lane);
-            if (++head == heads) { head = 0; ++row; }
-        }
-#pragma unroll
-        for (int u = 0; u < kSplitAhead; ++u) {
-            if (i + u >= n) break;
-            uint32_t w[2][2];
-            split(make_float2(x[u].x, x[u].y), w[0]);
-            split(make_float2(x[u].z, x[u].w), w[1]);
-            p.hi[(i + u) * 32 + lane] = make_uint2(w[0][0], w[1][0]);
-            p.lo[(i + u) * 32 + lane] = make_uint2(w[0][1], w[1][1]);
-        }
-    }
-}
-
 // Segments of a call and their pieces, by the time of their waves of CTAs in us: a chunk of the main kernel 2.3 (f32:
-// 3.4), of the state kernel 1.1 (f32: 1.9), a CTA's start and end 6, the two further launches 4.5.  (bf16, 4096 tokens
+// 3.9), of the state kernel 1.1 (f32: 1.5), a CTA's start and end 6, the two further launches 4.5.  (bf16, 4096 tokens
 // x 64 heads: whole 145 us, 2 segments of 2 pieces 113; 8192 x 8 heads: whole 272, 19 segments 47.)
 constexpr int kMaxSegs = 32;
 long most_segs(long chains, long chunks, int sms) {
@@ -933,7 +735,7 @@ long seq_chunks(const SeqLayout& s, const int* cu_host, int n) {
 bool may_cut(long chains, int sms) { return chains < 2L * sms; }
 
 Cut plan(const SeqLayout& s, const int* cu_host, int units, bool bf16) {
-    const double main_us = bf16 ? 2.3 : 3.4, state_us = bf16 ? 1.1 : 1.9, ends_us = 6.0, launches_us = 4.5;
+    const double main_us = bf16 ? 2.3 : 3.9, state_us = bf16 ? 1.1 : 1.5, ends_us = 6.0, launches_us = 4.5;
     const int sms = sm_count();
     long most = 1;
     for (int n = 0; n < s.N; ++n) most = std::max(most, seq_chunks(s, cu_host, n));
@@ -962,116 +764,71 @@ Cut plan(const SeqLayout& s, const int* cu_host, int units, bool bf16) {
     return best;
 }
 
-// `after`: as the programmatic dependent of the launch before, a launch of this file that it waits for itself.
-template <typename... P, typename... A>
-cudaError_t launch_as(int id, bool after, void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s,
-                      const A&... args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = after ? 1 : 0;
-    KernelTimer kt(id, s);
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <bool STATE, bool F32>
+template <bool STATE>
 cudaError_t launch(const LinArgs& a, const Cut& cut, const Maps& maps, bool after, cudaStream_t s) {
     static PerDevice<int> done;
-    const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE, F32>, smem_bytes<F32>(), done);
+    const cudaError_t e = set_smem(kda_linattn_chunk_kernel<STATE>, kSmemBytes, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.H * a.m), (unsigned)a.seq.N, (unsigned)(STATE ? cut.pieces() : cut.segs));
-    return launch_as(STATE ? kKLinState : kKLinChunk, after, kda_linattn_chunk_kernel<STATE, F32>, grid, kThr,
-                     smem_bytes<F32>(), s, a, cut, maps);
+    return launch_as(STATE ? kKLinState : kKLinChunk, after, kda_linattn_chunk_kernel<STATE>, grid, kThr, kSmemBytes, s,
+                     a, cut, maps);
 }
 
-template <bool F32>
-cudaError_t launch_all(const LinArgs& a, const Cut& cut, Maps& maps, const CUtensorMap& out, cudaStream_t s) {
-    if (cut.segs > 1) {
-        maps.out = maps.parts;
-        cudaError_t e = launch<true, F32>(a, cut, maps, F32, s);
-        if (e != cudaSuccess) return e;
-        const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
-        e = launch_as(kKLinJoin, true, kda_linattn_join_kernel, dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s, a,
-                      cut);
-        if (e != cudaSuccess) return e;
-    }
-    maps.out = out;
-    return launch<false, F32>(a, cut, maps, F32 || cut.segs > 1, s);
-}
-
-// bytes of q, k and v as bf16 hi and lo
-size_t split_bytes(long rows, int Hk, int units, bool bf16) {
-    return bf16 ? 0 : (size_t)rows * (2L * Hk + units) * kHeadDim * 4;
-}
+size_t states_bytes(long states) { return (size_t)states * kHeadDim * kHeadDim * sizeof(float); }
 
 }  // namespace
 
-// The workspace: q, k and v split (f32), then the segments' states.
-size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int Hk, int units, bool bf16) {
-    return split_bytes(seq.total_rows, Hk, units, bf16) +
-           (size_t)seq.N * plan(seq, cu_host, units, bf16).pieces() * units * kHeadDim * kHeadDim * sizeof(float);
+cudaError_t linattn::launch_join(const LinArgs& a, const Cut& cut, cudaStream_t s) {
+    const unsigned blocks = (unsigned)((long)a.H * a.m * kHeadDim * kHeadDim / 4 / kJoinThr);
+    return launch_as(kKLinJoin, true, kda_linattn_join_kernel, dim3(blocks, (unsigned)a.seq.N), kJoinThr, 0, s, a, cut);
 }
 
-// (more than any cut of total_T tokens into N sequences takes: the cut of the longest possible one)
+// The workspace: parts of q and k (f32), then the segments' states.
+size_t linattn_chunk_workspace_bytes(const SeqLayout& seq, const int* cu_host, int Hk, int units, bool bf16) {
+    return (bf16 ? 0 : f32_split_bytes(seq.total_rows, Hk)) +
+           states_bytes((long)seq.N * plan(seq, cu_host, units, bf16).pieces() * units);
+}
+
+// (more than any cut of total_T tokens into N sequences takes: the cut of the longest possible one; for f32 4 bytes an
+// element of q, k and v, which the 6 of q and k never pass)
 size_t linattn_chunk_workspace_bound(int N, long total_T, int Hk, int units, bool bf16) {
     const int sms = sm_count();
     const long chains = (long)N * units;
-    const size_t split = split_bytes(total_T, Hk, units, bf16);
+    const size_t split = bf16 ? 0 : (size_t)total_T * (2L * Hk + units) * kHeadDim * 4;
     if (!may_cut(chains, sms)) return split;
-    return split + (size_t)chains * (most_segs(chains, (total_T + kC - 1) / kC, sms) - 1) * kHeadDim * kHeadDim *
-                       sizeof(float);
+    return split + states_bytes(chains * (most_segs(chains, (total_T + kC - 1) / kC, sms) - 1));
 }
 
 cudaError_t launch_linattn_chunk(const LinArgs& a, const int* cu_host, void* workspace, cudaStream_t s) {
     const int units = a.H * a.m;
-    const long rows = a.seq.total_rows, qk = (long)a.Hk * kHeadDim, width[3] = {qk, qk, (long)units * kHeadDim};
-    const void* const in[3] = {a.q, a.k, a.v};
-    const long stride[3] = {a.q_stride, a.k_stride, a.v_stride};
+    const long rows = a.seq.total_rows, qk = (long)a.Hk * kHeadDim, vw = (long)units * kHeadDim;
     Cut cut = plan(a.seq, cu_host, units, a.bf16);
     cut.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
-                                         split_bytes(rows, a.Hk, units, a.bf16));
-    Maps maps;
-    std::memset(&maps, 0, sizeof(maps));
-    CUtensorMap* const to[3] = {maps.q, maps.k, maps.v};
-    SplitArgs sp;
-    sp.rows = rows;
-    unsigned char* at = static_cast<unsigned char*>(workspace);
-    for (int i = 0; i < 3; ++i) {
-        if (a.bf16) {
-            if (!make_tensor_map_2d_bf16_sw128(&to[i][0], in[i], rows, width[i], kC, stride[i]))
-                return cudaErrorInvalidValue;
-            continue;
-        }
-        unsigned char* const lo = at + (size_t)rows * width[i] * 2;
-        if (!make_tensor_map_2d_bf16_sw128(&to[i][0], at, rows, width[i], kC) ||
-            !make_tensor_map_2d_bf16_sw128(&to[i][1], lo, rows, width[i], kC))
-            return cudaErrorInvalidValue;
-        sp.p[i] = SplitPlane{static_cast<const float*>(in[i]), reinterpret_cast<uint2*>(at),
-                             reinterpret_cast<uint2*>(lo), stride[i], (int)(width[i] / kHeadDim)};
-        at = lo + (size_t)rows * width[i] * 2;
-    }
-    const auto states = [&](CUtensorMap* m, const float* base, long seqs) {
+                                         (a.bf16 ? 0 : f32_split_bytes(rows, a.Hk)));
+    StateMaps states;
+    std::memset(&states, 0, sizeof(states));
+    const auto rows_of = [&](CUtensorMap* m, const float* base, long seqs) {
         return make_tensor_map_2d_f32_sw128(m, base, seqs * units * kHeadDim, kHeadDim, kHeadDim);
     };
-    CUtensorMap out;
-    if ((a.state_in != nullptr && !states(&maps.in, a.state_in, a.seq.N)) || !states(&out, a.state_out, a.seq.N) ||
-        (cut.segs > 1 && !states(&maps.parts, cut.parts, (long)a.seq.N * cut.pieces())))
+    if ((a.state_in != nullptr && !rows_of(&states.in, a.state_in, a.seq.N)) ||
+        !rows_of(&states.out, a.state_out, a.seq.N) ||
+        (cut.segs > 1 && !rows_of(&states.parts, cut.parts, (long)a.seq.N * cut.pieces())))
         return cudaErrorInvalidValue;
-    if (a.bf16) return launch_all<false>(a, cut, maps, out, s);
-    {
-        KernelTimer kt(kKLinSplit, s);
-        const long blocks = (rows * units + kSplitThr / 32 * kSplitAhead - 1) / (kSplitThr / 32 * kSplitAhead);
-        kda_linattn_split_kernel<<<dim3((unsigned)std::min(blocks, 152L * 8), 3), kSplitThr, 0, s>>>(sp);
-        const cudaError_t e = cudaGetLastError();
+    if (!a.bf16) return launch_chunks_f32(a, cut, states, workspace, s);
+    Maps maps;
+    if (!make_tensor_map_2d_bf16_sw128(&maps.q, a.q, rows, qk, kC, a.q_stride) ||
+        !make_tensor_map_2d_bf16_sw128(&maps.k, a.k, rows, qk, kC, a.k_stride) ||
+        !make_tensor_map_2d_bf16_sw128(&maps.v, a.v, rows, vw, kC, a.v_stride))
+        return cudaErrorInvalidValue;
+    maps.in = states.in;
+    maps.parts = maps.out = states.parts;
+    if (cut.segs > 1) {
+        cudaError_t e = launch<true>(a, cut, maps, false, s);
+        if (e == cudaSuccess) e = launch_join(a, cut, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_all<true>(a, cut, maps, out, s);
+    maps.out = states.out;
+    return launch<false>(a, cut, maps, cut.segs > 1, s);
 }
 
 }  // namespace kda

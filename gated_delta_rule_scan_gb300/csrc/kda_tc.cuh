@@ -92,6 +92,22 @@ __device__ __forceinline__ uint64_t tc_smem_desc_sw128(uint32_t smem_addr) {
     return d;
 }
 
+// The same for an MN-major tile written by a TMA load in the 128-byte swizzle: k rows of 128 bytes (64
+// elements of M or N), 8-row groups 1024 bytes apart (SBO), the next 64 elements of M or N in a tile
+// `atom` bytes further (LBO).  The K-step ks of 16 rows starts 2048 * ks bytes further.
+__device__ __forceinline__ uint64_t tc_smem_desc_sw128_mn(uint32_t smem_addr, uint32_t atom) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((atom >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Added to an instruction descriptor: B is MN-major.
+constexpr uint32_t kTcBMajorMN = 1u << 16;
+
 // Instruction descriptor, kind::f16: f16 A and B, f32 accumulator, both K-major, dense.
 __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N) {
     return (1u << 4)                    // D format: f32 (A and B format fields 0: f16)

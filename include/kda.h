@@ -692,13 +692,13 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
  * Short prompts (bf16 below 20 tokens, f32 below 32, by the longest sequence) run the recurrence itself, in
  * f32, and equal chained kda_linattn_decode calls bit for bit; longer ones run in chunks of 64 tokens on
  * the tensor cores, few long ones cut into segments.  With KDA_LINATTN_SEQ or-ed into raw_dtype prompts of any
- * length run the recurrence, without a workspace (the size query with the flag gives 0): the choice for f32 q, k
- * and v that have to count with all their bits, and for a sequence's results not to depend on the others of its
- * batch (16384 f32 tokens x 32 heads: 3.9 ms against 0.58).
- * Precision of the chunks: bf16 q, k and v enter exactly, decayed scores and keys and the state within
- * 2^-25 of an element; the results are off by 6e-7, relative to their norm.  f32 q, k and v enter as
- * bf16 hi + lo, and so do scores, keys and the state: within 2^-17 of an element, the results off by
- * 7e-6.  The state itself and all sums are f32.
+ * length run the recurrence, without a workspace (the size query with the flag gives 0): the choice for f32 sums
+ * rounded to nearest throughout, and for a sequence's results not to depend on the others of its
+ * batch (16384 f32 tokens x 32 heads: 3.9 ms against 0.59).
+ * Precision of the chunks: bf16 q, k and v enter exactly; f32 ones, what is formed of them (scores, decayed keys or
+ * values) and the state as three bf16 parts, within 2^-24 of an element.  The state itself and all sums are f32; the
+ * tensor cores truncate theirs.  Measured, relative to a head's norm: o of bf16 off by 4e-7 to 8e-7, of f32 by 2e-7 to
+ * 5e-7, states by 1e-7 to 5e-7; the recurrence by 1e-7 to 3e-7, the more the longer a head remembers.
  * Products q k v and states must stay below 1e24 in magnitude.  A NaN or an infinity at a token reaches no
  * earlier token and no other sequence, one in v no other value column.
  */
