@@ -1075,7 +1075,8 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
 
 // Prompts take the chunked form when the longest has at least this many tokens.  Measured crossover, 4 to 4096
 // (sequence, head) pairs: bf16 between 16 and 24 tokens (4 sequences x 64 heads, 16 tokens: 18 us against 19,
-// 24: 25 against 19), f32 between 24 and 32 (24: 25 against 26, 32: 32 against 26).
+// 24: 25 against 19), f32 about 32 (4 x 64 heads, 32 tokens: 31 us against 23; 2 x 8 heads, 32: 10 against 11, 40: 12
+// against 11).
 static constexpr long kLinChunkMinLen = 20, kLinChunkMinLenF32 = 32;
 
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype) {

@@ -171,6 +171,10 @@ kda_linattn_chunk_f32_kernel(const LinArgs a, const Cut cut, const __grid_consta
             for (int i = 0; i < 4; ++i) mbar_init(&sm.st_out[i], 4);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             fence_mbar_init();
+            for (int p = 0; p < kParts; ++p) {
+                prefetch_tensormap(&maps.k[p]);
+                if (!STATE) prefetch_tensormap(&maps.q[p]);
+            }
         }
         __syncwarp();
         // (n = 0 apart, so that a log-decay of -infinity is a plain reset)
