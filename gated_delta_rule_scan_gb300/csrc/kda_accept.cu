@@ -11,9 +11,10 @@
 // Which index is drawn must not hang on the order of summation: next to a border an f32 running sum
 // over a flat row is off by several indices.  All sums are of f32 pairs (a value and what its rounding left,
 // the exact error of p - q among it), about 2^-45 of the sum.  (f64 has the same bits, but its additions took
-// some 600 cycles each here: 10 us of a call's 12.)
+// some 600 cycles each here: 10 us of a call's 12.)  A row of finite weights whose sum is past f32 is drawn from by one
+// warp, in another unit.
 // Measured, vocabulary 131072: one sequence 10.3 us in a stream of calls (three dependent reads, a reduction over
-// the cluster, a tile's read), 64 sequences x 4 drafts 20.3 us, 2.9 TB/s.
+// the cluster, a tile's read), 64 sequences x 4 drafts 19.3 us, 3.0 TB/s.
 #include "kda_device.cuh"
 
 namespace kda {

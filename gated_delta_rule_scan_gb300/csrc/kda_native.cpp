@@ -3,8 +3,9 @@
 // attention, the verification of drafts and the norms around a block.  One
 // token's kernels run a few microseconds; checking and unpacking 17 to 28 tensors attribute by
 // attribute in Python took 9 to 16 us a call, here it takes about one.  Each function checks that
-// every tensor is a contiguous CUDA tensor of the right type and size on one device (ValueError or
-// TypeError otherwise), calls the C entry of the same name and returns its status.  What torch throws
+// every tensor is a CUDA tensor of the right type and size on one device, contiguous but for what may
+// have its rows apart (linear attention's q, k and v, the probabilities) (ValueError or TypeError
+// otherwise), calls the C entry of the same name and returns its status.  What torch throws
 // on the way (a tensor without storage or strides) leaves as RuntimeError.
 #define PY_SSIZE_T_CLEAN
 #include <c10/cuda/CUDAStream.h>

@@ -699,8 +699,11 @@ int kda_proj_w4(const void* x, int x_dtype, int t, int in_f, int n_weights,
  * values) and the state as three bf16 parts, within 2^-24 of an element.  The state itself and all sums are f32; the
  * tensor cores truncate theirs.  Measured, relative to a head's norm: o of bf16 off by 4e-7 to 8e-7, of f32 by 2e-7 to
  * 5e-7, states by 1e-7 to 5e-7; the recurrence by 1e-7 to 3e-7, the more the longer a head remembers.
- * Products q k v and states must stay below 1e24 in magnitude.  A NaN or an infinity at a token reaches no
- * earlier token and no other sequence, one in v no other value column.
+ * The chunks take magnitudes (v, products q k v, states) up to 1e24; below 1e-20 heads with log-decays next to -1 lose
+ * bits, below 1e-24 most of them.  A NaN or an infinity at a token reaches no earlier token and no other sequence, one
+ * in v or in the state no other value column; an infinity in v makes its column's outputs and state NaN from there on
+ * (in the recurrence what the arithmetic gives).  A sequence's bits depend on the others of its call: the form goes by
+ * the longest, the cut into segments by all.
  */
 #define KDA_LINATTN_SEQ 8
 size_t kda_linattn_workspace_bytes(int N, int total_T, int H, int Hk, int Dk, int Dv, int raw_dtype);
@@ -753,8 +756,11 @@ int kda_linattn_decode(const void* q, long q_stride, const void* k, long k_strid
  * n_draft      int32 [N]: drafts of each sequence, at most T-1, or NULL: T-1 of all; a negative entry
  *              is padding: keep 0, no tokens.
  * T = 1..16 (1: plain sampling; tokens, u and draft are not read), N <= 65535, V >= 1 (40005).
- * Nothing needs to be normalised.  A drafted id outside the vocabulary is refused.  A weight that is
- * negative, NaN or infinite counts as 0; where no weight is left the new token is -1.
+ * The draw takes weights of any scale (a total past f32 too).  The test u q < p and max(p - q, 0) need target and draft
+ * on one scale, a lookup's q = 1 a target that sums to 1: unnormalised rows are for T = 1.
+ * A drafted id outside the vocabulary is refused.  An entry of draft that is negative or NaN weighs as 0; a weight that
+ * is negative, NaN or infinite counts as 0; where none is left the new token is -1.  (The test takes p and q as they
+ * are: an infinite p holds, a NaN is refused.)
  * Sums are exact to about 2^-45 of the row's total.  keep and out_tokens overlap nothing else (40003).
  */
 int kda_draft_accept(const void* target, long target_stride, const void* draft, long draft_stride,
@@ -775,8 +781,8 @@ int kda_draft_accept(const void* target, long target_stride, const void* draft, 
  * norm_w       [F] f32;  z in z_dtype, or NULL: not written (then norm_w may be NULL).  z may be the
  *              same buffer as y or as a gate per row, in the same type.
  * F            a multiple of 8, 8 .. 16384; rows 0 .. 2^31-1 (40005).  All pointers [16B].
- * h is rounded to its type after the second norm has taken it.  Other overlaps of h or z with an
- * input, or with each other, return 40003.
+ * h is rounded to its type after the second norm has taken it.  Squares are summed in f32: entries of y and h beyond
+ * 1e17 in magnitude overflow them.  Other overlaps of h or z with an input, or with each other, return 40003.
  */
 #define KDA_ACT_NONE 0
 #define KDA_ACT_SIGMOID 1

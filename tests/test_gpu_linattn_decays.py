@@ -71,3 +71,24 @@ def test_decays(lengths, cut, size, Hk, dtype):
             om, lm = _closed(*(x.abs() for x in a), gh, S[n, h].double().abs(), D ** -0.5)
             _check(head(out["o"], h), o, om, 12 * 2.0 ** -23 + more, tol, ("o", n, DECAYS[h]))
             _check(out["state_out"][n, h], last, lm, 8.5 * 2.0 ** -23 + more, tol, ("state", n, DECAYS[h]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [5, 64, 100, 1500])
+def test_minus_infinity_forgets_everything(T, dtype):
+    """A log-decay of -infinity beside an ordinary one: each token sees itself alone, the state is the last token's."""
+    from gated_delta_rule_scan_gb300 import kda, mixer
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    q, k, v = (torch.randn(T, 2 * D, generator=gen, device="cuda").to(dtype) for _ in range(3))
+    S = torch.randn(1, 2, D, D, generator=gen, device="cuda")
+    g = torch.tensor([-float("inf"), -0.1], device="cuda")
+    out = mixer.kda_linattn_prefill(q=q, k=k, v=v, log_decay=g, H=2, N=1, T=T, state_in=S)
+    torch.cuda.synchronize()
+    assert kda.kda_device_status() == 0 and torch.isfinite(out["o"]).all()
+    a = [x[:, :D].double() for x in (q, k, v)]
+    o = D ** -0.5 * (a[0] * a[1]).sum(1, keepdim=True) * a[2]
+    # (q k summed over 128 keys, its 8 largest truncated sums of 2^-23, and v's product)
+    mag = D ** -0.5 * (a[0] * a[1]).abs().sum(1, keepdim=True) * a[2].abs()
+    assert bool(((out["o"][:, :D].double() - o).abs() <= 64 * 2.0 ** -23 * mag).all())
+    last = a[2][-1][:, None] * a[1][-1][None]
+    assert bool(((out["state_out"][0, 0].double() - last).abs() <= 8 * 2.0 ** -23 * last.abs()).all())
