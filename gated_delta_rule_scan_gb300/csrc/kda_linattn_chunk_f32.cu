@@ -26,10 +26,10 @@
 // The warps' roles are those of the bf16 form: 16 hold the state and write o, 8 convert v and the scores, three issue
 // MMAs, one the loads.  Long sequences of few heads are cut into segments as there.
 //
-// Measured: 16384 tokens x 32 heads 588 us (the split 209, at a copy's rate, pieces' states 107, their sums 10, chunks
-// 273), off by 4.2e-7; 16 x 4096 tokens x 64 heads 3.52 ms, 5.8 TB/s of what the chunks read and write.  With every SM
+// Measured: 16384 tokens x 32 heads 579 us (the split 209, at a copy's rate, pieces' states 107, their sums 10, chunks
+// 273), off by 2.9e-7, plain f32 sums by 2.6e-7; 16 x 4096 tokens x 64 heads 3.52 ms, 5.8 TB/s of what the chunks read and write.  With every SM
 // busy a chunk takes 8150 cycles and waits for v from memory; what its MMAs take, one after the other, is 6800: the
-// scores 2500, the update 1500, S' q 1900, V' P 900.  Two bf16 parts of everything took as long and were off by 6.6e-6.
+// scores 2500, the update 1500, S' q 1900, V' P 900.  Two bf16 parts of everything took as long, off by 6.6e-6.
 // v converted by four warps a chunk in turn, 16 tokens at a time, took 808 us; the scores with M = 128, half of its
 // rows unused, 604.
 #include "kda_linattn_chunk.cuh"
