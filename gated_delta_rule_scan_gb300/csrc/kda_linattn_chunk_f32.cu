@@ -63,7 +63,7 @@ struct __align__(16) Tail {
     float down[kC];                              // v's factors: e^{g (31-s)}
     float up[kC];                                // the outputs': scale * e^{g (t-31)}, or scale * e^{g (t+1)}
     uint64_t k_full[2], k_free[2], q_full[2], q_free[2];
-    // (two each, by the chunk's parity: a converting group sees every other chunk)
+    // (two each, by the chunk's parity: some wait for a chunk's only after the next one's may have come)
     uint64_t v_full[2], v_free[2], vu_full[2], sc_full[2], oa_full[2];
     uint64_t sc_free, u_full, u_free, sp_full, p_full, os_full, oa_free, o_full, o_free;
     uint64_t st_full, st_free, st_out[4];        // the state on its way in and out
